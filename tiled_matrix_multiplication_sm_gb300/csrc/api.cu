@@ -174,6 +174,12 @@ int check_common(int M, int N, int K, const void* A, long lda, const void* B, lo
 
 namespace tgemm {
 unsigned long long wait_limit_ns() { return (unsigned long long)g_wait_limit_ns.load(); }
+int device_sms(int* num_sms) {
+    DeviceInfo dev;
+    const int st = current_device_info(&dev);
+    if (st == TGEMM_OK) *num_sms = dev.num_sms;
+    return st;
+}
 }  // namespace tgemm
 
 namespace {

@@ -210,6 +210,9 @@ cudaError_t repack_rows2(const RepackJob& a, const RepackJob& b, int esz, cudaSt
 // The bound on any single wait inside the tensor-core kernels, as last set
 // by gemm_set_wait_limit_ns (default 2 s).
 unsigned long long wait_limit_ns();
+// SM count of the current device: TGEMM_OK, TGEMM_ERR_UNSUPPORTED (not
+// sm_103) or TGEMM_ERR_CUDA.
+int device_sms(int* num_sms);
 
 // ---- shared helper (sgemm_f32.cu) -----------------------------------------
 // The K == 0 product: C = beta * C_old + bias (zeros for the default rule).
