@@ -4,6 +4,7 @@
 
 #include "../../include/tgemm.h"
 #include "tgemm_internal.h"
+#include "mx4_internal.h"
 
 #include <algorithm>
 #include <atomic>
@@ -174,6 +175,8 @@ int check_common(int M, int N, int K, const void* A, long lda, const void* B, lo
 
 namespace tgemm {
 unsigned long long wait_limit_ns() { return (unsigned long long)g_wait_limit_ns.load(); }
+int debug_stall() { return g_debug_stall.load(); }
+void* tensor_map_encoder() { return encode_fn(); }
 int device_sms(int* num_sms) {
     DeviceInfo dev;
     const int st = current_device_info(&dev);
@@ -841,9 +844,11 @@ int gemm_device_status(cudaStream_t stream) {
     DeviceInfo dev;
     int st = current_device_info(&dev);
     if (st != TGEMM_OK) return st;
-    int v = 0;
-    if (tgemm::tc_read_and_clear_status(&v, stream) != cudaSuccess) return TGEMM_ERR_CUDA;
-    return v == 0 ? TGEMM_OK : TGEMM_ERR_DEVICE_TIMEOUT;
+    int v = 0, v4 = 0;           // the 4-bit kernels' word is their own
+    if (tgemm::tc_read_and_clear_status(&v, stream) != cudaSuccess ||
+        tgemm::mx4_read_and_clear_status(&v4, stream) != cudaSuccess)
+        return TGEMM_ERR_CUDA;
+    return v == 0 && v4 == 0 ? TGEMM_OK : TGEMM_ERR_DEVICE_TIMEOUT;
 }
 
 int gemm_tc_peak(int in_type, int pair, long iters, double* flop_per_clk_sm, double* tflops,

@@ -99,6 +99,11 @@ cudaError_t mx4_pack(int rows, int cols, int fmt, const uint8_t* src_codes, long
 // ---- products (mx4_gemm.cu, mx4_weights.cu)
 cudaError_t mx4_gemm(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B, int fmt,
                      const Mx4Out& out, int num_sms, cudaStream_t s);
+// The K == 0 product: C = beta * C_old + bias.
+cudaError_t mx4_empty_sum(int M, int N, const Mx4Out& out, cudaStream_t s);
+// The device address of these kernels' status word on the current device.
+cudaError_t mx4_status_word(int** word);
+cudaError_t mx4_read_and_clear_status(int* status, cudaStream_t s);
 cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                         const Mx4Out& out, int num_sms, cudaStream_t s);
 

@@ -210,6 +210,10 @@ cudaError_t repack_rows2(const RepackJob& a, const RepackJob& b, int esz, cudaSt
 // The bound on any single wait inside the tensor-core kernels, as last set
 // by gemm_set_wait_limit_ns (default 2 s).
 unsigned long long wait_limit_ns();
+// Whether gemm_set_debug_stall is on.
+int debug_stall();
+// cuTensorMapEncodeTiled, or nullptr.
+void* tensor_map_encoder();
 // SM count of the current device: TGEMM_OK, TGEMM_ERR_UNSUPPORTED (not
 // sm_103) or TGEMM_ERR_CUDA.
 int device_sms(int* num_sms);
