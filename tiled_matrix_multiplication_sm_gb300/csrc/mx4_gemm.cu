@@ -273,7 +273,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
-        if (lane == 0 && leader) {
+        // The whole warp runs the loop, so that addresses and descriptors are
+        // uniform values; one elected lane issues.
+        if (leader) {
             int g = 0, it = 0;
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
@@ -281,16 +283,18 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 // memory (and with them all of the tile before it). Single:
                 // the tile two before, which used this accumulator.
                 if (PAIR ? it >= 1 : it >= 2)
-                    if (!mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
-                                               (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait))
+                    if (!__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
+                                                               (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait)))
                         break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + ((it & 1) ? S::ACC1 : 0);
                 const uint32_t sfa = tmem_base + S::SF, sfb = sfa + S::SF_TILES * 4;
                 for (int kb = 0; kb < p.kblocks; ++kb, ++g) {
                     const int s = g % STAGES;
-                    if (!mbar_wait(smem_u32(&sy->full[s]), (uint32_t)(g / STAGES) & 1u, wait)) { ok = false; break; }
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), (uint32_t)(g / STAGES) & 1u, wait));
+                    if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
                     const uint32_t sf = scales0 + s * (S::SFA_BYTES + S::SFB_BYTES);
 #pragma unroll
                     for (int k = 0; k < S::SF_TILES; ++k) {
@@ -311,10 +315,12 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                                            sfb + tile * 4 * (S::TN / 128), (kb | k) != 0);
                     }
                     tc_commit<PAIR>(smem_u32(&sy->empty[s]));
+                    if (kb == p.kblocks - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                    }
+                    __syncwarp();
                 }
-                if (ok) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
             }
-            tc_commit<PAIR>(smem_u32(&sy->drain));
+            if (elect_one()) tc_commit<PAIR>(smem_u32(&sy->drain));
             mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
         __syncwarp();
