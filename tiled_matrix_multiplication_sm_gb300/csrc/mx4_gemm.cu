@@ -95,86 +95,89 @@ __device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int
 // Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
-// Drains this warp's 32 rows of a tile. `first`: the chunk to begin with;
-// release() is called once FREE_FIRST columns have left tensor memory.
+// Drains this warp's 32 rows of a tile, 64 columns a turn. `last_first`: the
+// last 64 columns, which the next tile's accumulator shares, go first.
+// release() is called as soon as FREE_FIRST columns have left tensor memory.
 template <typename S, typename TC, typename Release>
 __device__ __forceinline__ void drain_tile(const Params& p, const CUtensorMap* tmC, uint32_t tmem,
                                            uint8_t* bufs, int row0, int col0, bool last_first,
-                                           float ga, float gb, int& turn, Release release) {
-    constexpr int CW = 128 / (int)sizeof(TC);             // columns of a 128-byte chunk
-    constexpr int NCH = S::TN / CW, REL = S::FREE_FIRST / CW;
+                                           float ga, float gb, Release release) {
+    constexpr int W = 64;
+    constexpr int TURNS = S::TN / W, REL = S::FREE_FIRST / W;
     const int lane = threadIdx.x & 31;
     const Mx4Out& o = p.out;
 #pragma unroll 1
-    for (int i = 0; i < NCH; ++i) {
-        const int ch = last_first ? (i + NCH - REL) % NCH : i;
-        const int col = col0 + ch * CW;
-        const bool live = col < p.N;
+    for (int i = 0; i < TURNS; ++i) {
+        const int part = last_first ? (i == 0 ? TURNS - 1 : i - 1) : i;
+        const int col = col0 + part * W;
+        uint32_t r[2][32];
+        tmem_ld32(tmem + (uint32_t)(part * W), r[0]);
+        tmem_ld32(tmem + (uint32_t)(part * W + 32), r[1]);
+        tmem_wait_ld(r[0]);
+        tmem_wait_ld(r[1]);
+        if (i == REL - 1) release();
         if (p.tma_c) {
-            uint8_t* buf = bufs + (turn & 1) * BUF_BYTES;
-            ++turn;
-            if (lane == 0) tma_store_wait_read<1>();
+            // FP32: two boxes of 32 columns, BF16: one of 64. The previous
+            // turn's boxes have to have left the buffers.
+            if (lane == 0) tma_store_wait_read<0>();
             __syncwarp();
 #pragma unroll
-            for (int h = 0; h < CW / 32; ++h) {
-                uint32_t r[32];
-                tmem_ld32(tmem + (uint32_t)(ch * CW + h * 32), r);
-                tmem_wait_ld(r);
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    float v = __uint_as_float(r[j]) * ga * gb * o.alpha;
+                    float v = __uint_as_float(r[h][j]) * ga * gb * o.alpha;
                     if (o.bias != nullptr && col + h * 32 + j < p.N) v += __ldg(o.bias + col + h * 32 + j);
-                    r[j] = __float_as_uint(v);
+                    r[h][j] = __float_as_uint(v);
                 }
                 if constexpr (sizeof(TC) == 4) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(buf + swizzled(lane, j)) =
-                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        *reinterpret_cast<uint4*>(bufs + h * BUF_BYTES + swizzled(lane, j)) =
+                            make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * k]),
-                                                                           __uint_as_float(r[8 * j + 2 * k + 1]));
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[h][8 * j + 2 * k]),
+                                                                           __uint_as_float(r[h][8 * j + 2 * k + 1]));
                             w[k] = *reinterpret_cast<const uint32_t*>(&b);
                         }
-                        *reinterpret_cast<uint4*>(buf + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(bufs + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
-            if (i == REL - 1) release();
             fence_async_smem();
             __syncwarp();
-            if (lane == 0 && live && row0 < p.M) tma_store_2d(tmC, col, row0, smem_u32(buf));
+            if (lane == 0 && row0 < p.M) {
+                if (col < p.N) tma_store_2d(tmC, col, row0, smem_u32(bufs));
+                if (sizeof(TC) == 4 && col + 32 < p.N) tma_store_2d(tmC, col + 32, row0, smem_u32(bufs) + BUF_BYTES);
+            }
         } else {
             // Any alignment, and beta: 32 x 32 FP32 blocks through shared
             // memory, then whole row segments under the output rule.
-#pragma unroll 1
-            for (int h = 0; h < CW / 32; ++h) {
-                uint32_t r[32];
-                tmem_ld32(tmem + (uint32_t)(ch * CW + h * 32), r);
-                tmem_wait_ld(r);
-                __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(bufs + swizzled(lane, j)) =
-                        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                __syncwarp();
+                    *reinterpret_cast<uint4*>(bufs + h * BUF_BYTES + swizzled(lane, j)) =
+                        make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
+            __syncwarp();
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
                 const int c = col + h * 32 + lane;
-                if (c < p.N) {
-                    TC* out = static_cast<TC*>(o.C) + c;
+                if (c >= p.N) continue;
+                TC* out = static_cast<TC*>(o.C) + c;
 #pragma unroll 4
-                    for (int k = 0; k < 32; ++k)
-                        if (row0 + k < p.M)
-                            mx4_store(out + (long)(row0 + k) * o.ldc,
-                                      *reinterpret_cast<const float*>(bufs + swizzled(k, lane >> 2) + (lane & 3) * 4),
-                                      ga, gb, o, c);
-                }
+                for (int k = 0; k < 32; ++k)
+                    if (row0 + k < p.M)
+                        mx4_store(out + (long)(row0 + k) * o.ldc,
+                                  *reinterpret_cast<const float*>(bufs + h * BUF_BYTES + swizzled(k, lane >> 2) +
+                                                                  (lane & 3) * 4),
+                                  ga, gb, o, c);
             }
-            if (i == REL - 1) release();
+            __syncwarp();
         }
     }
 }
@@ -232,19 +235,22 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
-        if (lane == 0) {
-            uint32_t armed = 0, armed_parity = 0;
-            int g = 0;
-            for (int t = unit; t < p.num_tiles; t += p.units) {
+        // The whole warp runs the loop (addresses stay uniform values), one
+        // elected lane issues.
+        {
+            uint32_t armed = 0, armed_parity = 0, ph = 0;
+            int s = 0;
+            bool ok = true, stall = p.debug_stall != 0;        // test hook: the first stage is never filled
+            for (int t = unit; ok && t < p.num_tiles; t += p.units) {
                 int mb, nb;
                 tile_coords(t, p, mb, nb);
                 const int row = mb * S::TM + (int)rank * 128;
                 const int col = nb * S::TN + (int)rank * 128;
-                for (int kb = 0; kb < p.kblocks; ++kb, ++g) {
-                    const int s = g % STAGES;
-                    const uint32_t ph = (uint32_t)(g / STAGES) & 1u;
-                    if (!mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait)) goto producer_done;
-                    if (p.debug_stall && g == 0) continue;         // test hook: stage 0 never filled
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                    if (!ok) break;
+                    if (!stall) {
+                    if (elect_one()) {
                     const uint32_t full = full0 + (uint32_t)(s * sizeof(uint64_t));
                     if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), (PAIR ? 2 : 1) * S::STAGE_BYTES);
                     const uint32_t a = codes0 + s * 2 * OPERAND_BYTES;
@@ -253,11 +259,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tma_load_2d<PAIR>(a + OPERAND_BYTES, &tmB, kb * SW, col, full);
                     tma_load_3d<PAIR>(sf, &tmSA, 0, kb * S::SF_TILES, row / 128, full);
                     tma_load_3d<PAIR>(sf + S::SFA_BYTES, &tmSB, 0, kb * S::SF_TILES, nb * (S::TN / 128), full);
+                    }
                     armed |= 1u << s;
                     armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                    }
+                    stall = false;
+                    __syncwarp();
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-        producer_done:
             if (leader) {
                 for (int s = 0; s < STAGES; ++s)
                     if (armed & (1u << s))
@@ -276,7 +286,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // The whole warp runs the loop, so that addresses and descriptors are
         // uniform values; one elected lane issues.
         if (leader) {
-            int g = 0, it = 0;
+            int it = 0, s = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
                 // Pair: the previous tile's shared columns have left tensor
@@ -289,9 +300,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tc_fence_after();
                 const uint32_t d = tmem_base + ((it & 1) ? S::ACC1 : 0);
                 const uint32_t sfa = tmem_base + S::SF, sfb = sfa + S::SF_TILES * 4;
-                for (int kb = 0; kb < p.kblocks; ++kb, ++g) {
-                    const int s = g % STAGES;
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), (uint32_t)(g / STAGES) & 1u, wait));
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -318,6 +328,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (kb == p.kblocks - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
                     }
                     __syncwarp();
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
             if (elect_one()) tc_commit<PAIR>(smem_u32(&sy->drain));
@@ -329,7 +340,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
         uint8_t* bufs = epi + (warp - 2) * 2 * BUF_BYTES;
         const float ga = mx4_g(p.ga), gb = mx4_g(p.gb);
-        int turn = 0, it = 0;
+        int it = 0;
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
             int mb, nb;
             tile_coords(t, p, mb, nb);
@@ -345,8 +356,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             };
             drain_tile<S, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
-                              mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb,
-                              turn, release);
+                              mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
         }
         tma_store_wait_all();
     }

@@ -71,6 +71,10 @@ struct Wait {
 // flag and records the timeout.
 template <bool HONOUR, bool CLUSTER>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
+    // The clock is read only once a wait is long: a read costs as much as
+    // several polls.
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try<CLUSTER>(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try<CLUSTER>(bar, parity)) return true;
