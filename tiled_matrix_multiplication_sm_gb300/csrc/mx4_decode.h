@@ -1,0 +1,54 @@
+// 4-bit weights to BF16, in registers.
+//
+// code x scale is a BF16 number exactly (2 significant bits times at most 4).
+// The three magnitude bits of a code, moved to bits 6..8 of a 16-bit half, are
+// a BF16 of 2^-126 times the code's value (subnormal for the code 0.5), so one
+// BF16 multiplication by 2^126 x scale makes both the value and its scaling.
+//   NVFP4: 2^126 x 448 is past BF16's range, so values carry 2^-16 (the
+//          factor is 2^110 x scale) and the product is multiplied by 2^16.
+//   MXFP4: the factor fits up to a scale of 2; blocks with larger scales
+//          (WIDE) take two multiplications.
+#pragma once
+
+#include "mx4_internal.h"
+
+namespace tgemm {
+namespace mx4_decode {
+
+template <int FMT> __device__ constexpr float unscale() { return FMT == TGEMM_NVFP4 ? 65536.0f : 1.0f; }
+
+// The factor of a scale byte, as two BF16 halves.
+template <int FMT>
+__device__ __forceinline__ uint32_t factor(uint32_t byte) {
+    uint32_t h;
+    if (FMT == TGEMM_MXFP4) h = byte == 255 ? 0x7FC0u : byte <= 128 ? (byte + 126) << 7 : byte << 7;
+    else h = __float_as_uint(e4m3_value(byte & 0x7F) * 1.298074214633707e33f) >> 16;     // 2^110
+    return h | h << 16;
+}
+// MXFP4 blocks with such a scale need 2^126 as a factor of its own.
+__device__ __forceinline__ bool wide(uint32_t byte) { return byte > 128; }
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes (a word) to four pairs: pair i holds the values of codes i
+// (low half) and i + 4.
+template <bool WIDE>
+__device__ __forceinline__ void values(uint32_t w, uint32_t f, uint32_t (&v)[4]) {
+    constexpr uint32_t MAG = 0x01C001C0u, SIGN = 0x80008000u;
+    v[0] = (w << 6 & MAG) | (w << 12 & SIGN);
+    v[1] = (w << 2 & MAG) | (w << 8 & SIGN);
+    v[2] = (w >> 2 & MAG) | (w << 4 & SIGN);
+    v[3] = (w >> 6 & MAG) | (w & SIGN);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (WIDE) v[i] = mul2(v[i], 0x7E807E80u);
+        v[i] = mul2(v[i], f);
+    }
+}
+
+}  // namespace mx4_decode
+}  // namespace tgemm

@@ -107,4 +107,9 @@ cudaError_t mx4_read_and_clear_status(int* status, cudaStream_t s);
 cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                         const Mx4Out& out, int num_sms, cudaStream_t s);
 
+// At most MX4_FEW_ROWS rows of A (mx4_weights_rows.cu).
+constexpr int MX4_FEW_ROWS = 16;
+cudaError_t mx4_weights_rows(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
+                             const Mx4Out& out, int num_sms, cudaStream_t s);
+
 }  // namespace tgemm
