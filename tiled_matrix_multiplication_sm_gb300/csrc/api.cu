@@ -175,6 +175,13 @@ int check_common(int M, int N, int K, const void* A, long lda, const void* B, lo
 
 namespace tgemm {
 unsigned long long wait_limit_ns() { return (unsigned long long)g_wait_limit_ns.load(); }
+cudaError_t scratch_take(void** ptr, size_t bytes, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaMemPool_t pool = scratch_pool(dev);
+    return pool != nullptr ? cudaMallocFromPoolAsync(ptr, bytes, pool, s) : cudaErrorMemoryAllocation;
+}
 int debug_stall() { return g_debug_stall.load(); }
 void* tensor_map_encoder() { return encode_fn(); }
 int device_sms(int* num_sms) {

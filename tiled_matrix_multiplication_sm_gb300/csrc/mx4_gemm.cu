@@ -23,7 +23,7 @@
 // Rows past M and N are read as zeros (TMA fill, zero scales) and not stored.
 // Waits are bounded as in the other tensor-core kernels.
 
-#include "mx4_ptx.h"
+#include "mx4_tile.h"
 
 #include <cstring>
 
@@ -33,18 +33,12 @@ __device__ int g_mx4_status;
 
 namespace {
 
-using namespace mx4_ptx;
+using namespace mx4_tile;
 
-constexpr int SW = 128;                       // bytes of a staged row: 256 codes
 constexpr int STAGE_K = MX4_SPAN;
 constexpr int OPERAND_BYTES = 128 * SW;       // 128 rows of codes
 constexpr int STAGES = 5;
 constexpr int THREADS = 192;
-constexpr int EPI_WARPS = 4;
-constexpr int BUF_BYTES = 32 * 128;           // 32 rows x 128 bytes of C
-constexpr int EPI_BYTES = EPI_WARPS * 2 * BUF_BYTES;
-constexpr int TMEM_COLS = 512;
-constexpr int GROUP_M = 8;
 
 template <int FMT, bool PAIR>
 struct Shape {
@@ -73,114 +67,10 @@ struct Sync {
 };
 static_assert(sizeof(Sync) <= 256, "barrier block");
 
-struct Params {
-    int M, N, kblocks;
-    int tiles_m, tiles_n, num_tiles, units;
+struct Params : Tiling {
+    int kblocks;
     const float *ga, *gb;
-    Mx4Out out;
-    int tma_c;                  // C leaves by TMA stores
-    unsigned long long wait_limit_ns;
-    int* status;
-    int debug_stall;
 };
-
-__device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int& nb) {
-    const int per_group = GROUP_M * p.tiles_n;
-    const int first = t / per_group * GROUP_M;
-    const int gm = min(p.tiles_m - first, GROUP_M);
-    mb = first + t % per_group % gm;
-    nb = t % per_group / gm;
-}
-
-// Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
-__device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
-
-// Drains this warp's 32 rows of a tile, 64 columns a turn. `last_first`: the
-// last 64 columns, which the next tile's accumulator shares, go first.
-// release() is called as soon as FREE_FIRST columns have left tensor memory.
-template <typename S, typename TC, typename Release>
-__device__ __forceinline__ void drain_tile(const Params& p, const CUtensorMap* tmC, uint32_t tmem,
-                                           uint8_t* bufs, int row0, int col0, bool last_first,
-                                           float ga, float gb, Release release) {
-    constexpr int W = 64;
-    constexpr int TURNS = S::TN / W, REL = S::FREE_FIRST / W;
-    const int lane = threadIdx.x & 31;
-    const Mx4Out& o = p.out;
-#pragma unroll 1
-    for (int i = 0; i < TURNS; ++i) {
-        const int part = last_first ? (i == 0 ? TURNS - 1 : i - 1) : i;
-        const int col = col0 + part * W;
-        uint32_t r[2][32];
-        tmem_ld32(tmem + (uint32_t)(part * W), r[0]);
-        tmem_ld32(tmem + (uint32_t)(part * W + 32), r[1]);
-        tmem_wait_ld(r[0]);
-        tmem_wait_ld(r[1]);
-        if (i == REL - 1) release();
-        if (p.tma_c) {
-            // FP32: two boxes of 32 columns, BF16: one of 64. The previous
-            // turn's boxes have to have left the buffers.
-            if (lane == 0) tma_store_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float v = __uint_as_float(r[h][j]) * ga * gb * o.alpha;
-                    if (o.bias != nullptr && col + h * 32 + j < p.N) v += __ldg(o.bias + col + h * 32 + j);
-                    r[h][j] = __float_as_uint(v);
-                }
-                if constexpr (sizeof(TC) == 4) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(bufs + h * BUF_BYTES + swizzled(lane, j)) =
-                            make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[h][8 * j + 2 * k]),
-                                                                           __uint_as_float(r[h][8 * j + 2 * k + 1]));
-                            w[k] = *reinterpret_cast<const uint32_t*>(&b);
-                        }
-                        *reinterpret_cast<uint4*>(bufs + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < p.M) {
-                if (col < p.N) tma_store_2d(tmC, col, row0, smem_u32(bufs));
-                if (sizeof(TC) == 4 && col + 32 < p.N) tma_store_2d(tmC, col + 32, row0, smem_u32(bufs) + BUF_BYTES);
-            }
-        } else {
-            // Any alignment, and beta: 32 x 32 FP32 blocks through shared
-            // memory, then whole row segments under the output rule.
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(bufs + h * BUF_BYTES + swizzled(lane, j)) =
-                        make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
-            __syncwarp();
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int c = col + h * 32 + lane;
-                if (c >= p.N) continue;
-                TC* out = static_cast<TC*>(o.C) + c;
-#pragma unroll 4
-                for (int k = 0; k < 32; ++k)
-                    if (row0 + k < p.M)
-                        mx4_store(out + (long)(row0 + k) * o.ldc,
-                                  *reinterpret_cast<const float*>(bufs + h * BUF_BYTES + swizzled(k, lane >> 2) +
-                                                                  (lane & 3) * 4),
-                                  ga, gb, o, c);
-            }
-            __syncwarp();
-        }
-    }
-}
 
 template <int FMT, bool PAIR, typename TC>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -355,7 +245,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
                 }
             };
-            drain_tile<S, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
+            drain_tile<S::TN, S::FREE_FIRST, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
                               mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
         }
         tma_store_wait_all();
@@ -378,52 +268,6 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(int M, int N, const Mx4O
         mx4_store(static_cast<TC*>(out.C) + r * out.ldc + c, 0.0f, 1.0f, 1.0f, out, (int)c);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool encode(EncodeTiledFn enc, CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
-            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-            CUtensorMapSwizzle swizzle) {
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Codes in boxes of 128 rows x 128 bytes.
-bool encode_codes(EncodeTiledFn enc, CUtensorMap* map, const Mx4Operand& m, int rows, int K) {
-    const cuuint64_t dims[2] = {(cuuint64_t)mx4_pitch(K), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)mx4_pitch(K)};
-    const cuuint32_t box[2] = {SW, 128};
-    return encode(enc, map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.codes, dims, strides, box,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// Scale tiles: x within a tile (as 128 words), y along K, z along the rows.
-bool encode_scales(EncodeTiledFn enc, CUtensorMap* map, const Mx4Operand& m, int rows, int K, int fmt,
-                   int tiles_y, int tiles_z) {
-    const cuuint64_t tk = (cuuint64_t)mx4_tiles_k(K, fmt);
-    const cuuint64_t dims[3] = {128, tk, (cuuint64_t)(rows + 127) / 128};
-    const cuuint64_t strides[2] = {MX4_TILE_BYTES, tk * MX4_TILE_BYTES};
-    const cuuint32_t box[3] = {128, (cuuint32_t)tiles_y, (cuuint32_t)tiles_z};
-    return encode(enc, map, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, m.scales, dims, strides, box,
-                  CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-// C in boxes of 32 rows x 128 bytes, when it may leave by TMA: beta = 0, its
-// rows on 16-byte boundaries and whole 16-byte pieces long (a box clipped
-// inside such a piece also writes the rest of it).
-bool encode_c(EncodeTiledFn enc, CUtensorMap* map, const Mx4Out& o, int M, int N) {
-    const int esz = o.c_type == TGEMM_TYPE_F32 ? 4 : 2;
-    if (o.beta != 0.0f || reinterpret_cast<uintptr_t>(o.C) % 16 != 0 || o.ldc * esz % 16 != 0 || (long)N * esz % 16 != 0)
-        return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)o.ldc * esz};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 32};
-    return encode(enc, map, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.C,
-                  dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int FMT, bool PAIR, typename TC>
 cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B, const Mx4Out& out,
                    int num_sms, cudaStream_t s) {
@@ -437,37 +281,14 @@ cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B
         return cudaErrorInvalidValue;
     memset(&tmC, 0, sizeof(tmC));
     Params p;
-    p.M = M; p.N = N;
+    cudaError_t e = make_tiling(p, M, N, S::TM, S::TN, PAIR ? num_sms / 2 : num_sms, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
-    p.tiles_m = (int)(((long)M + S::TM - 1) / S::TM);
-    p.tiles_n = (int)(((long)N + S::TN - 1) / S::TN);
-    if ((long)p.tiles_m * p.tiles_n > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    p.num_tiles = p.tiles_m * p.tiles_n;
-    const int slots = PAIR ? num_sms / 2 : num_sms;
-    p.units = p.num_tiles < slots ? p.num_tiles : slots;
     p.ga = A.g; p.gb = B.g;
-    p.out = out;
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
-    p.wait_limit_ns = wait_limit_ns();
-    p.debug_stall = debug_stall();
-    cudaError_t e = mx4_status_word(&p.status);
     if (e == cudaSuccess) e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, TC>>(S::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((PAIR ? 2 : 1) * p.units);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see launch_pdl
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<FMT, PAIR, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
+    PairLaunch cfg((PAIR ? 2 : 1) * p.units, THREADS, S::SMEM, PAIR, s);
+    return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
 }
 
 template <int FMT, bool PAIR>
@@ -475,11 +296,6 @@ cudaError_t launch_type(int M, int N, int K, const Mx4Operand& A, const Mx4Opera
                         int num_sms, cudaStream_t s) {
     return out.c_type == TGEMM_TYPE_F32 ? launch<FMT, PAIR, float>(M, N, K, A, B, out, num_sms, s)
                                         : launch<FMT, PAIR, __nv_bfloat16>(M, N, K, A, B, out, num_sms, s);
-}
-
-// Pair tiles once they occupy half of the SM pairs.
-bool use_pair(int M, int N, int num_sms) {
-    return (((long)M + 255) / 256) * (((long)N + 255) / 256) * 4 >= num_sms;
 }
 
 }  // namespace

@@ -1,16 +1,379 @@
-// Product of BF16 rows with a kept 4-bit matrix.
+// BF16 rows times a kept 4-bit matrix, C = alpha A W^T + beta C + bias, on the
+// tensor cores (tcgen05, kind f16): W is made BF16 on its way through shared
+// memory. (At most 16 rows go to mx4_weights_rows.cu.)
+//
+// The form is that of gemm_mx4's kernel -- 256 x 256 tiles on SM pairs or
+// 128 x 128 on one SM, persistent, two accumulators in tensor memory -- with
+// eight more warps: TMA brings A's rows (64 columns of K, one pipeline stage)
+// and, in chunks of 256 columns, W's codes and scales; the eight warps turn
+// each stage's 128 rows x 64 codes into the 128-byte-swizzled BF16 that the
+// MMA reads, and arrive on the stage's barrier beside A's bytes. A thread
+// takes 32 codes of a row: one 16-byte read, one or two scales, four 16-byte
+// writes. At 3 instructions a weight the warps need half of the 512 cycles
+// that the stage's MMAs take, so the tensor cores stay the bound while C has
+// rows enough for them.
 
-#include "mx4_simt.h"
+#include "mx4_decode.h"
+#include "mx4_tile.h"
+
+#include <cstring>
 
 namespace tgemm {
+namespace {
+
+using namespace mx4_tile;
+using namespace mx4_decode;
+
+constexpr int STAGES = 4;
+constexpr int STAGE_K = 64;
+constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
+constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
+constexpr int CHUNKS = 2;                            // code chunks in flight: 256 columns each
+constexpr int DECODE_WARPS = 8;
+constexpr int THREADS = 32 * (2 + EPI_WARPS + DECODE_WARPS);
+constexpr int PER_CHUNK = MX4_SPAN / STAGE_K;
+
+template <int FMT>
+struct Chunk {
+    static constexpr int SF_TILES = MX4_SPAN / mx4_block(FMT) / 4;
+    static constexpr int CODES = 128 * SW;           // 128 rows x 256 codes
+    static constexpr int BYTES = CODES + SF_TILES * MX4_TILE_BYTES;
+};
+
+struct Sync {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t codes_full[CHUNKS], codes_empty[CHUNKS];
+    uint64_t tmem_full[2], tmem_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    uint32_t factors[256];
+};
+constexpr int SYNC_BYTES = 1280;
+static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
+
+template <int FMT>
+constexpr int smem_bytes() {
+    return 1024 + STAGES * STAGE_BYTES + CHUNKS * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
+}
+static_assert(smem_bytes<TGEMM_NVFP4>() <= 227 * 1024, "shared memory");
+
+struct Params : Tiling {
+    int kblocks;                // of 64 columns
+    const float* gb;
+};
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 codes of a row (16 bytes) to 64 bytes of the swizzled stage.
+template <int FMT, bool WIDE>
+__device__ __forceinline__ void decode_run(uint8_t* dst, int row, int half, const uint4& codes, uint32_t f0,
+                                           uint32_t f1) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t v[4];
+        values<WIDE>(w[j], j < 2 ? f0 : f1, v);
+        *reinterpret_cast<uint4*>(dst + swizzled(row, half * 4 + j)) =
+            make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+    }
+}
+
+template <int FMT, bool PAIR, typename TC>
+__global__ void __launch_bounds__(THREADS, 1)
+weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC,
+               const Params p) {
+    constexpr int TM = PAIR ? 256 : 128, TN = TM;
+    using CH = Chunk<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* codes = smem + STAGES * STAGE_BYTES;            // the chunks' codes, then their scales
+    uint8_t* scales = codes + CHUNKS * CH::CODES;
+    uint8_t* epi = codes + CHUNKS * CH::BYTES;
+    Sync* sy = reinterpret_cast<Sync*>(epi + EPI_BYTES);
+    const uint32_t stage0 = smem_u32(smem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const bool leader = rank == 0;
+    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            // A's bytes of both blocks, and every decoding warp's arrival.
+            mbar_init(smem_u32(&sy->full[s]), 1 + (PAIR ? 2 : 1) * DECODE_WARPS);
+            mbar_init(smem_u32(&sy->empty[s]), 1);
+        }
+        for (int c = 0; c < CHUNKS; ++c) {
+            mbar_init(smem_u32(&sy->codes_full[c]), 1);
+            mbar_init(smem_u32(&sy->codes_empty[c]), DECODE_WARPS);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&sy->tmem_full[a]), 1);
+            mbar_init(smem_u32(&sy->tmem_empty[a]), (PAIR ? 2 : 1) * EPI_WARPS);
+        }
+        mbar_init(smem_u32(&sy->drain), 1);
+        sy->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        prefetch_map(&tmSB);
+    }
+    if (threadIdx.x < 256) sy->factors[threadIdx.x] = factor<FMT>(threadIdx.x);
+    if (warp == 1) tmem_alloc<PAIR, TMEM_COLS>(smem_u32(&sy->tmem_base));
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = sy->tmem_base;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const Wait wait{&sy->abort, p.status, p.wait_limit_ns};
+    // The leader's barriers, as cluster addresses.
+    const uint32_t full0 = PAIR ? map_to_rank(smem_u32(&sy->full[0]), 0) : smem_u32(&sy->full[0]);
+    const uint32_t tmem_empty0 =
+        PAIR ? map_to_rank(smem_u32(&sy->tmem_empty[0]), 0) : smem_u32(&sy->tmem_empty[0]);
+
+    if (warp == 0) {
+        // -------------------------------------------------- TMA producer
+        uint32_t armed = 0, armed_parity = 0, ph = 0, cph = 0, c_armed = 0, c_parity = 0;
+        int s = 0, c = 0;
+        bool ok = true, stall = p.debug_stall != 0;        // test hook: the first stage is never filled
+        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+            int mb, nb;
+            tile_coords(t, p, mb, nb);
+            const int row = mb * TM + (int)rank * 128;
+            const int col = nb * TN + (int)rank * 128;
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (kb % PER_CHUNK == 0) {
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), cph ^ 1u, wait));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t bar = smem_u32(&sy->codes_full[c]);
+                        mbar_arrive_expect_tx(bar, CH::BYTES);
+                        tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, kb / PER_CHUNK * SW, col, bar);
+                        tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0,
+                                           kb / PER_CHUNK * CH::SF_TILES, col / 128, bar);
+                    }
+                    c_armed |= 1u << c;
+                    c_parity = (c_parity & ~(1u << c)) | (cph << c);
+                    if (++c == CHUNKS) { c = 0; cph ^= 1u; }
+                }
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                if (!ok) break;
+                if (!stall) {
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), (PAIR ? 2 : 1) * OPERAND_BYTES);
+                        tma_load_2d<PAIR>(stage0 + s * STAGE_BYTES, &tmA, kb * STAGE_K, row,
+                                          full0 + (uint32_t)(s * sizeof(uint64_t)));
+                    }
+                    armed |= 1u << s;
+                    armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                }
+                stall = false;
+                __syncwarp();
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+        for (int i = 0; i < CHUNKS; ++i)
+            if (c_armed & (1u << i))
+                mbar_wait<false>(smem_u32(&sy->codes_full[i]), (c_parity >> i) & 1u, wait);
+        if (leader) {
+            for (int i = 0; i < STAGES; ++i)
+                if (armed & (1u << i))
+                    mbar_wait<false>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
+        } else if (*(volatile int*)&sy->abort) {
+            // After a timeout this block cannot observe its own copies; give
+            // any in flight time to land (a copy takes microseconds).
+            const unsigned long long t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        if (leader) {
+            constexpr uint32_t IDESC = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(TN >> 3) << 17 | (uint32_t)(TM >> 4) << 24;
+            int it = 0, s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
+                // The tile two before, which used this accumulator, is out.
+                if (it >= 2 && !__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[it & 1]),
+                                                                     (uint32_t)((it >> 1) - 1) & 1u, wait)))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)((it & 1) * TN);
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->full[s]), ph, wait));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t a = stage0 + s * STAGE_BYTES;
+#pragma unroll
+                        for (int k = 0; k < STAGE_K / 16; ++k)
+                            mma_bf16<PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
+                                           smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2), IDESC, (kb | k) != 0);
+                        tc_commit<PAIR>(smem_u32(&sy->empty[s]));
+                        if (kb == p.kblocks - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (elect_one()) tc_commit<PAIR>(smem_u32(&sy->drain));
+            mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
+        }
+        __syncwarp();
+    } else if (warp < 2 + EPI_WARPS) {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
+        uint8_t* bufs = epi + (warp - 2) * 2 * BUF_BYTES;
+        const float gb = mx4_g(p.gb);
+        int it = 0;
+        for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
+            int mb, nb;
+            tile_coords(t, p, mb, nb);
+            const bool ok = mbar_wait(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 31) {
+                    const uint32_t bar = tmem_empty0 + (uint32_t)((it & 1) * sizeof(uint64_t));
+                    if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
+                }
+            };
+            drain_tile<TN, TN, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
+                                   mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
+        }
+        tma_store_wait_all();
+    } else {
+        // ------------------------------------------------------ decoding
+        const int tid = threadIdx.x - 32 * (2 + EPI_WARPS);
+        const int row = tid & 127, half = tid >> 7;
+        uint32_t ph = 0, cph = 0;
+        int s = 0, c = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                const int q = kb % PER_CHUNK;
+                if (q == 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
+                if (!ok) break;
+                const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + swizzled(row, q * 2 + half));
+                const uint8_t* sc = scales + c * (CH::BYTES - CH::CODES) + (row & 31) * 16 + (row >> 5) * 4;
+                uint32_t b0, b1;
+                if (FMT == TGEMM_MXFP4) {
+                    b0 = b1 = sc[(q >> 1) * MX4_TILE_BYTES + (q & 1) * 2 + half];
+                } else {
+                    const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + q * MX4_TILE_BYTES + half * 2);
+                    b0 = two & 0xFF;
+                    b1 = two >> 8;
+                }
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                if (!ok) break;
+                uint8_t* dst = smem + s * STAGE_BYTES + OPERAND_BYTES;
+                if (FMT == TGEMM_MXFP4 && __any_sync(~0u, wide(b0))) {
+                    // Beside a wide block the others take their scale alone too.
+                    const uint32_t f = b0 == 255 ? 0x7FC07FC0u : b0 == 0 ? 0x00400040u : b0 << 7 | b0 << 23;
+                    decode_run<FMT, true>(dst, row, half, w, f, f);
+                } else {
+                    decode_run<FMT, false>(dst, row, half, w, sy->factors[b0], sy->factors[b1]);
+                }
+                fence_async_smem();          // the MMA reads through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = full0 + (uint32_t)(s * sizeof(uint64_t));
+                    if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
+                }
+                if (q == PER_CHUNK - 1 || kb == p.kblocks - 1) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
+                    if (++c == CHUNKS) { c = 0; cph ^= 1u; }
+                }
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
+}
+
+template <int FMT, bool PAIR, typename TC>
+cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, const Mx4Out& out,
+                   int num_sms, cudaStream_t s) {
+    const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (enc == nullptr) return cudaErrorNotSupported;
+    constexpr int TILE = PAIR ? 256 : 128;
+    CUtensorMap tmA, tmB, tmSB, tmC;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)lda * 2};
+    const cuuint32_t box[2] = {STAGE_K, 128};
+    if (!encode(enc, &tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_codes(enc, &tmB, B, N, K) || !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT>::SF_TILES, 1))
+        return cudaErrorInvalidValue;
+    memset(&tmC, 0, sizeof(tmC));
+    Params p;
+    cudaError_t e = make_tiling(p, M, N, TILE, TILE, PAIR ? num_sms / 2 : num_sms, out);
+    p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
+    p.gb = B.g;
+    p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
+    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(smem_bytes<FMT>());
+    if (e != cudaSuccess) return e;
+    PairLaunch cfg((PAIR ? 2 : 1) * p.units, THREADS, smem_bytes<FMT>(), PAIR, s);
+    return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, PAIR, TC>, tmA, tmB, tmSB, tmC, p);
+}
+
+template <int FMT, bool PAIR>
+cudaError_t launch_type(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, const Mx4Out& out,
+                        int num_sms, cudaStream_t s) {
+    return out.c_type == TGEMM_TYPE_F32 ? launch<FMT, PAIR, float>(M, N, K, A, lda, B, out, num_sms, s)
+                                        : launch<FMT, PAIR, __nv_bfloat16>(M, N, K, A, lda, B, out, num_sms, s);
+}
+
+cudaError_t run(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt, const Mx4Out& out,
+                int num_sms, cudaStream_t s) {
+    if (use_pair(M, N, num_sms))
+        return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4, true>(M, N, K, A, lda, B, out, num_sms, s)
+                                  : launch_type<TGEMM_NVFP4, true>(M, N, K, A, lda, B, out, num_sms, s);
+    return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4, false>(M, N, K, A, lda, B, out, num_sms, s)
+                              : launch_type<TGEMM_NVFP4, false>(M, N, K, A, lda, B, out, num_sms, s);
+}
+
+}  // namespace
 
 cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
     if (K == 0) return mx4_empty_sum(M, N, out, s);
     if (M <= MX4_FEW_ROWS) return mx4_weights_rows(M, N, K, A, lda, B, fmt, out, num_sms, s);
-    const Mx4Operand none{};
-    return fmt == TGEMM_MXFP4 ? mx4_simt::launch<TGEMM_MXFP4, false>(M, N, K, none, A, lda, B, out, s)
-                              : mx4_simt::launch<TGEMM_NVFP4, false>(M, N, K, none, A, lda, B, out, s);
+    if (reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 8 == 0)
+        return run(M, N, K, A, lda, B, fmt, out, num_sms, s);
+    // TMA copies rows that start on 16-byte boundaries: others are repacked.
+    const long ld = ((long)K + 63) / 64 * 64;
+    void* packed = nullptr;
+    cudaError_t e = scratch_take(&packed, (size_t)M * ld * 2, s);
+    if (e != cudaSuccess) return e;
+    e = repack_rows(A, lda, packed, ld, M, K, 2, s);
+    if (e == cudaSuccess) e = run(M, N, K, packed, ld, B, fmt, out, num_sms, s);
+    const cudaError_t f = cudaFreeAsync(packed, s);
+    return e != cudaSuccess ? e : f;
 }
 
 }  // namespace tgemm

@@ -210,6 +210,9 @@ cudaError_t repack_rows2(const RepackJob& a, const RepackJob& b, int esz, cudaSt
 // The bound on any single wait inside the tensor-core kernels, as last set
 // by gemm_set_wait_limit_ns (default 2 s).
 unsigned long long wait_limit_ns();
+// `bytes` of stream-ordered scratch from the library's pool on the current
+// device, given back with cudaFreeAsync on `s`.
+cudaError_t scratch_take(void** ptr, size_t bytes, cudaStream_t s);
 // Whether gemm_set_debug_stall is on.
 int debug_stall();
 // cuTensorMapEncodeTiled, or nullptr.
