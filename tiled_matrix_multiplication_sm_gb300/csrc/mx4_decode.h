@@ -30,22 +30,30 @@ __device__ __forceinline__ bool wide(uint32_t byte) { return byte > 128; }
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    // volatile: not moved below the wait for the slot that the values go to
+    asm volatile("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Eight codes (a word) to four pairs: pair i holds the values of codes i
-// (low half) and i + 4.
-template <bool WIDE>
-__device__ __forceinline__ void values(uint32_t w, uint32_t f, uint32_t (&v)[4]) {
+// Eight codes (a word) to four pairs, each a BF16 of 2^-126 times its value:
+// pair i holds codes i (low half) and i + 4.
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t (&v)[4]) {
     constexpr uint32_t MAG = 0x01C001C0u, SIGN = 0x80008000u;
     v[0] = (w << 6 & MAG) | (w << 12 & SIGN);
     v[1] = (w << 2 & MAG) | (w << 8 & SIGN);
     v[2] = (w >> 2 & MAG) | (w << 4 & SIGN);
     v[3] = (w >> 6 & MAG) | (w & SIGN);
+}
+
+constexpr uint32_t TWO_126 = 0x7E807E80u;
+
+// The pairs' values, scaled.
+template <bool WIDE>
+__device__ __forceinline__ void values(uint32_t w, uint32_t f, uint32_t (&v)[4]) {
+    pairs(w, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (WIDE) v[i] = mul2(v[i], 0x7E807E80u);
+        if (WIDE) v[i] = mul2(v[i], TWO_126);
         v[i] = mul2(v[i], f);
     }
 }

@@ -184,7 +184,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 // memory (and with them all of the tile before it). Single:
                 // the tile two before, which used this accumulator.
                 if (PAIR ? it >= 1 : it >= 2)
-                    if (!__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
+                    if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
                                                                (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait)))
                         break;
                 tc_fence_after();

@@ -35,26 +35,23 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
+// On a barrier that may be in the pair's other block. What the arrival hands
+// over is read by the tensor cores (shared memory behind fence_async_smem,
+// tensor memory behind tcgen05 fences), not by the other block's threads, so
+// the default scope is enough; a release at cluster scope took about 1900
+// cycles in a block with copies and writes in flight.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                 :: "r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                  :: "r"(bar), "r"(bytes) : "memory");
 }
-// CLUSTER: acquires what threads of the pair's other block released.
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    if constexpr (CLUSTER)
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 
@@ -69,15 +66,15 @@ struct Wait {
 // Wait for the phase of `bar` with parity `parity`. False when the block's
 // abort flag is raised (HONOUR) or the limit has passed, which raises the
 // flag and records the timeout.
-template <bool HONOUR, bool CLUSTER>
+template <bool HONOUR>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
     // The clock is read only once a wait is long: a read costs as much as
     // several polls.
     for (int i = 0; i < 32; ++i)
-        if (mbar_try<CLUSTER>(bar, parity)) return true;
+        if (mbar_try(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try<CLUSTER>(bar, parity)) return true;
+        if (mbar_try(bar, parity)) return true;
         if ((it & 15u) == 0) {
             if (HONOUR && *(volatile int*)w.abort) return false;
             if (globaltimer() - t0 > w.limit_ns || it >= (1u << 30)) {
@@ -88,9 +85,9 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const
         }
     }
 }
-template <bool HONOUR = true, bool CLUSTER = false>
+template <bool HONOUR = true>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Wait& w) {
-    return mbar_try<CLUSTER>(bar, parity) || mbar_wait_slow<HONOUR, CLUSTER>(bar, parity, w);
+    return mbar_try(bar, parity) || mbar_wait_slow<HONOUR>(bar, parity, w);
 }
 
 // ------------------------------------------------------- cluster of blocks

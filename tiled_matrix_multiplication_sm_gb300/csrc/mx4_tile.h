@@ -139,12 +139,12 @@ inline bool encode(EncodeTiledFn enc, CUtensorMap* map, CUtensorMapDataType type
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Codes in boxes of 128 rows x 128 bytes.
-inline bool encode_codes(EncodeTiledFn enc, CUtensorMap* map, const Mx4Operand& m, int rows, int K) {
+// Codes in boxes of 128 rows x `width` bytes (128 or 64), swizzled over as many.
+inline bool encode_codes(EncodeTiledFn enc, CUtensorMap* map, const Mx4Operand& m, int rows, int K, int width = SW) {
     const cuuint64_t dims[2] = {(cuuint64_t)mx4_pitch(K), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)mx4_pitch(K)};
-    const cuuint32_t box[2] = {SW, 128};
+    const cuuint32_t box[2] = {(cuuint32_t)width, 128};
     return encode(enc, map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.codes, dims, strides, box,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
+                  width == SW ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // Scale tiles: x within a tile (as 128 words), y along K, z along the rows.

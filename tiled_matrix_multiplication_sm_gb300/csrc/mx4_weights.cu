@@ -24,19 +24,22 @@ namespace {
 using namespace mx4_tile;
 using namespace mx4_decode;
 
-constexpr int STAGES = 4;
+constexpr int STAGES = 5;
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
-constexpr int CHUNKS = 2;                            // code chunks in flight: 256 columns each
+constexpr int CHUNKS = 3;                            // code chunks in flight
 constexpr int DECODE_WARPS = 8;
+constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
+constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + DECODE_WARPS);
-constexpr int PER_CHUNK = MX4_SPAN / STAGE_K;
+constexpr int CHUNK_K = 128;
+constexpr int PER_CHUNK = CHUNK_K / STAGE_K;
 
 template <int FMT>
 struct Chunk {
-    static constexpr int SF_TILES = MX4_SPAN / mx4_block(FMT) / 4;
-    static constexpr int CODES = 128 * SW;           // 128 rows x 256 codes
+    static constexpr int SF_TILES = CHUNK_K / mx4_block(FMT) / 4;
+    static constexpr int CODES = 128 * CHUNK_K / 2;  // 64-byte rows
     static constexpr int BYTES = CODES + SF_TILES * MX4_TILE_BYTES;
 };
 
@@ -75,18 +78,28 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
                      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// 32 codes of a row (16 bytes) to 64 bytes of the swizzled stage.
-template <int FMT, bool WIDE>
-__device__ __forceinline__ void decode_run(uint8_t* dst, int row, int half, const uint4& codes, uint32_t f0,
-                                           uint32_t f1) {
+// Where 16-byte piece j of row r lies in a chunk of codes (64-byte swizzle).
+__device__ __forceinline__ uint32_t swizzled64(int r, int j) {
+    return (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+}
+
+// 32 codes of a row (16 bytes) to BF16, in order.
+template <int FMT>
+__device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, uint32_t f0, uint32_t f1, bool is_wide) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t v[4];
-        values<WIDE>(w[j], j < 2 ? f0 : f1, v);
-        *reinterpret_cast<uint4*>(dst + swizzled(row, half * 4 + j)) =
-            make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+        pairs(w[j], v);
+        const uint32_t f = j < 2 ? f0 : f1;
+        uint32_t r[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                         __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)};
+        if (FMT == TGEMM_MXFP4 && is_wide)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], TWO_126);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], f);
+        out[j] = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 
@@ -99,10 +112,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     using CH = Chunk<FMT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t* codes = smem + STAGES * STAGE_BYTES;            // the chunks' codes, then their scales
-    uint8_t* scales = codes + CHUNKS * CH::CODES;
-    uint8_t* epi = codes + CHUNKS * CH::BYTES;
-    Sync* sy = reinterpret_cast<Sync*>(epi + EPI_BYTES);
+    uint8_t* codes = smem + STAGES * STAGE_BYTES;
+    uint8_t* epi = codes + CHUNKS * CH::CODES;               // 1 KB aligned, as its swizzle wants
+    uint8_t* scales = epi + EPI_BYTES;
+    Sync* sy = reinterpret_cast<Sync*>(scales + CHUNKS * (CH::BYTES - CH::CODES));
     const uint32_t stage0 = smem_u32(smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -112,8 +125,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // A's bytes of both blocks, and every decoding warp's arrival.
-            mbar_init(smem_u32(&sy->full[s]), 1 + (PAIR ? 2 : 1) * DECODE_WARPS);
+            // A's bytes of both blocks, and the decoding warps' arrivals.
+            mbar_init(smem_u32(&sy->full[s]), 1 + (PAIR ? 2 : 1) * GROUP_WARPS);
             mbar_init(smem_u32(&sy->empty[s]), 1);
         }
         for (int c = 0; c < CHUNKS; ++c) {
@@ -165,7 +178,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if (elect_one()) {
                         const uint32_t bar = smem_u32(&sy->codes_full[c]);
                         mbar_arrive_expect_tx(bar, CH::BYTES);
-                        tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, kb / PER_CHUNK * SW, col, bar);
+                        tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, kb / PER_CHUNK * (CHUNK_K / 2), col, bar);
                         tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0,
                                            kb / PER_CHUNK * CH::SF_TILES, col / 128, bar);
                     }
@@ -213,13 +226,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
                 // The tile two before, which used this accumulator, is out.
-                if (it >= 2 && !__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[it & 1]),
+                if (it >= 2 && !__all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[it & 1]),
                                                                      (uint32_t)((it >> 1) - 1) & 1u, wait)))
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)((it & 1) * TN);
                 for (int kb = 0; kb < p.kblocks; ++kb) {
-                    ok = __all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->full[s]), ph, wait));
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -265,47 +278,69 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         tma_store_wait_all();
     } else {
         // ------------------------------------------------------ decoding
-        const int tid = threadIdx.x - 32 * (2 + EPI_WARPS);
-        const int row = tid & 127, half = tid >> 7;
-        uint32_t ph = 0, cph = 0;
-        int s = 0, c = 0;
+        // Group i takes stages i, i + GROUPS, .. of the block's; all groups
+        // pass over every chunk. A stage's values are made before its slot is
+        // free: between a slot's release and its readiness lie only the
+        // writes, their fence and the arrival.
+        const int dw = warp - 2 - EPI_WARPS, group = dw / GROUP_WARPS;
+        const int tid = dw % GROUP_WARPS * 32 + lane;
+        constexpr int ITEMS = 256 / (32 * GROUP_WARPS);          // runs of 32 codes a thread and stage
+        const int chunks = (p.kblocks + PER_CHUNK - 1) / PER_CHUNK;
+        uint32_t cph = 0;
+        int c = 0, base = 0;                                     // base: the tile's first stage
         bool ok = true;
-        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
-            for (int kb = 0; kb < p.kblocks; ++kb) {
-                const int q = kb % PER_CHUNK;
-                if (q == 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
+        for (int t = unit; ok && t < p.num_tiles; t += p.units, base += p.kblocks) {
+            for (int ch = 0; ch < chunks; ++ch) {
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
                 if (!ok) break;
-                const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + swizzled(row, q * 2 + half));
-                const uint8_t* sc = scales + c * (CH::BYTES - CH::CODES) + (row & 31) * 16 + (row >> 5) * 4;
-                uint32_t b0, b1;
-                if (FMT == TGEMM_MXFP4) {
-                    b0 = b1 = sc[(q >> 1) * MX4_TILE_BYTES + (q & 1) * 2 + half];
-                } else {
-                    const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + q * MX4_TILE_BYTES + half * 2);
-                    b0 = two & 0xFF;
-                    b1 = two >> 8;
+#pragma unroll 1
+                for (int q = 0; q < PER_CHUNK; ++q) {
+                    const int kb = ch * PER_CHUNK + q, idx = base + kb, s = idx % STAGES;
+                    if (kb >= p.kblocks || idx % GROUPS != group) continue;
+                    uint4 w[ITEMS];
+                    uint32_t b0[ITEMS], b1[ITEMS];
+                    bool is_wide = false;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i) {
+                        const int item = i * 32 * GROUP_WARPS + tid, row = item & 127, half = item >> 7;
+                        w[i] = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + swizzled64(row, q * 2 + half));
+                        const uint8_t* sc = scales + c * (CH::BYTES - CH::CODES) + (row & 31) * 16 + (row >> 5) * 4;
+                        if (FMT == TGEMM_MXFP4) {
+                            b0[i] = b1[i] = sc[q * 2 + half];
+                            is_wide |= wide(b0[i]);
+                        } else {
+                            const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + q * MX4_TILE_BYTES + half * 2);
+                            b0[i] = two & 0xFF;
+                            b1[i] = two >> 8;
+                        }
+                    }
+                    is_wide = FMT == TGEMM_MXFP4 && __any_sync(~0u, is_wide);
+                    uint4 v[ITEMS][4];
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i) {
+                        // Beside a wide block the others take their scale alone too.
+                        const uint32_t alone = b0[i] == 255 ? 0x7FC07FC0u : b0[i] == 0 ? 0x00400040u : b0[i] << 7 | b0[i] << 23;
+                        const uint32_t f0 = is_wide ? alone : sy->factors[b0[i]];
+                        const uint32_t f1 = FMT == TGEMM_MXFP4 ? f0 : sy->factors[b1[i]];
+                        decode_run<FMT>(v[i], w[i], f0, f1, is_wide);
+                    }
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ((uint32_t)(idx / STAGES) & 1u) ^ 1u, wait));
+                    if (!ok) break;
+                    uint8_t* dst = smem + s * STAGE_BYTES + OPERAND_BYTES;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i) {
+                        const int item = i * 32 * GROUP_WARPS + tid, row = item & 127, half = item >> 7;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + swizzled(row, half * 4 + j)) = v[i][j];
+                    }
+                    fence_async_smem();          // the MMA reads through the async proxy
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(full0 + (uint32_t)(s * sizeof(uint64_t)));
                 }
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
-                uint8_t* dst = smem + s * STAGE_BYTES + OPERAND_BYTES;
-                if (FMT == TGEMM_MXFP4 && __any_sync(~0u, wide(b0))) {
-                    // Beside a wide block the others take their scale alone too.
-                    const uint32_t f = b0 == 255 ? 0x7FC07FC0u : b0 == 0 ? 0x00400040u : b0 << 7 | b0 << 23;
-                    decode_run<FMT, true>(dst, row, half, w, f, f);
-                } else {
-                    decode_run<FMT, false>(dst, row, half, w, sy->factors[b0], sy->factors[b1]);
-                }
-                fence_async_smem();          // the MMA reads through the async proxy
                 __syncwarp();
-                if (lane == 0) {
-                    const uint32_t bar = full0 + (uint32_t)(s * sizeof(uint64_t));
-                    if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
-                }
-                if (q == PER_CHUNK - 1 || kb == p.kblocks - 1) {
-                    if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
-                    if (++c == CHUNKS) { c = 0; cph ^= 1u; }
-                }
-                if (++s == STAGES) { s = 0; ph ^= 1u; }
+                if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
+                if (++c == CHUNKS) { c = 0; cph ^= 1u; }
             }
         }
     }
@@ -327,7 +362,7 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)lda * 2};
     const cuuint32_t box[2] = {STAGE_K, 128};
     if (!encode(enc, &tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_codes(enc, &tmB, B, N, K) || !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT>::SF_TILES, 1))
+        !encode_codes(enc, &tmB, B, N, K, CHUNK_K / 2) || !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT>::SF_TILES, 1))
         return cudaErrorInvalidValue;
     memset(&tmC, 0, sizeof(tmC));
     Params p;
