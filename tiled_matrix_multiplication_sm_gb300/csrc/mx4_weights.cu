@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t swizzled64(int r, int j) {
 }
 
 // 32 codes of a row (16 bytes) to BF16, in order.
-template <int FMT>
-__device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, uint32_t f0, uint32_t f1, bool is_wide) {
+template <bool WIDE>
+__device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, uint32_t f0, uint32_t f1) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -94,7 +94,7 @@ __device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, 
         const uint32_t f = j < 2 ? f0 : f1;
         uint32_t r[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
                          __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)};
-        if (FMT == TGEMM_MXFP4 && is_wide)
+        if (WIDE)
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], TWO_126);
 #pragma unroll
@@ -316,13 +316,19 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     is_wide = FMT == TGEMM_MXFP4 && __any_sync(~0u, is_wide);
                     uint4 v[ITEMS][4];
+                    if (is_wide) {
 #pragma unroll
-                    for (int i = 0; i < ITEMS; ++i) {
-                        // Beside a wide block the others take their scale alone too.
-                        const uint32_t alone = b0[i] == 255 ? 0x7FC07FC0u : b0[i] == 0 ? 0x00400040u : b0[i] << 7 | b0[i] << 23;
-                        const uint32_t f0 = is_wide ? alone : sy->factors[b0[i]];
-                        const uint32_t f1 = FMT == TGEMM_MXFP4 ? f0 : sy->factors[b1[i]];
-                        decode_run<FMT>(v[i], w[i], f0, f1, is_wide);
+                        for (int i = 0; i < ITEMS; ++i) {
+                            // Beside a wide block the others take their scale alone too.
+                            const uint32_t f = b0[i] == 255 ? 0x7FC07FC0u : b0[i] == 0 ? 0x00400040u : b0[i] << 7 | b0[i] << 23;
+                            decode_run<true>(v[i], w[i], f, f);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < ITEMS; ++i) {
+                            const uint32_t f0 = sy->factors[b0[i]];
+                            decode_run<false>(v[i], w[i], f0, FMT == TGEMM_MXFP4 ? f0 : sy->factors[b1[i]]);
+                        }
                     }
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ((uint32_t)(idx / STAGES) & 1u) ^ 1u, wait));
                     if (!ok) break;
