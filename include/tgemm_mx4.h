@@ -83,20 +83,24 @@ TGEMM_API long long gemm_mx4_scales_bytes(int rows, int cols, int fmt);
 TGEMM_API int gemm_mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_type,
                                     float* g, cudaStream_t stream);
 
+/* Flag of gemm_mx4_quantize: write g first, as gemm_mx4_tensor_scale does. */
+#define TGEMM_MX4_SET_G 1
+
 /*
  * gemm_mx4_quantize — X (rows x cols, ldx >= cols, TGEMM_TYPE_F32 or _BF16) in
  * 4 bits along its rows (codes, scales: a rows x cols matrix), along its
  * columns (codes_t, scales_t: the cols x rows matrix of its transpose), or
  * both in one reading of X. A pair that is not wanted is NULL, NULL.
  *
- * g: see above; for TGEMM_NVFP4 usually gemm_mx4_tensor_scale's, or that of
- * an earlier step. A g that is not finite or lies outside [2^-100, 2^117]
- * makes every scale NaN. Returns as gemm_mx4_tensor_scale, and
- * TGEMM_ERR_INVALID_ARG for half a pair, no pair, an unknown format or a g
- * with TGEMM_MXFP4.
+ * g: see above; with flags TGEMM_MX4_SET_G (TGEMM_NVFP4 only) it is computed
+ * from X and written, otherwise it is read, say one of an earlier step. A g
+ * that is not finite or lies outside [2^-100, 2^117] makes every scale NaN.
+ * Returns as gemm_mx4_tensor_scale, and TGEMM_ERR_INVALID_ARG for half a
+ * pair, no pair, an unknown format or flag, a g with TGEMM_MXFP4 or a flag
+ * without one.
  */
 TGEMM_API int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, int fmt,
-                                const float* g, void* codes, void* scales, void* codes_t,
+                                float* g, int flags, void* codes, void* scales, void* codes_t,
                                 void* scales_t, cudaStream_t stream);
 
 /*

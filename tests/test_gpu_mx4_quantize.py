@@ -121,6 +121,17 @@ def test_tensor_scale_of_zeros_and_of_nothing(tgemm):
         assert tgemm.mx4_tensor_scale(X).item() == 2.0 ** -100
 
 
+@pytest.mark.parametrize("R,C", [(1, 8191), (1, 8193), (31, 260), (500, 20), (20, 70000)])
+def test_tensor_scale_finds_the_largest_wherever_it_is(tgemm, R, C):
+    X = torch.full((R, C), 0.001, device="cuda")
+    for r, c in ((0, 0), (R - 1, C - 1), (R // 2, C // 3), (0, C - 1)):
+        Y = X.clone()
+        Y[r, c] = -4000.0
+        assert tgemm.mx4_tensor_scale(Y).item() == 2.0
+        assert tgemm.mx4_tensor_scale(Y.bfloat16()).item() == 2.0
+        assert tgemm.mx4_quantize(Y, "nvfp4").tensor_scale.item() == 2.0
+
+
 @pytest.mark.parametrize("value", [21.0, 21.000002, 20.999998, 2688.0, 2688.0002, 1e-30, 3e38, 1e-38])
 def test_tensor_scale_at_the_steps_of_its_powers(tgemm, value):
     X = torch.tensor([[value, -value / 3]], device="cuda")
@@ -188,7 +199,7 @@ def test_nothing_is_written_outside_the_buffers(tgemm, fmt):
             guarded(C * lib.gemm_mx4_codes_pitch(R)), guarded(lib.gemm_mx4_scales_bytes(C, R, code))]
     s = torch.cuda.current_stream().cuda_stream
     gp = g.data_ptr() if fmt == "nvfp4" else 0
-    assert lib.gemm_mx4_quantize(R, C, X.data_ptr(), X.stride(0), 1, code, gp, *(b[1] for b in bufs), s) == 0
+    assert lib.gemm_mx4_quantize(R, C, X.data_ptr(), X.stride(0), 1, code, gp, 0, *(b[1] for b in bufs), s) == 0
     back = torch.full((R + 2, C + 5), 7.0, device="cuda")
     assert lib.gemm_mx4_dequantize(R, C, bufs[0][1], bufs[1][1], code, gp, back[1:].data_ptr(), C + 5, 0, s) == 0
     for t, _, n in bufs:

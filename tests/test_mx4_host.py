@@ -60,11 +60,12 @@ def test_tensor_scale_refuses(lib, args, status):
     ({"rows": -1}, INVALID), ({"cols": -1}, INVALID), ({"ldx": 3}, INVALID), ({"X": 0}, INVALID),
     ({"X": FAKE + 1}, INVALID), ({"type": 7}, INVALID), ({"fmt": 0}, INVALID), ({"g": FAKE}, INVALID),
     ({"fmt": NV, "g": FAKE + 1}, INVALID), ({"codes": 0}, INVALID), ({"scales": 0}, INVALID),
+    ({"flags": 1}, INVALID), ({"fmt": NV, "g": FAKE, "flags": 2}, INVALID), ({"fmt": NV, "flags": 1}, INVALID),
     ({"codes_t": FAKE}, INVALID), ({"codes": 0, "scales": 0}, INVALID),
     ({"codes": FAKE + 8}, ALIGNMENT), ({"scales": FAKE + 1}, ALIGNMENT),
     ({"codes_t": FAKE + 8, "scales_t": FAKE}, ALIGNMENT)])
 def test_quantize_refuses(lib, change, status):
-    a = {"rows": 4, "cols": 4, "X": FAKE, "ldx": 4, "type": F32, "fmt": MX, "g": 0, "codes": FAKE,
+    a = {"rows": 4, "cols": 4, "X": FAKE, "ldx": 4, "type": F32, "fmt": MX, "g": 0, "flags": 0, "codes": FAKE,
          "scales": FAKE, "codes_t": 0, "scales_t": 0, "stream": 0, **change}
     assert lib.gemm_mx4_quantize(*a.values()) == status
 

@@ -77,12 +77,14 @@ int gemm_mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_typ
 }
 
 int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, int fmt,
-                      const float* g, void* codes, void* scales, void* codes_t, void* scales_t,
+                      float* g, int flags, void* codes, void* scales, void* codes_t, void* scales_t,
                       cudaStream_t stream) {
     if (rows < 0 || cols < 0 || !valid_type(x_type) || !valid_fmt(fmt) || ldx < cols)
         return TGEMM_ERR_INVALID_ARG;
-    if (check_g(g, fmt) != TGEMM_OK) return TGEMM_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return TGEMM_OK;
+    if (check_g(g, fmt) != TGEMM_OK || (flags & ~TGEMM_MX4_SET_G) != 0 || (flags != 0 && g == nullptr))
+        return TGEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return flags != 0 ? gemm_mx4_tensor_scale(rows, cols, X, ldx, x_type, g, stream) : TGEMM_OK;
     if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr) ||
         (codes == nullptr && codes_t == nullptr))
         return TGEMM_ERR_INVALID_ARG;
@@ -91,6 +93,7 @@ int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, i
     if (st == TGEMM_OK && codes_t != nullptr) st = check_mx4(codes_t, scales_t);
     int sms = 0;
     if (st == TGEMM_OK) st = tgemm::device_sms(&sms);
+    if (st == TGEMM_OK && flags != 0) st = done(tgemm::mx4_tensor_scale(rows, cols, X, ldx, x_type, g, sms, stream));
     if (st != TGEMM_OK) return st;
     return done(tgemm::mx4_quantize(rows, cols, X, ldx, x_type, fmt, g, static_cast<uint8_t*>(codes),
                                     static_cast<uint8_t*>(scales), static_cast<uint8_t*>(codes_t),

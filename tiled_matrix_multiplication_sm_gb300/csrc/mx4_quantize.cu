@@ -18,52 +18,95 @@ __device__ __forceinline__ uint32_t e4m3(float v) {
     return r & 0xFF;
 }
 
-// The scale byte of a block whose largest |x| has the bits `m`, the divisor d
-// of its values and 1 / d (0, 0: every code is 0).
-template <int FMT>
-__device__ __forceinline__ uint32_t block_scale(uint32_t m, float g, float& d, float& inv) {
-    d = inv = 0.0f;
-    if (m >= 0x7F800000u) return FMT == TGEMM_MXFP4 ? 0xFF : 0x7F;   // an infinity or a NaN in the block
-    if (FMT == TGEMM_MXFP4) {
-        const int e = (int)(m >> 23) - 2;         // biased floor(log2 m), minus 2
-        const uint32_t byte = e > 0 ? (uint32_t)e : 0u;
-        inv = __uint_as_float((254u - byte) << 23);     // exact: 2^(127 - byte)
-        return byte;
-    }
-    if (!(g >= kMinG && g <= kMaxG)) return 0x7F;
-    const uint32_t byte = e4m3(__fdiv_rn(__uint_as_float(m), 6.0f * g));
-    if (byte != 0) {
-        d = e4m3_value(byte) * g;
-        inv = __frcp_rn(d);
-    }
-    return byte;
-}
-
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// E4M3 bytes (not NaN) to FP32 through halves, which hold them exactly.
+__device__ __forceinline__ float e4m3_fast(uint32_t byte) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
+    return __half2float(__ushort_as_half((unsigned short)h));
+}
 
-// Two values over d. A power of two (MXFP4) multiplies exactly. An NVFP4
-// divisor needs a true quotient, or values that lie on the midpoint of two
-// codes (common: BF16 values over scales of 4 bits) would round either way:
-// q = x / d from the correctly rounded reciprocal with one correction step,
-// q + (x - q d) inv, which rounds correctly (Markstein, 1990).
+// An E4M3 byte as two equal halves; 0x7F gives NaN.
+__device__ __forceinline__ uint32_t e4m3_halves(uint32_t byte) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)((byte & 0x7F) * 0x0101u)));
+    return h;
+}
+
+// What the scales of a matrix are made with.
+struct Scaling {
+    float g, six_g, inv, cap;
+    __device__ __forceinline__ explicit Scaling(const float* gp) {
+        g = mx4_g(gp);
+        if (!(g >= kMinG && g <= kMaxG)) g = 0.0f;       // every scale NaN
+        six_g = 6.0f * g;
+        inv = __frcp_rn(six_g);
+        cap = 896.0f * six_g;                            // quotients from 464 on all give 448
+    }
+};
+
+// The scale byte of a block whose largest |x| is m (an infinity or a NaN if
+// the block holds one), and what its values are divided with: 1 / d and -d (0
+// and 0: every code is 0). Quotients are q = x (1 / d) with one correction
+// step, q + (x - q d) (1 / d) (Markstein, 1990): a quotient that is the
+// midpoint of two codes, common for BF16 values over scales of 4 bits, comes
+// out exact, where x (1 / d) alone would fall to either side.
 template <int FMT>
-__device__ __forceinline__ void divide2(float& x0, float& x1, uint64_t inv2, uint64_t negd2) {
+__device__ __forceinline__ uint32_t block_scale(float m, const Scaling& k, float& inv, float& neg_d) {
+    const bool bad = __float_as_uint(m) >= 0x7F800000u;
+    if (FMT == TGEMM_MXFP4) {
+        const int e = (int)(__float_as_uint(m) >> 23) - 2;     // biased floor(log2 m), minus 2
+        const uint32_t byte = e > 0 ? (uint32_t)e : 0u;
+        inv = bad ? 0.0f : __uint_as_float((254u - byte) << 23);       // 2^(127 - byte): exact
+        neg_d = 0.0f;
+        return bad ? 0xFFu : byte;
+    }
+    const float c = fminf(m, k.cap);
+    float q = c * k.inv;
+    q = fmaf(fmaf(-q, k.six_g, c), k.inv, q);
+    const uint32_t byte = e4m3(q);
+    const float d = e4m3_fast(byte) * k.g;
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+    y = fmaf(y, fmaf(-d, y, 1.0f), y);                         // Newton
+    const bool none = bad || byte == 0 || k.g == 0.0f;
+    inv = none ? 0.0f : y;
+    neg_d = none ? 0.0f : -d;
+    return bad || k.g == 0.0f ? 0x7Fu : byte;
+}
+
+// Two values over their divisors.
+template <int FMT>
+__device__ __forceinline__ float2 divide2(float x0, float x1, uint64_t inv2, uint64_t neg_d2) {
     const uint64_t x = pack2(x0, x1);
     uint64_t q = fma2(x, inv2, 0);
-    if (FMT == TGEMM_NVFP4) q = fma2(fma2(q, negd2, x), inv2, q);
-    unpack2(q, x0, x1);
+    if (FMT == TGEMM_NVFP4) q = fma2(fma2(q, neg_d2, x), inv2, q);
+    return unpack2(q);
+}
+
+// Eight values to a word of codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8(float a, float b, float c, float d, float e, float f, float g, float h) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+        "mov.b32 %0, {p, q, r, s};\n\t}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h));
+    return r;
 }
 
 __global__ void __launch_bounds__(32) scale_init_kernel(float* g) {
@@ -124,8 +167,11 @@ tensor_scale_kernel(int rows, int cols, const T* X, long ldx, bool vec, int shif
         m = __reduce_max_sync(0xffu, most[threadIdx.x]);
         // Positive floats order as their bits, and g only grows with |x|: the
         // result does not depend on the order of the blocks.
-        if (threadIdx.x == 0 && m != 0)
-            atomicMax(reinterpret_cast<unsigned*>(g), __float_as_uint(power_for(__uint_as_float(m))));
+        if (threadIdx.x == 0) {
+            const float p = power_for(__uint_as_float(m));
+            if (gridDim.x == 1) *g = p;
+            else atomicMax(reinterpret_cast<unsigned*>(g), __float_as_uint(p));
+        }
     }
 }
 
@@ -140,46 +186,94 @@ constexpr int Q_CODES = 80;       // bytes between staged rows of transposed cod
 template <typename T> __host__ __device__ constexpr int q_pitch() { return QT * (int)sizeof(T) + 16; }   // bytes
 template <typename T> __host__ __device__ constexpr int q_smem() { return QT * q_pitch<T>() + QT * Q_CODES + 2 * 1024; }
 
-// Largest |x| of two packed BF16, or of one FP32, as an integer per half.
+// The larger magnitude of each half (BF16) or of the word (FP32), its sign
+// arbitrary; NaN if either is.
 template <typename T>
-__device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t v) {
-    if constexpr (sizeof(T) == 2) return __vmaxu2(m, v & 0x7FFF7FFFu);
-    else return max(m, v & 0x7FFFFFFFu);
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (sizeof(T) == 2) {
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+        float f;
+        asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        r = __float_as_uint(f);
+    }
+    return r;
 }
+__device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// The codes of B values held as words of T, and the block's scale byte.
+// A block along a row: its values in words of T, in order, to codes and the
+// scale byte.
 template <typename T, int FMT>
-__device__ __forceinline__ uint32_t quantize_block(const uint32_t* w, float g, uint32_t* codes) {
+__device__ __forceinline__ uint32_t quantize_row(const uint32_t* w, const Scaling& k, uint32_t* codes) {
     constexpr int B = mx4_block(FMT), WORDS = B * (int)sizeof(T) / 4;
-    uint32_t m = 0;
+    uint32_t m = w[0];
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) m = max_abs<T>(m, w[i]);
-    if constexpr (sizeof(T) == 2) m = max(m << 16, m & 0xFFFF0000u);
-    float d, inv;
-    const uint32_t byte = block_scale<FMT>(m, g, d, inv);
-    const uint64_t inv2 = pack2(inv, inv), negd2 = pack2(-d, -d);
+    for (int i = 1; i < WORDS; ++i) m = max_abs<T>(m, w[i]);
+    float most = fabsf(__uint_as_float(m));
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t lo = m << 16 & 0x7FFF0000u, hi = m & 0x7FFF0000u;      // magnitudes order as their bits
+        most = __uint_as_float(max(lo, hi));
+    }
+    float inv, neg_d;
+    const uint32_t byte = block_scale<FMT>(most, k, inv, neg_d);
+    const uint64_t inv2 = pack2(inv, inv), neg_d2 = pack2(neg_d, neg_d);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
-        float x[8];
+        float2 q[4];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            if constexpr (sizeof(T) == 2) {
-                const uint32_t v = w[i * 4 + j / 2];
-                x[j] = __uint_as_float(v << 16);
-                x[j + 1] = __uint_as_float(v & 0xFFFF0000u);
-            } else {
-                x[j] = __uint_as_float(w[i * 8 + j]);
-                x[j + 1] = __uint_as_float(w[i * 8 + j + 1]);
-            }
-            divide2<FMT>(x[j], x[j + 1], inv2, negd2);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 2)
+                q[j] = divide2<FMT>(low_bf16(w[i * 4 + j]), high_bf16(w[i * 4 + j]), inv2, neg_d2);
+            else
+                q[j] = divide2<FMT>(__uint_as_float(w[i * 8 + 2 * j]), __uint_as_float(w[i * 8 + 2 * j + 1]), inv2, neg_d2);
         }
-        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-            "mov.b32 %0, {a, b, c, d};\n\t}"
-            : "=r"(codes[i]) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+        codes[i] = e2m1x8(q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y);
     }
     return byte;
+}
+
+// Blocks of two neighbouring columns, their values side by side (a word of
+// two BF16, or two words of FP32, to a row). Codes of the first column, then
+// of the second; the scale bytes in the low and high half.
+template <typename T, int FMT>
+__device__ __forceinline__ uint32_t quantize_columns(const uint32_t* w, const Scaling& k, uint32_t (&codes)[2][mx4_block(FMT) / 8]) {
+    constexpr int B = mx4_block(FMT);
+    float most[2];
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = w[0];
+#pragma unroll
+        for (int i = 1; i < B; ++i) m = max_abs<T>(m, w[i]);
+        most[0] = fabsf(low_bf16(m));
+        most[1] = fabsf(high_bf16(m));
+    } else {
+        uint32_t m[2] = {w[0], w[1]};
+#pragma unroll
+        for (int i = 1; i < B; ++i) {
+            m[0] = max_abs<T>(m[0], w[2 * i]);
+            m[1] = max_abs<T>(m[1], w[2 * i + 1]);
+        }
+        most[0] = fabsf(__uint_as_float(m[0]));
+        most[1] = fabsf(__uint_as_float(m[1]));
+    }
+    float inv[2], neg_d[2];
+    const uint32_t b0 = block_scale<FMT>(most[0], k, inv[0], neg_d[0]), b1 = block_scale<FMT>(most[1], k, inv[1], neg_d[1]);
+    const uint64_t inv2 = pack2(inv[0], inv[1]), neg_d2 = pack2(neg_d[0], neg_d[1]);
+#pragma unroll
+    for (int i = 0; i < B / 8; ++i) {
+        float2 q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(T) == 2)
+                q[j] = divide2<FMT>(low_bf16(w[i * 8 + j]), high_bf16(w[i * 8 + j]), inv2, neg_d2);
+            else
+                q[j] = divide2<FMT>(__uint_as_float(w[i * 16 + 2 * j]), __uint_as_float(w[i * 16 + 2 * j + 1]), inv2, neg_d2);
+        }
+        codes[0][i] = e2m1x8(q[0].x, q[1].x, q[2].x, q[3].x, q[4].x, q[5].x, q[6].x, q[7].x);
+        codes[1][i] = e2m1x8(q[0].y, q[1].y, q[2].y, q[3].y, q[4].y, q[5].y, q[6].y, q[7].y);
+    }
+    return b0 | b1 << 16;
 }
 
 // Where a tile's scale byte of row r, block b lies in its 128 / B / 4 scale tiles.
@@ -195,7 +289,7 @@ __device__ __forceinline__ void write_scales(uint8_t* dst, const uint8_t* staged
 }
 
 template <typename T, int FMT, bool ROWS, bool TRANS>
-__global__ void __launch_bounds__(Q_THREADS)
+__global__ void __launch_bounds__(Q_THREADS, sizeof(T) == 2 ? 4 : 2)
 quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, uint8_t* codes,
                 uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t) {
     constexpr int B = mx4_block(FMT), NB = QT / B, WORDS = B * (int)sizeof(T) / 4;
@@ -207,7 +301,7 @@ quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, u
     const long c0 = (long)blockIdx.x * QT;
     pdl_launch_dependents();
     pdl_wait();
-    const float g = mx4_g(gp);
+    const Scaling k(gp);
     // The scales cover spans of 256, so the grid goes on to an even tile.
     const long end = ((long)R + 2 * QT - 1) / (2 * QT) * (2 * QT);
     for (long r0 = (long)blockIdx.y * QT; r0 < end; r0 += (long)gridDim.y * QT) {
@@ -247,11 +341,11 @@ quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, u
                 const int row = i / (NB / 4) * 8 + (lane & 7), b = i % (NB / 4) * 4 + (lane >> 3);
                 uint32_t w[WORDS], out[B / 8];
 #pragma unroll
-                for (int k = 0; k < WORDS / 4; ++k) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * PITCH + b * B * (int)sizeof(T) + k * 16);
-                    w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+                for (int j = 0; j < WORDS / 4; ++j) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * PITCH + b * B * (int)sizeof(T) + j * 16);
+                    w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
                 }
-                sc[tile_scale_at(row, b)] = (uint8_t)quantize_block<T, FMT>(w, g, out);
+                sc[tile_scale_at(row, b)] = (uint8_t)quantize_row<T, FMT>(w, k, out);
                 const long at = c0 / 2 + b * (B / 2);
                 if (r0 + row < R && at < pitch) {
                     uint8_t* dst = codes + (r0 + row) * pitch + at;
@@ -265,27 +359,26 @@ quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, u
 #pragma unroll 1
             for (int i = t; i < QT / 2 * NB; i += Q_THREADS) {
                 const int c = i % (QT / 2) * 2, b = i / (QT / 2);
-                uint32_t w[2][WORDS], out[B / 8];
+                constexpr int W = (int)sizeof(T) / 2;            // words of a row of two columns
+                uint32_t w[B * W], out[2][B / 8];
                 const uint8_t* src = smem + b * B * PITCH + c * (int)sizeof(T);
 #pragma unroll
-                for (int k = 0; k < WORDS; ++k) {
-                    if constexpr (sizeof(T) == 2) {
-                        const uint32_t u = *reinterpret_cast<const uint32_t*>(src + 2 * k * PITCH);
-                        const uint32_t v = *reinterpret_cast<const uint32_t*>(src + (2 * k + 1) * PITCH);
-                        w[0][k] = __byte_perm(u, v, 0x5410);
-                        w[1][k] = __byte_perm(u, v, 0x7632);
+                for (int j = 0; j < B; ++j) {
+                    if constexpr (W == 1) {
+                        w[j] = *reinterpret_cast<const uint32_t*>(src + j * PITCH);
                     } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(src + k * PITCH);
-                        w[0][k] = u.x;
-                        w[1][k] = u.y;
+                        const uint2 u = *reinterpret_cast<const uint2*>(src + j * PITCH);
+                        w[2 * j] = u.x;
+                        w[2 * j + 1] = u.y;
                     }
                 }
+                const uint32_t bytes = quantize_columns<T, FMT>(w, k, out);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    sc[1024 + tile_scale_at(c + h, b)] = (uint8_t)quantize_block<T, FMT>(w[h], g, out);
+                    sc[1024 + tile_scale_at(c + h, b)] = (uint8_t)(bytes >> 16 * h);
                     uint8_t* dst = staged + (c + h) * Q_CODES + b * (B / 2);
-                    if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-                    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+                    if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+                    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[h][0], out[h][1]);
                 }
             }
         }
@@ -309,7 +402,8 @@ quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, u
     }
 }
 
-// Eight codes a thread, several rows in flight; bound by writing X.
+// Eight codes of each of eight rows a thread, all loads before the first use;
+// a warp stores 512 bytes of a row side by side. Bound by writing X.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, const float* gp, T* X,
@@ -320,35 +414,54 @@ dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, con
     const long c = ((long)blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (c >= C) return;
     const float g = mx4_g(gp);
-    const long pitch = mx4_pitch(C), tiles_k = mx4_tiles_k(C, FMT);
-#pragma unroll 4
-    for (long r = blockIdx.y; r < R; r += gridDim.y) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + c / 2));
-        const float s = mx4_scale_value<FMT>(__ldg(scales + mx4_scale_at(r, c / B, tiles_k)));
-        float v[8];
+    const long pitch = mx4_pitch(C), row_of_tiles = mx4_tiles_k(C, FMT) * MX4_TILE_BYTES;
+    const uint8_t* code = codes + c / 2;
+    const uint8_t* scale = scales + mx4_scale_at(0, c / B, 0);
+    constexpr int ROWS = 8;                                  // consecutive rows a thread
+    const long r0 = (long)blockIdx.y * ROWS;
+    for (long r = r0; r < R; r += (long)gridDim.y * ROWS) {
+        const int n = (int)min((long)ROWS, R - r);
+        uint32_t w[ROWS], b[ROWS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t h;      // two codes as halves
-            asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(w >> 8 * j));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            v[2 * j] = f.x * s * g;
-            v[2 * j + 1] = f.y * s * g;
-        }
-        T* dst = X + r * ldx + c;
-        if (vec && c + 8 <= C) {
-            if constexpr (sizeof(T) == 4) {
-                reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                __nv_bfloat162 b[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(b);
+        for (int i = 0; i < ROWS; ++i) {
+            if (i < n) {
+                w[i] = __ldg(reinterpret_cast<const uint32_t*>(code + (r + i) * pitch));
+                // Eight rows from a multiple of 8 on lie in one column of a tile.
+                b[i] = __ldg(scale + (r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4);
             }
-        } else {
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < C) dst[j] = (T)v[j];
+        for (int i = 0; i < ROWS; ++i) {
+            if (i >= n) break;
+            float v[8];
+            const float s = FMT == TGEMM_MXFP4 ? e8m0_value(b[i]) : 1.0f;
+            const uint32_t sh = FMT == TGEMM_MXFP4 ? 0 : e4m3_halves(b[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t h;      // two codes as halves; NVFP4 scales multiply exactly in them
+                asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(w[i] >> 8 * j));
+                __half2 x = *reinterpret_cast<const __half2*>(&h);
+                if (FMT == TGEMM_NVFP4) x = __hmul2(x, *reinterpret_cast<const __half2*>(&sh));
+                const float2 f = __half22float2(x);
+                v[2 * j] = FMT == TGEMM_MXFP4 ? f.x * s : f.x * g;
+                v[2 * j + 1] = FMT == TGEMM_MXFP4 ? f.y * s : f.y * g;
+            }
+            T* dst = X + (r + i) * ldx + c;
+            if (vec && c + 8 <= C) {
+                if constexpr (sizeof(T) == 4) {
+                    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    __nv_bfloat162 o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < C) dst[j] = (T)v[j];
+            }
         }
     }
 }
@@ -381,10 +494,25 @@ bool rows_on_16(const void* X, long ldx, int esz) {
     return reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * esz % 16 == 0;
 }
 
+// As much of the SM's memory as shared as there is: with the default split
+// fewer blocks than the registers allow were resident.
+template <auto KERNEL>
+cudaError_t most_shared_memory_once() {
+    static std::atomic<unsigned long long> done{0};    // bit d: set on device d
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (e != cudaSuccess || (done.load(std::memory_order_acquire) & bit) != 0) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <typename T, int FMT, bool ROWS, bool TRANS>
 cudaError_t launch_quantize(int R, int C, const void* X, long ldx, const float* g, uint8_t* codes,
                             uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, cudaStream_t s) {
-    const cudaError_t e = set_smem_limit_once<quantize_kernel<T, FMT, ROWS, TRANS>>(q_smem<T>());
+    cudaError_t e = set_smem_limit_once<quantize_kernel<T, FMT, ROWS, TRANS>>(q_smem<T>());
+    if (e == cudaSuccess) e = most_shared_memory_once<quantize_kernel<T, FMT, ROWS, TRANS>>();
     if (e != cudaSuccess) return e;
     const long rows = ((long)R + 255) / 256 * 2;
     const dim3 grid((unsigned)(((long)C + 255) / 256 * 2), (unsigned)(rows < 65535 ? rows : 65535));
@@ -407,15 +535,20 @@ cudaError_t quantize_type(int R, int C, const void* X, long ldx, const float* g,
 
 cudaError_t mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_type, float* g,
                              int num_sms, cudaStream_t s) {
-    cudaError_t e = launch_pdl(scale_init_kernel, dim3(1), dim3(32), 0, s, g);
-    if (e != cudaSuccess || rows == 0 || cols == 0) return e;
     const int esz = x_type == TGEMM_TYPE_F32 ? 4 : 2;
     const bool vec = rows_on_16(X, ldx, esz);
     const long pieces = vec ? ((long)cols * esz + 15) / 16 : cols;
     int shift = 5;
     while (shift < 8 && (1L << shift) < pieces) ++shift;
     const long blocks = ((long)rows + (256 >> shift) - 1) / (256 >> shift);
-    const dim3 grid((unsigned)(blocks < 8L * num_sms ? blocks : 8L * num_sms));
+    // One block, which needs no initial value, takes up to 32 loads a thread:
+    // less than a second launch costs.
+    const bool one = ((long)rows + (256 >> shift) - 1) / (256 >> shift) * ((pieces + (1L << shift) - 1) >> shift) <= 32;
+    const dim3 grid((unsigned)(one ? 1 : blocks < 8L * num_sms ? blocks : 8L * num_sms));
+    if (!one) {
+        const cudaError_t e = launch_pdl(scale_init_kernel, dim3(1), dim3(32), 0, s, g);
+        if (e != cudaSuccess) return e;
+    }
     return x_type == TGEMM_TYPE_F32
                ? launch_pdl(tensor_scale_kernel<float>, grid, dim3(256), 0, s, rows, cols,
                             static_cast<const float*>(X), ldx, vec, shift, g)
@@ -438,7 +571,7 @@ cudaError_t mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type
 template <typename T>
 static cudaError_t dequantize_type(int rows, int cols, const uint8_t* codes, const uint8_t* scales,
                                    int fmt, const float* g, void* X, long ldx, cudaStream_t s) {
-    const dim3 grid((unsigned)(((long)cols + 2047) / 2048), grid_rows(((long)rows + 3) / 4));
+    const dim3 grid((unsigned)(((long)cols + 2047) / 2048), grid_rows(((long)rows + 7) / 8));
     const bool vec = rows_on_16(X, ldx, sizeof(T));
     auto x = static_cast<T*>(X);
     return fmt == TGEMM_MXFP4

@@ -10,7 +10,6 @@ current one), and what a call allocates belongs to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -21,6 +20,7 @@ from .binding import TGEMM_OK, TgemmError, _check_matrix, _on_device, _stream_ha
 
 TGEMM_MXFP4 = 1
 TGEMM_NVFP4 = 2
+TGEMM_MX4_SET_G = 1
 TGEMM_TYPE_F32 = 0
 TGEMM_TYPE_BF16 = 1
 
@@ -34,7 +34,7 @@ _SIGNATURES = {
     "gemm_mx4_codes_pitch": (ctypes.c_longlong, [_INT]),
     "gemm_mx4_scales_bytes": (ctypes.c_longlong, [_INT, _INT, _INT]),
     "gemm_mx4_tensor_scale": (_INT, [_INT, _INT, _VP, _LONG, _INT, _VP, _VP]),
-    "gemm_mx4_quantize": (_INT, [_INT, _INT, _VP, _LONG, _INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "gemm_mx4_quantize": (_INT, [_INT, _INT, _VP, _LONG, _INT, _INT, _VP, _INT, _VP, _VP, _VP, _VP, _VP]),
     "gemm_mx4_dequantize": (_INT, [_INT, _INT, _VP, _VP, _INT, _VP, _VP, _LONG, _INT, _VP]),
     "gemm_mx4_pack": (_INT, [_INT, _INT, _INT, _VP, _LONG, _VP, _LONG, _VP, _VP, _VP]),
     "gemm_mx4": (_INT, [_INT, _INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP, _INT] + _OUT),
@@ -69,9 +69,12 @@ def _type(dtype: torch.dtype, name: str) -> int:
     return _TYPES[dtype]
 
 
-def _allocating(stream: Optional[torch.cuda.Stream]):
-    """What is allocated inside belongs to ``stream``."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(stream: Optional[torch.cuda.Stream], *size, dtype, device) -> torch.Tensor:
+    """torch.empty, of memory that belongs to ``stream`` (default: the current one)."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
 
 
 def _check_scale(g: Optional[torch.Tensor], fmt: str, device: torch.device) -> int:
@@ -87,54 +90,57 @@ def _check_scale(g: Optional[torch.Tensor], fmt: str, device: torch.device) -> i
     return g.data_ptr()
 
 
+def _sizes(rows: int, cols: int, fmt: str) -> Tuple[int, int]:
+    """Bytes of the codes and of the scales of a matrix."""
+    lib = load()
+    codes = int(lib.gemm_mx4_codes_pitch(cols))
+    scales = int(lib.gemm_mx4_scales_bytes(rows, cols, _format(fmt)))
+    if codes < 0 or scales < 0:
+        raise ValueError(f"a 4-bit matrix cannot be {rows} x {cols}")
+    return rows * codes, scales
+
+
 class Mx4Matrix:
     """A ``rows`` x ``cols`` matrix in 4 bits, quantised along its columns
     (the axis a product sums over): ``codes``, ``scales`` (uint8, in the
     library's layout) and, for nvfp4, ``tensor_scale`` (one float32)."""
 
-    __slots__ = ("fmt", "rows", "cols", "codes", "scales", "tensor_scale")
+    __slots__ = ("fmt", "rows", "cols", "shape", "device", "tensor_scale", "_held", "_codes", "_scales", "_g")
 
     def __init__(self, fmt: str, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor,
                  tensor_scale: Optional[torch.Tensor] = None):
-        code = _format(fmt)
-        lib = load()
-        pitch = int(lib.gemm_mx4_codes_pitch(cols))
-        need = int(lib.gemm_mx4_scales_bytes(rows, cols, code))
-        if pitch < 0 or need < 0:
-            raise ValueError(f"a 4-bit matrix cannot be {rows} x {cols}")
-        for t, size, name in ((codes, rows * pitch, "codes"), (scales, need, "scales")):
+        for t, size, name in zip((codes, scales), _sizes(rows, cols, fmt), ("codes", "scales")):
             if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() < size:
                 raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of {size} bytes")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
-        _check_scale(tensor_scale, fmt, codes.device)
-        self.fmt, self.rows, self.cols = fmt, rows, cols
-        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+        self._set(fmt, rows, cols, (codes, scales), codes.data_ptr(), scales.data_ptr(), codes.device,
+                  tensor_scale, _check_scale(tensor_scale, fmt, codes.device))
+
+    def _set(self, fmt, rows, cols, held, codes, scales, device, tensor_scale, g):
+        self.fmt, self.rows, self.cols, self.shape, self.device = fmt, rows, cols, (rows, cols), device
+        self._held, self._codes, self._scales = held, codes, scales
+        self.tensor_scale, self._g = tensor_scale, g
 
     @classmethod
-    def empty(cls, fmt: str, rows: int, cols: int, device,
-              tensor_scale: Optional[torch.Tensor] = None) -> "Mx4Matrix":
-        code = _format(fmt)
-        if rows < 0 or cols < 0:
-            raise ValueError(f"a 4-bit matrix cannot be {rows} x {cols}")
-        m = cls.__new__(cls)
-        lib = load()
-        m.fmt, m.rows, m.cols, m.tensor_scale = fmt, rows, cols, tensor_scale
-        m.codes = torch.empty(rows * lib.gemm_mx4_codes_pitch(cols), dtype=torch.uint8, device=device)
-        m.scales = torch.empty(lib.gemm_mx4_scales_bytes(rows, cols, code), dtype=torch.uint8,
-                               device=device)
-        return m
+    def _empty(cls, fmt, rows, cols, device, tensor_scale, g, stream) -> "Mx4Matrix":
+        """An unwritten matrix, codes and scales in one allocation."""
+        n, m = _sizes(rows, cols, fmt)
+        data = _empty(stream, n + m, dtype=torch.uint8, device=device)
+        at = data.data_ptr()
+        self = cls.__new__(cls)
+        self._set(fmt, rows, cols, (data, n), at, at + n, device, tensor_scale, g)
+        return self
 
     @property
-    def shape(self) -> Tuple[int, int]:
-        return self.rows, self.cols
+    def codes(self) -> torch.Tensor:
+        data, n = self._held
+        return data[:n] if isinstance(n, int) else data
 
     @property
-    def device(self) -> torch.device:
-        return self.codes.device
-
-    def _g(self) -> int:
-        return 0 if self.tensor_scale is None else self.tensor_scale.data_ptr()
+    def scales(self) -> torch.Tensor:
+        data, n = self._held
+        return data[n:] if isinstance(n, int) else n
 
     def __repr__(self) -> str:
         return f"Mx4Matrix({self.fmt}, {self.rows} x {self.cols}, {self.device})"
@@ -161,8 +167,7 @@ def mx4_tensor_scale(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None
     """The nvfp4 scale of X: the smallest power of two g with 2688 g >= |X|
     (one float32 on X's device; infinities and NaN are left out)."""
     ldx, kind = _check_values(X, "X")
-    with _allocating(stream):
-        g = torch.empty(1, dtype=torch.float32, device=X.device)
+    g = _empty(stream, 1, dtype=torch.float32, device=X.device)
     _done(_on_device(X.device, lambda dev: load().gemm_mx4_tensor_scale(
         X.shape[0], X.shape[1], X.data_ptr(), ldx, kind, g.data_ptr(), _stream_handle(stream, dev))),
         "gemm_mx4_tensor_scale")
@@ -173,16 +178,16 @@ def _quantize(X, fmt, tensor_scale, stream, rows: bool, trans: bool):
     code = _format(fmt)
     ldx, kind = _check_values(X, "X")
     R, C = X.shape
-    if fmt == "nvfp4" and tensor_scale is None:
-        tensor_scale = mx4_tensor_scale(X, stream=stream)
-    g = _check_scale(tensor_scale, fmt, X.device)
-    with _allocating(stream):
-        q = Mx4Matrix.empty(fmt, R, C, X.device, tensor_scale) if rows else None
-        t = Mx4Matrix.empty(fmt, C, R, X.device, tensor_scale) if trans else None
-    ptrs = [x.data_ptr() for m in (q, t) for x in ((m.codes, m.scales) if m else ())]
-    ptrs = ptrs if rows and trans else ptrs + [0, 0] if rows else [0, 0] + ptrs
-    _done(_on_device(X.device, lambda dev: load().gemm_mx4_quantize(
-        R, C, X.data_ptr(), ldx, kind, code, g, *ptrs, _stream_handle(stream, dev))),
+    device = X.device
+    set_g = fmt == "nvfp4" and tensor_scale is None
+    if set_g:
+        tensor_scale = _empty(stream, 1, dtype=torch.float32, device=device)
+    g = _check_scale(tensor_scale, fmt, device)
+    q = Mx4Matrix._empty(fmt, R, C, device, tensor_scale, g, stream) if rows else None
+    t = Mx4Matrix._empty(fmt, C, R, device, tensor_scale, g, stream) if trans else None
+    _done(_on_device(device, lambda dev: load().gemm_mx4_quantize(
+        R, C, X.data_ptr(), ldx, kind, code, g, TGEMM_MX4_SET_G if set_g else 0, q._codes if rows else 0, q._scales if rows else 0,
+        t._codes if trans else 0, t._scales if trans else 0, _stream_handle(stream, dev))),
         "gemm_mx4_quantize")
     return q, t
 
@@ -212,13 +217,12 @@ def mx4_dequantize(Q: Mx4Matrix, dtype: torch.dtype = torch.float32,
     _check_mx4(Q, "Q")
     if out is None:
         _type(dtype, "dtype")
-        with _allocating(stream):
-            out = torch.empty(Q.shape, dtype=dtype, device=Q.device)
+        out = _empty(stream, Q.rows, Q.cols, dtype=dtype, device=Q.device)
     elif tuple(out.shape) != Q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {Q.shape}")
     ldx, kind = _check_values(out, "out")
     _done(_on_device(Q.device, lambda dev: load().gemm_mx4_dequantize(
-        Q.rows, Q.cols, Q.codes.data_ptr(), Q.scales.data_ptr(), _FORMATS[Q.fmt], Q._g(),
+        Q.rows, Q.cols, Q._codes, Q._scales, _FORMATS[Q.fmt], Q._g,
         out.data_ptr(), ldx, kind, _stream_handle(stream, dev))), "gemm_mx4_dequantize")
     return out
 
@@ -244,12 +248,11 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: str = "mxfp4",
         raise ValueError(f"scales have shape {tuple(scales.shape)}, expected {(rows, blocks)}")
     if scales.device != codes.device:
         raise ValueError("codes and scales are on different devices")
-    _check_scale(tensor_scale, fmt, codes.device)
-    with _allocating(stream):
-        q = Mx4Matrix.empty(fmt, rows, cols, codes.device, tensor_scale)
+    g = _check_scale(tensor_scale, fmt, codes.device)
+    q = Mx4Matrix._empty(fmt, rows, cols, codes.device, tensor_scale, g, stream)
     _done(_on_device(codes.device, lambda dev: load().gemm_mx4_pack(
-        rows, cols, code, codes.data_ptr(), ldc, scales.data_ptr(), lds, q.codes.data_ptr(),
-        q.scales.data_ptr(), _stream_handle(stream, dev))), "gemm_mx4_pack")
+        rows, cols, code, codes.data_ptr(), ldc, scales.data_ptr(), lds, q._codes,
+        q._scales, _stream_handle(stream, dev))), "gemm_mx4_pack")
     return q
 
 
@@ -258,10 +261,8 @@ def _output(out, M, N, out_dtype, device, beta, bias, stream):
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out, the C it scales")
-        _type(out_dtype, "out_dtype")
-        with _allocating(stream):
-            out = torch.empty((M, N), dtype=out_dtype, device=device)
-        ldc, kind = max(N, 1), _TYPES[out_dtype]
+        ldc, kind = max(N, 1), _type(out_dtype, "out_dtype")
+        out = _empty(stream, M, N, dtype=out_dtype, device=device)
     else:
         ldc, kind = _check_values(out, "out")
         if tuple(out.shape) != (M, N):
@@ -293,8 +294,8 @@ def gemm_mx4(A: Mx4Matrix, B: Mx4Matrix, out_dtype: torch.dtype = torch.float32,
         raise ValueError(f"A is on {A.device}, B on {B.device}")
     C, ldc, kind, bias_ptr = _output(out, A.rows, B.rows, out_dtype, A.device, beta, bias, stream)
     _done(_on_device(A.device, lambda dev: load().gemm_mx4(
-        A.rows, B.rows, A.cols, A.codes.data_ptr(), A.scales.data_ptr(), A._g(),
-        B.codes.data_ptr(), B.scales.data_ptr(), B._g(), _FORMATS[A.fmt], C.data_ptr(), ldc, kind,
+        A.rows, B.rows, A.cols, A._codes, A._scales, A._g, B._codes, B._scales, B._g,
+        _FORMATS[A.fmt], C.data_ptr(), ldc, kind,
         alpha, beta, bias_ptr, _stream_handle(stream, dev))), "gemm_mx4")
     return C
 
@@ -313,7 +314,7 @@ def gemm_w4(A: torch.Tensor, W: Mx4Matrix, out_dtype: torch.dtype = torch.float3
         raise ValueError(f"A is on {A.device}, W on {W.device}")
     C, ldc, kind, bias_ptr = _output(out, A.shape[0], W.rows, out_dtype, A.device, beta, bias, stream)
     _done(_on_device(A.device, lambda dev: load().gemm_w4(
-        A.shape[0], W.rows, W.cols, A.data_ptr(), lda, W.codes.data_ptr(), W.scales.data_ptr(),
-        W._g(), _FORMATS[W.fmt], C.data_ptr(), ldc, kind, alpha, beta, bias_ptr,
+        A.shape[0], W.rows, W.cols, A.data_ptr(), lda, W._codes, W._scales,
+        W._g, _FORMATS[W.fmt], C.data_ptr(), ldc, kind, alpha, beta, bias_ptr,
         _stream_handle(stream, dev))), "gemm_w4")
     return C
