@@ -97,7 +97,7 @@ int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, i
     if (st != TGEMM_OK) return st;
     return done(tgemm::mx4_quantize(rows, cols, X, ldx, x_type, fmt, g, static_cast<uint8_t*>(codes),
                                     static_cast<uint8_t*>(scales), static_cast<uint8_t*>(codes_t),
-                                    static_cast<uint8_t*>(scales_t), stream));
+                                    static_cast<uint8_t*>(scales_t), sms, stream));
 }
 
 int gemm_mx4_dequantize(int rows, int cols, const void* codes, const void* scales, int fmt,

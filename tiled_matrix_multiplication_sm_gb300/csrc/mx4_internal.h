@@ -89,7 +89,7 @@ cudaError_t mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_
                              int num_sms, cudaStream_t s);
 cudaError_t mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, int fmt,
                          const float* g, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
-                         uint8_t* scales_t, cudaStream_t s);
+                         uint8_t* scales_t, int num_sms, cudaStream_t s);
 cudaError_t mx4_dequantize(int rows, int cols, const uint8_t* codes, const uint8_t* scales,
                            int fmt, const float* g, void* X, long ldx, int x_type, cudaStream_t s);
 cudaError_t mx4_pack(int rows, int cols, int fmt, const uint8_t* src_codes, long src_ldc,

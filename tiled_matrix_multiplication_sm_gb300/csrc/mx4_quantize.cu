@@ -2,7 +2,7 @@
 // import of row-major codes and scales. Formats and layout are described in
 // include/tgemm_mx4.h.
 
-#include "mx4_internal.h"
+#include "mx4_tile.h"
 
 #include <cuda_fp16.h>
 
@@ -175,16 +175,36 @@ tensor_scale_kernel(int rows, int cols, const T* X, long ldx, bool vec, int shif
     }
 }
 
-// Quantising, one block of threads to a 128 x 128 tile of X staged in shared
-// memory: in it both directions read 128 rows of 128 / B blocks, and both
-// write whole scale tiles and 64-byte runs of codes, so X is read once even
-// when its transpose is wanted too. Bound by HBM (X in, codes and scales out).
+// Quantising, tile by tile of 128 x 128 elements of X in shared memory: in it
+// both directions read 128 rows of 128 / B blocks, and both write whole scale
+// tiles and 64-byte runs of codes, so X is read once even when its transpose
+// is wanted too.
+//
+// A tile lies in panels of 128-byte rows (64 BF16 or 32 FP32 columns) in the
+// 128-byte swizzle, as TMA writes them: the 16-byte reads of eight rows along
+// the rows, and a row's 128 bytes read across the columns, fall in different
+// banks.
 constexpr int QT = 128;
-constexpr int Q_THREADS = 256;
+constexpr int Q_THREADS = 512;
+constexpr int Q_STAGES = 3;       // tiles in flight
 constexpr int Q_CODES = 80;       // bytes between staged rows of transposed codes (64 used)
+constexpr int Q_OUT = QT * Q_CODES + 2 * 1024;        // transposed codes, scales of both directions
 
-template <typename T> __host__ __device__ constexpr int q_pitch() { return QT * (int)sizeof(T) + 16; }   // bytes
-template <typename T> __host__ __device__ constexpr int q_smem() { return QT * q_pitch<T>() + QT * Q_CODES + 2 * 1024; }
+template <typename T> __host__ __device__ constexpr int q_tile() { return QT * QT * (int)sizeof(T); }
+template <typename T> __host__ __device__ constexpr int q_panel() { return 128 / (int)sizeof(T); }   // columns
+
+struct QSync {
+    uint64_t full[Q_STAGES];
+    int abort;
+};
+template <typename T> __host__ __device__ constexpr int q_smem() { return 1024 + Q_STAGES * q_tile<T>() + Q_OUT + 64; }
+
+// Byte of a tile's element (r, c).
+template <typename T>
+__device__ __forceinline__ int tile_at(int r, int c) {
+    const int panel = c / q_panel<T>(), byte = c % q_panel<T>() * (int)sizeof(T);
+    return panel * QT * 128 + r * 128 + ((byte >> 4 ^ (r & 7)) << 4) + (byte & 15);
+}
 
 // The larger magnitude of each half (BF16) or of the word (FP32), its sign
 // arbitrary; NaN if either is.
@@ -288,116 +308,166 @@ __device__ __forceinline__ void write_scales(uint8_t* dst, const uint8_t* staged
     if (t < BYTES / 16) reinterpret_cast<uint4*>(dst)[t] = reinterpret_cast<const uint4*>(staged)[t];
 }
 
+// One tile (at row r0, column c0 of X) from shared memory.
 template <typename T, int FMT, bool ROWS, bool TRANS>
-__global__ void __launch_bounds__(Q_THREADS, sizeof(T) == 2 ? 4 : 2)
-quantize_kernel(int R, int C, const T* X, long ldx, bool vec, const float* gp, uint8_t* codes,
-                uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t) {
+__device__ __forceinline__ void quantize_tile(int R, int C, long r0, long c0, const uint8_t* tile, uint8_t* staged,
+                                              const Scaling& k, uint8_t* codes) {
     constexpr int B = mx4_block(FMT), NB = QT / B, WORDS = B * (int)sizeof(T) / 4;
-    constexpr int PITCH = q_pitch<T>(), SCALE_BYTES = NB / 4 * MX4_TILE_BYTES;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t* staged = smem + QT * PITCH;                    // transposed codes
     uint8_t* sc = staged + QT * Q_CODES;                    // scales, then those of the transpose
     const int t = threadIdx.x, lane = t & 31;
-    const long c0 = (long)blockIdx.x * QT;
+    if (ROWS) {
+        const long pitch = mx4_pitch(C);
+#pragma unroll 1
+        for (int i = t >> 5; i < QT * NB / 32; i += Q_THREADS / 32) {
+            const int row = i / (NB / 4) * 8 + (lane & 7), b = i % (NB / 4) * 4 + (lane >> 3);
+            uint32_t w[WORDS], out[B / 8];
+#pragma unroll
+            for (int j = 0; j < WORDS / 4; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + tile_at<T>(row, b * B + j * (16 / (int)sizeof(T))));
+                w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+            }
+            sc[tile_scale_at(row, b)] = (uint8_t)quantize_row<T, FMT>(w, k, out);
+            const long at = c0 / 2 + b * (B / 2);
+            if (r0 + row < R && at < pitch) {
+                uint8_t* dst = codes + (r0 + row) * pitch + at;
+                if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+                else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+            }
+        }
+    }
+    if (TRANS) {
+        // Two columns a thread; lanes on neighbouring columns.
+#pragma unroll 1
+        for (int i = t; i < QT / 2 * NB; i += Q_THREADS) {
+            const int c = i % (QT / 2) * 2, b = i / (QT / 2);
+            constexpr int W = (int)sizeof(T) / 2;            // words of a row of two columns
+            uint32_t w[B * W], out[2][B / 8];
+            const uint8_t* src = tile + c / q_panel<T>() * QT * 128 + b * B * 128;
+            const int byte = c % q_panel<T>() * (int)sizeof(T), piece = byte >> 4 << 4, in = byte & 15;
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const uint8_t* at = src + j * 128 + ((piece ^ (j & 7) << 4) | in);      // rows from a multiple of 8 on
+                if constexpr (W == 1) {
+                    w[j] = *reinterpret_cast<const uint32_t*>(at);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(at);
+                    w[2 * j] = u.x;
+                    w[2 * j + 1] = u.y;
+                }
+            }
+            const uint32_t bytes = quantize_columns<T, FMT>(w, k, out);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sc[1024 + tile_scale_at(c + h, b)] = (uint8_t)(bytes >> 16 * h);
+                uint8_t* dst = staged + (c + h) * Q_CODES + b * (B / 2);
+                if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+                else *reinterpret_cast<uint2*>(dst) = make_uint2(out[h][0], out[h][1]);
+            }
+        }
+    }
+}
+
+// What quantize_tile left in shared memory.
+template <int FMT, bool ROWS, bool TRANS>
+__device__ __forceinline__ void write_tile(int R, int C, long r0, long c0, const uint8_t* staged, uint8_t* scales,
+                                           uint8_t* codes_t, uint8_t* scales_t) {
+    constexpr int SCALE_BYTES = QT / mx4_block(FMT) / 4 * MX4_TILE_BYTES;
+    const uint8_t* sc = staged + QT * Q_CODES;
+    const int t = threadIdx.x;
+    if (ROWS && r0 < R)
+        write_scales<FMT>(scales + ((r0 / QT) * mx4_tiles_k(C, FMT)) * MX4_TILE_BYTES + (c0 / QT) * SCALE_BYTES, sc, t);
+    if (TRANS && c0 < C) {
+        write_scales<FMT>(scales_t + ((c0 / QT) * mx4_tiles_k(R, FMT)) * MX4_TILE_BYTES + (r0 / QT) * SCALE_BYTES,
+                          sc + 1024, t);
+        const long pitch = mx4_pitch(R);
+#pragma unroll
+        for (int i = t; i < QT * 4; i += Q_THREADS) {
+            const int c = i >> 2;
+            const long at = r0 / 2 + (i & 3) * 16;
+            if (c0 + c < C && at < pitch)
+                *reinterpret_cast<uint4*>(codes_t + (c0 + c) * pitch + at) =
+                    *reinterpret_cast<const uint4*>(staged + c * Q_CODES + (i & 3) * 16);
+        }
+    }
+}
+
+// Persistent blocks over the tiles (the scales cover spans of 256, so rows and
+// columns go on to an even tile), TMA three tiles ahead with zeros outside X.
+// Bound by HBM (X in, codes and scales out) in one direction, by instruction
+// issue in both.
+template <typename T, int FMT, bool ROWS, bool TRANS>
+__global__ void __launch_bounds__(Q_THREADS, sizeof(T) == 2 ? 2 : 1)
+quantize_kernel(const __grid_constant__ CUtensorMap tmX, int R, int C, const float* gp, uint8_t* codes, uint8_t* scales,
+                uint8_t* codes_t, uint8_t* scales_t, unsigned long long wait_limit_ns, int* status) {
+    using namespace mx4_ptx;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* staged = smem + Q_STAGES * q_tile<T>();
+    QSync* sy = reinterpret_cast<QSync*>(staged + Q_OUT);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Q_STAGES; ++s) mbar_init(smem_u32(&sy->full[s]), 1);
+        sy->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        prefetch_map(&tmX);
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tiles_c = (int)(((long)C + 255) / 256 * 2);
+    const long tiles = ((long)R + 255) / 256 * 2 * tiles_c;
+    auto fetch = [&](long i, int s) {
+        if (i >= tiles) return;
+        const uint32_t bar = smem_u32(&sy->full[s]), dst = smem_u32(smem) + s * q_tile<T>();
+        mbar_arrive_expect_tx(bar, q_tile<T>());
+        for (int j = 0; j < QT / q_panel<T>(); ++j)
+            tma_load_2d<false>(dst + j * QT * 128, &tmX, (int)(i % tiles_c) * QT + j * q_panel<T>(), (int)(i / tiles_c) * QT, bar);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < Q_STAGES; ++s) fetch(blockIdx.x + (long)s * gridDim.x, s);
+    const Scaling k(gp);
+    const Wait wait{&sy->abort, status, wait_limit_ns};
+    int s = 0;
+    uint32_t ph = 0;
+    for (long i = blockIdx.x; i < tiles; i += gridDim.x) {
+        const long r0 = i / tiles_c * QT, c0 = i % tiles_c * QT;
+        // A copy that has not landed within the limit ends the block (its other
+        // copies are older than that wait).
+        if (__syncthreads_or(!mbar_wait<false>(smem_u32(&sy->full[s]), ph, wait))) return;
+        quantize_tile<T, FMT, ROWS, TRANS>(R, C, r0, c0, smem + s * q_tile<T>(), staged, k, codes);
+        __syncthreads();
+        if (threadIdx.x == 0) fetch(i + (long)Q_STAGES * gridDim.x, s);
+        write_tile<FMT, ROWS, TRANS>(R, C, r0, c0, staged, scales, codes_t, scales_t);
+        if (++s == Q_STAGES) { s = 0; ph ^= 1u; }
+    }
+}
+
+// The same for rows that do not start on 16-byte boundaries, which TMA cannot
+// copy: one tile to a block, element by element.
+template <typename T, int FMT, bool ROWS, bool TRANS>
+__global__ void __launch_bounds__(Q_THREADS)
+quantize_any_kernel(int R, int C, const T* X, long ldx, const float* gp, uint8_t* codes, uint8_t* scales,
+                    uint8_t* codes_t, uint8_t* scales_t) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (mx4_ptx::smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* staged = smem + q_tile<T>();
     pdl_launch_dependents();
     pdl_wait();
     const Scaling k(gp);
-    // The scales cover spans of 256, so the grid goes on to an even tile.
-    const long end = ((long)R + 2 * QT - 1) / (2 * QT) * (2 * QT);
-    for (long r0 = (long)blockIdx.y * QT; r0 < end; r0 += (long)gridDim.y * QT) {
-        // Load, zeros outside.
-        if (vec) {
-            constexpr int V = 16 / (int)sizeof(T), PER_ROW = QT / V;
-#pragma unroll 4
-            for (int i = t; i < QT * PER_ROW; i += Q_THREADS) {
-                const int r = i / PER_ROW, c = i % PER_ROW * V;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r0 + r < R && c0 + c < C) {
-                    const T* src = X + (r0 + r) * ldx + c0 + c;
-                    if (c0 + c + V <= C) v = __ldg(reinterpret_cast<const uint4*>(src));
-                    else {
-                        alignas(16) T part[V];
-#pragma unroll
-                        for (int k = 0; k < V; ++k) part[k] = c0 + c + k < C ? src[k] : (T)0.0f;
-                        v = *reinterpret_cast<const uint4*>(part);
-                    }
-                }
-                *reinterpret_cast<uint4*>(smem + r * PITCH + c * (int)sizeof(T)) = v;
-            }
-        } else {
+    const int tiles_c = (int)(((long)C + 255) / 256 * 2);
+    const long tiles = ((long)R + 255) / 256 * 2 * tiles_c;
+    for (long i = blockIdx.x; i < tiles; i += gridDim.x) {
+        const long r0 = i / tiles_c * QT, c0 = i % tiles_c * QT;
 #pragma unroll 8
-            for (int i = t; i < QT * QT; i += Q_THREADS) {
-                const int r = i / QT, c = i % QT;
-                *reinterpret_cast<T*>(smem + r * PITCH + c * (int)sizeof(T)) =
-                    r0 + r < R && c0 + c < C ? X[(r0 + r) * ldx + c0 + c] : (T)0.0f;
-            }
+        for (int e = threadIdx.x; e < QT * QT; e += Q_THREADS) {
+            const int r = e / QT, c = e % QT;
+            *reinterpret_cast<T*>(smem + tile_at<T>(r, c)) =
+                r0 + r < R && c0 + c < C ? X[(r0 + r) * ldx + c0 + c] : (T)0.0f;
         }
         __syncthreads();
-        if (ROWS) {
-            const long pitch = mx4_pitch(C);
-            // 8 lanes take 8 rows: their 16-byte reads fall in different banks.
-#pragma unroll 1
-            for (int i = t >> 5; i < QT * NB / 32; i += Q_THREADS / 32) {
-                const int row = i / (NB / 4) * 8 + (lane & 7), b = i % (NB / 4) * 4 + (lane >> 3);
-                uint32_t w[WORDS], out[B / 8];
-#pragma unroll
-                for (int j = 0; j < WORDS / 4; ++j) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * PITCH + b * B * (int)sizeof(T) + j * 16);
-                    w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
-                }
-                sc[tile_scale_at(row, b)] = (uint8_t)quantize_row<T, FMT>(w, k, out);
-                const long at = c0 / 2 + b * (B / 2);
-                if (r0 + row < R && at < pitch) {
-                    uint8_t* dst = codes + (r0 + row) * pitch + at;
-                    if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-                    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-                }
-            }
-        }
-        if (TRANS) {
-            // Two columns a thread; lanes on neighbouring columns.
-#pragma unroll 1
-            for (int i = t; i < QT / 2 * NB; i += Q_THREADS) {
-                const int c = i % (QT / 2) * 2, b = i / (QT / 2);
-                constexpr int W = (int)sizeof(T) / 2;            // words of a row of two columns
-                uint32_t w[B * W], out[2][B / 8];
-                const uint8_t* src = smem + b * B * PITCH + c * (int)sizeof(T);
-#pragma unroll
-                for (int j = 0; j < B; ++j) {
-                    if constexpr (W == 1) {
-                        w[j] = *reinterpret_cast<const uint32_t*>(src + j * PITCH);
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(src + j * PITCH);
-                        w[2 * j] = u.x;
-                        w[2 * j + 1] = u.y;
-                    }
-                }
-                const uint32_t bytes = quantize_columns<T, FMT>(w, k, out);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sc[1024 + tile_scale_at(c + h, b)] = (uint8_t)(bytes >> 16 * h);
-                    uint8_t* dst = staged + (c + h) * Q_CODES + b * (B / 2);
-                    if constexpr (B == 32) *reinterpret_cast<uint4*>(dst) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
-                    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[h][0], out[h][1]);
-                }
-            }
-        }
+        quantize_tile<T, FMT, ROWS, TRANS>(R, C, r0, c0, smem, staged, k, codes);
         __syncthreads();
-        if (ROWS && r0 < R)
-            write_scales<FMT>(scales + ((r0 / QT) * mx4_tiles_k(C, FMT)) * MX4_TILE_BYTES + (c0 / QT) * SCALE_BYTES, sc, t);
-        if (TRANS && c0 < C) {
-            write_scales<FMT>(scales_t + ((c0 / QT) * mx4_tiles_k(R, FMT)) * MX4_TILE_BYTES + (r0 / QT) * SCALE_BYTES,
-                              sc + 1024, t);
-            const long pitch = mx4_pitch(R);
-#pragma unroll
-            for (int i = t; i < QT * 4; i += Q_THREADS) {
-                const int c = i >> 2;
-                const long at = r0 / 2 + (i & 3) * 16;
-                if (c0 + c < C && at < pitch)
-                    *reinterpret_cast<uint4*>(codes_t + (c0 + c) * pitch + at) =
-                        *reinterpret_cast<const uint4*>(staged + c * Q_CODES + (i & 3) * 16);
-            }
-        }
+        write_tile<FMT, ROWS, TRANS>(R, C, r0, c0, staged, scales, codes_t, scales_t);
         __syncthreads();
     }
 }
@@ -494,41 +564,42 @@ bool rows_on_16(const void* X, long ldx, int esz) {
     return reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * esz % 16 == 0;
 }
 
-// As much of the SM's memory as shared as there is: with the default split
-// fewer blocks than the registers allow were resident.
-template <auto KERNEL>
-cudaError_t most_shared_memory_once() {
-    static std::atomic<unsigned long long> done{0};    // bit d: set on device d
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (e != cudaSuccess || (done.load(std::memory_order_acquire) & bit) != 0) return e;
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 template <typename T, int FMT, bool ROWS, bool TRANS>
 cudaError_t launch_quantize(int R, int C, const void* X, long ldx, const float* g, uint8_t* codes,
-                            uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, cudaStream_t s) {
-    cudaError_t e = set_smem_limit_once<quantize_kernel<T, FMT, ROWS, TRANS>>(q_smem<T>());
-    if (e == cudaSuccess) e = most_shared_memory_once<quantize_kernel<T, FMT, ROWS, TRANS>>();
+                            uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, int num_sms, cudaStream_t s) {
+    const long tiles = ((long)R + 255) / 256 * 2 * (((long)C + 255) / 256 * 2);
+    const auto enc = reinterpret_cast<mx4_tile::EncodeTiledFn>(tensor_map_encoder());
+    if (!rows_on_16(X, ldx, sizeof(T)) || enc == nullptr) {
+        const int smem = 1024 + q_tile<T>() + Q_OUT;
+        const cudaError_t e = set_smem_limit_once<quantize_any_kernel<T, FMT, ROWS, TRANS>>(smem);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(quantize_any_kernel<T, FMT, ROWS, TRANS>, dim3((unsigned)(tiles < 1 << 30 ? tiles : 1 << 30)),
+                          dim3(Q_THREADS), smem, s, R, C, static_cast<const T*>(X), ldx, g, codes, scales, codes_t, scales_t);
+    }
+    CUtensorMap tmX;
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)R}, strides[1] = {(cuuint64_t)ldx * sizeof(T)};
+    const cuuint32_t box[2] = {(cuuint32_t)q_panel<T>(), QT};
+    if (!mx4_tile::encode(enc, &tmX, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          2, X, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    int* status = nullptr;
+    cudaError_t e = mx4_status_word(&status);
+    if (e == cudaSuccess) e = set_smem_limit_once<quantize_kernel<T, FMT, ROWS, TRANS>>(q_smem<T>());
     if (e != cudaSuccess) return e;
-    const long rows = ((long)R + 255) / 256 * 2;
-    const dim3 grid((unsigned)(((long)C + 255) / 256 * 2), (unsigned)(rows < 65535 ? rows : 65535));
-    return launch_pdl(quantize_kernel<T, FMT, ROWS, TRANS>, grid, dim3(Q_THREADS), q_smem<T>(), s, R, C,
-                      static_cast<const T*>(X), ldx, rows_on_16(X, ldx, sizeof(T)), g, codes, scales, codes_t,
-                      scales_t);
+    const long slots = (sizeof(T) == 2 ? 2L : 1L) * num_sms;
+    return launch_pdl(quantize_kernel<T, FMT, ROWS, TRANS>, dim3((unsigned)(tiles < slots ? tiles : slots)),
+                      dim3(Q_THREADS), q_smem<T>(), s, tmX, R, C, g, codes, scales, codes_t, scales_t, wait_limit_ns(),
+                      status);
 }
 
 template <typename T, int FMT>
 cudaError_t quantize_type(int R, int C, const void* X, long ldx, const float* g, uint8_t* codes,
-                          uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, cudaStream_t s) {
+                          uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, int num_sms, cudaStream_t s) {
     if (codes_t == nullptr)
-        return launch_quantize<T, FMT, true, false>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, s);
+        return launch_quantize<T, FMT, true, false>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s);
     if (codes == nullptr)
-        return launch_quantize<T, FMT, false, true>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, s);
-    return launch_quantize<T, FMT, true, true>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, s);
+        return launch_quantize<T, FMT, false, true>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s);
+    return launch_quantize<T, FMT, true, true>(R, C, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s);
 }
 
 }  // namespace
@@ -558,14 +629,14 @@ cudaError_t mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_
 
 cudaError_t mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, int fmt,
                          const float* g, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
-                         uint8_t* scales_t, cudaStream_t s) {
+                         uint8_t* scales_t, int num_sms, cudaStream_t s) {
     if (x_type == TGEMM_TYPE_F32)
         return fmt == TGEMM_MXFP4
-                   ? quantize_type<float, TGEMM_MXFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, s)
-                   : quantize_type<float, TGEMM_NVFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, s);
+                   ? quantize_type<float, TGEMM_MXFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s)
+                   : quantize_type<float, TGEMM_NVFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s);
     return fmt == TGEMM_MXFP4
-               ? quantize_type<__nv_bfloat16, TGEMM_MXFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, s)
-               : quantize_type<__nv_bfloat16, TGEMM_NVFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, s);
+               ? quantize_type<__nv_bfloat16, TGEMM_MXFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s)
+               : quantize_type<__nv_bfloat16, TGEMM_NVFP4>(rows, cols, X, ldx, g, codes, scales, codes_t, scales_t, num_sms, s);
 }
 
 template <typename T>
