@@ -122,12 +122,41 @@ __device__ __forceinline__ float power_for(float m) {
     return fminf(fmaxf(__uint_as_float(up), kMinG), kMaxG);
 }
 
-// 1 << shift threads to a row (rows that start on 16-byte boundaries in
-// 16-byte pieces, `vec`); bound by reading X.
+// The larger magnitude of each half (BF16) or of the word (FP32), its sign
+// arbitrary. With NAN_WINS it is NaN if either is, without if both are.
+template <typename T, bool NAN_WINS = true>
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (sizeof(T) == 2) {
+        if constexpr (NAN_WINS) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+        float f;
+        if constexpr (NAN_WINS)
+            asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        else
+            asm("max.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+        r = __float_as_uint(f);
+    }
+    return r;
+}
+__device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// The largest magnitude that max_abs left in a word, as the bits of an FP32.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude(uint32_t m) {
+    if constexpr (sizeof(T) == 2) return max(m << 16 & 0x7FFF0000u, m & 0x7FFF0000u);
+    else return m & 0x7FFFFFFFu;
+}
+
+// Eight loads a thread, all in flight before the first is used; bound by
+// reading X. Rows that start on 16-byte boundaries are read in 16-byte pieces
+// (`vec`). A block takes a run of 8 x 256 pieces of a row (shift 8), or eight
+// times 256 >> shift rows of up to 1 << shift pieces.
 template <typename T>
 __global__ void __launch_bounds__(256)
-tensor_scale_kernel(int rows, int cols, const T* X, long ldx, bool vec, int shift, float* g) {
-    constexpr int V = 16 / (int)sizeof(T);
+tensor_scale_kernel(long rows, long cols, const T* X, long ldx, bool vec, int shift, float* g) {
+    constexpr int V = 16 / (int)sizeof(T), LOADS = 8;
     pdl_launch_dependents();
     pdl_wait();
     uint32_t m = 0;
@@ -135,27 +164,50 @@ tensor_scale_kernel(int rows, int cols, const T* X, long ldx, bool vec, int shif
         b &= 0x7FFFFFFFu;
         if (b < 0x7F800000u) m = max(m, b);
     };
-    const int width = vec ? V : 1, step = width << shift;
-    const int first = (threadIdx.x & ((1 << shift) - 1)) * width;
-    const int per_block = 256 >> shift;
-    for (long r = (long)blockIdx.x * per_block + (threadIdx.x >> shift); r < rows; r += (long)gridDim.x * per_block) {
-        const T* row = X + r * ldx;
-#pragma unroll 8
-        for (long c = first; c < cols; c += step) {
-            if (vec && c + V <= cols) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + c));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const long width = vec ? V : 1, pieces = (cols + width - 1) / width;
+    const long parts = shift == 8 ? (pieces + 256 * LOADS - 1) / (256 * LOADS) : 1;      // runs of a row
+    const long dr = shift == 8 ? 0 : 256 >> shift, dc = shift == 8 ? 256 : 0;
+    const long runs = shift == 8 ? rows * parts : (rows + dr * LOADS - 1) / (dr * LOADS);
+    for (long run = blockIdx.x; run < runs; run += gridDim.x) {
+        const long r0 = shift == 8 ? run / parts : run * dr * LOADS + (threadIdx.x >> shift);
+        const long p0 = shift == 8 ? run % parts * 256 * LOADS + threadIdx.x : threadIdx.x & ((1 << shift) - 1);
+        if (vec) {
+            uint4 v[LOADS];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (sizeof(T) == 4) take(w[k]);
-                    else {
-                        take(w[k] << 16);
-                        take(w[k] & 0xFFFF0000u);
+            for (int j = 0; j < LOADS; ++j) {
+                const long r = r0 + j * dr, c = (p0 + j * dc) * V;
+                v[j] = r < rows && c + V <= cols ? __ldg(reinterpret_cast<const uint4*>(X + r * ldx + c)) : make_uint4(0, 0, 0, 0);
+            }
+            uint32_t all = 0;
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j)
+                all = max_abs<T, false>(max_abs<T, false>(max_abs<T, false>(all, v[j].x), max_abs<T, false>(v[j].y, v[j].z)), v[j].w);
+            if (magnitude<T>(all) < 0x7F800000u) m = max(m, magnitude<T>(all));
+            else                                         // infinities or NaN among them: one by one
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) {
+                    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (sizeof(T) == 4) take(w[k]);
+                        else {
+                            take(w[k] << 16);
+                            take(w[k] & 0xFFFF0000u);
+                        }
                     }
                 }
-            } else {
-                for (int k = 0; k < width; ++k)
-                    if (c + k < cols) take(__float_as_uint((float)row[c + k]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) {
+                const long r = r0 + j * dr, c = p0 + j * dc;
+                if (r < rows && c < cols) take(__float_as_uint((float)X[r * ldx + c]));
+            }
+        }
+        if (vec && cols % V != 0) {                      // the piece that the row's end cuts
+            for (int j = 0; j < LOADS; ++j) {
+                const long r = r0 + j * dr, c = (p0 + j * dc) * V;
+                if (r < rows && c < cols && c + V > cols)
+                    for (long k = c; k < cols; ++k) take(__float_as_uint((float)X[r * ldx + k]));
             }
         }
     }
@@ -206,23 +258,6 @@ __device__ __forceinline__ int tile_at(int r, int c) {
     return panel * QT * 128 + r * 128 + ((byte >> 4 ^ (r & 7)) << 4) + (byte & 15);
 }
 
-// The larger magnitude of each half (BF16) or of the word (FP32), its sign
-// arbitrary; NaN if either is.
-template <typename T>
-__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (sizeof(T) == 2) {
-        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    } else {
-        float f;
-        asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
-        r = __float_as_uint(f);
-    }
-    return r;
-}
-__device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
 // A block along a row: its values in words of T, in order, to codes and the
 // scale byte.
 template <typename T, int FMT>
@@ -231,13 +266,8 @@ __device__ __forceinline__ uint32_t quantize_row(const uint32_t* w, const Scalin
     uint32_t m = w[0];
 #pragma unroll
     for (int i = 1; i < WORDS; ++i) m = max_abs<T>(m, w[i]);
-    float most = fabsf(__uint_as_float(m));
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t lo = m << 16 & 0x7FFF0000u, hi = m & 0x7FFF0000u;      // magnitudes order as their bits
-        most = __uint_as_float(max(lo, hi));
-    }
     float inv, neg_d;
-    const uint32_t byte = block_scale<FMT>(most, k, inv, neg_d);
+    const uint32_t byte = block_scale<FMT>(__uint_as_float(magnitude<T>(m)), k, inv, neg_d);
     const uint64_t inv2 = pack2(inv, inv), neg_d2 = pack2(neg_d, neg_d);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
@@ -477,7 +507,7 @@ quantize_any_kernel(int R, int C, const T* X, long ldx, const float* gp, uint8_t
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, const float* gp, T* X,
-                  long ldx, bool vec) {
+                  long ldx) {
     constexpr int B = mx4_block(FMT);
     pdl_launch_dependents();
     pdl_wait();
@@ -517,7 +547,7 @@ dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, con
                 v[2 * j + 1] = FMT == TGEMM_MXFP4 ? f.y * s : f.y * g;
             }
             T* dst = X + (r + i) * ldx + c;
-            if (vec && c + 8 <= C) {
+            if (c + 8 <= C) {
                 if constexpr (sizeof(T) == 4) {
                     reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
                     reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -533,6 +563,34 @@ dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, con
                     if (c + j < C) dst[j] = (T)v[j];
             }
         }
+    }
+}
+
+// The same for rows of X that do not start on 16-byte boundaries: a column of
+// eight rows a thread, so that a warp's stores lie side by side.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256)
+dequantize_any_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, const float* gp, T* X, long ldx) {
+    constexpr int B = mx4_block(FMT), ROWS = 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    const long c = (long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (c >= C) return;
+    const float g = mx4_g(gp);
+    const long pitch = mx4_pitch(C), row_of_tiles = mx4_tiles_k(C, FMT) * MX4_TILE_BYTES;
+    const uint8_t* code = codes + c / 2;
+    const uint8_t* scale = scales + mx4_scale_at(0, c / B, 0);
+    for (long r = (long)blockIdx.y * ROWS; r < R; r += (long)gridDim.y * ROWS) {
+        uint32_t w[ROWS], b[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (r + i < R) {
+                w[i] = __ldg(code + (r + i) * pitch) >> (c & 1) * 4;
+                b[i] = __ldg(scale + (r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4);
+            }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (r + i < R) X[(r + i) * ldx + c] = (T)(e2m1_value(w[i] & 15) * mx4_scale_value<FMT>(b[i]) * g);
     }
 }
 
@@ -607,23 +665,27 @@ cudaError_t quantize_type(int R, int C, const void* X, long ldx, const float* g,
 cudaError_t mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_type, float* g,
                              int num_sms, cudaStream_t s) {
     const int esz = x_type == TGEMM_TYPE_F32 ? 4 : 2;
-    const bool vec = rows_on_16(X, ldx, esz);
-    const long pieces = vec ? ((long)cols * esz + 15) / 16 : cols;
-    int shift = 5;
+    long r = rows, c = cols;
+    if (ldx == cols) {                                   // one long row
+        r = 1;
+        c = (long)rows * cols;
+    }
+    const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && (r == 1 || ldx * esz % 16 == 0);
+    const long pieces = vec ? (c * esz + 15) / 16 : c;
+    int shift = 0;
     while (shift < 8 && (1L << shift) < pieces) ++shift;
-    const long blocks = ((long)rows + (256 >> shift) - 1) / (256 >> shift);
-    // One block, which needs no initial value, takes up to 32 loads a thread:
-    // less than a second launch costs.
-    const bool one = ((long)rows + (256 >> shift) - 1) / (256 >> shift) * ((pieces + (1L << shift) - 1) >> shift) <= 32;
-    const dim3 grid((unsigned)(one ? 1 : blocks < 8L * num_sms ? blocks : 8L * num_sms));
-    if (!one) {
+    const long runs = shift == 8 ? r * ((pieces + 2047) / 2048) : (r + (2048 >> shift) - 1) / (2048 >> shift);
+    // One block, which needs no initial value, takes up to four runs: less
+    // than a second launch costs.
+    const dim3 grid((unsigned)(runs <= 4 ? 1 : runs < 8L * num_sms ? runs : 8L * num_sms));
+    if (runs > 4) {
         const cudaError_t e = launch_pdl(scale_init_kernel, dim3(1), dim3(32), 0, s, g);
         if (e != cudaSuccess) return e;
     }
     return x_type == TGEMM_TYPE_F32
-               ? launch_pdl(tensor_scale_kernel<float>, grid, dim3(256), 0, s, rows, cols,
-                            static_cast<const float*>(X), ldx, vec, shift, g)
-               : launch_pdl(tensor_scale_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, rows, cols,
+               ? launch_pdl(tensor_scale_kernel<float>, grid, dim3(256), 0, s, r, c, static_cast<const float*>(X), ldx,
+                            vec, shift, g)
+               : launch_pdl(tensor_scale_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, r, c,
                             static_cast<const __nv_bfloat16*>(X), ldx, vec, shift, g);
 }
 
@@ -643,11 +705,15 @@ template <typename T>
 static cudaError_t dequantize_type(int rows, int cols, const uint8_t* codes, const uint8_t* scales,
                                    int fmt, const float* g, void* X, long ldx, cudaStream_t s) {
     const dim3 grid((unsigned)(((long)cols + 2047) / 2048), grid_rows(((long)rows + 7) / 8));
-    const bool vec = rows_on_16(X, ldx, sizeof(T));
+    const dim3 any((unsigned)(((long)cols + 255) / 256), grid.y);
     auto x = static_cast<T*>(X);
+    if (!rows_on_16(X, ldx, sizeof(T)))
+        return fmt == TGEMM_MXFP4
+                   ? launch_pdl(dequantize_any_kernel<T, TGEMM_MXFP4>, any, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx)
+                   : launch_pdl(dequantize_any_kernel<T, TGEMM_NVFP4>, any, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx);
     return fmt == TGEMM_MXFP4
-               ? launch_pdl(dequantize_kernel<T, TGEMM_MXFP4>, grid, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx, vec)
-               : launch_pdl(dequantize_kernel<T, TGEMM_NVFP4>, grid, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx, vec);
+               ? launch_pdl(dequantize_kernel<T, TGEMM_MXFP4>, grid, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx)
+               : launch_pdl(dequantize_kernel<T, TGEMM_NVFP4>, grid, dim3(256), 0, s, rows, cols, codes, scales, g, x, ldx);
 }
 
 cudaError_t mx4_dequantize(int rows, int cols, const uint8_t* codes, const uint8_t* scales,
