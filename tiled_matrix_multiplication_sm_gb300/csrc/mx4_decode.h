@@ -30,8 +30,7 @@ __device__ __forceinline__ bool wide(uint32_t byte) { return byte > 128; }
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
-    // volatile: not moved below the wait for the slot that the values go to
-    asm volatile("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 

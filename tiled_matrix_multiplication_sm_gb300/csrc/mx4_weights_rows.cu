@@ -33,14 +33,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight consecutive values of a row of X from column k on, 0 past K.
-__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* row, long k, int K, bool vec) {
-    if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+// Eight consecutive values of X of which the row has `left` more; 0 past them.
+__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* x, int left) {
     uint32_t w[4];
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + k;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < K ? p[2 * i] : 0, hi = k + 2 * i + 1 < K ? p[2 * i + 1] : 0;
+        const uint32_t lo = 2 * i < left ? p[2 * i] : 0, hi = 2 * i + 1 < left ? p[2 * i + 1] : 0;
         w[i] = lo | hi << 16;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -53,8 +52,11 @@ struct Unit {
     uint32_t scales[2 * RW];        // one byte (MXFP4) or two (NVFP4)
 };
 
+// Blocks meant to be resident on an SM: with 64 and 128 registers a thread.
+__host__ __device__ constexpr int blocks_per_sm(int nt) { return nt == 1 ? 4 : 2; }
+
 template <int FMT, int NT, int RW, typename TC>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(THREADS, blocks_per_sm(NT))
 weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool vec, Mx4Operand W,
                     Mx4Out out, int split) {
     constexpr int TN = 16 * RW, TM = 8 * NT;
@@ -69,97 +71,120 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
     pdl_wait();
     __syncthreads();
 
-    const long pitch = mx4_pitch(K), tiles_k = mx4_tiles_k(K, FMT);
     const int units = (K + UNIT_K - 1) / UNIT_K;
-    const uint8_t* code_row[2 * RW];
-    const uint8_t* scale_row[2 * RW];
+    // Addresses are a base of the block's and 32-bit offsets. Rows past N and
+    // past M repeat the last one: their sums are not stored.
+    const uint32_t pitch = (uint32_t)mx4_pitch(K);
+    const uint8_t* code_base = W.codes + n0 * pitch;
+    const uint8_t* scale_base = W.scales + mx4_scale_at(n0, 0, mx4_tiles_k(K, FMT));
+    uint32_t code_at[2 * RW], scale_at[2 * RW];
 #pragma unroll
     for (int i = 0; i < 2 * RW; ++i) {
-        const long r = min(n0 + i * 8 + g, (long)N - 1);     // rows past N: read, not stored
-        code_row[i] = W.codes + r * pitch + t * 16;
-        scale_row[i] = W.scales + mx4_scale_at(r, 0, tiles_k) +
-                       (FMT == TGEMM_MXFP4 ? t : (t >> 1) * MX4_TILE_BYTES + (t & 1) * 2);
+        const uint32_t r = (uint32_t)min((long)(i * 8 + g), N - 1 - n0);
+        code_at[i] = r * pitch;
+        const uint32_t in = (uint32_t)(n0 % 32) + r;               // the block's rows lie in one tile
+        scale_at[i] = (in / 32 * 4 + in % 32 * 16) - (uint32_t)(n0 % 32 * 16) +
+                      (FMT == TGEMM_MXFP4 ? t : (t >> 1) * MX4_TILE_BYTES + (t & 1) * 2);
     }
     const __nv_bfloat16* x_row[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x_row[i] = i * 8 + g < M ? X + (long)(i * 8 + g) * ldx : nullptr;
+    for (int i = 0; i < NT; ++i) x_row[i] = X + (long)min(i * 8 + g, M - 1) * ldx + t * 32;
 
     using U = Unit<RW>;
     auto load = [&](U& u, int unit) {
-        const bool in = (long)unit * 64 + t * 16 < pitch;
+        // Past the row's end any codes do: X is 0 there.
+        const uint32_t at = min((uint32_t)unit * 64 + t * 16, pitch - 16);
 #pragma unroll
         for (int i = 0; i < 2 * RW; ++i) {
-            u.codes[i] = in ? __ldg(reinterpret_cast<const uint4*>(code_row[i] + (long)unit * 64)) : make_uint4(0, 0, 0, 0);
-            if (FMT == TGEMM_MXFP4) u.scales[i] = __ldg(scale_row[i] + (long)unit * MX4_TILE_BYTES);
-            else u.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scale_row[i] + (long)unit * 2 * MX4_TILE_BYTES));
+            u.codes[i] = __ldg(reinterpret_cast<const uint4*>(code_base + (code_at[i] + at)));
+            if (FMT == TGEMM_MXFP4) u.scales[i] = __ldg(scale_base + (scale_at[i] + (uint32_t)unit * MX4_TILE_BYTES));
+            else u.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scale_base + (scale_at[i] + (uint32_t)unit * (2 * MX4_TILE_BYTES))));
         }
     };
 
     float acc[RW][NT][4] = {};
-    auto multiply = [&](const U& u, const uint4 (&xs)[NT][4], auto is_wide) {
-        constexpr bool WIDE = decltype(is_wide)::value;
+    // Columns j * 8 .. j * 8 + 7 of a lane's 32: X's fragments, and the product.
+    auto step8 = [&](const U& u, int j, const uint4 (&xs)[NT], const uint32_t (&f)[2 * RW][2], auto is_wide) {
+        uint32_t b[NT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t b[NT][4];
+        for (int i = 0; i < NT; ++i) {
+            b[i][0] = __byte_perm(xs[i].x, xs[i].z, 0x5410);       // columns 0 and 4
+            b[i][1] = __byte_perm(xs[i].x, xs[i].z, 0x7632);       // 1 and 5
+            b[i][2] = __byte_perm(xs[i].y, xs[i].w, 0x5410);       // 2 and 6
+            b[i][3] = __byte_perm(xs[i].y, xs[i].w, 0x7632);       // 3 and 7
+        }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const uint4 x = xs[i][j];
-                b[i][0] = __byte_perm(x.x, x.z, 0x5410);       // columns 0 and 4
-                b[i][1] = __byte_perm(x.x, x.z, 0x7632);       // 1 and 5
-                b[i][2] = __byte_perm(x.y, x.w, 0x5410);       // 2 and 6
-                b[i][3] = __byte_perm(x.y, x.w, 0x7632);       // 3 and 7
+        for (int r = 0; r < RW; ++r) {
+            uint32_t v[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 c = u.codes[2 * r + h];
+                values<decltype(is_wide)::value>(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w,
+                                                 f[2 * r + h][j / 2], v[h]);
             }
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                uint32_t v[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 c = u.codes[2 * r + h];
-                    const uint32_t s = u.scales[2 * r + h];
-                    const uint32_t byte = FMT == TGEMM_MXFP4 ? s : j < 2 ? s & 0xFF : s >> 8;
-                    uint32_t f = factors[byte];
-                    // Beside a wide block the others take their scale alone too.
-                    if (WIDE && byte != 255) f = byte == 0 ? 0x00400040u : byte << 7 | byte << 23;
-                    values<WIDE>(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w, f, v[h]);
-                }
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    mma_bf16(acc[r][i], v[0][0], v[1][0], v[0][1], v[1][1], b[i][0], b[i][1]);
-                    mma_bf16(acc[r][i], v[0][2], v[1][2], v[0][3], v[1][3], b[i][2], b[i][3]);
-                }
+            for (int i = 0; i < NT; ++i) {
+                mma_bf16(acc[r][i], v[0][0], v[1][0], v[0][1], v[1][1], b[i][0], b[i][1]);
+                mma_bf16(acc[r][i], v[0][2], v[1][2], v[0][3], v[1][3], b[i][2], b[i][3]);
             }
         }
     };
     // X comes from the caches: loaded when its unit is due, not ahead.
     auto run = [&](const U& u, int unit) {
-        uint4 xs[NT][4];
+        uint32_t f[2 * RW][2];                     // the factors of a row's first and last 16 codes
+        bool w = false;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < 2 * RW; ++i) {
+            if (FMT == TGEMM_NVFP4) {
+                f[i][0] = factors[u.scales[i] & 0xFF];
+                f[i][1] = factors[u.scales[i] >> 8];
+            } else {
+                f[i][0] = f[i][1] = (u.scales[i] + 126) * 0x00800080u;
+                w |= wide(u.scales[i]);
+            }
+        }
+        const int k0 = unit * UNIT_K;
+        if (vec && K - k0 >= UNIT_K && !(FMT == TGEMM_MXFP4 && __any_sync(~0u, w))) {
+            uint4 xs[4][NT];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                xs[i][j] = x_row[i] != nullptr ? load_x(x_row[i], (long)unit * UNIT_K + t * 32 + j * 8, K, vec)
-                                               : make_uint4(0, 0, 0, 0);
-        bool w = false;
-        if (FMT == TGEMM_MXFP4)
 #pragma unroll
-            for (int i = 0; i < 2 * RW; ++i) w |= wide(u.scales[i]);
-        if (FMT == TGEMM_MXFP4 && __any_sync(~0u, w)) multiply(u, xs, std::true_type());
-        else multiply(u, xs, std::false_type());
+                for (int i = 0; i < NT; ++i) xs[j][i] = __ldg(reinterpret_cast<const uint4*>(x_row[i] + k0) + j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) step8(u, j, xs[j], f, std::false_type());
+            return;
+        }
+        // The last columns, rows off 16 bytes, wide scales.
+        if (FMT == TGEMM_MXFP4) {
+            w = __any_sync(~0u, w);
+#pragma unroll
+            for (int i = 0; i < 2 * RW; ++i) {
+                // Beside a wide block the others take their scale alone too.
+                const uint32_t c = u.scales[i];
+                f[i][0] = f[i][1] = !w ? f[i][0] : c == 255 ? 0x7FC07FC0u : c == 0 ? 0x00400040u : c * 0x00800080u;
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            uint4 xs[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) xs[i] = load_x(x_row[i] + k0 + j * 8, K - k0 - t * 32 - j * 8);
+            if (FMT == TGEMM_MXFP4 && w) step8(u, j, xs, f, std::true_type());
+            else step8(u, j, xs, f, std::false_type());
+        }
     };
 
-    // Two units in flight.
+    // The next unit's codes are on their way while one is multiplied.
     const int step = WARPS * split;
     int unit = rank * WARPS + warp;
-    U u0, u1;
-    if (unit < units) load(u0, unit);
+    U now, next;
+    if (unit < units) load(now, unit);
+#pragma unroll 1
     while (unit < units) {
-        if (unit + step < units) load(u1, unit + step);
-        run(u0, unit);
+        if (unit + step < units) load(next, unit + step);
+        run(now, unit);
         unit += step;
-        if (unit >= units) break;
-        if (unit + step < units) load(u0, unit + step);
-        run(u1, unit);
-        unit += step;
+        now = next;
     }
 
 #pragma unroll
@@ -205,11 +230,20 @@ template <int FMT, int NT, int RW, typename TC>
 cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
                    int num_sms, cudaStream_t s) {
     const long tiles = ((long)N + 16 * RW - 1) / (16 * RW);
-    // Blocks of a cluster split K while there are too few blocks to fill the
-    // SMs and each keeps two units a warp.
+    // The blocks of a cluster split K. Time goes by the rounds of resident
+    // blocks and what a warp does in each: its units and about three units'
+    // worth of start and end.
     const int units = (K + UNIT_K - 1) / UNIT_K;
+    const long slots = (long)blocks_per_sm(NT) * num_sms;
     int split = 1;
-    while (split < 8 && tiles * split < 2L * num_sms && units >= 2 * WARPS * (split + 1)) ++split;
+    long best = 0;
+    for (int c = 1; c <= 8; ++c) {
+        const long cost = (tiles * c + slots - 1) / slots * ((units + WARPS * c - 1) / (WARPS * c) + 3);
+        if (c == 1 || cost < best) {
+            best = cost;
+            split = c;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split));
     cfg.blockDim = dim3(THREADS);
@@ -230,7 +264,7 @@ cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const 
 template <int FMT, typename TC>
 cudaError_t launch_rows(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W,
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
-    return M <= 8 ? launch<FMT, 1, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s)
+    return M <= 8 ? launch<FMT, 1, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s)
                   : launch<FMT, 2, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
 }
 
