@@ -46,6 +46,13 @@ def test_scales_bytes(lib, rows, cols, fmt, size):
     assert lib.gemm_mx4_scales_bytes(rows, cols, fmt) == size
 
 
+@pytest.mark.parametrize("rows,cols", [(0, 0), (1, 1), (127, 31), (128, 32), (129, 33), (3000, 1537), (5, 4096), (1 << 17, 257)])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_the_binding_allocates_what_the_library_asks_for(lib, fmt, rows, cols):
+    assert mx4._sizes(rows, cols, fmt) == (rows * lib.gemm_mx4_codes_pitch(cols),
+                                           lib.gemm_mx4_scales_bytes(rows, cols, mx4._FORMATS[fmt]))
+
+
 @pytest.mark.parametrize("args,status", [
     ((-1, 4, FAKE, 4, F32, FAKE, 0), INVALID), ((4, -1, FAKE, 4, F32, FAKE, 0), INVALID),
     ((4, 4, FAKE, 3, F32, FAKE, 0), INVALID), ((4, 4, 0, 4, F32, FAKE, 0), INVALID),

@@ -301,9 +301,15 @@ cudaError_t launch_type(int M, int N, int K, const Mx4Operand& A, const Mx4Opera
 }  // namespace
 
 cudaError_t mx4_status_word(int** word) {
+    static std::atomic<int*> known[64];                   // looked up once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*word = known[dev].load(std::memory_order_acquire)) != nullptr) return cudaSuccess;
     void* p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_mx4_status);
+    e = cudaGetSymbolAddress(&p, g_mx4_status);
     *word = static_cast<int*>(p);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*word, std::memory_order_release);
     return e;
 }
 

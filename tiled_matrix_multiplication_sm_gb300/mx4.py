@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import binding
-from .binding import TGEMM_OK, TgemmError, _check_matrix, _on_device, _stream_handle
+from .binding import TGEMM_OK, TgemmError, _check_matrix, _stream_handle
 
 TGEMM_MXFP4 = 1
 TGEMM_NVFP4 = 2
@@ -57,6 +57,20 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+def _call(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Run entry point ``name`` with ``args`` and the stream on ``device``;
+    switches devices only when another one is current."""
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        status = fn(*args, _stream_handle(stream, index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream_handle(stream, index))
+    if status != TGEMM_OK:
+        raise TgemmError(status, name)
+
+
 def _format(fmt: str) -> int:
     if fmt not in _FORMATS:
         raise ValueError(f"unknown 4-bit format {fmt!r}; have {sorted(_FORMATS)}")
@@ -91,13 +105,13 @@ def _check_scale(g: Optional[torch.Tensor], fmt: str, device: torch.device) -> i
 
 
 def _sizes(rows: int, cols: int, fmt: str) -> Tuple[int, int]:
-    """Bytes of the codes and of the scales of a matrix."""
-    lib = load()
-    codes = int(lib.gemm_mx4_codes_pitch(cols))
-    scales = int(lib.gemm_mx4_scales_bytes(rows, cols, _format(fmt)))
-    if codes < 0 or scales < 0:
+    """Bytes of the codes and of the scales of a matrix: rows times
+    gemm_mx4_codes_pitch, and gemm_mx4_scales_bytes."""
+    _format(fmt)
+    if rows < 0 or cols < 0:
         raise ValueError(f"a 4-bit matrix cannot be {rows} x {cols}")
-    return rows * codes, scales
+    return (rows * ((cols + 31) // 32 * 16),
+            (rows + 127) // 128 * ((cols + 255) // 256) * (32768 // _BLOCK[fmt]))
 
 
 class Mx4Matrix:
@@ -158,19 +172,12 @@ def _check_values(X: torch.Tensor, name: str) -> Tuple[int, int]:
     return _check_matrix(X, name, X.dtype), _type(X.dtype, name)
 
 
-def _done(status: int, what: str) -> None:
-    if status != TGEMM_OK:
-        raise TgemmError(status, what)
-
-
 def mx4_tensor_scale(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The nvfp4 scale of X: the smallest power of two g with 2688 g >= |X|
     (one float32 on X's device; infinities and NaN are left out)."""
     ldx, kind = _check_values(X, "X")
     g = _empty(stream, 1, dtype=torch.float32, device=X.device)
-    _done(_on_device(X.device, lambda dev: load().gemm_mx4_tensor_scale(
-        X.shape[0], X.shape[1], X.data_ptr(), ldx, kind, g.data_ptr(), _stream_handle(stream, dev))),
-        "gemm_mx4_tensor_scale")
+    _call("gemm_mx4_tensor_scale", X.device, stream, X.shape[0], X.shape[1], X.data_ptr(), ldx, kind, g.data_ptr())
     return g
 
 
@@ -185,10 +192,9 @@ def _quantize(X, fmt, tensor_scale, stream, rows: bool, trans: bool):
     g = _check_scale(tensor_scale, fmt, device)
     q = Mx4Matrix._empty(fmt, R, C, device, tensor_scale, g, stream) if rows else None
     t = Mx4Matrix._empty(fmt, C, R, device, tensor_scale, g, stream) if trans else None
-    _done(_on_device(device, lambda dev: load().gemm_mx4_quantize(
-        R, C, X.data_ptr(), ldx, kind, code, g, TGEMM_MX4_SET_G if set_g else 0, q._codes if rows else 0, q._scales if rows else 0,
-        t._codes if trans else 0, t._scales if trans else 0, _stream_handle(stream, dev))),
-        "gemm_mx4_quantize")
+    _call("gemm_mx4_quantize", device, stream, R, C, X.data_ptr(), ldx, kind, code, g,
+          TGEMM_MX4_SET_G if set_g else 0, q._codes if rows else 0, q._scales if rows else 0,
+          t._codes if trans else 0, t._scales if trans else 0)
     return q, t
 
 
@@ -221,9 +227,8 @@ def mx4_dequantize(Q: Mx4Matrix, dtype: torch.dtype = torch.float32,
     elif tuple(out.shape) != Q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {Q.shape}")
     ldx, kind = _check_values(out, "out")
-    _done(_on_device(Q.device, lambda dev: load().gemm_mx4_dequantize(
-        Q.rows, Q.cols, Q._codes, Q._scales, _FORMATS[Q.fmt], Q._g,
-        out.data_ptr(), ldx, kind, _stream_handle(stream, dev))), "gemm_mx4_dequantize")
+    _call("gemm_mx4_dequantize", Q.device, stream, Q.rows, Q.cols, Q._codes, Q._scales, _FORMATS[Q.fmt], Q._g,
+          out.data_ptr(), ldx, kind)
     return out
 
 
@@ -250,9 +255,8 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: str = "mxfp4",
         raise ValueError("codes and scales are on different devices")
     g = _check_scale(tensor_scale, fmt, codes.device)
     q = Mx4Matrix._empty(fmt, rows, cols, codes.device, tensor_scale, g, stream)
-    _done(_on_device(codes.device, lambda dev: load().gemm_mx4_pack(
-        rows, cols, code, codes.data_ptr(), ldc, scales.data_ptr(), lds, q._codes,
-        q._scales, _stream_handle(stream, dev))), "gemm_mx4_pack")
+    _call("gemm_mx4_pack", codes.device, stream, rows, cols, code, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+          q._codes, q._scales)
     return q
 
 
@@ -293,10 +297,8 @@ def gemm_mx4(A: Mx4Matrix, B: Mx4Matrix, out_dtype: torch.dtype = torch.float32,
     if A.device != B.device:
         raise ValueError(f"A is on {A.device}, B on {B.device}")
     C, ldc, kind, bias_ptr = _output(out, A.rows, B.rows, out_dtype, A.device, beta, bias, stream)
-    _done(_on_device(A.device, lambda dev: load().gemm_mx4(
-        A.rows, B.rows, A.cols, A._codes, A._scales, A._g, B._codes, B._scales, B._g,
-        _FORMATS[A.fmt], C.data_ptr(), ldc, kind,
-        alpha, beta, bias_ptr, _stream_handle(stream, dev))), "gemm_mx4")
+    _call("gemm_mx4", A.device, stream, A.rows, B.rows, A.cols, A._codes, A._scales, A._g, B._codes, B._scales,
+          B._g, _FORMATS[A.fmt], C.data_ptr(), ldc, kind, alpha, beta, bias_ptr)
     return C
 
 
@@ -313,8 +315,6 @@ def gemm_w4(A: torch.Tensor, W: Mx4Matrix, out_dtype: torch.dtype = torch.float3
     if A.device != W.device:
         raise ValueError(f"A is on {A.device}, W on {W.device}")
     C, ldc, kind, bias_ptr = _output(out, A.shape[0], W.rows, out_dtype, A.device, beta, bias, stream)
-    _done(_on_device(A.device, lambda dev: load().gemm_w4(
-        A.shape[0], W.rows, W.cols, A.data_ptr(), lda, W._codes, W._scales,
-        W._g, _FORMATS[W.fmt], C.data_ptr(), ldc, kind, alpha, beta, bias_ptr,
-        _stream_handle(stream, dev))), "gemm_w4")
+    _call("gemm_w4", A.device, stream, A.shape[0], W.rows, W.cols, A.data_ptr(), lda, W._codes, W._scales, W._g,
+          _FORMATS[W.fmt], C.data_ptr(), ldc, kind, alpha, beta, bias_ptr)
     return C
