@@ -10,6 +10,8 @@ roundings of terms no larger than the sum of the terms' magnitudes (2^-20 of
 it), a BF16 result half a unit in the last place (2^-8 of it, with the next
 binade).
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -225,6 +227,32 @@ def test_on_another_stream_and_in_a_graph(tgemm, op, M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [5, 40, 2100])
+@pytest.mark.parametrize("op", OPS)
+def test_the_first_cuda_call_of_a_thread(tgemm, op, M):
+    """A thread whose first work on the device is a call of this library, as
+    the one that runs backward passes."""
+    A, B, a, b = operands(tgemm, op, M, 2600, 64, "mxfp4", "whole")
+    X = torch.zeros(M, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(M, 2600, device="cuda")
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(f):
+        try:
+            f()
+        except Exception as e:               # noqa: BLE001 - reported below
+            failed.append(e)
+
+    for f in (lambda: call(tgemm, op)(A, B, out=out), lambda: tgemm.mx4_quantize_both(X)):
+        t = threading.Thread(target=work, args=(f,))
+        t.start()
+        t.join()
+    assert not failed
+    torch.cuda.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), a @ b.T)
 
 
 @pytest.mark.parametrize("op", OPS)

@@ -155,12 +155,22 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline bool encode(EncodeTiledFn enc, CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
-            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-            CUtensorMapSwizzle swizzle) {
+                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle) {
     const cuuint32_t ones[3] = {1, 1, 1};
-    return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto call = [&]() {
+        return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = call();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // A thread that has made no runtime call yet (a backward pass runs on
+        // one) has no current context: the encoder is the driver's.
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = call();
+    }
+    return r == CUDA_SUCCESS;
 }
 
 // Codes in boxes of 128 rows x `width` bytes (128 or 64), swizzled over as many.
