@@ -18,7 +18,9 @@
 //           columns of scales do not fit the 512 of tensor memory, so the
 //           accumulators share 48 columns: the epilogue drains the shared
 //           ones first and then lets the next tile's MMAs start.
-//   single  128 x 128 tiles on one SM, for products with few tiles.
+//   single  128 x 128 tiles on one SM, for products with few tiles; of very
+//           few, a cluster's blocks split K and add their shares through
+//           distributed shared memory.
 //
 // Rows past M and N are read as zeros (TMA fill, zero scales) and not stored.
 // Waits are bounded as in the other tensor-core kernels.
@@ -89,7 +91,10 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
     const bool leader = rank == 0;
-    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int part = PAIR ? 0 : blockIdx.x % p.split;
+    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x / p.split;
+    const int kb0 = PAIR ? 0 : (int)((long)p.kblocks * part / p.split);
+    const int kb1 = PAIR ? p.kblocks : (int)((long)p.kblocks * (part + 1) / p.split);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -136,7 +141,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tile_coords(t, p, mb, nb);
                 const int row = mb * S::TM + (int)rank * 128;
                 const int col = nb * S::TN + (int)rank * 128;
-                for (int kb = 0; kb < p.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                     if (!ok) break;
                     if (!stall) {
@@ -190,7 +195,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tc_fence_after();
                 const uint32_t d = tmem_base + ((it & 1) ? S::ACC1 : 0);
                 const uint32_t sfa = tmem_base + S::SF, sfb = sfa + S::SF_TILES * 4;
-                for (int kb = 0; kb < p.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
@@ -212,10 +217,10 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         mma_mx4<FMT, PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
                                            smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2),
                                            mx4_instr<FMT, S::TM, S::TN>(half), sfa + tile * 4,
-                                           sfb + tile * 4 * (S::TN / 128), (kb | k) != 0);
+                                           sfb + tile * 4 * (S::TN / 128), kb != kb0 || k != 0);
                     }
                     tc_commit<PAIR>(smem_u32(&sy->empty[s]));
-                    if (kb == p.kblocks - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                    if (kb == kb1 - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -245,6 +250,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
                 }
             };
+            if (!PAIR && p.split > 1) {
+                // The tile's copies and MMAs are done: its stages hold the share.
+                store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
+                break;
+            }
             drain_tile<S::TN, S::FREE_FIRST, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
                               mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
         }
@@ -254,6 +264,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     tc_fence_before();
     if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
     tc_fence_after();
+    if (!PAIR && p.split > 1) {
+        int mb, nb;
+        tile_coords(unit, p, mb, nb);
+        join_shares<TC>(p, smem, part, mb * S::TM, nb * S::TN, mx4_g(p.ga), mx4_g(p.gb));
+    }
     if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
 }
 
@@ -284,10 +299,14 @@ cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B
     cudaError_t e = make_tiling(p, M, N, S::TM, S::TN, PAIR ? num_sms / 2 : num_sms, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.ga = A.g; p.gb = B.g;
+    if (!PAIR && p.num_tiles * 2 <= num_sms) {
+        p.split = split_for(p.num_tiles, p.kblocks, num_sms);
+        p.units = p.num_tiles;
+    }
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
     if (e == cudaSuccess) e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, TC>>(S::SMEM);
     if (e != cudaSuccess) return e;
-    PairLaunch cfg((PAIR ? 2 : 1) * p.units, THREADS, S::SMEM, PAIR, s);
+    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, S::SMEM, PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
 }
 

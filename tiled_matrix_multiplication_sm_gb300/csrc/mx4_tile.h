@@ -19,6 +19,7 @@ constexpr int TMEM_COLS = 512;
 struct Tiling {
     int M, N;
     int tiles_m, tiles_n, num_tiles, units;
+    int split;                  // blocks of a cluster that share a tile's sum (1: none; then units tiles in all)
     int group_m;                // rows of tiles walked together, so that they share panels of B in L2
     Mx4Out out;
     int tma_c;                  // C leaves by TMA stores
@@ -149,6 +150,52 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
     }
 }
 
+// A tile whose sum is split over a cluster: this warp's 32 rows of the block's
+// share, FP32, to `partial` (128 rows of 128 columns, 16-byte pieces permuted
+// by the row so that neither side's accesses conflict).
+__device__ __forceinline__ void store_share(uint8_t* partial, uint32_t tmem, int q) {
+    const int row = q * 32 + (threadIdx.x & 31);
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + (uint32_t)c, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(partial + row * 512 + (((c / 4 + j) ^ (row & 31)) << 4)) =
+                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+    }
+}
+
+// The cluster's shares added in the order of their ranks, and stored: block
+// `part` takes every split-th row. All threads of all the cluster's blocks.
+template <typename TC>
+__device__ __forceinline__ void join_shares(const Tiling& p, const uint8_t* partial, int part, int row0, int col0,
+                                            float ga, float gb) {
+    cluster_sync_all();
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int r = part + p.split * (int)(threadIdx.x >> 5); r < 128 && row0 + r < p.M; r += p.split * warps) {
+        float v[4] = {};
+        for (int i = 0; i < p.split; ++i) {
+            const uint32_t base = map_to_rank(smem_u32(partial), (uint32_t)i) + r * 512;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = k * 32 + lane;
+                float w;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w)
+                             : "r"(base + (((c >> 2) ^ (r & 31)) << 4) + (c & 3) * 4) : "memory");
+                v[k] += w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = col0 + k * 32 + lane;
+            if (c < p.N) mx4_store(static_cast<TC*>(p.out.C) + (long)(row0 + r) * p.out.ldc + c, v[k], ga, gb, p.out, c);
+        }
+    }
+    cluster_sync_all();           // no block leaves while another reads its share
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -205,6 +252,15 @@ inline bool encode_c(EncodeTiledFn enc, CUtensorMap* map, const Mx4Out& o, int M
                   dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How many blocks of a cluster share the sum of one of few 128 x 128 tiles:
+// as many as leave a tenth of the SMs (clusters do not pack the GPU fully),
+// each with two steps of K at least.
+inline int split_for(long tiles, int steps, int num_sms) {
+    long c = num_sms * 9L / 10 / tiles;
+    if (c > steps / 2) c = steps / 2;
+    return c < 1 ? 1 : c > 8 ? 8 : (int)c;
+}
+
 inline cudaError_t make_tiling(Tiling& p, int M, int N, int tile_m, int tile_n, int slots, const Mx4Out& out) {
     p.M = M; p.N = N;
     p.tiles_m = (int)(((long)M + tile_m - 1) / tile_m);
@@ -214,6 +270,7 @@ inline cudaError_t make_tiling(Tiling& p, int M, int N, int tile_m, int tile_n, 
     p.units = p.num_tiles < slots ? p.num_tiles : slots;
     // 8192 x 14336 x 4096 NVFP4: 152 us with 16 and 158 with 8; 4096^3: 40 and 38.
     p.group_m = p.tiles_m >= 32 ? 16 : 8;
+    p.split = 1;
     p.out = out;
     p.tma_c = 0;
     p.wait_limit_ns = wait_limit_ns();
@@ -221,12 +278,12 @@ inline cudaError_t make_tiling(Tiling& p, int M, int N, int tile_m, int tile_n, 
     return mx4_status_word(&p.status);
 }
 
-// Launch attributes: programmatic dependent launch (see launch_pdl) and, for
-// SM pairs, clusters of two blocks.
-struct PairLaunch {
+// Launch attributes: programmatic dependent launch (see launch_pdl) and
+// clusters of `cluster` blocks.
+struct ClusterLaunch {
     cudaLaunchConfig_t config = {};
     cudaLaunchAttribute attr[2];
-    PairLaunch(int blocks, int threads, int smem, bool pair, cudaStream_t s) {
+    ClusterLaunch(int blocks, int threads, int smem, int cluster, cudaStream_t s) {
         config.gridDim = dim3((unsigned)blocks);
         config.blockDim = dim3((unsigned)threads);
         config.dynamicSmemBytes = (size_t)smem;
@@ -234,11 +291,11 @@ struct PairLaunch {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
         attr[1].val.clusterDim.y = 1;
         attr[1].val.clusterDim.z = 1;
         config.attrs = attr;
-        config.numAttrs = pair ? 2 : 1;
+        config.numAttrs = cluster > 1 ? 2 : 1;
     }
 };
 

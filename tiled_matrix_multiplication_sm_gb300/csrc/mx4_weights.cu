@@ -24,11 +24,15 @@ namespace {
 using namespace mx4_tile;
 using namespace mx4_decode;
 
-constexpr int STAGES = 5;
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
-constexpr int CHUNKS = 3;                            // code chunks in flight
+// Pipeline stages, and chunks of codes in flight. Pair tiles read each chunk
+// from L2 and want stages; few tiles read W from memory once and want bytes
+// in flight (72 KB of codes).
+template <bool PAIR> constexpr int STAGES_OF = PAIR ? 5 : 3;
+template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 3 : 9;
+constexpr int MAX_STAGES = 5, MAX_CHUNKS = 9;
 constexpr int DECODE_WARPS = 8;
 constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
 constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
@@ -44,22 +48,24 @@ struct Chunk {
 };
 
 struct Sync {
-    uint64_t full[STAGES], empty[STAGES];
-    uint64_t codes_full[CHUNKS], codes_empty[CHUNKS];
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t codes_full[MAX_CHUNKS], codes_empty[MAX_CHUNKS];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     uint32_t factors[256];
 };
-constexpr int SYNC_BYTES = 1280;
+constexpr int SYNC_BYTES = 1408;
 static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
 
-template <int FMT>
+template <int FMT, bool PAIR>
 constexpr int smem_bytes() {
-    return 1024 + STAGES * STAGE_BYTES + CHUNKS * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
+    return 1024 + STAGES_OF<PAIR> * STAGE_BYTES + CHUNKS_OF<PAIR> * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
 }
-static_assert(smem_bytes<TGEMM_NVFP4>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<TGEMM_NVFP4, true>() <= 227 * 1024 && smem_bytes<TGEMM_NVFP4, false>() <= 227 * 1024,
+              "shared memory");
+static_assert(3 * STAGE_BYTES >= 128 * 512, "a share fits the stages");
 
 struct Params : Tiling {
     int kblocks;                // of 64 columns
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC,
                const Params p) {
-    constexpr int TM = PAIR ? 256 : 128, TN = TM;
+    constexpr int TM = PAIR ? 256 : 128, TN = TM, STAGES = STAGES_OF<PAIR>, CHUNKS = CHUNKS_OF<PAIR>;
     using CH = Chunk<FMT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -121,7 +127,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
     const bool leader = rank == 0;
-    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int part = PAIR ? 0 : blockIdx.x % p.split;
+    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x / p.split;
+    // This block's chunks and K blocks of a tile.
+    const int chunks = (p.kblocks + PER_CHUNK - 1) / PER_CHUNK;
+    const int ch0 = PAIR ? 0 : (int)((long)chunks * part / p.split);
+    const int ch1 = PAIR ? chunks : (int)((long)chunks * (part + 1) / p.split);
+    const int kb0 = ch0 * PER_CHUNK, kb1 = min(ch1 * PER_CHUNK, p.kblocks);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -171,7 +183,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tile_coords(t, p, mb, nb);
             const int row = mb * TM + (int)rank * 128;
             const int col = nb * TN + (int)rank * 128;
-            for (int kb = 0; kb < p.kblocks; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (kb % PER_CHUNK == 0) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), cph ^ 1u, wait));
                     if (!ok) break;
@@ -231,7 +243,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)((it & 1) * TN);
-                for (int kb = 0; kb < p.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
@@ -240,9 +252,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                         for (int k = 0; k < STAGE_K / 16; ++k)
                             mma_bf16<PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
-                                           smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2), IDESC, (kb | k) != 0);
+                                           smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2), IDESC, kb != kb0 || k != 0);
                         tc_commit<PAIR>(smem_u32(&sy->empty[s]));
-                        if (kb == p.kblocks - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                        if (kb == kb1 - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -272,6 +284,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
                 }
             };
+            if (!PAIR && p.split > 1) {
+                // The tile's copies and MMAs are done: its stages hold the share.
+                store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
+                break;
+            }
             drain_tile<TN, TN, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
                                    mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
         }
@@ -285,18 +302,17 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int dw = warp - 2 - EPI_WARPS, group = dw / GROUP_WARPS;
         const int tid = dw % GROUP_WARPS * 32 + lane;
         constexpr int ITEMS = 256 / (32 * GROUP_WARPS);          // runs of 32 codes a thread and stage
-        const int chunks = (p.kblocks + PER_CHUNK - 1) / PER_CHUNK;
         uint32_t cph = 0;
-        int c = 0, base = 0;                                     // base: the tile's first stage
+        int c = 0, base = -kb0;                                  // the stage of a tile's K block 0
         bool ok = true;
-        for (int t = unit; ok && t < p.num_tiles; t += p.units, base += p.kblocks) {
-            for (int ch = 0; ch < chunks; ++ch) {
+        for (int t = unit; ok && t < p.num_tiles; t += p.units, base += kb1 - kb0) {
+            for (int ch = ch0; ch < ch1; ++ch) {
                 ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
                 if (!ok) break;
 #pragma unroll 1
                 for (int q = 0; q < PER_CHUNK; ++q) {
                     const int kb = ch * PER_CHUNK + q, idx = base + kb, s = idx % STAGES;
-                    if (kb >= p.kblocks || idx % GROUPS != group) continue;
+                    if (kb >= kb1 || idx % GROUPS != group) continue;
                     uint4 w[ITEMS];
                     uint32_t b0[ITEMS], b1[ITEMS];
                     bool is_wide = false;
@@ -355,6 +371,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
+    if (!PAIR && p.split > 1) {
+        int mb, nb;
+        tile_coords(unit, p, mb, nb);
+        join_shares<TC>(p, smem, part, mb * TM, nb * TN, unscale<FMT>(), mx4_g(p.gb));
+    }
     if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
 }
 
@@ -375,10 +396,14 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     cudaError_t e = make_tiling(p, M, N, TILE, TILE, PAIR ? num_sms / 2 : num_sms, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.gb = B.g;
+    if (!PAIR && p.num_tiles * 2 <= num_sms) {
+        p.split = split_for(p.num_tiles, p.kblocks / PER_CHUNK, num_sms);
+        p.units = p.num_tiles;
+    }
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
-    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(smem_bytes<FMT>());
+    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(smem_bytes<FMT, PAIR>());
     if (e != cudaSuccess) return e;
-    PairLaunch cfg((PAIR ? 2 : 1) * p.units, THREADS, smem_bytes<FMT>(), PAIR, s);
+    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, smem_bytes<FMT, PAIR>(), PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, PAIR, TC>, tmA, tmB, tmSB, tmC, p);
 }
 
