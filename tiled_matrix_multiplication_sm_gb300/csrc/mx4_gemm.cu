@@ -255,7 +255,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<S::TN, S::FREE_FIRST, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
+            drain_tile<S::TN, S::FREE_FIRST, true, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
                               mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
         }
         tma_store_wait_all();

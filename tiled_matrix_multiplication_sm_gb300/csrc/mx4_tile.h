@@ -41,36 +41,44 @@ __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r
 
 // Drains this warp's 32 rows of a tile, 64 columns a turn. `last_first`: the
 // last 64 columns, which the next tile's accumulator shares, go first.
-// release() is called as soon as FREE_FIRST columns have left tensor memory.
-template <int TN, int FREE_FIRST, typename TC, typename Release>
+// release() is called as soon as FREE_FIRST columns have left tensor memory;
+// BOTH: a turn's columns are in registers before any is stored (an earlier
+// release for 32 registers more).
+template <int TN, int FREE_FIRST, bool BOTH, typename TC, typename Release>
 __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* tmC, uint32_t tmem,
                                            uint8_t* bufs, int row0, int col0, bool last_first,
                                            float ga, float gb, Release release) {
-    constexpr int W = 64;
+    constexpr int W = 64, CW = 128 / (int)sizeof(TC);
     constexpr int TURNS = TN / W, REL = FREE_FIRST / W;
     const int lane = threadIdx.x & 31;
     const Mx4Out& o = p.out;
+    const int rows = min(32, p.M - row0);
 #pragma unroll 1
     for (int i = 0; i < TURNS; ++i) {
         const int part = last_first ? (i == 0 ? TURNS - 1 : i - 1) : i;
         const int col = col0 + part * W;
-        uint32_t r[2][32];
-        tmem_ld32(tmem + (uint32_t)(part * W), r[0]);
-        tmem_ld32(tmem + (uint32_t)(part * W + 32), r[1]);
-        tmem_wait_ld(r[0]);
-        tmem_wait_ld(r[1]);
-        if (i == REL - 1) release();
+        uint32_t held[BOTH ? 2 : 1][32];
+        if constexpr (BOTH) {
+            tmem_ld32(tmem + (uint32_t)(part * W), held[0]);
+            tmem_ld32(tmem + (uint32_t)(part * W + 32), held[1]);
+            tmem_wait_ld(held[0]);
+            tmem_wait_ld(held[1]);
+            if (i == REL - 1) release();
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            uint32_t (&r)[32] = held[BOTH ? h : 0];
+            if constexpr (!BOTH) {
+                tmem_ld32(tmem + (uint32_t)(part * W + h * 32), r);
+                tmem_wait_ld(r);
+                if (h == 1 && i == REL - 1) release();
+            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[h][j] = __float_as_uint(__uint_as_float(r[h][j]) * ga * gb * o.alpha);
-        if (p.tma_c) {
-            // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16: one of
-            // 64 -- through two buffers in turn: the box before the last has
-            // to have left its buffer.
-            constexpr int CW = 128 / (int)sizeof(TC);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ga * gb * o.alpha);
+            if (p.tma_c) {
+                // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16:
+                // one of 64 -- through two buffers in turn: the box before
+                // the last has to have left its buffer.
                 uint8_t* buf = bufs + ((sizeof(TC) == 4 ? h : i) & 1) * BUF_BYTES;
                 if (sizeof(TC) == 4 || h == 0) {
                     if (lane == 0) tma_store_wait_read<1>();
@@ -80,20 +88,20 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (col + h * 32 + j < p.N)
-                            r[h][j] = __float_as_uint(__uint_as_float(r[h][j]) + __ldg(o.bias + col + h * 32 + j));
+                            r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldg(o.bias + col + h * 32 + j));
                 if constexpr (sizeof(TC) == 4) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         *reinterpret_cast<uint4*>(buf + swizzled(lane, j)) =
-                            make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
+                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[h][8 * j + 2 * k]),
-                                                                           __uint_as_float(r[h][8 * j + 2 * k + 1]));
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * k]),
+                                                                           __uint_as_float(r[8 * j + 2 * k + 1]));
                             w[k] = *reinterpret_cast<const uint32_t*>(&b);
                         }
                         *reinterpret_cast<uint4*>(buf + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -104,48 +112,43 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
                     __syncwarp();
                     const int c = col + (sizeof(TC) == 4 ? h * CW : 0);
                     if (lane == 0) {
-                        if (row0 < p.M && c < p.N) tma_store_2d(tmC, c, row0, smem_u32(buf));
+                        if (rows > 0 && c < p.N) tma_store_2d(tmC, c, row0, smem_u32(buf));
                         tma_store_commit();                       // counted even when there is none
                     }
                 }
-            }
-        } else {
-            // Any alignment, and beta: 32 x 32 FP32 blocks through shared
-            // memory, then whole row segments, a column a lane, eight rows'
-            // loads ahead of their stores.
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+            } else {
+                // Any alignment, and beta: 32 x 32 FP32 blocks through shared
+                // memory, then whole row segments, a column a lane, eight
+                // rows' loads ahead of their stores.
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(bufs + h * BUF_BYTES + swizzled(lane, j)) =
-                        make_uint4(r[h][4 * j], r[h][4 * j + 1], r[h][4 * j + 2], r[h][4 * j + 3]);
-            __syncwarp();
-            const int rows = min(32, p.M - row0);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+                    *reinterpret_cast<uint4*>(bufs + swizzled(lane, j)) =
+                        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                __syncwarp();
                 const int c = col + h * 32 + lane;
-                if (c >= p.N) continue;
-                TC* out = static_cast<TC*>(o.C) + (long)row0 * o.ldc + c;
-                const uint8_t* buf = bufs + h * BUF_BYTES + (lane & 3) * 4;
-                const float bias = o.bias != nullptr ? __ldg(o.bias + c) : 0.0f;
+                if (c < p.N) {
+                    TC* out = static_cast<TC*>(o.C) + (long)row0 * o.ldc + c;
+                    const uint8_t* buf = bufs + (lane & 3) * 4;
+                    const float bias = o.bias != nullptr ? __ldg(o.bias + c) : 0.0f;
 #pragma unroll 1
-                for (int k = 0; k < rows; k += 8) {
-                    float v[8], old[8];
+                    for (int k = 0; k < rows; k += 8) {
+                        float v[8], old[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        v[i] = *reinterpret_cast<const float*>(buf + swizzled(k + i, lane >> 2));
-                        old[i] = o.beta != 0.0f && k + i < rows ? (float)out[i * o.ldc] : 0.0f;
-                    }
+                        for (int j = 0; j < 8; ++j) {
+                            v[j] = *reinterpret_cast<const float*>(buf + swizzled(k + j, lane >> 2));
+                            old[j] = o.beta != 0.0f && k + j < rows ? (float)out[j * o.ldc] : 0.0f;
+                        }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (o.beta != 0.0f) v[i] = fmaf(o.beta, old[i], v[i]);
-                        if (o.bias != nullptr) v[i] += bias;
-                        if (k + i < rows) out[i * o.ldc] = (TC)v[i];
+                        for (int j = 0; j < 8; ++j) {
+                            if (o.beta != 0.0f) v[j] = fmaf(o.beta, old[j], v[j]);
+                            if (o.bias != nullptr) v[j] += bias;
+                            if (k + j < rows) out[j * o.ldc] = (TC)v[j];
+                        }
+                        out += 8 * o.ldc;
                     }
-                    out += 8 * o.ldc;
                 }
             }
-            __syncwarp();
         }
     }
 }

@@ -26,13 +26,11 @@ using namespace mx4_decode;
 
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
-constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
-// Pipeline stages, and chunks of codes in flight. Pair tiles read each chunk
-// from L2 and want stages; few tiles read W from memory once and want bytes
-// in flight (72 KB of codes).
-template <bool PAIR> constexpr int STAGES_OF = PAIR ? 5 : 3;
-template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 3 : 9;
-constexpr int MAX_STAGES = 5, MAX_CHUNKS = 9;
+// Chunks of codes in flight. Pair tiles read each from L2; few tiles read W
+// from memory once and want bytes in flight.
+template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 3 : 5;
+constexpr int PAIR_STAGES = 5;
+constexpr int MAX_STAGES = 8, MAX_CHUNKS = 5;
 constexpr int DECODE_WARPS = 8;
 constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
 constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
@@ -59,16 +57,25 @@ struct Sync {
 constexpr int SYNC_BYTES = 1408;
 static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
 
+// Shared memory beside the stages.
 template <int FMT, bool PAIR>
-constexpr int smem_bytes() {
-    return 1024 + STAGES_OF<PAIR> * STAGE_BYTES + CHUNKS_OF<PAIR> * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
+constexpr int fixed_bytes() {
+    return 1024 + CHUNKS_OF<PAIR> * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
 }
-static_assert(smem_bytes<TGEMM_NVFP4, true>() <= 227 * 1024 && smem_bytes<TGEMM_NVFP4, false>() <= 227 * 1024,
-              "shared memory");
-static_assert(3 * STAGE_BYTES >= 128 * 512, "a share fits the stages");
+constexpr int SMEM_LIMIT = 227 * 1024;
+static_assert(fixed_bytes<TGEMM_NVFP4, true>() + PAIR_STAGES * 2 * OPERAND_BYTES <= SMEM_LIMIT, "shared memory");
+// A warp that waits for a slot has seen the slot's last use but one freed only
+// if its previous stage was at most as many stages back as there are slots
+// (barriers tell phases apart by parity).
+static_assert(PAIR_STAGES >= GROUPS && (SMEM_LIMIT - fixed_bytes<TGEMM_NVFP4, false>()) / (2 * OPERAND_BYTES) >= GROUPS,
+              "fewer slots than groups");
+static_assert(GROUPS * OPERAND_BYTES >= 128 * 512, "a share fits the stages");
 
 struct Params : Tiling {
     int kblocks;                // of 64 columns
+    // One SM: slots of the pipeline, and the rows of A that a slot holds (the
+    // MMA reads 128: what lies beyond them makes rows of C that are not stored).
+    int stages, a_rows;
     const float* gb;
 };
 
@@ -114,7 +121,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC,
                const Params p) {
-    constexpr int TM = PAIR ? 256 : 128, TN = TM, STAGES = STAGES_OF<PAIR>, CHUNKS = CHUNKS_OF<PAIR>;
+    constexpr int TM = PAIR ? 256 : 128, TN = TM, CHUNKS = CHUNKS_OF<PAIR>;
+    const int STAGES = PAIR ? PAIR_STAGES : p.stages;
+    const int A_BYTES = PAIR ? OPERAND_BYTES : p.a_rows * SW, STAGE_BYTES = A_BYTES + OPERAND_BYTES;
     using CH = Chunk<FMT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -202,7 +211,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (!ok) break;
                 if (!stall) {
                     if (elect_one()) {
-                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), (PAIR ? 2 : 1) * OPERAND_BYTES);
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), (PAIR ? 2 : 1) * A_BYTES);
                         tma_load_2d<PAIR>(stage0 + s * STAGE_BYTES, &tmA, kb * STAGE_K, row,
                                           full0 + (uint32_t)(s * sizeof(uint64_t)));
                     }
@@ -252,7 +261,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                         for (int k = 0; k < STAGE_K / 16; ++k)
                             mma_bf16<PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
-                                           smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2), IDESC, kb != kb0 || k != 0);
+                                           smem_desc(a + A_BYTES + k * 32, 16, 1024, 2), IDESC, kb != kb0 || k != 0);
                         tc_commit<PAIR>(smem_u32(&sy->empty[s]));
                         if (kb == kb1 - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
                     }
@@ -289,7 +298,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<TN, TN, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
+            drain_tile<TN, TN, false, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
                                    mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
         }
         tma_store_wait_all();
@@ -348,7 +357,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ((uint32_t)(idx / STAGES) & 1u) ^ 1u, wait));
                     if (!ok) break;
-                    uint8_t* dst = smem + s * STAGE_BYTES + OPERAND_BYTES;
+                    uint8_t* dst = smem + s * STAGE_BYTES + A_BYTES;
 #pragma unroll
                     for (int i = 0; i < ITEMS; ++i) {
                         const int item = i * 32 * GROUP_WARPS + tid, row = item & 127, half = item >> 7;
@@ -387,7 +396,8 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     constexpr int TILE = PAIR ? 256 : 128;
     CUtensorMap tmA, tmB, tmSB, tmC;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)lda * 2};
-    const cuuint32_t box[2] = {STAGE_K, 128};
+    const int a_rows = PAIR || M > 96 ? 128 : (M + 31) / 32 * 32;
+    const cuuint32_t box[2] = {STAGE_K, (cuuint32_t)a_rows};
     if (!encode(enc, &tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_codes(enc, &tmB, B, N, K, CHUNK_K / 2) || !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT>::SF_TILES, 1))
         return cudaErrorInvalidValue;
@@ -396,14 +406,19 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     cudaError_t e = make_tiling(p, M, N, TILE, TILE, PAIR ? num_sms / 2 : num_sms, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.gb = B.g;
+    p.a_rows = a_rows;
+    const int slot = a_rows * SW + OPERAND_BYTES;
+    p.stages = PAIR ? PAIR_STAGES : (SMEM_LIMIT - fixed_bytes<FMT, PAIR>()) / slot;
+    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    const int smem = fixed_bytes<FMT, PAIR>() + p.stages * slot;
     if (!PAIR && p.num_tiles * 2 <= num_sms) {
         p.split = split_for(p.num_tiles, p.kblocks / PER_CHUNK, num_sms);
         p.units = p.num_tiles;
     }
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
-    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(smem_bytes<FMT, PAIR>());
+    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(SMEM_LIMIT);
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, smem_bytes<FMT, PAIR>(), PAIR ? 2 : p.split, s);
+    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, smem, PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, PAIR, TC>, tmA, tmB, tmSB, tmC, p);
 }
 
