@@ -34,7 +34,8 @@ constexpr int MAX_STAGES = 8, MAX_CHUNKS = 5;
 constexpr int DECODE_WARPS = 8;
 constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
 constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
-constexpr int THREADS = 32 * (2 + EPI_WARPS + DECODE_WARPS);
+constexpr int CODES_WARP = 2 + EPI_WARPS + DECODE_WARPS;
+constexpr int THREADS = 32 * (CODES_WARP + 1);
 constexpr int CHUNK_K = 128;
 constexpr int PER_CHUNK = CHUNK_K / STAGE_K;
 
@@ -184,29 +185,14 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
-        uint32_t armed = 0, armed_parity = 0, ph = 0, cph = 0, c_armed = 0, c_parity = 0;
-        int s = 0, c = 0;
+        uint32_t armed = 0, armed_parity = 0, ph = 0;
+        int s = 0;
         bool ok = true, stall = p.debug_stall != 0;        // test hook: the first stage is never filled
         for (int t = unit; ok && t < p.num_tiles; t += p.units) {
             int mb, nb;
             tile_coords(t, p, mb, nb);
             const int row = mb * TM + (int)rank * 128;
-            const int col = nb * TN + (int)rank * 128;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (kb % PER_CHUNK == 0) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), cph ^ 1u, wait));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        const uint32_t bar = smem_u32(&sy->codes_full[c]);
-                        mbar_arrive_expect_tx(bar, CH::BYTES);
-                        tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, kb / PER_CHUNK * (CHUNK_K / 2), col, bar);
-                        tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0,
-                                           kb / PER_CHUNK * CH::SF_TILES, col / 128, bar);
-                    }
-                    c_armed |= 1u << c;
-                    c_parity = (c_parity & ~(1u << c)) | (cph << c);
-                    if (++c == CHUNKS) { c = 0; cph ^= 1u; }
-                }
                 ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
                 if (!stall) {
@@ -223,9 +209,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
         }
-        for (int i = 0; i < CHUNKS; ++i)
-            if (c_armed & (1u << i))
-                mbar_wait<false>(smem_u32(&sy->codes_full[i]), (c_parity >> i) & 1u, wait);
         if (leader) {
             for (int i = 0; i < STAGES; ++i)
                 if (armed & (1u << i))
@@ -302,6 +285,35 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                                    mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
         }
         tma_store_wait_all();
+    } else if (warp == CODES_WARP) {
+        // ---------------------------------------- TMA producer of the codes
+        // A warp of its own: it runs as far ahead as there are chunks, A's
+        // producer as far as there are slots.
+        uint32_t armed = 0, armed_parity = 0, ph = 0;
+        int c = 0;
+        bool ok = true;
+        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+            int mb, nb;
+            tile_coords(t, p, mb, nb);
+            const int col = nb * TN + (int)rank * 128;
+            for (int ch = ch0; ch < ch1; ++ch) {
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), ph ^ 1u, wait));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = smem_u32(&sy->codes_full[c]);
+                    mbar_arrive_expect_tx(bar, CH::BYTES);
+                    tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, ch * (CHUNK_K / 2), col, bar);
+                    tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0, ch * CH::SF_TILES,
+                                       col / 128, bar);
+                }
+                __syncwarp();
+                armed |= 1u << c;
+                armed_parity = (armed_parity & ~(1u << c)) | (ph << c);
+                if (++c == CHUNKS) { c = 0; ph ^= 1u; }
+            }
+        }
+        for (int i = 0; i < CHUNKS; ++i)
+            if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->codes_full[i]), (armed_parity >> i) & 1u, wait);
     } else {
         // ------------------------------------------------------ decoding
         // Group i takes stages i, i + GROUPS, .. of the block's; all groups
