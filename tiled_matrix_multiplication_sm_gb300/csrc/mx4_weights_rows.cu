@@ -45,24 +45,43 @@ __device__ __forceinline__ uint4 load_x(const __nv_bfloat16* x, int left) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One 128-column unit of a lane: codes of its 2 RW rows and their scales.
+// One 128-column unit of a lane: codes of its 2 RW rows and the words that
+// hold their scales. A lane copies what it will use itself (cp.async) into
+// slots of its own, DEPTH units ahead, so the copies need no registers and no
+// barrier.
+constexpr int DEPTH = 2;
 template <int RW>
 struct Unit {
     uint4 codes[2 * RW];
-    uint32_t scales[2 * RW];        // one byte (MXFP4) or two (NVFP4)
+    uint32_t scales[2 * RW];
+};
+template <int RW>
+struct Slots {
+    uint4 codes[WARPS][DEPTH][2 * RW][32];
+    uint32_t scales[WARPS][DEPTH][2 * RW][32];
 };
 
-// Blocks meant to be resident on an SM: with 64 and 128 registers a thread.
-__host__ __device__ constexpr int blocks_per_sm(int nt) { return nt == 1 ? 4 : 2; }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(d), "l"(src) : "memory");
+}
 
-template <int FMT, int NT, int RW, typename TC>
-__global__ void __launch_bounds__(THREADS, blocks_per_sm(NT))
+// BLOCKS: how many blocks are resident on an SM, 2 (up to 128 registers a
+// thread) or 3 (80).
+template <int FMT, int NT, int RW, int BLOCKS, typename TC>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
 weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool vec, Mx4Operand W,
                     Mx4Out out, int split) {
     constexpr int TN = 16 * RW, TM = 8 * NT;
     __shared__ uint32_t factors[256];
-    __shared__ float part[WARPS][TN][TM + 1];
+    extern __shared__ __align__(16) uint8_t slots_raw[];
+    Slots<RW>& slots = *reinterpret_cast<Slots<RW>*>(slots_raw);
+    // The sums, once every warp is done with its slots.
+    float (&part)[WARPS][TN][TM + 1] = *reinterpret_cast<float (*)[WARPS][TN][TM + 1]>(slots_raw);
     __shared__ float total[TN * TM];
+    static_assert(sizeof(part) <= sizeof(Slots<RW>), "sums in place of the slots");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
     const long n0 = (long)(blockIdx.x / split) * TN;
@@ -84,21 +103,33 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         code_at[i] = r * pitch;
         const uint32_t in = (uint32_t)(n0 % 32) + r;               // the block's rows lie in one tile
         scale_at[i] = (in / 32 * 4 + in % 32 * 16) - (uint32_t)(n0 % 32 * 16) +
-                      (FMT == TGEMM_MXFP4 ? t : (t >> 1) * MX4_TILE_BYTES + (t & 1) * 2);
+                      (FMT == TGEMM_MXFP4 ? 0 : (t >> 1) * MX4_TILE_BYTES);
     }
     const __nv_bfloat16* x_row[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) x_row[i] = X + (long)min(i * 8 + g, M - 1) * ldx + t * 32;
 
     using U = Unit<RW>;
-    auto load = [&](U& u, int unit) {
-        // Past the row's end any codes do: X is 0 there.
-        const uint32_t at = min((uint32_t)unit * 64 + t * 16, pitch - 16);
+    // A unit's copies, one group; past the last unit an empty one.
+    auto fetch = [&](int unit, int slot) {
+        if (unit < units) {
+            // Past the row's end any codes do: X is 0 there.
+            const uint32_t at = min((uint32_t)unit * 64 + t * 16, pitch - 16);
+            const uint32_t sc = (uint32_t)unit * (FMT == TGEMM_MXFP4 ? MX4_TILE_BYTES : 2 * MX4_TILE_BYTES);
+#pragma unroll
+            for (int i = 0; i < 2 * RW; ++i) {
+                copy_async<16>(&slots.codes[warp][slot][i][lane], code_base + (code_at[i] + at));
+                copy_async<4>(&slots.scales[warp][slot][i][lane], scale_base + (scale_at[i] + sc));
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](U& u, int slot) {
 #pragma unroll
         for (int i = 0; i < 2 * RW; ++i) {
-            u.codes[i] = __ldg(reinterpret_cast<const uint4*>(code_base + (code_at[i] + at)));
-            if (FMT == TGEMM_MXFP4) u.scales[i] = __ldg(scale_base + (scale_at[i] + (uint32_t)unit * MX4_TILE_BYTES));
-            else u.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scale_base + (scale_at[i] + (uint32_t)unit * (2 * MX4_TILE_BYTES))));
+            u.codes[i] = slots.codes[warp][slot][i][lane];
+            const uint32_t w = slots.scales[warp][slot][i][lane];
+            u.scales[i] = FMT == TGEMM_MXFP4 ? w >> t * 8 & 0xFF : w >> (t & 1) * 16 & 0xFFFF;
         }
     };
 
@@ -164,7 +195,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
                 f[i][0] = f[i][1] = !w ? f[i][0] : c == 255 ? 0x7FC07FC0u : c == 0 ? 0x00400040u : c * 0x00800080u;
             }
         }
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 xs[NT];
 #pragma unroll
@@ -174,18 +205,21 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         }
     };
 
-    // The next unit's codes are on their way while one is multiplied.
     const int step = WARPS * split;
-    int unit = rank * WARPS + warp;
-    U now, next;
-    if (unit < units) load(now, unit);
+    int unit = rank * WARPS + warp, slot = 0;
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) fetch(unit + i * step, i);
 #pragma unroll 1
-    while (unit < units) {
-        if (unit + step < units) load(next, unit + step);
-        run(now, unit);
-        unit += step;
-        now = next;
+    for (; unit < units; unit += step) {
+        asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory");
+        U u;
+        take(u, slot);
+        fetch(unit + DEPTH * step, slot);            // the lane's own slot, read just before
+        run(u, unit);
+        if (++slot == DEPTH) slot = 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
 
 #pragma unroll
     for (int r = 0; r < RW; ++r)
@@ -226,27 +260,14 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int FMT, int NT, int RW, typename TC>
+template <int FMT, int NT, int RW, int BLOCKS, typename TC>
 cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
-                   int num_sms, cudaStream_t s) {
+                   int split, cudaStream_t s) {
     const long tiles = ((long)N + 16 * RW - 1) / (16 * RW);
-    // The blocks of a cluster split K. Time goes by the rounds of resident
-    // blocks and what a warp does in each: its units and about three units'
-    // worth of start and end.
-    const int units = (K + UNIT_K - 1) / UNIT_K;
-    const long slots = (long)blocks_per_sm(NT) * num_sms;
-    int split = 1;
-    long best = 0;
-    for (int c = 1; c <= 8; ++c) {
-        const long cost = (tiles * c + slots - 1) / slots * ((units + WARPS * c - 1) / (WARPS * c) + 3);
-        if (c == 1 || cost < best) {
-            best = cost;
-            split = c;
-        }
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split));
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = sizeof(Slots<RW>);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -257,15 +278,49 @@ cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
+    const cudaError_t e = set_smem_limit_once<weights_rows_kernel<FMT, NT, RW, BLOCKS, TC>>(sizeof(Slots<RW>));
+    if (e != cudaSuccess) return e;
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
-    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, RW, TC>, M, N, K, X, ldx, vec, W, out, split);
+    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, RW, BLOCKS, TC>, M, N, K, X, ldx, vec, W, out, split);
+}
+
+// Resident blocks (2 or 3) and the blocks of a cluster that split K. The
+// kernel is bound by instruction issue, so a round of resident blocks takes as
+// long as there are blocks on an SM, times a warp's units and about three
+// units' worth of start and end. Two against three: 16 x 4096 x 14336 NVFP4
+// 16.6 us (clusters of 2) and 19.4 (of 3), 16 x 14336 x 4096 19.2 and 15.6.
+struct Choice {
+    int blocks, split;
+};
+Choice choose(long tiles, int K, int num_sms) {
+    const int units = (K + UNIT_K - 1) / UNIT_K;
+    Choice best{2, 1};
+    long least = -1;
+    for (int blocks = 2; blocks <= 3; ++blocks)
+        for (int c = 1; c <= 8; ++c) {
+            const long slots = (long)blocks * num_sms;
+            const long cost = (tiles * c + slots - 1) / slots * ((units + WARPS * c - 1) / (WARPS * c) + 3) * blocks;
+            if (least < 0 || cost < least) {
+                least = cost;
+                best = {blocks, c};
+            }
+        }
+    return best;
+}
+
+template <int FMT, int NT, typename TC>
+cudaError_t launch_blocks(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W,
+                          const Mx4Out& out, int num_sms, cudaStream_t s) {
+    const Choice c = choose(((long)N + 31) / 32, K, num_sms);
+    return c.blocks == 2 ? launch<FMT, NT, 2, 2, TC>(M, N, K, X, ldx, W, out, c.split, s)
+                         : launch<FMT, NT, 2, 3, TC>(M, N, K, X, ldx, W, out, c.split, s);
 }
 
 template <int FMT, typename TC>
 cudaError_t launch_rows(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W,
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
-    return M <= 8 ? launch<FMT, 1, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s)
-                  : launch<FMT, 2, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
+    return M <= 8 ? launch_blocks<FMT, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s)
+                  : launch_blocks<FMT, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
 }
 
 }  // namespace
