@@ -24,7 +24,7 @@ OPS = ["mx4", "w4"]
 F32_REL = 1e-5
 SIZES = [(1, 1, 1), (1, 1, 16), (1, 8, 31), (2, 3, 33), (3, 17, 32), (16, 128, 64), (17, 129, 96), (127, 255, 100),
          (128, 256, 256), (129, 257, 257), (130, 64, 513), (256, 512, 300), (300, 520, 1537), (1, 4096, 1024),
-         (8, 1000, 2048), (33, 97, 1600), (64, 320, 1999), (65, 40, 1024), (260, 1030, 768), (2100, 2600, 300)]
+         (8, 1000, 2048), (9, 33, 1027), (24, 200, 700), (25, 130, 640), (33, 97, 1600), (64, 320, 1999), (65, 40, 1024), (260, 1030, 768), (2100, 2600, 300)]
 
 
 class Operand:

@@ -107,8 +107,9 @@ cudaError_t mx4_read_and_clear_status(int* status, cudaStream_t s);
 cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                         const Mx4Out& out, int num_sms, cudaStream_t s);
 
-// At most MX4_FEW_ROWS rows of A (mx4_weights_rows.cu).
-constexpr int MX4_FEW_ROWS = 16;
+// At most MX4_FEW_ROWS rows of A (mx4_weights_rows.cu). 24 x 14336 x 4096 NVFP4
+// takes 24 us there and 27 in mx4_weights.cu; 32 rows 29 and 27.
+constexpr int MX4_FEW_ROWS = 24;
 cudaError_t mx4_weights_rows(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                              const Mx4Out& out, int num_sms, cudaStream_t s);
 

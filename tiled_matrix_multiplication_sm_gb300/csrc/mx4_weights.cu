@@ -1,6 +1,6 @@
 // BF16 rows times a kept 4-bit matrix, C = alpha A W^T + beta C + bias, on the
 // tensor cores (tcgen05, kind f16): W is made BF16 on its way through shared
-// memory. (At most 16 rows go to mx4_weights_rows.cu.)
+// memory. (Up to MX4_FEW_ROWS rows go to mx4_weights_rows.cu.)
 //
 // The form is that of gemm_mx4's kernel -- 256 x 256 tiles on SM pairs or
 // 128 x 128 on one SM, persistent, two accumulators in tensor memory -- with

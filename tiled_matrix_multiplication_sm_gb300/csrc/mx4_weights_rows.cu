@@ -1,5 +1,5 @@
 // Few BF16 rows times a kept 4-bit matrix, C = alpha X W^T + beta C + bias
-// with at most 16 rows of X: bound by reading W once.
+// with at most MX4_FEW_ROWS rows of X: bound by reading W once.
 //
 // A warp multiplies 16 RW rows of W (the 16-row side of mma.sync m16n8k16)
 // with 8 NT rows of X. A lane takes 16 bytes of codes of two rows -- 32
@@ -292,11 +292,11 @@ cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const 
 struct Choice {
     int blocks, split;
 };
-Choice choose(long tiles, int K, int num_sms) {
+Choice choose(long tiles, int K, int num_sms, int most = 3) {
     const int units = (K + UNIT_K - 1) / UNIT_K;
     Choice best{2, 1};
     long least = -1;
-    for (int blocks = 2; blocks <= 3; ++blocks)
+    for (int blocks = 2; blocks <= most; ++blocks)
         for (int c = 1; c <= 8; ++c) {
             const long slots = (long)blocks * num_sms;
             const long cost = (tiles * c + slots - 1) / slots * ((units + WARPS * c - 1) / (WARPS * c) + 3) * blocks;
@@ -319,8 +319,9 @@ cudaError_t launch_blocks(int M, int N, int K, const __nv_bfloat16* X, long ldx,
 template <int FMT, typename TC>
 cudaError_t launch_rows(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W,
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
-    return M <= 8 ? launch_blocks<FMT, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s)
-                  : launch_blocks<FMT, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
+    if (M <= 8) return launch_blocks<FMT, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s);
+    if (M <= 16) return launch_blocks<FMT, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
+    return launch<FMT, 3, 2, 2, TC>(M, N, K, X, ldx, W, out, choose(((long)N + 31) / 32, K, num_sms, 2).split, s);
 }
 
 }  // namespace
