@@ -41,6 +41,7 @@ constexpr int STAGE_K = MX4_SPAN;
 constexpr int OPERAND_BYTES = 128 * SW;       // 128 rows of codes
 constexpr int STAGES = 5;
 constexpr int THREADS = 192;
+constexpr int EPI_BYTES = EPI_WARPS * 2 * BUF_BYTES;
 
 template <int FMT, bool PAIR>
 struct Shape {
@@ -255,7 +256,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<S::TN, S::FREE_FIRST, true, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
+            drain_tile<S::TN, S::FREE_FIRST, true, 2, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
                               mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
         }
         tma_store_wait_all();

@@ -12,7 +12,6 @@ using namespace mx4_ptx;
 constexpr int SW = 128;                       // bytes of a staged row (128-byte swizzle)
 constexpr int EPI_WARPS = 4;
 constexpr int BUF_BYTES = 32 * 128;           // 32 rows x 128 bytes of C
-constexpr int EPI_BYTES = EPI_WARPS * 2 * BUF_BYTES;
 constexpr int TMEM_COLS = 512;
 
 // A product's output in tiles, walked by `units` blocks or pairs of blocks.
@@ -44,7 +43,7 @@ __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r
 // release() is called as soon as FREE_FIRST columns have left tensor memory;
 // BOTH: a turn's columns are in registers before any is stored (an earlier
 // release for 32 registers more).
-template <int TN, int FREE_FIRST, bool BOTH, typename TC, typename Release>
+template <int TN, int FREE_FIRST, bool BOTH, int BUFS, typename TC, typename Release>
 __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* tmC, uint32_t tmem,
                                            uint8_t* bufs, int row0, int col0, bool last_first,
                                            float ga, float gb, Release release) {
@@ -77,11 +76,11 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ga * gb * o.alpha);
             if (p.tma_c) {
                 // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16:
-                // one of 64 -- through two buffers in turn: the box before
-                // the last has to have left its buffer.
-                uint8_t* buf = bufs + ((sizeof(TC) == 4 ? h : i) & 1) * BUF_BYTES;
+                // one of 64 -- through BUFS buffers in turn: the last box in
+                // this one has to have left it.
+                uint8_t* buf = bufs + (sizeof(TC) == 4 ? h : i) % BUFS * BUF_BYTES;
                 if (sizeof(TC) == 4 || h == 0) {
-                    if (lane == 0) tma_store_wait_read<1>();
+                    if (lane == 0) tma_store_wait_read<BUFS - 1>();
                     __syncwarp();
                 }
                 if (o.bias != nullptr)

@@ -26,23 +26,27 @@ using namespace mx4_decode;
 
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
-// Chunks of codes in flight. Pair tiles read each from L2; few tiles read W
-// from memory once and want bytes in flight.
-template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 3 : 5;
+// Codes come in chunks. Pair tiles read each from L2 and take chunks of as
+// many stages as there are groups of decoding warps, so that a group meets
+// each chunk once; few tiles read W from memory once and take smaller ones.
+template <bool PAIR> constexpr int CHUNK_K_OF = PAIR ? 256 : 128;
+template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 2 : 6;
+constexpr int EPI_BYTES = EPI_WARPS * BUF_BYTES;
 constexpr int PAIR_STAGES = 5;
-constexpr int MAX_STAGES = 8, MAX_CHUNKS = 5;
+constexpr int MAX_STAGES = 8, MAX_CHUNKS = 6;
 constexpr int DECODE_WARPS = 8;
 constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
 constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
 constexpr int CODES_WARP = 2 + EPI_WARPS + DECODE_WARPS;
 constexpr int THREADS = 32 * (CODES_WARP + 1);
-constexpr int CHUNK_K = 128;
-constexpr int PER_CHUNK = CHUNK_K / STAGE_K;
 
-template <int FMT>
+template <int FMT, bool PAIR>
 struct Chunk {
-    static constexpr int SF_TILES = CHUNK_K / mx4_block(FMT) / 4;
-    static constexpr int CODES = 128 * CHUNK_K / 2;  // 64-byte rows
+    static constexpr int K = CHUNK_K_OF<PAIR>;
+    static constexpr int STAGES = K / STAGE_K;
+    static constexpr int ROW = K / 2;                // bytes of a row of codes
+    static constexpr int SF_TILES = K / mx4_block(FMT) / 4;
+    static constexpr int CODES = 128 * ROW;
     static constexpr int BYTES = CODES + SF_TILES * MX4_TILE_BYTES;
 };
 
@@ -61,7 +65,7 @@ static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
 // Shared memory beside the stages.
 template <int FMT, bool PAIR>
 constexpr int fixed_bytes() {
-    return 1024 + CHUNKS_OF<PAIR> * Chunk<FMT>::BYTES + EPI_BYTES + SYNC_BYTES;
+    return 1024 + CHUNKS_OF<PAIR> * Chunk<FMT, PAIR>::BYTES + EPI_BYTES + SYNC_BYTES;
 }
 constexpr int SMEM_LIMIT = 227 * 1024;
 static_assert(fixed_bytes<TGEMM_NVFP4, true>() + PAIR_STAGES * 2 * OPERAND_BYTES <= SMEM_LIMIT, "shared memory");
@@ -92,9 +96,11 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
                      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Where 16-byte piece j of row r lies in a chunk of codes (64-byte swizzle).
-__device__ __forceinline__ uint32_t swizzled64(int r, int j) {
-    return (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+// Where 16-byte piece j of row r lies in a chunk of codes, of 128-byte rows or
+// of 64-byte rows in the 64-byte swizzle.
+template <int ROW>
+__device__ __forceinline__ uint32_t codes_at(int r, int j) {
+    return ROW == 128 ? swizzled(r, j) : (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
 }
 
 // 32 codes of a row (16 bytes) to BF16, in order.
@@ -125,7 +131,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr int TM = PAIR ? 256 : 128, TN = TM, CHUNKS = CHUNKS_OF<PAIR>;
     const int STAGES = PAIR ? PAIR_STAGES : p.stages;
     const int A_BYTES = PAIR ? OPERAND_BYTES : p.a_rows * SW, STAGE_BYTES = A_BYTES + OPERAND_BYTES;
-    using CH = Chunk<FMT>;
+    using CH = Chunk<FMT, PAIR>;
+    constexpr int PER_CHUNK = CH::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* codes = smem + STAGES * STAGE_BYTES;
@@ -259,7 +266,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
-        uint8_t* bufs = epi + (warp - 2) * 2 * BUF_BYTES;
+        uint8_t* bufs = epi + (warp - 2) * BUF_BYTES;
         const float gb = mx4_g(p.gb);
         int it = 0;
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
@@ -281,7 +288,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<TN, TN, false, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
+            drain_tile<TN, TN, false, 1, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
                                    mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
         }
         tma_store_wait_all();
@@ -302,7 +309,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (elect_one()) {
                     const uint32_t bar = smem_u32(&sy->codes_full[c]);
                     mbar_arrive_expect_tx(bar, CH::BYTES);
-                    tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, ch * (CHUNK_K / 2), col, bar);
+                    tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, ch * CH::ROW, col, bar);
                     tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0, ch * CH::SF_TILES,
                                        col / 128, bar);
                 }
@@ -340,10 +347,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < ITEMS; ++i) {
                         const int item = i * 32 * GROUP_WARPS + tid, row = item & 127, half = item >> 7;
-                        w[i] = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + swizzled64(row, q * 2 + half));
+                        w[i] = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + codes_at<CH::ROW>(row, q * 2 + half));
                         const uint8_t* sc = scales + c * (CH::BYTES - CH::CODES) + (row & 31) * 16 + (row >> 5) * 4;
                         if (FMT == TGEMM_MXFP4) {
-                            b0[i] = b1[i] = sc[q * 2 + half];
+                            b0[i] = b1[i] = sc[(q >> 1) * MX4_TILE_BYTES + (q & 1) * 2 + half];
                             is_wide |= wide(b0[i]);
                         } else {
                             const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + q * MX4_TILE_BYTES + half * 2);
@@ -411,7 +418,8 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     const int a_rows = PAIR || M > 96 ? 128 : (M + 31) / 32 * 32;
     const cuuint32_t box[2] = {STAGE_K, (cuuint32_t)a_rows};
     if (!encode(enc, &tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_codes(enc, &tmB, B, N, K, CHUNK_K / 2) || !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT>::SF_TILES, 1))
+        !encode_codes(enc, &tmB, B, N, K, Chunk<FMT, PAIR>::ROW) ||
+        !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT, PAIR>::SF_TILES, 1))
         return cudaErrorInvalidValue;
     memset(&tmC, 0, sizeof(tmC));
     Params p;
@@ -424,7 +432,7 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     const int smem = fixed_bytes<FMT, PAIR>() + p.stages * slot;
     if (!PAIR && p.num_tiles * 2 <= num_sms) {
-        p.split = split_for(p.num_tiles, p.kblocks / PER_CHUNK, num_sms);
+        p.split = split_for(p.num_tiles, p.kblocks / Chunk<FMT, PAIR>::STAGES, num_sms);
         p.units = p.num_tiles;
     }
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
