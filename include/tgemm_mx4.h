@@ -32,7 +32,9 @@
  *           covers whole spans of 256 columns; gemm_mx4_scales_bytes gives
  *           the size. Bytes of rows and blocks outside the matrix are zero.
  * Both buffers start on 16-byte boundaries (TGEMM_ERR_ALIGNMENT otherwise).
- * gemm_mx4_pack makes this layout from row-major codes and scales.
+ * gemm_mx4_pack makes this layout from row-major codes and scales. Rows,
+ * columns, M, N and K are at most TGEMM_MX4_MAX_DIM
+ * (TGEMM_ERR_INVALID_ARG beyond).
  *
  * Quantising a block whose largest magnitude is m:
  *   TGEMM_MXFP4: scale = 2^clamp(floor(log2 m) - 2, -127, 127)
@@ -50,6 +52,9 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Largest number of rows or columns: tiles' ends stay in an int. */
+#define TGEMM_MX4_MAX_DIM 2147482624
 
 /* Formats of a 4-bit matrix. */
 #define TGEMM_MXFP4 1
@@ -154,6 +159,11 @@ TGEMM_API int gemm_mx4(int M, int N, int K,
  * with weights in 4. Each weight's code x scale is a BF16 number exactly;
  * products are summed in FP32 and
  *     v = acc * gb * alpha, then beta and bias as in gemm_mx4.
+ * With TGEMM_NVFP4 the sums are held times 2^-16, so that terms below 2^-110
+ * may lose bits. With more than 24 rows an A whose rows do not start on
+ * 16-byte boundaries is copied first, to 2 M round_up(K, 64) bytes of
+ * stream-ordered scratch from the library's pool (see tgemm.h).
+ *
  * Errors as gemm_mx4, and TGEMM_ERR_INVALID_ARG for lda < K or A off 2 bytes.
  */
 TGEMM_API int gemm_w4(int M, int N, int K, const void* A, long lda,

@@ -229,6 +229,24 @@ def test_on_another_stream_and_in_a_graph(tgemm, op, M):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("M", [20, 300])
+def test_rows_off_16_bytes_in_a_graph(tgemm, M):
+    """With many rows such an A is copied to scratch first."""
+    N, K = 500, 321
+    X, x = activations(M, K, "whole", 3, ld=K + 2)
+    B = Operand(tgemm, N, K, "nvfp4", "whole", 4)
+    want = torch.from_numpy(x @ B.v.T).float().cuda()
+    assert torch.equal(tgemm.gemm_w4(X, B.q), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tgemm.gemm_w4(X, B.q)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("M", [5, 40, 2100])
 @pytest.mark.parametrize("op", OPS)
 def test_the_first_cuda_call_of_a_thread(tgemm, op, M):
@@ -271,6 +289,7 @@ def test_binding_refusals(tgemm):
     odd, nv = Operand(tgemm, 5, 63, "mxfp4", "whole", 1).q, Operand(tgemm, 5, 64, "nvfp4", "whole", 1).q
     for bad in (lambda: tgemm.gemm_mx4(A, odd), lambda: tgemm.gemm_mx4(A, nv), lambda: tgemm.gemm_w4(X, odd),
                 lambda: tgemm.gemm_mx4(A, B, beta=1.0), lambda: tgemm.gemm_w4(X.t(), B),
+                lambda: tgemm.gemm_w4(X[:1].expand(4, 64), B),
                 lambda: tgemm.gemm_mx4(A, B, out=torch.empty(5, 4, device="cuda")),
                 lambda: tgemm.gemm_mx4(A, B, bias=torch.zeros(4, device="cuda")),
                 lambda: tgemm.gemm_w4(X, B, bias=torch.zeros(5))):

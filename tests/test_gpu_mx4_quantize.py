@@ -259,7 +259,9 @@ def test_refusals(tgemm):
     X = torch.zeros(4, 64, device="cuda")
     g = torch.ones(1, device="cuda")
     for bad in (lambda: tgemm.mx4_quantize(X, "mxfp4", tensor_scale=g), lambda: tgemm.mx4_quantize(X.t()),
-                lambda: tgemm.mx4_quantize(X[0]),
+                lambda: tgemm.mx4_quantize(X[0]), lambda: tgemm.mx4_quantize(X[:1].expand(4, 64)),
+                lambda: tgemm.mx4_quantize(X.view(-1).as_strided((4, 64), (32, 1))),
+                lambda: tgemm.mx4_dequantize(tgemm.mx4_quantize(X), out=torch.empty(1, 64, device="cuda").expand(4, 64)),
                 lambda: tgemm.mx4_dequantize(tgemm.mx4_quantize(X), out=torch.empty(4, 63, device="cuda")),
                 lambda: tgemm.mx4_pack(torch.zeros(4, 3, dtype=torch.uint8, device="cuda"),
                                        torch.zeros(4, 1, dtype=torch.uint8, device="cuda"), cols=7),

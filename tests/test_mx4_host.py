@@ -33,6 +33,26 @@ def test_header_and_binding_declare_the_same_symbols(lib):
         assert hasattr(lib, name)
 
 
+MOST = 2147482624
+
+
+@pytest.mark.parametrize("where", ["rows", "cols"])
+def test_sizes_past_the_largest_are_refused(lib, where):
+    r, c = (MOST + 1, 1) if where == "rows" else (1, MOST + 1)
+    ld = max(c, 64)
+    assert lib.gemm_mx4_codes_pitch(MOST + 1) == -INVALID
+    assert lib.gemm_mx4_codes_pitch(MOST) == MOST // 2
+    assert lib.gemm_mx4_scales_bytes(r, c, MX) == -INVALID
+    assert lib.gemm_mx4_tensor_scale(r, c, FAKE, ld, F32, FAKE, 0) == INVALID
+    assert lib.gemm_mx4_quantize(r, c, FAKE, ld, F32, MX, 0, 0, FAKE, FAKE, 0, 0, 0) == INVALID
+    assert lib.gemm_mx4_dequantize(r, c, FAKE, FAKE, MX, 0, FAKE, ld, F32, 0) == INVALID
+    assert lib.gemm_mx4_pack(r, c, MX, FAKE, ld, FAKE, ld, FAKE, FAKE, 0) == INVALID
+    for M, N, K in ((MOST + 1, 1, 1), (1, MOST + 1, 1), (1, 1, MOST + 1)):
+        out = (MX, FAKE, 2 ** 31, F32, 1.0, 0.0, 0, 0)
+        assert lib.gemm_mx4(M, N, K, FAKE, FAKE, 0, FAKE, FAKE, 0, *out) == INVALID
+        assert lib.gemm_w4(M, N, K, FAKE, 2 ** 31, FAKE, FAKE, 0, *out) == INVALID
+
+
 @pytest.mark.parametrize("cols,pitch", [(0, 0), (1, 16), (32, 16), (33, 32), (4096, 2048), (-1, -INVALID)])
 def test_codes_pitch(lib, cols, pitch):
     assert lib.gemm_mx4_codes_pitch(cols) == pitch

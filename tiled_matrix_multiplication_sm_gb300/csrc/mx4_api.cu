@@ -13,6 +13,7 @@ using tgemm::Mx4Out;
 bool valid_fmt(int fmt) { return fmt == TGEMM_MXFP4 || fmt == TGEMM_NVFP4; }
 bool valid_type(int t) { return t == TGEMM_TYPE_F32 || t == TGEMM_TYPE_BF16; }
 bool off(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+bool valid_dim(int n) { return n >= 0 && n <= TGEMM_MX4_MAX_DIM; }
 size_t type_bytes(int t) { return t == TGEMM_TYPE_F32 ? 4 : 2; }
 
 // A matrix of `type` elements that is not empty.
@@ -37,7 +38,7 @@ int done(cudaError_t e) { return e == cudaSuccess ? TGEMM_OK : TGEMM_ERR_CUDA; }
 // an error, or -1 for an empty output.
 int check_product(int M, int N, int K, const float* ga, const Mx4Operand& B, int fmt,
                   const Mx4Out& o) {
-    if (M < 0 || N < 0 || K < 0 || !valid_fmt(fmt) || !valid_type(o.c_type) || o.ldc < N)
+    if (!valid_dim(M) || !valid_dim(N) || !valid_dim(K) || !valid_fmt(fmt) || !valid_type(o.c_type) || o.ldc < N)
         return TGEMM_ERR_INVALID_ARG;
     if (check_g(ga, fmt) != TGEMM_OK || check_g(B.g, fmt) != TGEMM_OK || off(o.bias, 4))
         return TGEMM_ERR_INVALID_ARG;
@@ -56,17 +57,17 @@ Mx4Operand operand(const void* codes, const void* scales, const float* g) {
 extern "C" {
 
 long long gemm_mx4_codes_pitch(int cols) {
-    return cols < 0 ? -TGEMM_ERR_INVALID_ARG : tgemm::mx4_pitch(cols);
+    return !valid_dim(cols) ? -TGEMM_ERR_INVALID_ARG : tgemm::mx4_pitch(cols);
 }
 
 long long gemm_mx4_scales_bytes(int rows, int cols, int fmt) {
-    if (rows < 0 || cols < 0 || !valid_fmt(fmt)) return -TGEMM_ERR_INVALID_ARG;
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_fmt(fmt)) return -TGEMM_ERR_INVALID_ARG;
     return (long long)tgemm::mx4_scale_bytes(rows, cols, fmt);
 }
 
 int gemm_mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_type, float* g,
                           cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || !valid_type(x_type) || g == nullptr || off(g, 4) || ldx < cols)
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_type(x_type) || g == nullptr || off(g, 4) || ldx < cols)
         return TGEMM_ERR_INVALID_ARG;
     if (rows > 0 && cols > 0 && check_matrix(X, ldx, cols, x_type) != TGEMM_OK)
         return TGEMM_ERR_INVALID_ARG;
@@ -79,7 +80,7 @@ int gemm_mx4_tensor_scale(int rows, int cols, const void* X, long ldx, int x_typ
 int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, int fmt,
                       float* g, int flags, void* codes, void* scales, void* codes_t, void* scales_t,
                       cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || !valid_type(x_type) || !valid_fmt(fmt) || ldx < cols)
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_type(x_type) || !valid_fmt(fmt) || ldx < cols)
         return TGEMM_ERR_INVALID_ARG;
     if (check_g(g, fmt) != TGEMM_OK || (flags & ~TGEMM_MX4_SET_G) != 0 || (flags != 0 && g == nullptr))
         return TGEMM_ERR_INVALID_ARG;
@@ -102,7 +103,7 @@ int gemm_mx4_quantize(int rows, int cols, const void* X, long ldx, int x_type, i
 
 int gemm_mx4_dequantize(int rows, int cols, const void* codes, const void* scales, int fmt,
                         const float* g, void* X, long ldx, int x_type, cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || !valid_type(x_type) || !valid_fmt(fmt) || ldx < cols)
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_type(x_type) || !valid_fmt(fmt) || ldx < cols)
         return TGEMM_ERR_INVALID_ARG;
     if (check_g(g, fmt) != TGEMM_OK) return TGEMM_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return TGEMM_OK;
@@ -119,7 +120,7 @@ int gemm_mx4_dequantize(int rows, int cols, const void* codes, const void* scale
 int gemm_mx4_pack(int rows, int cols, int fmt, const void* src_codes, long src_ldc,
                   const void* src_scales, long src_lds, void* codes, void* scales,
                   cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || !valid_fmt(fmt)) return TGEMM_ERR_INVALID_ARG;
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_fmt(fmt)) return TGEMM_ERR_INVALID_ARG;
     const int block = tgemm::mx4_block(fmt);
     if (src_ldc < ((long)cols + 1) / 2 || src_lds < ((long)cols + block - 1) / block)
         return TGEMM_ERR_INVALID_ARG;

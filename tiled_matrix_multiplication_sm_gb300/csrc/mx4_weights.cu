@@ -463,7 +463,8 @@ cudaError_t run(int M, int N, int K, const void* A, long lda, const Mx4Operand& 
 cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
     if (K == 0) return mx4_empty_sum(M, N, out, s);
-    if (M <= MX4_FEW_ROWS) return mx4_weights_rows(M, N, K, A, lda, B, fmt, out, num_sms, s);
+    // (Its offsets within 32 rows of codes are 32-bit.)
+    if (M <= MX4_FEW_ROWS && K < 1 << 27) return mx4_weights_rows(M, N, K, A, lda, B, fmt, out, num_sms, s);
     if (reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 8 == 0)
         return run(M, N, K, A, lda, B, fmt, out, num_sms, s);
     // TMA copies rows that start on 16-byte boundaries: others are repacked.

@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import binding
-from .binding import TGEMM_OK, TgemmError, _check_matrix, _stream_handle
+from .binding import TGEMM_OK, TgemmError, _stream_handle
 
 TGEMM_MXFP4 = 1
 TGEMM_NVFP4 = 2
@@ -165,6 +165,15 @@ def _check_mx4(m, name: str) -> None:
         raise TypeError(f"{name} must be an Mx4Matrix, got {type(m).__name__}")
 
 
+def _check_matrix(x: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+    """The leading dimension of a row-major matrix whose rows do not overlap
+    (an expanded one's do)."""
+    ld = binding._check_matrix(x, name, dtype)
+    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name}'s rows overlap: stride {x.stride(0)} for {x.shape[1]} columns")
+    return ld
+
+
 def _check_values(X: torch.Tensor, name: str) -> Tuple[int, int]:
     """(leading dimension, TGEMM_TYPE_*) of a float32 or bfloat16 matrix."""
     if not isinstance(X, torch.Tensor):
@@ -226,6 +235,8 @@ def mx4_dequantize(Q: Mx4Matrix, dtype: torch.dtype = torch.float32,
         out = _empty(stream, Q.rows, Q.cols, dtype=dtype, device=Q.device)
     elif tuple(out.shape) != Q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {Q.shape}")
+    elif out.device != Q.device:
+        raise ValueError(f"out is on {out.device}, the matrix on {Q.device}")
     ldx, kind = _check_values(out, "out")
     _call("gemm_mx4_dequantize", Q.device, stream, Q.rows, Q.cols, Q._codes, Q._scales, _FORMATS[Q.fmt], Q._g,
           out.data_ptr(), ldx, kind)
