@@ -10,8 +10,8 @@
 // memory, copied from shared memory by the thread that issues the MMAs
 // (tcgen05.cp; it runs in order with them).
 //
-// Two forms, both persistent, one block on an SM, six warps (0: TMA, 1: MMA,
-// 2-5: epilogue):
+// Two forms, both persistent, one block on an SM, six or ten warps (0: TMA,
+// 1: MMA, from 2 on: epilogue):
 //   pair    256 x 256 tiles on an SM pair (cta_group::2). Each block stages
 //           its 128 rows of A, its 128 rows of B, A's scales for its rows
 //           and B's for all 256. Two accumulators of 256 columns and 48
@@ -40,13 +40,18 @@ using namespace mx4_tile;
 constexpr int STAGE_K = MX4_SPAN;
 constexpr int OPERAND_BYTES = 128 * SW;       // 128 rows of codes
 constexpr int STAGES = 5;
-constexpr int THREADS = 192;
-constexpr int EPI_BYTES = EPI_WARPS * 2 * BUF_BYTES;
+constexpr int EPI_BYTES = 8 * BUF_BYTES;
 
 template <int FMT, bool PAIR>
 struct Shape {
     static constexpr int TM = PAIR ? 256 : 128;           // rows of a tile
     static constexpr int TN = PAIR ? 256 : 128;           // columns
+    // Epilogue: sets of four warps (one to a quarter of tensor memory's lanes)
+    // with BUFS buffers a warp. A second set shortens the only tile's way out
+    // (1024^3 MXFP4 8.5 -> 7.4 us); between tiles shared memory is the bound,
+    // and it costs (8192 x 14336 x 4096 NVFP4 155 -> 158 us).
+    static constexpr int SETS = PAIR ? 1 : 2, BUFS = 2 / SETS;
+    static constexpr int EPI_WARPS = 4 * SETS, THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int SF_TILES = STAGE_K / mx4_block(FMT) / 4;     // scale tiles of 128 rows a stage
     static constexpr int SFA_BYTES = SF_TILES * MX4_TILE_BYTES;
     static constexpr int SFB_BYTES = SFA_BYTES * (TN / 128);
@@ -56,8 +61,7 @@ struct Shape {
     static constexpr int SF_COLS = SF_TILES * 4 * (1 + TN / 128);
     static constexpr int SF = PAIR ? 464 : 256;
     static constexpr int ACC1 = PAIR ? SF - TN : 128;
-    static constexpr int FREE_FIRST = PAIR ? 64 : TN;     // columns drained before the next tile may start
-    static_assert(SF + SF_COLS <= TMEM_COLS && TN - ACC1 <= FREE_FIRST, "tensor memory");
+    static_assert(SF + SF_COLS <= TMEM_COLS && (!PAIR || TN - ACC1 <= 64), "tensor memory");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -76,7 +80,7 @@ struct Params : Tiling {
 };
 
 template <int FMT, bool PAIR, typename TC>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<FMT, PAIR>::THREADS, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmC, const Params p) {
@@ -104,7 +108,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&sy->tmem_full[a]), 1);
-            mbar_init(smem_u32(&sy->tmem_empty[a]), (PAIR ? 2 : 1) * EPI_WARPS);
+            mbar_init(smem_u32(&sy->tmem_empty[a]), (PAIR ? 2 : 1) * S::EPI_WARPS);
         }
         mbar_init(smem_u32(&sy->drain), 1);
         sy->abort = 0;
@@ -234,7 +238,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
-        uint8_t* bufs = epi + (warp - 2) * 2 * BUF_BYTES;
+        const int set = (warp - 2) >> 2;
+        uint8_t* bufs = epi + (warp - 2) * S::BUFS * BUF_BYTES;
         const float ga = mx4_g(p.ga), gb = mx4_g(p.gb);
         int it = 0;
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
@@ -253,11 +258,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             };
             if (!PAIR && p.split > 1) {
                 // The tile's copies and MMAs are done: its stages hold the share.
-                store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
+                if (set == 0) store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<S::TN, S::FREE_FIRST, true, 2, TC>(p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
-                              mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), ga, gb, release);
+            // Pair: the next tile may start once the shared columns, turn 0,
+            // are out; single: once this accumulator is.
+            drain_tile<S::TN, S::SETS, true, S::BUFS, TC>(
+                p, &tmC, tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16), bufs,
+                mb * S::TM + (int)rank * 128 + q * 32, nb * S::TN, PAIR && !(it & 1), set,
+                PAIR ? 0 : S::TN / 64 - S::SETS + set, ga, gb, release);
         }
         tma_store_wait_all();
     }
@@ -307,7 +316,7 @@ cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
     if (e == cudaSuccess) e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, TC>>(S::SMEM);
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, S::SMEM, PAIR ? 2 : p.split, s);
+    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, S::THREADS, S::SMEM, PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
 }
 

@@ -10,7 +10,6 @@ namespace mx4_tile {
 using namespace mx4_ptx;
 
 constexpr int SW = 128;                       // bytes of a staged row (128-byte swizzle)
-constexpr int EPI_WARPS = 4;
 constexpr int BUF_BYTES = 32 * 128;           // 32 rows x 128 bytes of C
 constexpr int TMEM_COLS = 512;
 
@@ -38,22 +37,23 @@ __device__ __forceinline__ void tile_coords(int t, const Tiling& p, int& mb, int
 // Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
-// Drains this warp's 32 rows of a tile, 64 columns a turn. `last_first`: the
-// last 64 columns, which the next tile's accumulator shares, go first.
-// release() is called as soon as FREE_FIRST columns have left tensor memory;
-// BOTH: a turn's columns are in registers before any is stored (an earlier
-// release for 32 registers more).
-template <int TN, int FREE_FIRST, bool BOTH, int BUFS, typename TC, typename Release>
+// Drains this warp's 32 rows of a tile, 64 columns a turn; of SETS sets of
+// epilogue warps, set `set` takes every SETS-th turn. `last_first`: the last
+// 64 columns, which the next tile's accumulator shares, are turn 0. release()
+// is called as soon as turn `release_turn` has left tensor memory. BOTH: a
+// turn's columns are in registers before any is stored (an earlier release for
+// 32 registers more).
+template <int TN, int SETS, bool BOTH, int BUFS, typename TC, typename Release>
 __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* tmC, uint32_t tmem,
-                                           uint8_t* bufs, int row0, int col0, bool last_first,
-                                           float ga, float gb, Release release) {
+                                           uint8_t* bufs, int row0, int col0, bool last_first, int set,
+                                           int release_turn, float ga, float gb, Release release) {
     constexpr int W = 64, CW = 128 / (int)sizeof(TC);
-    constexpr int TURNS = TN / W, REL = FREE_FIRST / W;
+    constexpr int TURNS = TN / W;
     const int lane = threadIdx.x & 31;
     const Mx4Out& o = p.out;
     const int rows = min(32, p.M - row0);
 #pragma unroll 1
-    for (int i = 0; i < TURNS; ++i) {
+    for (int i = set; i < TURNS; i += SETS) {
         const int part = last_first ? (i == 0 ? TURNS - 1 : i - 1) : i;
         const int col = col0 + part * W;
         uint32_t held[BOTH ? 2 : 1][32];
@@ -62,7 +62,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
             tmem_ld32(tmem + (uint32_t)(part * W + 32), held[1]);
             tmem_wait_ld(held[0]);
             tmem_wait_ld(held[1]);
-            if (i == REL - 1) release();
+            if (i == release_turn) release();
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -70,7 +70,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
             if constexpr (!BOTH) {
                 tmem_ld32(tmem + (uint32_t)(part * W + h * 32), r);
                 tmem_wait_ld(r);
-                if (h == 1 && i == REL - 1) release();
+                if (h == 1 && i == release_turn) release();
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ga * gb * o.alpha);
@@ -78,7 +78,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
                 // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16:
                 // one of 64 -- through BUFS buffers in turn: the last box in
                 // this one has to have left it.
-                uint8_t* buf = bufs + (sizeof(TC) == 4 ? h : i) % BUFS * BUF_BYTES;
+                uint8_t* buf = bufs + (sizeof(TC) == 4 ? h : i / SETS) % BUFS * BUF_BYTES;
                 if (sizeof(TC) == 4 || h == 0) {
                     if (lane == 0) tma_store_wait_read<BUFS - 1>();
                     __syncwarp();

@@ -31,6 +31,7 @@ constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
 // each chunk once; few tiles read W from memory once and take smaller ones.
 template <bool PAIR> constexpr int CHUNK_K_OF = PAIR ? 256 : 128;
 template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 2 : 6;
+constexpr int EPI_WARPS = 4;
 constexpr int EPI_BYTES = EPI_WARPS * BUF_BYTES;
 constexpr int PAIR_STAGES = 5;
 constexpr int MAX_STAGES = 8, MAX_CHUNKS = 6;
@@ -288,8 +289,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
                 break;
             }
-            drain_tile<TN, TN, false, 1, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
-                                   mb * TM + (int)rank * 128 + q * 32, nb * TN, false, unscale<FMT>(), gb, release);
+            drain_tile<TN, 1, false, 1, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
+                                   mb * TM + (int)rank * 128 + q * 32, nb * TN, false, 0, TN / 64 - 1,
+                                        unscale<FMT>(), gb, release);
         }
         tma_store_wait_all();
     } else if (warp == CODES_WARP) {
