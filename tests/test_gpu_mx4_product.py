@@ -141,6 +141,18 @@ def test_a_long_sum(tgemm, op):
     assert (np.abs(got - a @ b.T) <= (F32_REL + 2.0 ** -20) * (np.abs(a) @ np.abs(b).T)).all()
 
 
+@pytest.mark.parametrize("tiles", [2, 16, 25, 30, 40, 70])      # shared by 8, 6, 5, 4, 3 and 2 blocks each on 152 SMs
+@pytest.mark.parametrize("op", OPS)
+def test_tiles_shared_by_clusters_of_each_size(tgemm, op, tiles):
+    M, N, K = 26, 128 * tiles - 5, 5300
+    A, B, a, b = operands(tgemm, op, M, N, K, FMTS[tiles % 4 // 2], "wide")
+    store, out = guarded(M, N, torch.float32, 3)
+    call(tgemm, op)(A, B, out=out)
+    err = np.abs(out.double().cpu().numpy() - a @ b.T)
+    assert (err <= F32_REL * (np.abs(a) @ np.abs(b).T)).all()
+    assert untouched(store, M, N) and tgemm.device_status() == 0
+
+
 @pytest.mark.parametrize("M", [1, 40, 200, 600])
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("op", OPS)

@@ -254,15 +254,6 @@ inline bool encode_c(EncodeTiledFn enc, CUtensorMap* map, const Mx4Out& o, int M
                   dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How many blocks of a cluster share the sum of one of few 128 x 128 tiles:
-// as many as leave a tenth of the SMs (clusters do not pack the GPU fully),
-// each with two steps of K at least.
-inline int split_for(long tiles, int steps, int num_sms) {
-    long c = num_sms * 9L / 10 / tiles;
-    if (c > steps / 2) c = steps / 2;
-    return c < 1 ? 1 : c > 8 ? 8 : (int)c;
-}
-
 inline cudaError_t make_tiling(Tiling& p, int M, int N, int tile_m, int tile_n, int slots, const Mx4Out& out) {
     p.M = M; p.N = N;
     p.tiles_m = (int)(((long)M + tile_m - 1) / tile_m);
@@ -300,6 +291,40 @@ struct ClusterLaunch {
         config.numAttrs = cluster > 1 ? 2 : 1;
     }
 };
+
+// How many clusters of c blocks the GPU holds at once, in byte c - 1 of *fits
+// (2 <= c <= 8), for a kernel of one block per SM. The SMs come in groups that
+// a cluster does not cross: 152 hold 36 clusters of 4, 23 of 6 but 15 of 8.
+template <auto KERNEL>
+cudaError_t clusters_that_fit(int threads, int smem, unsigned long long* fits) {
+    static std::atomic<unsigned long long> known[64];      // of each device; byte 0: asked
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *fits = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*fits != 0) return cudaSuccess;
+    *fits = 1;
+    for (int c = 2; c <= 8; ++c) {
+        ClusterLaunch cfg(c, threads, smem, c, nullptr);
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg.config);
+        if (e != cudaSuccess) return e;
+        *fits |= (unsigned long long)(n < 0 ? 0 : n > 255 ? 255 : n) << 8 * (c - 1);
+    }
+    if (dev < 64) known[dev].store(*fits, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// How many blocks of a cluster share the sum of one of few 128 x 128 tiles:
+// as many as fit for all tiles at once (16 tiles of gemm_w4, 64 x 2048 x 2048
+// MXFP4: 8.5 us with 6 blocks each, 15.1 with 8, which run one after another),
+// each with two steps of K at least; none if that saves a block fewer than
+// `worth` steps, what joining the shares takes.
+inline int split_for(long tiles, int steps, unsigned long long fits, int worth) {
+    int c = steps / 2 < 8 ? steps / 2 : 8;
+    while (c > 1 && (long)(fits >> 8 * (c - 1) & 255) < tiles) --c;
+    return c < 2 || steps - (steps + c - 1) / c < worth ? 1 : c;
+}
 
 // Pair tiles (256 x 256) once they occupy half of the SM pairs.
 inline bool use_pair(int M, int N, int num_sms) {

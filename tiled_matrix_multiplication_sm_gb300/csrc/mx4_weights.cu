@@ -433,12 +433,16 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     p.stages = PAIR ? PAIR_STAGES : (SMEM_LIMIT - fixed_bytes<FMT, PAIR>()) / slot;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     const int smem = fixed_bytes<FMT, PAIR>() + p.stages * slot;
-    if (!PAIR && p.num_tiles * 2 <= num_sms) {
-        p.split = split_for(p.num_tiles, p.kblocks / Chunk<FMT, PAIR>::STAGES, num_sms);
-        p.units = p.num_tiles;
-    }
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
     if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(SMEM_LIMIT);
+    if (!PAIR && p.num_tiles * 2 <= num_sms) {
+        // 3 chunks: 64 x 2048 x 512, 2 saved, 7.0 us both whole and split;
+        // x 1024 in halves, 4 saved, 10.0 and 8.5.
+        unsigned long long fits = 0;
+        if (e == cudaSuccess) e = clusters_that_fit<weights_kernel<FMT, PAIR, TC>>(THREADS, SMEM_LIMIT, &fits);
+        p.split = split_for(p.num_tiles, p.kblocks / Chunk<FMT, PAIR>::STAGES, fits, 3);
+        p.units = p.num_tiles;
+    }
     if (e != cudaSuccess) return e;
     ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, smem, PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, PAIR, TC>, tmA, tmB, tmSB, tmC, p);
