@@ -75,6 +75,7 @@ static_assert(fixed_bytes<TGEMM_NVFP4, true>() + PAIR_STAGES * 2 * OPERAND_BYTES
 // (barriers tell phases apart by parity).
 static_assert(PAIR_STAGES >= GROUPS && (SMEM_LIMIT - fixed_bytes<TGEMM_NVFP4, false>()) / (2 * OPERAND_BYTES) >= GROUPS,
               "fewer slots than groups");
+static_assert(CHUNK_K_OF<true> / STAGE_K == GROUPS && CHUNK_K_OF<false> / STAGE_K * 2 == GROUPS, "chunks and groups");
 static_assert(GROUPS * OPERAND_BYTES >= 128 * 512, "a share fits the stages");
 
 struct Params : Tiling {
@@ -161,7 +162,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         for (int c = 0; c < CHUNKS; ++c) {
             mbar_init(smem_u32(&sy->codes_full[c]), 1);
-            mbar_init(smem_u32(&sy->codes_empty[c]), DECODE_WARPS);
+            mbar_init(smem_u32(&sy->codes_empty[c]), PER_CHUNK * GROUP_WARPS);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&sy->tmem_full[a]), 1);
@@ -325,24 +326,28 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->codes_full[i]), (armed_parity >> i) & 1u, wait);
     } else {
         // ------------------------------------------------------ decoding
-        // Group i takes stages i, i + GROUPS, .. of the block's; all groups
-        // pass over every chunk. A stage's values are made before its slot is
-        // free: between a slot's release and its readiness lie only the
-        // writes, their fence and the arrival.
+        // Group i takes stages i, i + GROUPS, .. of the block's. A stage's
+        // values are made before its slot is free: between a slot's release
+        // and its readiness lie only the writes, their fence and the arrival.
+        // A chunk of pair tiles has a stage for every group; all release it,
+        // in a tile's last one those without a stage too. Without pairs a
+        // block has one tile, whose chunks have stages for half of the groups
+        // in turn; the others pass them by.
         const int dw = warp - 2 - EPI_WARPS, group = dw / GROUP_WARPS;
         const int tid = dw % GROUP_WARPS * 32 + lane;
         constexpr int ITEMS = 256 / (32 * GROUP_WARPS);          // runs of 32 codes a thread and stage
-        uint32_t cph = 0;
-        int c = 0, base = -kb0;                                  // the stage of a tile's K block 0
+        uint32_t cph = 0, sph = 1;                               // parities to wait for
+        int c = 0, s = group, next = kb0 + group;                // this group's next stage: its slot, its K block
         bool ok = true;
-        for (int t = unit; ok && t < p.num_tiles; t += p.units, base += kb1 - kb0) {
+        for (int t = unit; ok && t < p.num_tiles; t += p.units, next -= kb1 - kb0) {
             for (int ch = ch0; ch < ch1; ++ch) {
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
-                if (!ok) break;
-#pragma unroll 1
-                for (int q = 0; q < PER_CHUNK; ++q) {
-                    const int kb = ch * PER_CHUNK + q, idx = base + kb, s = idx % STAGES;
-                    if (kb >= kb1 || idx % GROUPS != group) continue;
+                const bool mine = next < min((ch + 1) * PER_CHUNK, kb1);
+                if (PAIR || mine) {
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
+                    if (!ok) break;
+                }
+                if (mine) {
+                    const int q = next - ch * PER_CHUNK;
                     uint4 w[ITEMS];
                     uint32_t b0[ITEMS], b1[ITEMS];
                     bool is_wide = false;
@@ -376,7 +381,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             decode_run<false>(v[i], w[i], f0, FMT == TGEMM_MXFP4 ? f0 : sy->factors[b1[i]]);
                         }
                     }
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ((uint32_t)(idx / STAGES) & 1u) ^ 1u, wait));
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
                     if (!ok) break;
                     uint8_t* dst = smem + s * STAGE_BYTES + A_BYTES;
 #pragma unroll
@@ -388,10 +393,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     fence_async_smem();          // the MMA reads through the async proxy
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(full0 + (uint32_t)(s * sizeof(uint64_t)));
+                    next += GROUPS;
+                    s += GROUPS;
+                    if (s >= STAGES) { s -= STAGES; sph ^= 1u; }
                 }
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
+                if ((PAIR || mine) && lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
                 if (++c == CHUNKS) { c = 0; cph ^= 1u; }
             }
         }
