@@ -57,5 +57,25 @@ __device__ __forceinline__ void values(uint32_t w, uint32_t f, uint32_t (&v)[4])
     }
 }
 
+// 32 codes of a row (16 bytes) to BF16, in order.
+template <bool WIDE>
+__device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, uint32_t f0, uint32_t f1) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t v[4];
+        pairs(w[j], v);
+        const uint32_t f = j < 2 ? f0 : f1;
+        uint32_t r[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                         __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)};
+        if (WIDE)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], TWO_126);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], f);
+        out[j] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
 }  // namespace mx4_decode
 }  // namespace tgemm

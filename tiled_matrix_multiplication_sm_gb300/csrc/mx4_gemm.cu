@@ -277,7 +277,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (!PAIR && p.split > 1) {
         int mb, nb;
         tile_coords(unit, p, mb, nb);
-        join_shares<TC>(p, smem, part, mb * S::TM, nb * S::TN, mx4_g(p.ga), mx4_g(p.gb));
+        join_shares<TC>(p, smem, 128, part, mb * S::TM, nb * S::TN, mx4_g(p.ga), mx4_g(p.gb));
     }
     if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
 }

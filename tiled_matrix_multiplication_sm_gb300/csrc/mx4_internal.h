@@ -113,4 +113,8 @@ constexpr int MX4_FEW_ROWS = 24;
 cudaError_t mx4_weights_rows(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,
                              const Mx4Out& out, int num_sms, cudaStream_t s);
 
+// C of few tiles (mx4_weights_tmem.cu); X's rows on 16-byte boundaries.
+cudaError_t mx4_weights_tmem(int M, int N, int K, const void* X, long ldx, const Mx4Operand& W, int fmt,
+                             const Mx4Out& out, cudaStream_t s);
+
 }  // namespace tgemm

@@ -37,6 +37,13 @@ __device__ __forceinline__ void tile_coords(int t, const Tiling& p, int& mb, int
 // Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
+// Where it lies in a chunk of codes, of 128-byte rows or of 64-byte rows in the
+// 64-byte swizzle.
+template <int ROW>
+__device__ __forceinline__ uint32_t codes_at(int r, int j) {
+    return ROW == 128 ? swizzled(r, j) : (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+}
+
 // Drains this warp's 32 rows of a tile, 64 columns a turn; of SETS sets of
 // epilogue warps, set `set` takes every SETS-th turn. `last_first`: the last
 // 64 columns, which the next tile's accumulator shares, are turn 0. release()
@@ -169,14 +176,15 @@ __device__ __forceinline__ void store_share(uint8_t* partial, uint32_t tmem, int
     }
 }
 
-// The cluster's shares added in the order of their ranks, and stored: block
-// `part` takes every split-th row. All threads of all the cluster's blocks.
+// The cluster's shares, of `rows` rows, added in the order of their ranks and
+// stored: block `part` takes every split-th row. All threads of all the
+// cluster's blocks.
 template <typename TC>
-__device__ __forceinline__ void join_shares(const Tiling& p, const uint8_t* partial, int part, int row0, int col0,
-                                            float ga, float gb) {
+__device__ __forceinline__ void join_shares(const Tiling& p, const uint8_t* partial, int rows, int part, int row0,
+                                            int col0, float ga, float gb) {
     cluster_sync_all();
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int r = part + p.split * (int)(threadIdx.x >> 5); r < 128 && row0 + r < p.M; r += p.split * warps) {
+    for (int r = part + p.split * (int)(threadIdx.x >> 5); r < rows && row0 + r < p.M; r += p.split * warps) {
         float v[4] = {};
         for (int i = 0; i < p.split; ++i) {
             const uint32_t base = map_to_rank(smem_u32(partial), (uint32_t)i) + r * 512;
@@ -328,7 +336,7 @@ inline int split_for(long tiles, int steps, unsigned long long fits, int worth) 
 
 // Pair tiles (256 x 256) once they occupy half of the SM pairs.
 inline bool use_pair(int M, int N, int num_sms) {
-    return (((long)M + 255) / 256) * (((long)N + 255) / 256) * 4 >= num_sms;
+    return M > 128 && (((long)M + 255) / 256) * (((long)N + 255) / 256) * 4 >= num_sms;
 }
 
 }  // namespace mx4_tile

@@ -98,33 +98,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
                      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Where 16-byte piece j of row r lies in a chunk of codes, of 128-byte rows or
-// of 64-byte rows in the 64-byte swizzle.
-template <int ROW>
-__device__ __forceinline__ uint32_t codes_at(int r, int j) {
-    return ROW == 128 ? swizzled(r, j) : (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
-}
-
-// 32 codes of a row (16 bytes) to BF16, in order.
-template <bool WIDE>
-__device__ __forceinline__ void decode_run(uint4 (&out)[4], const uint4& codes, uint32_t f0, uint32_t f1) {
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t v[4];
-        pairs(w[j], v);
-        const uint32_t f = j < 2 ? f0 : f1;
-        uint32_t r[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                         __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)};
-        if (WIDE)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], TWO_126);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], f);
-        out[j] = make_uint4(r[0], r[1], r[2], r[3]);
-    }
-}
-
 template <int FMT, bool PAIR, typename TC>
 __global__ void __launch_bounds__(THREADS, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -410,7 +383,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (!PAIR && p.split > 1) {
         int mb, nb;
         tile_coords(unit, p, mb, nb);
-        join_shares<TC>(p, smem, part, mb * TM, nb * TN, unscale<FMT>(), mx4_g(p.gb));
+        join_shares<TC>(p, smem, 128, part, mb * TM, nb * TN, unscale<FMT>(), mx4_g(p.gb));
     }
     if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
 }
@@ -466,8 +439,7 @@ cudaError_t run(int M, int N, int K, const void* A, long lda, const Mx4Operand& 
     if (use_pair(M, N, num_sms))
         return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4, true>(M, N, K, A, lda, B, out, num_sms, s)
                                   : launch_type<TGEMM_NVFP4, true>(M, N, K, A, lda, B, out, num_sms, s);
-    return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4, false>(M, N, K, A, lda, B, out, num_sms, s)
-                              : launch_type<TGEMM_NVFP4, false>(M, N, K, A, lda, B, out, num_sms, s);
+    return mx4_weights_tmem(M, N, K, A, lda, B, fmt, out, s);
 }
 
 }  // namespace

@@ -1,0 +1,326 @@
+// BF16 rows times a kept 4-bit matrix, C = alpha X W^T + beta C + bias, where
+// C has too few tiles for mx4_weights.cu: W is made BF16 on its way into
+// tensor memory.
+//
+// The MMA (tcgen05, kind f16) takes W as its first operand, 128 rows of W from
+// tensor memory, and up to 128 rows of X from shared memory as its second, so
+// its result is a tile of C transposed: lanes are columns of C, tensor-memory
+// columns rows of C. The decoded weights are the bulk of the data; in shared
+// memory, written and read by the MMA, they take 32 of the 64 KB that a stage
+// of 64 columns of K moves there (of 512 cycles at 128 bytes a cycle), and the
+// MMA over padded rows of X has 128 rows' cost.
+//
+// A block has one tile (or a share of its sum over K), and two blocks share an
+// SM, so that one's start and end are behind the other's work. TMA brings X's
+// rows, a stage of 64 columns of K at a time, and W's codes and scales in
+// chunks of two stages; two groups of four warps take a stage of each chunk, a
+// thread one row of W: two 16-byte reads, two to four scales, 32 columns of
+// tensor memory written.
+
+#include "mx4_decode.h"
+#include "mx4_tile.h"
+
+#include <cstring>
+
+namespace tgemm {
+namespace {
+
+using namespace mx4_tile;
+using namespace mx4_decode;
+
+constexpr int TW = 128;                              // rows of W in a tile: lanes of tensor memory
+constexpr int STAGE_K = 64;
+constexpr int GROUPS = 4;                            // of the decoding warps, each on its own stages
+constexpr int CHUNK_STAGES = 2;
+constexpr int ROW = CHUNK_STAGES * STAGE_K / 2;      // bytes of a row of a chunk's codes
+constexpr int CODES_BYTES = TW * ROW;
+constexpr int SLOTS = 8, CHUNKS = 10;
+constexpr int SUM_COLS = 128, SLOT_COLS = STAGE_K / 2;   // of tensor memory: sums, then slots of weights
+constexpr int DECODE_WARPS = 4 * GROUPS;
+constexpr int CODES_WARP = 2 + DECODE_WARPS;
+constexpr int THREADS = 32 * (CODES_WARP + 1);
+constexpr int SMEM_LIMIT = 227 * 1024;
+// A group that waits for a slot or a chunk has seen its last use but one
+// (barriers tell phases apart by parity).
+static_assert(SLOTS >= GROUPS && CHUNKS * CHUNK_STAGES % GROUPS == 0 && GROUPS % CHUNK_STAGES == 0, "groups");
+static_assert(SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * SW >= TW * 4, "room for the slots, and for a share in them");
+
+template <int FMT> constexpr int SF_TILES = CHUNK_STAGES * STAGE_K / mx4_block(FMT) / 4;
+template <int FMT> constexpr int SF_BYTES = SF_TILES<FMT> * MX4_TILE_BYTES;
+
+struct Sync {
+    uint64_t full[SLOTS], empty[SLOTS];
+    uint64_t codes_full[CHUNKS], codes_empty[CHUNKS];
+    uint64_t done, drain;
+    uint32_t tmem_base;
+    int abort;
+    uint32_t factors[256];
+};
+constexpr int SYNC_BYTES = 1408;
+static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
+
+// Rows of X in a tile: a multiple of 16, 128 at most, as even as tiles allow.
+inline int rows_of(int M) {
+    const long tiles = ((long)M + 127) / 128;
+    return (int)(((M + tiles - 1) / tiles + 15) / 16 * 16);
+}
+template <int FMT>
+constexpr int smem_bytes(int rows) {
+    return 1024 + SLOTS * rows * SW + CHUNKS * (CODES_BYTES + SF_BYTES<FMT>) + SYNC_BYTES;
+}
+static_assert(smem_bytes<TGEMM_NVFP4>(128) <= SMEM_LIMIT, "shared memory");
+
+struct Params : Tiling {
+    int kblocks;                // of 64 columns
+    int rows;                   // of X in a tile
+    const float* gb;
+};
+
+// D (+)= W X^T over 16 columns of K: W in tensor memory, X in shared memory.
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+template <int FMT, typename TC>
+__global__ void __launch_bounds__(THREADS, 1)
+weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmS, const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const int slot_bytes = p.rows * SW;
+    uint8_t* codes = smem + SLOTS * slot_bytes;
+    uint8_t* scales = codes + CHUNKS * CODES_BYTES;
+    Sync* sy = reinterpret_cast<Sync*>(scales + CHUNKS * SF_BYTES<FMT>);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x % p.split;
+    int mb, nb;
+    tile_coords(blockIdx.x / p.split, p, mb, nb);
+    // This block's chunks and K blocks of its tile.
+    const int chunks = (p.kblocks + CHUNK_STAGES - 1) / CHUNK_STAGES;
+    const int ch0 = (int)((long)chunks * part / p.split), ch1 = (int)((long)chunks * (part + 1) / p.split);
+    const int kb0 = ch0 * CHUNK_STAGES, kb1 = min(ch1 * CHUNK_STAGES, p.kblocks);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(smem_u32(&sy->full[s]), 1 + 4);          // X's bytes, the four warps of a group
+            mbar_init(smem_u32(&sy->empty[s]), 1);
+        }
+        for (int c = 0; c < CHUNKS; ++c) {
+            mbar_init(smem_u32(&sy->codes_full[c]), 1);
+            mbar_init(smem_u32(&sy->codes_empty[c]), CHUNK_STAGES * 4);
+        }
+        mbar_init(smem_u32(&sy->done), 1);
+        mbar_init(smem_u32(&sy->drain), 1);
+        sy->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        prefetch_map(&tmX);
+        prefetch_map(&tmW);
+        prefetch_map(&tmS);
+    }
+    if (threadIdx.x < 256) sy->factors[threadIdx.x] = factor<FMT>(threadIdx.x);
+    if (warp == 1) tmem_alloc<false, TMEM_COLS>(smem_u32(&sy->tmem_base));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = sy->tmem_base, tmem_slots = tmem_base + SUM_COLS;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const Wait wait{&sy->abort, p.status, p.wait_limit_ns};
+
+    if (warp == 0) {
+        // ------------------------------------------------- TMA producer of X
+        uint32_t armed = 0, armed_parity = 0, ph = 0;
+        int s = 0;
+        bool stall = p.debug_stall != 0;                   // test hook: the first stage is never filled
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait))) break;
+            if (!stall) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(smem_u32(&sy->full[s]), slot_bytes);
+                    tma_load_2d<false>(smem_u32(smem) + s * slot_bytes, &tmX, kb * STAGE_K, mb * p.rows,
+                                       smem_u32(&sy->full[s]));
+                }
+                armed |= 1u << s;
+                armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+            }
+            stall = false;
+            __syncwarp();
+            if (++s == SLOTS) { s = 0; ph ^= 1u; }
+        }
+        for (int i = 0; i < SLOTS; ++i)
+            if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(p.rows >> 3) << 17 | (uint32_t)(TW >> 4) << 24;
+        if (elect_one()) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(smem_u32(&sy->full[s]), ph, wait)) break;
+                tc_fence_after();
+                const uint32_t x = smem_u32(smem) + s * slot_bytes, w = tmem_slots + (uint32_t)(s * SLOT_COLS);
+#pragma unroll
+                for (int k = 0; k < STAGE_K / 16; ++k)
+                    mma_bf16(tmem_base, w + k * 8, smem_desc(x + k * 32, 16, 1024, 2), idesc, kb != kb0 || k != 0);
+                tc_commit<false>(smem_u32(&sy->empty[s]));
+                if (kb == kb1 - 1) tc_commit<false>(smem_u32(&sy->done));
+                if (++s == SLOTS) { s = 0; ph ^= 1u; }
+            }
+            tc_commit<false>(smem_u32(&sy->drain));
+            mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
+        }
+        __syncwarp();
+    } else if (warp == CODES_WARP) {
+        // ---------------------------------------- TMA producer of the codes
+        uint32_t armed = 0, armed_parity = 0, ph = 0;
+        int c = 0;
+        for (int ch = ch0; ch < ch1; ++ch) {
+            if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), ph ^ 1u, wait))) break;
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(&sy->codes_full[c]);
+                mbar_arrive_expect_tx(bar, CODES_BYTES + SF_BYTES<FMT>);
+                tma_load_2d<false>(smem_u32(codes) + c * CODES_BYTES, &tmW, ch * ROW, nb * TW, bar);
+                tma_load_3d<false>(smem_u32(scales) + c * SF_BYTES<FMT>, &tmS, 0, ch * SF_TILES<FMT>, nb, bar);
+            }
+            __syncwarp();
+            armed |= 1u << c;
+            armed_parity = (armed_parity & ~(1u << c)) | (ph << c);
+            if (++c == CHUNKS) { c = 0; ph ^= 1u; }
+        }
+        for (int i = 0; i < CHUNKS; ++i)
+            if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->codes_full[i]), (armed_parity >> i) & 1u, wait);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ decoding
+        // Group i takes stages i, i + GROUPS, .. of the block's, and has none
+        // in the chunks between. A stage's values are made before its slot is
+        // free.
+        const int quarter = warp & 3, group = (warp - 2) / 4, row = quarter * 32 + lane;
+        const int half = group % CHUNK_STAGES;                   // its stage of a chunk
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // those of tensor memory that this warp reaches
+        uint32_t cph = 0, sph = 1;
+        int c = group / CHUNK_STAGES, s = group;
+        bool ok = true;
+        for (int kb = kb0 + group; kb < kb1; kb += GROUPS) {
+            ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
+            if (!ok) break;
+            uint32_t b[4];                           // the scales of each 16 columns
+            bool is_wide = false;
+            const uint8_t* sc = scales + c * SF_BYTES<FMT> + (row & 31) * 16 + (row >> 5) * 4;
+            if (FMT == TGEMM_MXFP4) {
+                const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + half * 2);
+                b[0] = b[1] = two & 0xFF;
+                b[2] = b[3] = two >> 8;
+                is_wide = __any_sync(~0u, wide(b[0]) || wide(b[2]));
+            } else {
+                const uint32_t four = *reinterpret_cast<const uint32_t*>(sc + half * MX4_TILE_BYTES);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = four >> 8 * i & 0xFF;
+            }
+            uint32_t v[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES +
+                                                                codes_at<ROW>(row, half * 2 + h));
+                uint4 out[4];
+                if (is_wide) {
+                    // Beside a wide block the others take their scale alone too.
+                    const uint32_t f = b[2 * h] == 255 ? 0x7FC07FC0u : b[2 * h] == 0 ? 0x00400040u
+                                                                     : b[2 * h] << 7 | b[2 * h] << 23;
+                    decode_run<true>(out, w, f, f);
+                } else {
+                    const uint32_t f0 = sy->factors[b[2 * h]];
+                    decode_run<false>(out, w, f0, FMT == TGEMM_MXFP4 ? f0 : sy->factors[b[2 * h + 1]]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[h * 16 + j * 4] = out[j].x;
+                    v[h * 16 + j * 4 + 1] = out[j].y;
+                    v[h * 16 + j * 4 + 2] = out[j].z;
+                    v[h * 16 + j * 4 + 3] = out[j].w;
+                }
+            }
+            ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
+            if (!ok) break;
+            tc_fence_after();
+            tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS), v);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sy->full[s]));
+            if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
+            s += GROUPS;
+            if (s >= SLOTS) { s -= SLOTS; sph ^= 1u; }
+            c += GROUPS / CHUNK_STAGES;
+            if (c >= CHUNKS) { c -= CHUNKS; cph ^= 1u; }
+        }
+        // ------------------------------------------------------ the sums
+        // They go where X's stages were (copies and MMAs are done), a row of C
+        // in 512 bytes, in the order that join_shares reads.
+        ok = __all_sync(~0u, ok && mbar_wait(smem_u32(&sy->done), 0, wait));
+        if (ok) {
+            tc_fence_after();
+            const int piece = row >> 2;
+            uint8_t* at = smem + (row & 3) * 4;
+#pragma unroll 1
+            for (int m = group * 32; m < p.rows; m += 32 * GROUPS) {
+                uint32_t r[32];
+                tmem_ld32(tmem_base + lanes + (uint32_t)m, r);
+                tmem_wait_ld(r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (m + j < p.rows) *reinterpret_cast<uint32_t*>(at + (m + j) * 512 + ((piece ^ j) << 4)) = r[j];
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    join_shares<TC>(p, smem, p.rows, part, mb * p.rows, nb * TW, unscale<FMT>(), mx4_g(p.gb));
+    if (warp == 1) tmem_free<false, TMEM_COLS>(tmem_base);
+}
+
+template <int FMT, typename TC>
+cudaError_t launch(int M, int N, int K, const void* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
+                   cudaStream_t s) {
+    const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (enc == nullptr) return cudaErrorNotSupported;
+    Params p;
+    p.rows = rows_of(M);
+    CUtensorMap tmX, tmW, tmS;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)ldx * 2};
+    const cuuint32_t box[2] = {STAGE_K, (cuuint32_t)p.rows};
+    if (!encode(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, X, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_codes(enc, &tmW, W, N, K, ROW) || !encode_scales(enc, &tmS, W, N, K, FMT, SF_TILES<FMT>, 1))
+        return cudaErrorInvalidValue;
+    cudaError_t e = make_tiling(p, M, N, p.rows, TW, 0x3FFFFFFF, out);
+    p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
+    p.gb = W.g;
+    if (e == cudaSuccess) e = set_smem_limit_once<weights_tmem_kernel<FMT, TC>>(SMEM_LIMIT);
+    unsigned long long fits = 0;
+    if (e == cudaSuccess) e = clusters_that_fit<weights_tmem_kernel<FMT, TC>>(THREADS, SMEM_LIMIT, &fits);
+    if (e != cudaSuccess) return e;
+    p.split = split_for(p.num_tiles, (p.kblocks + CHUNK_STAGES - 1) / CHUNK_STAGES, fits, 3);
+    ClusterLaunch cfg(p.split * p.num_tiles, THREADS, smem_bytes<FMT>(p.rows), p.split, s);
+    return cudaLaunchKernelEx(&cfg.config, weights_tmem_kernel<FMT, TC>, tmX, tmW, tmS, p);
+}
+
+}  // namespace
+
+cudaError_t mx4_weights_tmem(int M, int N, int K, const void* X, long ldx, const Mx4Operand& W, int fmt,
+                             const Mx4Out& out, cudaStream_t s) {
+    if (out.c_type == TGEMM_TYPE_F32)
+        return fmt == TGEMM_MXFP4 ? launch<TGEMM_MXFP4, float>(M, N, K, X, ldx, W, out, s)
+                                  : launch<TGEMM_NVFP4, float>(M, N, K, X, ldx, W, out, s);
+    return fmt == TGEMM_MXFP4 ? launch<TGEMM_MXFP4, __nv_bfloat16>(M, N, K, X, ldx, W, out, s)
+                              : launch<TGEMM_NVFP4, __nv_bfloat16>(M, N, K, X, ldx, W, out, s);
+}
+
+}  // namespace tgemm
