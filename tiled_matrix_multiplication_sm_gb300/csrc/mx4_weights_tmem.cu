@@ -10,12 +10,12 @@
 // of 64 columns of K moves there (of 512 cycles at 128 bytes a cycle), and the
 // MMA over padded rows of X has 128 rows' cost.
 //
-// A block has one tile (or a share of its sum over K), and two blocks share an
-// SM, so that one's start and end are behind the other's work. TMA brings X's
-// rows, a stage of 64 columns of K at a time, and W's codes and scales in
-// chunks of two stages; two groups of four warps take a stage of each chunk, a
-// thread one row of W: two 16-byte reads, two to four scales, 32 columns of
-// tensor memory written.
+// A block has one tile, or a share of its sum over K. A stage is 128 columns
+// of K: of fewer, the handshakes of the warp that issues the MMAs were the
+// bound (64 columns: XX). TMA brings X's rows into a stage's slot, and W's codes and
+// scales into a longer ring; two groups of four warps decode half of the stage
+// each (a thread one row of W: two 16-byte reads, two to four scales, 32
+// columns of tensor memory written), two other groups the next stage.
 
 #include "mx4_decode.h"
 #include "mx4_tile.h"
@@ -29,23 +29,25 @@ using namespace mx4_tile;
 using namespace mx4_decode;
 
 constexpr int TW = 128;                              // rows of W in a tile: lanes of tensor memory
-constexpr int STAGE_K = 64;
-constexpr int GROUPS = 4;                            // of the decoding warps, each on its own stages
-constexpr int CHUNK_STAGES = 2;
-constexpr int ROW = CHUNK_STAGES * STAGE_K / 2;      // bytes of a row of a chunk's codes
+constexpr int STAGE_K = 128;
+constexpr int PARTS = 2, PART_K = STAGE_K / PARTS;   // of a stage, each decoded by a group of warps
+constexpr int GROUPS = 4;
+constexpr int AHEAD = GROUPS / PARTS;                // a group takes every AHEAD-th stage
+constexpr int ROW = STAGE_K / 2;                     // bytes of a row of a stage's codes
 constexpr int CODES_BYTES = TW * ROW;
-constexpr int SLOTS = 8, CHUNKS = 10;
+constexpr int SLOTS = 4, CHUNKS = 10;                // rings of X and decoded weights, of codes
 constexpr int SUM_COLS = 128, SLOT_COLS = STAGE_K / 2;   // of tensor memory: sums, then slots of weights
 constexpr int DECODE_WARPS = 4 * GROUPS;
 constexpr int CODES_WARP = 2 + DECODE_WARPS;
 constexpr int THREADS = 32 * (CODES_WARP + 1);
 constexpr int SMEM_LIMIT = 227 * 1024;
-// A group that waits for a slot or a chunk has seen its last use but one
-// (barriers tell phases apart by parity).
-static_assert(SLOTS >= GROUPS && CHUNKS * CHUNK_STAGES % GROUPS == 0 && GROUPS % CHUNK_STAGES == 0, "groups");
-static_assert(SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * SW >= TW * 4, "room for the slots, and for a share in them");
+// A group meets all uses of the slots and codes that it meets at all (barriers
+// tell phases apart by parity).
+static_assert(SLOTS % AHEAD == 0 && CHUNKS % AHEAD == 0, "groups");
+static_assert(SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * PARTS * SW >= TW * 4,
+              "room for the slots, and for a share in them");
 
-template <int FMT> constexpr int SF_TILES = CHUNK_STAGES * STAGE_K / mx4_block(FMT) / 4;
+template <int FMT> constexpr int SF_TILES = STAGE_K / mx4_block(FMT) / 4;
 template <int FMT> constexpr int SF_BYTES = SF_TILES<FMT> * MX4_TILE_BYTES;
 
 struct Sync {
@@ -66,12 +68,12 @@ inline int rows_of(int M) {
 }
 template <int FMT>
 constexpr int smem_bytes(int rows) {
-    return 1024 + SLOTS * rows * SW + CHUNKS * (CODES_BYTES + SF_BYTES<FMT>) + SYNC_BYTES;
+    return 1024 + SLOTS * PARTS * rows * SW + CHUNKS * (CODES_BYTES + SF_BYTES<FMT>) + SYNC_BYTES;
 }
 static_assert(smem_bytes<TGEMM_NVFP4>(128) <= SMEM_LIMIT, "shared memory");
 
 struct Params : Tiling {
-    int kblocks;                // of 64 columns
+    int stages;                 // of K
     int rows;                   // of X in a tile
     const float* gb;
 };
@@ -89,7 +91,7 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
                     const __grid_constant__ CUtensorMap tmS, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    const int slot_bytes = p.rows * SW;
+    const int part_bytes = p.rows * SW, slot_bytes = PARTS * part_bytes;      // of X
     uint8_t* codes = smem + SLOTS * slot_bytes;
     uint8_t* scales = codes + CHUNKS * CODES_BYTES;
     Sync* sy = reinterpret_cast<Sync*>(scales + CHUNKS * SF_BYTES<FMT>);
@@ -98,19 +100,17 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
     const int part = blockIdx.x % p.split;
     int mb, nb;
     tile_coords(blockIdx.x / p.split, p, mb, nb);
-    // This block's chunks and K blocks of its tile.
-    const int chunks = (p.kblocks + CHUNK_STAGES - 1) / CHUNK_STAGES;
-    const int ch0 = (int)((long)chunks * part / p.split), ch1 = (int)((long)chunks * (part + 1) / p.split);
-    const int kb0 = ch0 * CHUNK_STAGES, kb1 = min(ch1 * CHUNK_STAGES, p.kblocks);
+    // This block's stages of its tile.
+    const int k0 = (int)((long)p.stages * part / p.split), k1 = (int)((long)p.stages * (part + 1) / p.split);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_u32(&sy->full[s]), 1 + 4);          // X's bytes, the four warps of a group
+            mbar_init(smem_u32(&sy->full[s]), 1 + 4 * PARTS);  // X's bytes, the decoding warps
             mbar_init(smem_u32(&sy->empty[s]), 1);
         }
         for (int c = 0; c < CHUNKS; ++c) {
             mbar_init(smem_u32(&sy->codes_full[c]), 1);
-            mbar_init(smem_u32(&sy->codes_empty[c]), CHUNK_STAGES * 4);
+            mbar_init(smem_u32(&sy->codes_empty[c]), 4 * PARTS);
         }
         mbar_init(smem_u32(&sy->done), 1);
         mbar_init(smem_u32(&sy->drain), 1);
@@ -137,13 +137,15 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         uint32_t armed = 0, armed_parity = 0, ph = 0;
         int s = 0;
         bool stall = p.debug_stall != 0;                   // test hook: the first stage is never filled
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int k = k0; k < k1; ++k) {
             if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait))) break;
             if (!stall) {
                 if (elect_one()) {
                     mbar_arrive_expect_tx(smem_u32(&sy->full[s]), slot_bytes);
-                    tma_load_2d<false>(smem_u32(smem) + s * slot_bytes, &tmX, kb * STAGE_K, mb * p.rows,
-                                       smem_u32(&sy->full[s]));
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i)
+                        tma_load_2d<false>(smem_u32(smem) + s * slot_bytes + i * part_bytes, &tmX,
+                                           k * STAGE_K + i * PART_K, mb * p.rows, smem_u32(&sy->full[s]));
                 }
                 armed |= 1u << s;
                 armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
@@ -161,15 +163,16 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         if (elect_one()) {
             int s = 0;
             uint32_t ph = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int k = k0; k < k1; ++k) {
                 if (!mbar_wait(smem_u32(&sy->full[s]), ph, wait)) break;
                 tc_fence_after();
                 const uint32_t x = smem_u32(smem) + s * slot_bytes, w = tmem_slots + (uint32_t)(s * SLOT_COLS);
 #pragma unroll
-                for (int k = 0; k < STAGE_K / 16; ++k)
-                    mma_bf16(tmem_base, w + k * 8, smem_desc(x + k * 32, 16, 1024, 2), idesc, kb != kb0 || k != 0);
+                for (int j = 0; j < STAGE_K / 16; ++j)
+                    mma_bf16(tmem_base, w + j * 8, smem_desc(x + j / 4 * part_bytes + j % 4 * 32, 16, 1024, 2), idesc,
+                             k != k0 || j != 0);
                 tc_commit<false>(smem_u32(&sy->empty[s]));
-                if (kb == kb1 - 1) tc_commit<false>(smem_u32(&sy->done));
+                if (k == k1 - 1) tc_commit<false>(smem_u32(&sy->done));
                 if (++s == SLOTS) { s = 0; ph ^= 1u; }
             }
             tc_commit<false>(smem_u32(&sy->drain));
@@ -180,13 +183,13 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         // ---------------------------------------- TMA producer of the codes
         uint32_t armed = 0, armed_parity = 0, ph = 0;
         int c = 0;
-        for (int ch = ch0; ch < ch1; ++ch) {
+        for (int k = k0; k < k1; ++k) {
             if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), ph ^ 1u, wait))) break;
             if (elect_one()) {
                 const uint32_t bar = smem_u32(&sy->codes_full[c]);
                 mbar_arrive_expect_tx(bar, CODES_BYTES + SF_BYTES<FMT>);
-                tma_load_2d<false>(smem_u32(codes) + c * CODES_BYTES, &tmW, ch * ROW, nb * TW, bar);
-                tma_load_3d<false>(smem_u32(scales) + c * SF_BYTES<FMT>, &tmS, 0, ch * SF_TILES<FMT>, nb, bar);
+                tma_load_2d<false>(smem_u32(codes) + c * CODES_BYTES, &tmW, k * ROW, nb * TW, bar);
+                tma_load_3d<false>(smem_u32(scales) + c * SF_BYTES<FMT>, &tmS, 0, k * SF_TILES<FMT>, nb, bar);
             }
             __syncwarp();
             armed |= 1u << c;
@@ -198,16 +201,14 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         __syncwarp();
     } else {
         // ------------------------------------------------------ decoding
-        // Group i takes stages i, i + GROUPS, .. of the block's, and has none
-        // in the chunks between. A stage's values are made before its slot is
-        // free.
+        // A stage's values are made before its slot is free.
         const int quarter = warp & 3, group = (warp - 2) / 4, row = quarter * 32 + lane;
-        const int half = group % CHUNK_STAGES;                   // its stage of a chunk
+        const int half = group % PARTS;                          // its part of a stage
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // those of tensor memory that this warp reaches
         uint32_t cph = 0, sph = 1;
-        int c = group / CHUNK_STAGES, s = group;
+        int c = group / PARTS, s = c;
         bool ok = true;
-        for (int kb = kb0 + group; kb < kb1; kb += GROUPS) {
+        for (int k = k0 + c; k < k1; k += AHEAD) {
             ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
             if (!ok) break;
             uint32_t b[4];                           // the scales of each 16 columns
@@ -249,15 +250,17 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
             if (!ok) break;
             tc_fence_after();
-            tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS), v);
+            tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS + half * (PART_K / 2)), v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sy->full[s]));
-            if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
-            s += GROUPS;
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sy->full[s]));
+                mbar_arrive(smem_u32(&sy->codes_empty[c]));
+            }
+            s += AHEAD;
             if (s >= SLOTS) { s -= SLOTS; sph ^= 1u; }
-            c += GROUPS / CHUNK_STAGES;
+            c += AHEAD;
             if (c >= CHUNKS) { c -= CHUNKS; cph ^= 1u; }
         }
         // ------------------------------------------------------ the sums
@@ -296,18 +299,18 @@ cudaError_t launch(int M, int N, int K, const void* X, long ldx, const Mx4Operan
     p.rows = rows_of(M);
     CUtensorMap tmX, tmW, tmS;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)ldx * 2};
-    const cuuint32_t box[2] = {STAGE_K, (cuuint32_t)p.rows};
+    const cuuint32_t box[2] = {PART_K, (cuuint32_t)p.rows};
     if (!encode(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, X, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_codes(enc, &tmW, W, N, K, ROW) || !encode_scales(enc, &tmS, W, N, K, FMT, SF_TILES<FMT>, 1))
         return cudaErrorInvalidValue;
     cudaError_t e = make_tiling(p, M, N, p.rows, TW, 0x3FFFFFFF, out);
-    p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
+    p.stages = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.gb = W.g;
     if (e == cudaSuccess) e = set_smem_limit_once<weights_tmem_kernel<FMT, TC>>(SMEM_LIMIT);
     unsigned long long fits = 0;
     if (e == cudaSuccess) e = clusters_that_fit<weights_tmem_kernel<FMT, TC>>(THREADS, SMEM_LIMIT, &fits);
     if (e != cudaSuccess) return e;
-    p.split = split_for(p.num_tiles, (p.kblocks + CHUNK_STAGES - 1) / CHUNK_STAGES, fits, 3);
+    p.split = split_for(p.num_tiles, p.stages, fits, 3);
     ClusterLaunch cfg(p.split * p.num_tiles, THREADS, smem_bytes<FMT>(p.rows), p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_tmem_kernel<FMT, TC>, tmX, tmW, tmS, p);
 }
