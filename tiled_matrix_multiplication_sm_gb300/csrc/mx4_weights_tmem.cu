@@ -30,12 +30,11 @@ using namespace mx4_decode;
 
 constexpr int TW = 128;                              // rows of W in a tile: lanes of tensor memory
 constexpr int STAGE_K = 128;
-constexpr int PARTS = 2, PART_K = STAGE_K / PARTS;   // of a stage, each decoded by a group of warps
-constexpr int GROUPS = 4;
-constexpr int AHEAD = GROUPS / PARTS;                // a group takes every AHEAD-th stage
+constexpr int PARTS = 2, PART_K = STAGE_K / PARTS;   // a row of X or of decoded weights in 128 bytes
+constexpr int GROUPS = 4;                            // of decoding warps, each on its own stages
 constexpr int ROW = STAGE_K / 2;                     // bytes of a row of a stage's codes
 constexpr int CODES_BYTES = TW * ROW;
-constexpr int SLOTS = 4, CHUNKS = 10;                // rings of X and decoded weights, of codes
+constexpr int SLOTS = 4, CHUNKS = 8;                // rings of X and decoded weights, of codes
 constexpr int SUM_COLS = 128, SLOT_COLS = STAGE_K / 2;   // of tensor memory: sums, then slots of weights
 constexpr int DECODE_WARPS = 4 * GROUPS;
 constexpr int CODES_WARP = 2 + DECODE_WARPS;
@@ -43,7 +42,7 @@ constexpr int THREADS = 32 * (CODES_WARP + 1);
 constexpr int SMEM_LIMIT = 227 * 1024;
 // A group meets all uses of the slots and codes that it meets at all (barriers
 // tell phases apart by parity).
-static_assert(SLOTS % AHEAD == 0 && CHUNKS % AHEAD == 0, "groups");
+static_assert(SLOTS % GROUPS == 0 && CHUNKS % GROUPS == 0, "groups");
 static_assert(SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * PARTS * SW >= TW * 4,
               "room for the slots, and for a share in them");
 
@@ -105,12 +104,12 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(smem_u32(&sy->full[s]), 1 + 4 * PARTS);  // X's bytes, the decoding warps
+            mbar_init(smem_u32(&sy->full[s]), 1 + 4);          // X's bytes, a group's warps
             mbar_init(smem_u32(&sy->empty[s]), 1);
         }
         for (int c = 0; c < CHUNKS; ++c) {
             mbar_init(smem_u32(&sy->codes_full[c]), 1);
-            mbar_init(smem_u32(&sy->codes_empty[c]), 4 * PARTS);
+            mbar_init(smem_u32(&sy->codes_empty[c]), 4);
         }
         mbar_init(smem_u32(&sy->done), 1);
         mbar_init(smem_u32(&sy->drain), 1);
@@ -203,54 +202,57 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         // ------------------------------------------------------ decoding
         // A stage's values are made before its slot is free.
         const int quarter = warp & 3, group = (warp - 2) / 4, row = quarter * 32 + lane;
-        const int half = group % PARTS;                          // its part of a stage
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;   // those of tensor memory that this warp reaches
         uint32_t cph = 0, sph = 1;
-        int c = group / PARTS, s = c;
+        int c = group, s = group % SLOTS;
         bool ok = true;
-        for (int k = k0 + c; k < k1; k += AHEAD) {
+        for (int k = k0 + group; k < k1; k += GROUPS) {
             ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
             if (!ok) break;
-            uint32_t b[4];                           // the scales of each 16 columns
-            bool is_wide = false;
             const uint8_t* sc = scales + c * SF_BYTES<FMT> + (row & 31) * 16 + (row >> 5) * 4;
-            if (FMT == TGEMM_MXFP4) {
-                const uint32_t two = *reinterpret_cast<const uint16_t*>(sc + half * 2);
-                b[0] = b[1] = two & 0xFF;
-                b[2] = b[3] = two >> 8;
-                is_wide = __any_sync(~0u, wide(b[0]) || wide(b[2]));
-            } else {
-                const uint32_t four = *reinterpret_cast<const uint32_t*>(sc + half * MX4_TILE_BYTES);
+            uint32_t sf[SF_TILES<FMT>];                  // the row's scales
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = four >> 8 * i & 0xFF;
-            }
-            uint32_t v[32];
+            for (int i = 0; i < SF_TILES<FMT>; ++i) sf[i] = *reinterpret_cast<const uint32_t*>(sc + i * MX4_TILE_BYTES);
+            const bool is_wide =
+                FMT == TGEMM_MXFP4 && __any_sync(~0u, wide(sf[0] & 0xFF) || wide(sf[0] >> 8 & 0xFF) ||
+                                                          wide(sf[0] >> 16 & 0xFF) || wide(sf[0] >> 24));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES +
-                                                                codes_at<ROW>(row, half * 2 + h));
-                uint4 out[4];
-                if (is_wide) {
-                    // Beside a wide block the others take their scale alone too.
-                    const uint32_t f = b[2 * h] == 255 ? 0x7FC07FC0u : b[2 * h] == 0 ? 0x00400040u
-                                                                     : b[2 * h] << 7 | b[2 * h] << 23;
-                    decode_run<true>(out, w, f, f);
-                } else {
-                    const uint32_t f0 = sy->factors[b[2 * h]];
-                    decode_run<false>(out, w, f0, FMT == TGEMM_MXFP4 ? f0 : sy->factors[b[2 * h + 1]]);
+            for (int i = 0; i < PARTS; ++i) {
+                uint32_t v[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES + codes_at<ROW>(row, i * 2 + h));
+                    uint4 out[4];
+                    if (FMT == TGEMM_MXFP4) {
+                        const uint32_t b = sf[0] >> (i * 2 + h) * 8 & 0xFF;
+                        if (is_wide) {
+                            // Beside a wide block the others take their scale alone too.
+                            const uint32_t f = b == 255 ? 0x7FC07FC0u : b == 0 ? 0x00400040u : b << 7 | b << 23;
+                            decode_run<true>(out, w, f, f);
+                        } else {
+                            const uint32_t f = sy->factors[b];
+                            decode_run<false>(out, w, f, f);
+                        }
+                    } else {
+                        const uint32_t b = sf[i % SF_TILES<FMT>] >> h * 16;
+                        decode_run<false>(out, w, sy->factors[b & 0xFF], sy->factors[b >> 8 & 0xFF]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[h * 16 + j * 4] = out[j].x;
+                        v[h * 16 + j * 4 + 1] = out[j].y;
+                        v[h * 16 + j * 4 + 2] = out[j].z;
+                        v[h * 16 + j * 4 + 3] = out[j].w;
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[h * 16 + j * 4] = out[j].x;
-                    v[h * 16 + j * 4 + 1] = out[j].y;
-                    v[h * 16 + j * 4 + 2] = out[j].z;
-                    v[h * 16 + j * 4 + 3] = out[j].w;
+                if (i == 0) {
+                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
+                tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS + i * (PART_K / 2)), v);
             }
-            ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
             if (!ok) break;
-            tc_fence_after();
-            tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS + half * (PART_K / 2)), v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -258,9 +260,9 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
                 mbar_arrive(smem_u32(&sy->full[s]));
                 mbar_arrive(smem_u32(&sy->codes_empty[c]));
             }
-            s += AHEAD;
+            s += GROUPS;
             if (s >= SLOTS) { s -= SLOTS; sph ^= 1u; }
-            c += AHEAD;
+            c += GROUPS;
             if (c >= CHUNKS) { c -= CHUNKS; cph ^= 1u; }
         }
         // ------------------------------------------------------ the sums
