@@ -21,6 +21,7 @@
 #include "mx4_tile.h"
 
 #include <cstring>
+#include <type_traits>
 
 namespace tgemm {
 namespace {
@@ -216,42 +217,45 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             const bool is_wide =
                 FMT == TGEMM_MXFP4 && __any_sync(~0u, wide(sf[0] & 0xFF) || wide(sf[0] >> 8 & 0xFF) ||
                                                           wide(sf[0] >> 16 & 0xFF) || wide(sf[0] >> 24));
+            const uint32_t slot = tmem_slots + lanes + (uint32_t)(s * SLOT_COLS);
+            auto decode = [&](auto wide_scales) {
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                uint32_t v[32];
+                for (int i = 0; i < PARTS; ++i) {
+                    uint32_t v[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES + codes_at<ROW>(row, i * 2 + h));
-                    uint4 out[4];
-                    if (FMT == TGEMM_MXFP4) {
-                        const uint32_t b = sf[0] >> (i * 2 + h) * 8 & 0xFF;
-                        if (is_wide) {
-                            // Beside a wide block the others take their scale alone too.
-                            const uint32_t f = b == 255 ? 0x7FC07FC0u : b == 0 ? 0x00400040u : b << 7 | b << 23;
-                            decode_run<true>(out, w, f, f);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES +
+                                                                        codes_at<ROW>(row, i * 2 + h));
+                        uint32_t f0, f1;
+                        if (FMT == TGEMM_NVFP4) {
+                            const uint32_t b = sf[i % SF_TILES<FMT>] >> h * 16;
+                            f0 = sy->factors[b & 0xFF];
+                            f1 = sy->factors[b >> 8 & 0xFF];
                         } else {
-                            const uint32_t f = sy->factors[b];
-                            decode_run<false>(out, w, f, f);
+                            const uint32_t b = sf[0] >> (i * 2 + h) * 8 & 0xFF;
+                            // Beside a wide block the others take their scale alone too.
+                            f0 = f1 = !decltype(wide_scales)::value ? sy->factors[b] : b == 255 ? 0x7FC07FC0u : b == 0 ? 0x00400040u
+                                                                                              : b << 7 | b << 23;
                         }
-                    } else {
-                        const uint32_t b = sf[i % SF_TILES<FMT>] >> h * 16;
-                        decode_run<false>(out, w, sy->factors[b & 0xFF], sy->factors[b >> 8 & 0xFF]);
-                    }
+                        uint4 out[4];
+                        decode_run<decltype(wide_scales)::value>(out, w, f0, f1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[h * 16 + j * 4] = out[j].x;
-                        v[h * 16 + j * 4 + 1] = out[j].y;
-                        v[h * 16 + j * 4 + 2] = out[j].z;
-                        v[h * 16 + j * 4 + 3] = out[j].w;
+                        for (int j = 0; j < 4; ++j) {
+                            v[h * 16 + j * 4] = out[j].x;
+                            v[h * 16 + j * 4 + 1] = out[j].y;
+                            v[h * 16 + j * 4 + 2] = out[j].z;
+                            v[h * 16 + j * 4 + 3] = out[j].w;
+                        }
                     }
+                    if (i == 0) {
+                        if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait))) return false;
+                        tc_fence_after();
+                    }
+                    tmem_st32(slot + (uint32_t)(i * (PART_K / 2)), v);
                 }
-                if (i == 0) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                tmem_st32(tmem_slots + lanes + (uint32_t)(s * SLOT_COLS + i * (PART_K / 2)), v);
-            }
+                return true;
+            };
+            ok = is_wide ? decode(std::true_type()) : decode(std::false_type());
             if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
