@@ -153,6 +153,18 @@ def test_tiles_shared_by_clusters_of_each_size(tgemm, op, tiles):
     assert untouched(store, M, N) and tgemm.device_status() == 0
 
 
+@pytest.mark.parametrize("M", [9, 16, 24])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows_of_much_weight(tgemm, fmt, M):
+    N, K = 4100, 4130
+    A, B, a, b = operands(tgemm, "w4", M, N, K, fmt, "wide")
+    store, out = guarded(M, N, torch.float32, 1)
+    call(tgemm, "w4")(A, B, out=out)
+    err = np.abs(out.double().cpu().numpy() - a @ b.T)
+    assert (err <= F32_REL * (np.abs(a) @ np.abs(b).T)).all()
+    assert untouched(store, M, N) and tgemm.device_status() == 0
+
+
 @pytest.mark.parametrize("M", [1, 40, 200, 600])
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("op", OPS)

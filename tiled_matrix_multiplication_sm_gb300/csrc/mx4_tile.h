@@ -37,13 +37,6 @@ __device__ __forceinline__ void tile_coords(int t, const Tiling& p, int& mb, int
 // Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
-// Where it lies in a chunk of codes, of 128-byte rows or of 64-byte rows in the
-// 64-byte swizzle.
-template <int ROW>
-__device__ __forceinline__ uint32_t codes_at(int r, int j) {
-    return ROW == 128 ? swizzled(r, j) : (uint32_t)(r * 64 + ((j ^ (r >> 1 & 3)) << 4));
-}
-
 // Drains this warp's 32 rows of a tile, 64 columns a turn; of SETS sets of
 // epilogue warps, set `set` takes every SETS-th turn. `last_first`: the last
 // 64 columns, which the next tile's accumulator shares, are turn 0. release()
@@ -334,7 +327,10 @@ inline int split_for(long tiles, int steps, unsigned long long fits, int worth) 
     return c < 2 || steps - (steps + c - 1) / c < worth ? 1 : c;
 }
 
-// Pair tiles (256 x 256) once they occupy half of the SM pairs.
+// Pair tiles (256 x 256) once they occupy half of the SM pairs: past that, 128 x
+// 128 tiles are more than the SMs (512 x 5120 x 4096: gemm_w4 26 us, in small
+// tiles 34; gemm_mx4 10.6 and 13.4). Up to 128 rows half of a pair tile would be
+// padding (128 x 14336 x 4096 MXFP4 weights: 27 us, in small tiles 18).
 inline bool use_pair(int M, int N, int num_sms) {
     return M > 128 && (((long)M + 255) / 256) * (((long)N + 255) / 256) * 4 >= num_sms;
 }

@@ -1,17 +1,17 @@
 // BF16 rows times a kept 4-bit matrix, C = alpha A W^T + beta C + bias, on the
 // tensor cores (tcgen05, kind f16): W is made BF16 on its way through shared
-// memory. (Up to MX4_FEW_ROWS rows go to mx4_weights_rows.cu.)
+// memory. (C of few tiles goes to mx4_weights_tmem.cu, few rows to
+// mx4_weights_rows.cu.)
 //
-// The form is that of gemm_mx4's kernel -- 256 x 256 tiles on SM pairs or
-// 128 x 128 on one SM, persistent, two accumulators in tensor memory -- with
-// eight more warps: TMA brings A's rows (64 columns of K, one pipeline stage)
-// and, in chunks of 256 columns, W's codes and scales; the eight warps turn
-// each stage's 128 rows x 64 codes into the 128-byte-swizzled BF16 that the
-// MMA reads, and arrive on the stage's barrier beside A's bytes. A thread
-// takes 32 codes of a row: one 16-byte read, one or two scales, four 16-byte
-// writes. At 3 instructions a weight the warps need half of the 512 cycles
-// that the stage's MMAs take, so the tensor cores stay the bound while C has
-// rows enough for them.
+// The form is that of gemm_mx4's kernel for many tiles -- 256 x 256 tiles on SM
+// pairs, persistent, two accumulators in tensor memory (which leave no room
+// there for W) -- with eight more warps: TMA brings A's rows (64 columns of K,
+// one pipeline stage) and, in chunks of 256 columns, W's codes and scales; the
+// eight warps, two on each of a chunk's four stages, turn 128 rows x 64 codes
+// into the 128-byte-swizzled BF16 that the MMA reads, and arrive on the
+// stage's barrier beside A's bytes. A thread takes 32 codes of a row: one
+// 16-byte read, one or two scales, four 16-byte writes. 8192 x 14336 x 4096
+// MXFP4: 490 us, 620 cycles a stage for 512 of MMAs.
 
 #include "mx4_decode.h"
 #include "mx4_tile.h"
@@ -26,34 +26,28 @@ using namespace mx4_decode;
 
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // 128 rows x 64 BF16
-// Codes come in chunks. Pair tiles read each from L2 and take chunks of as
-// many stages as there are groups of decoding warps, so that a group meets
-// each chunk once; few tiles read W from memory once and take smaller ones.
-template <bool PAIR> constexpr int CHUNK_K_OF = PAIR ? 256 : 128;
-template <bool PAIR> constexpr int CHUNKS_OF = PAIR ? 2 : 6;
+// Codes come in chunks of as many stages as there are groups of decoding
+// warps, so that a group meets each chunk once.
+constexpr int CHUNK_K = 256, CHUNKS = 2;
 constexpr int EPI_WARPS = 4;
 constexpr int EPI_BYTES = EPI_WARPS * BUF_BYTES;
-constexpr int PAIR_STAGES = 5;
-constexpr int MAX_STAGES = 8, MAX_CHUNKS = 6;
+constexpr int STAGES = 5;
+constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;       // a block's rows of A and of W
 constexpr int DECODE_WARPS = 8;
 constexpr int GROUPS = 4;                          // the decoding warps' groups, each on its own stages
 constexpr int GROUP_WARPS = DECODE_WARPS / GROUPS;
 constexpr int CODES_WARP = 2 + EPI_WARPS + DECODE_WARPS;
 constexpr int THREADS = 32 * (CODES_WARP + 1);
 
-template <int FMT, bool PAIR>
-struct Chunk {
-    static constexpr int K = CHUNK_K_OF<PAIR>;
-    static constexpr int STAGES = K / STAGE_K;
-    static constexpr int ROW = K / 2;                // bytes of a row of codes
-    static constexpr int SF_TILES = K / mx4_block(FMT) / 4;
-    static constexpr int CODES = 128 * ROW;
-    static constexpr int BYTES = CODES + SF_TILES * MX4_TILE_BYTES;
-};
+constexpr int CHUNK_STAGES = CHUNK_K / STAGE_K;
+constexpr int ROW = CHUNK_K / 2;                     // bytes of a row of a chunk's codes
+constexpr int CODES_BYTES = 128 * ROW;
+template <int FMT> constexpr int SF_TILES = CHUNK_K / mx4_block(FMT) / 4;
+template <int FMT> constexpr int SF_BYTES = SF_TILES<FMT> * MX4_TILE_BYTES;
 
 struct Sync {
-    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-    uint64_t codes_full[MAX_CHUNKS], codes_empty[MAX_CHUNKS];
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t codes_full[CHUNKS], codes_empty[CHUNKS];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -63,83 +57,58 @@ struct Sync {
 constexpr int SYNC_BYTES = 1408;
 static_assert(sizeof(Sync) <= SYNC_BYTES, "barrier block");
 
-// Shared memory beside the stages.
-template <int FMT, bool PAIR>
-constexpr int fixed_bytes() {
-    return 1024 + CHUNKS_OF<PAIR> * Chunk<FMT, PAIR>::BYTES + EPI_BYTES + SYNC_BYTES;
-}
-constexpr int SMEM_LIMIT = 227 * 1024;
-static_assert(fixed_bytes<TGEMM_NVFP4, true>() + PAIR_STAGES * 2 * OPERAND_BYTES <= SMEM_LIMIT, "shared memory");
+template <int FMT>
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + CHUNKS * (CODES_BYTES + SF_BYTES<FMT>) + EPI_BYTES + SYNC_BYTES;
+static_assert(SMEM<TGEMM_NVFP4> <= 227 * 1024, "shared memory");
 // A warp that waits for a slot has seen the slot's last use but one freed only
 // if its previous stage was at most as many stages back as there are slots
 // (barriers tell phases apart by parity).
-static_assert(PAIR_STAGES >= GROUPS && (SMEM_LIMIT - fixed_bytes<TGEMM_NVFP4, false>()) / (2 * OPERAND_BYTES) >= GROUPS,
-              "fewer slots than groups");
-static_assert(CHUNK_K_OF<true> / STAGE_K == GROUPS && CHUNK_K_OF<false> / STAGE_K * 2 == GROUPS, "chunks and groups");
-static_assert(GROUPS * OPERAND_BYTES >= 128 * 512, "a share fits the stages");
+static_assert(STAGES >= GROUPS && CHUNK_STAGES == GROUPS && ROW == SW, "slots, chunks and groups");
 
 struct Params : Tiling {
     int kblocks;                // of 64 columns
-    // One SM: slots of the pipeline, and the rows of A that a slot holds (the
-    // MMA reads 128: what lies beyond them makes rows of C that are not stored).
-    int stages, a_rows;
     const float* gb;
 };
 
-template <bool PAIR>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (PAIR)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-template <int FMT, bool PAIR, typename TC>
+template <int FMT, typename TC>
 __global__ void __launch_bounds__(THREADS, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC,
                const Params p) {
-    constexpr int TM = PAIR ? 256 : 128, TN = TM, CHUNKS = CHUNKS_OF<PAIR>;
-    const int STAGES = PAIR ? PAIR_STAGES : p.stages;
-    const int A_BYTES = PAIR ? OPERAND_BYTES : p.a_rows * SW, STAGE_BYTES = A_BYTES + OPERAND_BYTES;
-    using CH = Chunk<FMT, PAIR>;
-    constexpr int PER_CHUNK = CH::STAGES;
+    constexpr int TM = 256, TN = 256, A_BYTES = OPERAND_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* codes = smem + STAGES * STAGE_BYTES;
-    uint8_t* epi = codes + CHUNKS * CH::CODES;               // 1 KB aligned, as its swizzle wants
+    uint8_t* epi = codes + CHUNKS * CODES_BYTES;               // 1 KB aligned, as its swizzle wants
     uint8_t* scales = epi + EPI_BYTES;
-    Sync* sy = reinterpret_cast<Sync*>(scales + CHUNKS * (CH::BYTES - CH::CODES));
+    Sync* sy = reinterpret_cast<Sync*>(scales + CHUNKS * SF_BYTES<FMT>);
     const uint32_t stage0 = smem_u32(smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
-    const int part = PAIR ? 0 : blockIdx.x % p.split;
-    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x / p.split;
-    // This block's chunks and K blocks of a tile.
-    const int chunks = (p.kblocks + PER_CHUNK - 1) / PER_CHUNK;
-    const int ch0 = PAIR ? 0 : (int)((long)chunks * part / p.split);
-    const int ch1 = PAIR ? chunks : (int)((long)chunks * (part + 1) / p.split);
-    const int kb0 = ch0 * PER_CHUNK, kb1 = min(ch1 * PER_CHUNK, p.kblocks);
+    const int unit = blockIdx.x >> 1;
+    const int chunks = (p.kblocks + CHUNK_STAGES - 1) / CHUNK_STAGES;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             // A's bytes of both blocks, and the decoding warps' arrivals.
-            mbar_init(smem_u32(&sy->full[s]), 1 + (PAIR ? 2 : 1) * GROUP_WARPS);
+            mbar_init(smem_u32(&sy->full[s]), 1 + 2 * GROUP_WARPS);
             mbar_init(smem_u32(&sy->empty[s]), 1);
         }
         for (int c = 0; c < CHUNKS; ++c) {
             mbar_init(smem_u32(&sy->codes_full[c]), 1);
-            mbar_init(smem_u32(&sy->codes_empty[c]), PER_CHUNK * GROUP_WARPS);
+            mbar_init(smem_u32(&sy->codes_empty[c]), DECODE_WARPS);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&sy->tmem_full[a]), 1);
-            mbar_init(smem_u32(&sy->tmem_empty[a]), (PAIR ? 2 : 1) * EPI_WARPS);
+            mbar_init(smem_u32(&sy->tmem_empty[a]), 2 * EPI_WARPS);
         }
         mbar_init(smem_u32(&sy->drain), 1);
         sy->abort = 0;
@@ -150,10 +119,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         prefetch_map(&tmSB);
     }
     if (threadIdx.x < 256) sy->factors[threadIdx.x] = factor<FMT>(threadIdx.x);
-    if (warp == 1) tmem_alloc<PAIR, TMEM_COLS>(smem_u32(&sy->tmem_base));
+    if (warp == 1) tmem_alloc<true, TMEM_COLS>(smem_u32(&sy->tmem_base));
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = sy->tmem_base;
     pdl_launch_dependents();
@@ -161,9 +130,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     const Wait wait{&sy->abort, p.status, p.wait_limit_ns};
     // The leader's barriers, as cluster addresses.
-    const uint32_t full0 = PAIR ? map_to_rank(smem_u32(&sy->full[0]), 0) : smem_u32(&sy->full[0]);
-    const uint32_t tmem_empty0 =
-        PAIR ? map_to_rank(smem_u32(&sy->tmem_empty[0]), 0) : smem_u32(&sy->tmem_empty[0]);
+    const uint32_t full0 = map_to_rank(smem_u32(&sy->full[0]), 0);
+    const uint32_t tmem_empty0 = map_to_rank(smem_u32(&sy->tmem_empty[0]), 0);
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
@@ -174,13 +142,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int mb, nb;
             tile_coords(t, p, mb, nb);
             const int row = mb * TM + (int)rank * 128;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int kb = 0; kb < p.kblocks; ++kb) {
                 ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
                 if (!stall) {
                     if (elect_one()) {
-                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), (PAIR ? 2 : 1) * A_BYTES);
-                        tma_load_2d<PAIR>(stage0 + s * STAGE_BYTES, &tmA, kb * STAGE_K, row,
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), 2 * A_BYTES);
+                        tma_load_2d<true>(stage0 + s * STAGE_BYTES, &tmA, kb * STAGE_K, row,
                                           full0 + (uint32_t)(s * sizeof(uint64_t)));
                     }
                     armed |= 1u << s;
@@ -217,7 +185,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)((it & 1) * TN);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = 0; kb < p.kblocks; ++kb) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
@@ -225,16 +193,16 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         const uint32_t a = stage0 + s * STAGE_BYTES;
 #pragma unroll
                         for (int k = 0; k < STAGE_K / 16; ++k)
-                            mma_bf16<PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
-                                           smem_desc(a + A_BYTES + k * 32, 16, 1024, 2), IDESC, kb != kb0 || k != 0);
-                        tc_commit<PAIR>(smem_u32(&sy->empty[s]));
-                        if (kb == kb1 - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                            mma_bf16(d, smem_desc(a + k * 32, 16, 1024, 2),
+                                           smem_desc(a + A_BYTES + k * 32, 16, 1024, 2), IDESC, kb != 0 || k != 0);
+                        tc_commit<true>(smem_u32(&sy->empty[s]));
+                        if (kb == p.kblocks - 1) tc_commit<true>(smem_u32(&sy->tmem_full[it & 1]));
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (elect_one()) tc_commit<PAIR>(smem_u32(&sy->drain));
+            if (elect_one()) tc_commit<true>(smem_u32(&sy->drain));
             mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
         __syncwarp();
@@ -255,14 +223,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 31) {
                     const uint32_t bar = tmem_empty0 + (uint32_t)((it & 1) * sizeof(uint64_t));
-                    if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
+                    mbar_arrive_cluster(bar);
                 }
             };
-            if (!PAIR && p.split > 1) {
-                // The tile's copies and MMAs are done: its stages hold the share.
-                store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
-                break;
-            }
             drain_tile<TN, 1, false, 1, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
                                    mb * TM + (int)rank * 128 + q * 32, nb * TN, false, 0, TN / 64 - 1,
                                         unscale<FMT>(), gb, release);
@@ -279,14 +242,14 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int mb, nb;
             tile_coords(t, p, mb, nb);
             const int col = nb * TN + (int)rank * 128;
-            for (int ch = ch0; ch < ch1; ++ch) {
+            for (int ch = 0; ch < chunks; ++ch) {
                 ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_empty[c]), ph ^ 1u, wait));
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = smem_u32(&sy->codes_full[c]);
-                    mbar_arrive_expect_tx(bar, CH::BYTES);
-                    tma_load_2d<false>(smem_u32(codes) + c * CH::CODES, &tmB, ch * CH::ROW, col, bar);
-                    tma_load_3d<false>(smem_u32(scales) + c * (CH::BYTES - CH::CODES), &tmSB, 0, ch * CH::SF_TILES,
+                    mbar_arrive_expect_tx(bar, CODES_BYTES + SF_BYTES<FMT>);
+                    tma_load_2d<false>(smem_u32(codes) + c * CODES_BYTES, &tmB, ch * ROW, col, bar);
+                    tma_load_3d<false>(smem_u32(scales) + c * SF_BYTES<FMT>, &tmSB, 0, ch * SF_TILES<FMT>,
                                        col / 128, bar);
                 }
                 __syncwarp();
@@ -302,33 +265,28 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // Group i takes stages i, i + GROUPS, .. of the block's. A stage's
         // values are made before its slot is free: between a slot's release
         // and its readiness lie only the writes, their fence and the arrival.
-        // A chunk of pair tiles has a stage for every group; all release it,
-        // in a tile's last one those without a stage too. Without pairs a
-        // block has one tile, whose chunks have stages for half of the groups
-        // in turn; the others pass them by.
+        // All groups release each chunk, in a tile's last one those without a
+        // stage too.
         const int dw = warp - 2 - EPI_WARPS, group = dw / GROUP_WARPS;
         const int tid = dw % GROUP_WARPS * 32 + lane;
         constexpr int ITEMS = 256 / (32 * GROUP_WARPS);          // runs of 32 codes a thread and stage
         uint32_t cph = 0, sph = 1;                               // parities to wait for
-        int c = 0, s = group, next = kb0 + group;                // this group's next stage: its slot, its K block
+        int c = 0, s = group, next = group;                      // this group's next stage: its slot, its K block
         bool ok = true;
-        for (int t = unit; ok && t < p.num_tiles; t += p.units, next -= kb1 - kb0) {
-            for (int ch = ch0; ch < ch1; ++ch) {
-                const bool mine = next < min((ch + 1) * PER_CHUNK, kb1);
-                if (PAIR || mine) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
-                    if (!ok) break;
-                }
-                if (mine) {
-                    const int q = next - ch * PER_CHUNK;
+        for (int t = unit; ok && t < p.num_tiles; t += p.units, next -= p.kblocks) {
+            for (int ch = 0; ch < chunks; ++ch) {
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->codes_full[c]), cph, wait));
+                if (!ok) break;
+                if (next < min((ch + 1) * CHUNK_STAGES, p.kblocks)) {
+                    const int q = next - ch * CHUNK_STAGES;
                     uint4 w[ITEMS];
                     uint32_t b0[ITEMS], b1[ITEMS];
                     bool is_wide = false;
 #pragma unroll
                     for (int i = 0; i < ITEMS; ++i) {
                         const int item = i * 32 * GROUP_WARPS + tid, row = item & 127, half = item >> 7;
-                        w[i] = *reinterpret_cast<const uint4*>(codes + c * CH::CODES + codes_at<CH::ROW>(row, q * 2 + half));
-                        const uint8_t* sc = scales + c * (CH::BYTES - CH::CODES) + (row & 31) * 16 + (row >> 5) * 4;
+                        w[i] = *reinterpret_cast<const uint4*>(codes + c * CODES_BYTES + swizzled(row, q * 2 + half));
+                        const uint8_t* sc = scales + c * SF_BYTES<FMT> + (row & 31) * 16 + (row >> 5) * 4;
                         if (FMT == TGEMM_MXFP4) {
                             b0[i] = b1[i] = sc[(q >> 1) * MX4_TILE_BYTES + (q & 1) * 2 + half];
                             is_wide |= wide(b0[i]);
@@ -370,7 +328,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     s += GROUPS;
                     if (s >= STAGES) { s -= STAGES; sph ^= 1u; }
                 }
-                if ((PAIR || mine) && lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
+                if (lane == 0) mbar_arrive(smem_u32(&sy->codes_empty[c]));
                 if (++c == CHUNKS) { c = 0; cph ^= 1u; }
             }
         }
@@ -378,67 +336,46 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
-    if (!PAIR && p.split > 1) {
-        int mb, nb;
-        tile_coords(unit, p, mb, nb);
-        join_shares<TC>(p, smem, 128, part, mb * TM, nb * TN, unscale<FMT>(), mx4_g(p.gb));
-    }
-    if (warp == 1) tmem_free<PAIR, TMEM_COLS>(tmem_base);
+    if (warp == 1) tmem_free<true, TMEM_COLS>(tmem_base);
 }
 
-template <int FMT, bool PAIR, typename TC>
+template <int FMT, typename TC>
 cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, const Mx4Out& out,
                    int num_sms, cudaStream_t s) {
     const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (enc == nullptr) return cudaErrorNotSupported;
-    constexpr int TILE = PAIR ? 256 : 128;
     CUtensorMap tmA, tmB, tmSB, tmC;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)lda * 2};
-    const int a_rows = PAIR || M > 96 ? 128 : (M + 31) / 32 * 32;
-    const cuuint32_t box[2] = {STAGE_K, (cuuint32_t)a_rows};
+    const cuuint32_t box[2] = {STAGE_K, 128};
     if (!encode(enc, &tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_codes(enc, &tmB, B, N, K, Chunk<FMT, PAIR>::ROW) ||
-        !encode_scales(enc, &tmSB, B, N, K, FMT, Chunk<FMT, PAIR>::SF_TILES, 1))
+        !encode_codes(enc, &tmB, B, N, K) || !encode_scales(enc, &tmSB, B, N, K, FMT, SF_TILES<FMT>, 1))
         return cudaErrorInvalidValue;
     memset(&tmC, 0, sizeof(tmC));
     Params p;
-    cudaError_t e = make_tiling(p, M, N, TILE, TILE, PAIR ? num_sms / 2 : num_sms, out);
+    cudaError_t e = make_tiling(p, M, N, 256, 256, num_sms / 2, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.gb = B.g;
-    p.a_rows = a_rows;
-    const int slot = a_rows * SW + OPERAND_BYTES;
-    p.stages = PAIR ? PAIR_STAGES : (SMEM_LIMIT - fixed_bytes<FMT, PAIR>()) / slot;
-    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-    const int smem = fixed_bytes<FMT, PAIR>() + p.stages * slot;
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
-    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, PAIR, TC>>(SMEM_LIMIT);
-    if (!PAIR && p.num_tiles * 2 <= num_sms) {
-        // 3 chunks: 64 x 2048 x 512, 2 saved, 7.0 us both whole and split;
-        // x 1024 in halves, 4 saved, 10.0 and 8.5.
-        unsigned long long fits = 0;
-        if (e == cudaSuccess) e = clusters_that_fit<weights_kernel<FMT, PAIR, TC>>(THREADS, SMEM_LIMIT, &fits);
-        p.split = split_for(p.num_tiles, p.kblocks / Chunk<FMT, PAIR>::STAGES, fits, 3);
-        p.units = p.num_tiles;
-    }
+    if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, TC>>(SMEM<FMT>);
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, THREADS, smem, PAIR ? 2 : p.split, s);
-    return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, PAIR, TC>, tmA, tmB, tmSB, tmC, p);
+    ClusterLaunch cfg(2 * p.units, THREADS, SMEM<FMT>, 2, s);
+    return cudaLaunchKernelEx(&cfg.config, weights_kernel<FMT, TC>, tmA, tmB, tmSB, tmC, p);
 }
 
-template <int FMT, bool PAIR>
+template <int FMT>
 cudaError_t launch_type(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, const Mx4Out& out,
                         int num_sms, cudaStream_t s) {
-    return out.c_type == TGEMM_TYPE_F32 ? launch<FMT, PAIR, float>(M, N, K, A, lda, B, out, num_sms, s)
-                                        : launch<FMT, PAIR, __nv_bfloat16>(M, N, K, A, lda, B, out, num_sms, s);
+    return out.c_type == TGEMM_TYPE_F32 ? launch<FMT, float>(M, N, K, A, lda, B, out, num_sms, s)
+                                        : launch<FMT, __nv_bfloat16>(M, N, K, A, lda, B, out, num_sms, s);
 }
 
 cudaError_t run(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt, const Mx4Out& out,
                 int num_sms, cudaStream_t s) {
     if (use_pair(M, N, num_sms))
-        return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4, true>(M, N, K, A, lda, B, out, num_sms, s)
-                                  : launch_type<TGEMM_NVFP4, true>(M, N, K, A, lda, B, out, num_sms, s);
+        return fmt == TGEMM_MXFP4 ? launch_type<TGEMM_MXFP4>(M, N, K, A, lda, B, out, num_sms, s)
+                                  : launch_type<TGEMM_NVFP4>(M, N, K, A, lda, B, out, num_sms, s);
     return mx4_weights_tmem(M, N, K, A, lda, B, fmt, out, s);
 }
 
@@ -448,7 +385,7 @@ cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4O
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
     if (K == 0) return mx4_empty_sum(M, N, out, s);
     // (Its offsets within 32 rows of codes are 32-bit.)
-    if (M <= MX4_FEW_ROWS && K < 1 << 27) return mx4_weights_rows(M, N, K, A, lda, B, fmt, out, num_sms, s);
+    if (mx4_few_rows(M, N, K) && K < 1 << 27) return mx4_weights_rows(M, N, K, A, lda, B, fmt, out, num_sms, s);
     if (reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 8 == 0)
         return run(M, N, K, A, lda, B, fmt, out, num_sms, s);
     // TMA copies rows that start on 16-byte boundaries: others are repacked.
