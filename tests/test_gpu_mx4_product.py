@@ -38,6 +38,8 @@ class Operand:
             scales = rng.integers(126, 129, (R, nb)) if kind == "whole" else rng.integers(100, 150, (R, nb))
         else:
             scales = rng.integers(0x38, 0x42, (R, nb)) if kind == "whole" else rng.integers(0, 0x7F, (R, nb))
+        if kind == "normal":
+            scales = rng.integers(*{"mxfp4": (117, 121), "nvfp4": (0x58, 0x7F)}[fmt], (R, nb))
         self.g = None if g is None else torch.tensor([g], device="cuda")
         self.q = tgemm.mx4_pack(torch.from_numpy(ref.pack_codes(codes)).cuda(),
                                 torch.from_numpy(np.ascontiguousarray(scales.astype(np.uint8))).cuda(), fmt, cols=C, tensor_scale=self.g)
@@ -49,6 +51,8 @@ class Operand:
 def activations(M, K, kind, seed, ld=None):
     rng = np.random.default_rng(seed)
     x = rng.integers(-4, 5, (M, K)) / 2.0 if kind == "whole" else rng.standard_normal((M, K)) * 2.0 ** rng.integers(-9, 9, (M, 1))
+    if kind == "normal":
+        x = rng.standard_normal((M, K))
     X = torch.full((M, ld or K), float("nan"), dtype=torch.bfloat16)
     X[:, :K] = torch.from_numpy(x).to(torch.bfloat16)
     X = X.cuda()[:, :K]
@@ -139,6 +143,43 @@ def test_a_long_sum(tgemm, op):
     A, B, a, b = operands(tgemm, op, 20, 260, 14336, "nvfp4", "wide", 0.5)
     got = call(tgemm, op)(A, B).double().cpu().numpy()
     assert (np.abs(got - a @ b.T) <= (F32_REL + 2.0 ** -20) * (np.abs(a) @ np.abs(b).T)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 4096, 14336), (100, 300, 9000), (60, 20000, 4096), (2100, 1100, 14336)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_long_sums_keep_their_low_bits(tgemm, fmt, M, N, K):
+    """Positive terms, whose roundings all go one way where they are cut off.
+
+    A part of 1024 columns is 64 steps of an MMA; each step cuts off at most
+    2^-23 of the partial sum in adding its 16 products up and as much in adding
+    to the accumulator. Partial sums of such terms grow evenly: (64 + 1) / 2 of
+    the part's in all. Fourteen parts, a cluster's shares and the output rule
+    round to nearest, 20 additions at most. 5 % for the uneven growth.
+    """
+    rng = np.random.default_rng(K + N)
+    codes = rng.integers(1, 8, (N, K))
+    scales = np.full((N, ref.blocks(K, fmt)), {"mxfp4": 127, "nvfp4": 0x38}[fmt], np.uint8)
+    B = tgemm.mx4_pack(torch.from_numpy(ref.pack_codes(codes)).cuda(), torch.from_numpy(scales).cuda(), fmt, cols=K)
+    A = torch.from_numpy(rng.uniform(0.5, 1.5, (M, K))).to(torch.bfloat16)
+    want = A.double().numpy() @ ref.values(codes, scales, fmt).T
+    got = tgemm.gemm_w4(A.cuda(), B).double().cpu().numpy()
+    rel = np.abs(got / want - 1.0).max()
+    assert rel <= 1.05 * (2 * 2.0 ** -23 * (64 + 1) / 2 + 20 * 2.0 ** -24), rel
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 4096, 14336), (128, 2000, 14336), (300, 4096, 14336)])
+def test_long_sums_are_as_exact_as_fp32(tgemm, M, N, K):
+    """Terms of both signs, against the result's norm.
+
+    A step of an MMA cuts off 2^-24 of the partial sum on average. Partial sums
+    of such terms grow as the root of their number: 2/3 of a part's end on
+    average over its 64 steps, and the parts' errors add up as the parts do.
+    """
+    A, B, a, b = operands(tgemm, "w4", M, N, K, "nvfp4", "normal")
+    got = tgemm.gemm_w4(A, B).double().cpu().numpy()
+    want = a @ b.T
+    rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert rel <= 64 * (2 / 3) * 2.0 ** -24, rel
 
 
 @pytest.mark.parametrize("tiles", [2, 16, 25, 30, 40, 70])      # shared by 8, 6, 5, 4, 3 and 2 blocks each on 152 SMs

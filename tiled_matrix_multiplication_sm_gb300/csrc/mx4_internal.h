@@ -110,7 +110,7 @@ cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4O
 // At most MX4_FEW_ROWS rows of A (mx4_weights_rows.cu): all products with up to
 // 8, and small ones with more, where its shorter start counts. 24 x 1024 x 1024
 // MXFP4 takes 3.9 us there and 4.6 in mx4_weights_tmem.cu; 24 x 4096 x 4096 NVFP4
-// 8.9 and 7.7; 16 x 4096 x 14336 16.6 and 15.0; 8 x 4096 x 14336 13.4 and 14.9.
+// 8.9 and 7.7; 16 x 4096 x 14336 16.6 and 16.0; 8 x 4096 x 14336 13.4 and 14.9.
 constexpr int MX4_FEW_ROWS = 24;
 inline bool mx4_few_rows(int M, int N, int K) { return M <= 8 || (M <= MX4_FEW_ROWS && (long)N * K < 1L << 24); }
 cudaError_t mx4_weights_rows(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,

@@ -67,6 +67,10 @@ static_assert(STAGES >= GROUPS && CHUNK_STAGES == GROUPS && ROW == SW, "slots, c
 
 struct Params : Tiling {
     int kblocks;                // of 64 columns
+    // The sum of a tile in `parts` parts (a long one, FP32 C): each is made in
+    // the second accumulator and added to the first (8192 x 14336 x 4096 MXFP4
+    // with FP32 C: 615 us, in one part 541).
+    int parts, part_blocks;
     const float* gb;
 };
 
@@ -175,17 +179,20 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // ---------------------------------------------------- MMA issuer
         if (leader) {
             constexpr uint32_t IDESC = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(TN >> 3) << 17 | (uint32_t)(TM >> 4) << 24;
-            int it = 0, s = 0;
+            int s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
-                // The tile two before, which used this accumulator, is out.
-                if (it >= 2 && !__all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[it & 1]),
-                                                                     (uint32_t)((it >> 1) - 1) & 1u, wait)))
-                    break;
+            for (int i = 0; ok; ++i) {
+                const int t = unit + i / p.parts * p.units, part = i % p.parts;
+                if (t >= p.num_tiles) break;
+                // What this accumulator held before is out.
+                const int acc = p.parts > 1 ? 1 : i & 1, turn = p.parts > 1 ? i : i >> 1;
+                ok = turn == 0 || __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[acc]), (uint32_t)(turn - 1) & 1u, wait));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)((it & 1) * TN);
-                for (int kb = 0; kb < p.kblocks; ++kb) {
+                const uint32_t d = tmem_base + (uint32_t)(acc * TN);
+                const int first = part * p.part_blocks, last = min(first + p.part_blocks, p.kblocks) - 1;
+                for (int kb = first; kb <= last; ++kb) {
                     ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
@@ -193,10 +200,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         const uint32_t a = stage0 + s * STAGE_BYTES;
 #pragma unroll
                         for (int k = 0; k < STAGE_K / 16; ++k)
-                            mma_bf16(d, smem_desc(a + k * 32, 16, 1024, 2),
-                                           smem_desc(a + A_BYTES + k * 32, 16, 1024, 2), IDESC, kb != 0 || k != 0);
+                            mma_bf16(d, smem_desc(a + k * 32, 16, 1024, 2), smem_desc(a + A_BYTES + k * 32, 16, 1024, 2),
+                                     IDESC, kb != first || k != 0);
                         tc_commit<true>(smem_u32(&sy->empty[s]));
-                        if (kb == p.kblocks - 1) tc_commit<true>(smem_u32(&sy->tmem_full[it & 1]));
+                        if (kb == last) tc_commit<true>(smem_u32(&sy->tmem_full[acc]));
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -211,24 +218,43 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
         uint8_t* bufs = epi + (warp - 2) * BUF_BYTES;
         const float gb = mx4_g(p.gb);
-        int it = 0;
-        for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
+        const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+        bool ok = true;
+        uint32_t it = 0;
+        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
             int mb, nb;
             tile_coords(t, p, mb, nb);
-            const bool ok = mbar_wait(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            auto release = [&]() {
+            auto release = [&](int acc) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 31) {
-                    const uint32_t bar = tmem_empty0 + (uint32_t)((it & 1) * sizeof(uint64_t));
-                    mbar_arrive_cluster(bar);
-                }
+                if (lane == 31) mbar_arrive_cluster(tmem_empty0 + (uint32_t)(acc * sizeof(uint64_t)));
             };
-            drain_tile<TN, 1, false, 1, TC>(p, &tmC, tmem_base + (uint32_t)((it & 1) * TN) + ((uint32_t)(q * 32) << 16), bufs,
-                                   mb * TM + (int)rank * 128 + q * 32, nb * TN, false, 0, TN / 64 - 1,
-                                        unscale<FMT>(), gb, release);
+            const int row0 = mb * TM + (int)rank * 128 + q * 32;
+            bool stored = false;
+            if constexpr (sizeof(TC) == 4) {
+                if (p.parts > 1) {
+                    for (int part = 0; ok && part < p.parts; ++part, ++it) {
+                        ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_full[1]), it & 1u, wait));
+                        if (!ok) break;
+                        tc_fence_after();
+                        add_sums(lanes, lanes + TN, TN, part == 0);
+                        release(1);
+                    }
+                    if (!ok) break;
+                    drain_tile<TN, 1, false, 1, TC>(p, &tmC, lanes, bufs, row0, nb * TN, false, 0, TN / 64 - 1,
+                                                    unscale<FMT>(), gb, [] {});
+                    stored = true;
+                }
+            }
+            if (!stored) {
+                const int acc = (int)(it & 1);
+                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_full[acc]), it >> 1 & 1u, wait));
+                if (!ok) break;
+                ++it;
+                tc_fence_after();
+                drain_tile<TN, 1, false, 1, TC>(p, &tmC, lanes + (uint32_t)(acc * TN), bufs, row0, nb * TN, false, 0,
+                                                TN / 64 - 1, unscale<FMT>(), gb, [&] { release(acc); });
+            }
         }
         tma_store_wait_all();
     } else if (warp == CODES_WARP) {
@@ -356,6 +382,8 @@ cudaError_t launch(int M, int N, int K, const void* A, long lda, const Mx4Operan
     Params p;
     cudaError_t e = make_tiling(p, M, N, 256, 256, num_sms / 2, out);
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
+    p.part_blocks = sizeof(TC) == 4 ? SUM_K / STAGE_K : p.kblocks;
+    p.parts = (p.kblocks + p.part_blocks - 1) / p.part_blocks;
     p.gb = B.g;
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
     if (e == cudaSuccess) e = set_smem_limit_once<weights_kernel<FMT, TC>>(SMEM<FMT>);

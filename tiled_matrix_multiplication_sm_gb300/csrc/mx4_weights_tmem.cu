@@ -12,10 +12,12 @@
 //
 // A block has one tile, or a share of its sum over K. A stage is 128 columns
 // of K: with 64, the handshakes of the warp that issues the MMAs take longer
-// than the MMAs (64 x 14336 x 4096 MXFP4: 18.3 us, with 128 17.7). TMA brings X's rows into a stage's slot, and W's codes and
-// scales into a longer ring; two groups of four warps decode half of the stage
-// each (a thread one row of W: two 16-byte reads, two to four scales, 32
-// columns of tensor memory written), two other groups the next stage.
+// than the MMAs (64 x 14336 x 4096 MXFP4: 18.3 us, with 128 17.7). TMA brings
+// X's rows into a stage's slot, and W's codes and scales into a longer ring;
+// four groups of four warps decode every fourth stage each (a thread one row of W:
+// four 16-byte reads, four to eight scales, 64 columns of tensor memory
+// written; half stages to twice as many groups' turns: 17.7 us, whole ones 16.4).
+// Four more warps add up the parts of long sums (SUM_K).
 
 #include "mx4_decode.h"
 #include "mx4_tile.h"
@@ -36,15 +38,17 @@ constexpr int GROUPS = 4;                            // of decoding warps, each 
 constexpr int ROW = STAGE_K / 2;                     // bytes of a row of a stage's codes
 constexpr int CODES_BYTES = TW * ROW;
 constexpr int SLOTS = 4, CHUNKS = 8;                // rings of X and decoded weights, of codes
-constexpr int SUM_COLS = 128, SLOT_COLS = STAGE_K / 2;   // of tensor memory: sums, then slots of weights
+constexpr int SUM_COLS = 128, SLOT_COLS = STAGE_K / 2;   // of tensor memory: a sum, a long sum's total, slots of weights
+constexpr int PART_STAGES = SUM_K / STAGE_K;
 constexpr int DECODE_WARPS = 4 * GROUPS;
 constexpr int CODES_WARP = 2 + DECODE_WARPS;
-constexpr int THREADS = 32 * (CODES_WARP + 1);
+template <typename TC> constexpr bool LONG_SUMS = sizeof(TC) == 4;
+template <typename TC> constexpr int THREADS = 32 * (CODES_WARP + 1 + (LONG_SUMS<TC> ? 4 : 0));
 constexpr int SMEM_LIMIT = 227 * 1024;
 // A group meets all uses of the slots and codes that it meets at all (barriers
 // tell phases apart by parity).
 static_assert(SLOTS % GROUPS == 0 && CHUNKS % GROUPS == 0, "groups");
-static_assert(SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * PARTS * SW >= TW * 4,
+static_assert(2 * SUM_COLS + SLOTS * SLOT_COLS <= TMEM_COLS && SLOTS * PARTS * SW >= TW * 4,
               "room for the slots, and for a share in them");
 
 template <int FMT> constexpr int SF_TILES = STAGE_K / mx4_block(FMT) / 4;
@@ -53,7 +57,7 @@ template <int FMT> constexpr int SF_BYTES = SF_TILES<FMT> * MX4_TILE_BYTES;
 struct Sync {
     uint64_t full[SLOTS], empty[SLOTS];
     uint64_t codes_full[CHUNKS], codes_empty[CHUNKS];
-    uint64_t done, drain;
+    uint64_t done, drain, part_full[2], part_empty[2];
     uint32_t tmem_base;
     int abort;
     uint32_t factors[256];
@@ -89,7 +93,7 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint32_t a, uint64_t b, uin
 }
 
 template <int FMT, typename TC>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS<TC>, 1)
 weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmS, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -106,6 +110,12 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
     // This block's stages of its tile.
     const int k0 = (int)((long)p.stages * part / p.split), k1 = (int)((long)p.stages * (part + 1) / p.split);
 
+    // A long sum's parts alternate between two accumulators where there is room
+    // (FP32 C, MXFP4, 14336 x 4096: 64 rows 17.3 us, with one 17.8, in one part
+    // 16.4; 128 rows, with one 21.9, in one part 18.4).
+    const bool long_sum = LONG_SUMS<TC> && k1 - k0 > PART_STAGES;
+    const int accs = p.rows <= SUM_COLS / 2 ? 2 : 1;
+
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(smem_u32(&sy->full[s]), 1 + 4);          // X's bytes, a group's warps
@@ -115,7 +125,11 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             mbar_init(smem_u32(&sy->codes_full[c]), 1);
             mbar_init(smem_u32(&sy->codes_empty[c]), 4);
         }
-        mbar_init(smem_u32(&sy->done), 1);
+        mbar_init(smem_u32(&sy->done), long_sum ? 4 : 1);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&sy->part_full[a]), 1);
+            mbar_init(smem_u32(&sy->part_empty[a]), 4);
+        }
         mbar_init(smem_u32(&sy->drain), 1);
         sy->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -129,7 +143,7 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = sy->tmem_base, tmem_slots = tmem_base + SUM_COLS;
+    const uint32_t tmem_base = sy->tmem_base, tmem_slots = tmem_base + 2 * SUM_COLS;
     pdl_launch_dependents();
     pdl_wait();
 
@@ -164,18 +178,26 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         // ---------------------------------------------------- MMA issuer
         const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(p.rows >> 3) << 17 | (uint32_t)(TW >> 4) << 24;
         if (elect_one()) {
-            int s = 0;
+            int s = 0, in_part = 0, acc = 0, turn = 0;     // of a part: stages done, its accumulator and that one's turn
             uint32_t ph = 0;
-            for (int k = k0; k < k1; ++k) {
+            for (int k = k0; k < k1; ++k, ++in_part) {
+                if (long_sum && in_part == PART_STAGES) {
+                    in_part = 0;
+                    if (++acc == accs) { acc = 0; ++turn; }
+                }
+                if (in_part == 0 && turn > 0 &&
+                    !mbar_wait(smem_u32(&sy->part_empty[acc]), (uint32_t)(turn - 1) & 1u, wait)) break;
                 if (!mbar_wait(smem_u32(&sy->full[s]), ph, wait)) break;
                 tc_fence_after();
                 const uint32_t x = smem_u32(smem) + s * slot_bytes, w = tmem_slots + (uint32_t)(s * SLOT_COLS);
 #pragma unroll
                 for (int j = 0; j < STAGE_K / 16; ++j)
-                    mma_bf16(tmem_base, w + j * 8, smem_desc(x + j / 4 * part_bytes + j % 4 * 32, 16, 1024, 2), idesc,
-                             k != k0 || j != 0);
+                    mma_bf16(tmem_base + acc * (SUM_COLS / 2), w + j * 8, smem_desc(x + j / 4 * part_bytes + j % 4 * 32, 16, 1024, 2), idesc,
+                             in_part != 0 || j != 0);
                 tc_commit<false>(smem_u32(&sy->empty[s]));
-                if (k == k1 - 1) tc_commit<false>(smem_u32(&sy->done));
+                if (long_sum && (in_part == PART_STAGES - 1 || k == k1 - 1))
+                    tc_commit<false>(smem_u32(&sy->part_full[acc]));
+                if (!long_sum && k == k1 - 1) tc_commit<false>(smem_u32(&sy->done));
                 if (++s == SLOTS) { s = 0; ph ^= 1u; }
             }
             tc_commit<false>(smem_u32(&sy->drain));
@@ -202,6 +224,20 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         for (int i = 0; i < CHUNKS; ++i)
             if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->codes_full[i]), (armed_parity >> i) & 1u, wait);
         __syncwarp();
+    } else if (warp > CODES_WARP) {
+        // -------------------------------------------- parts of long sums
+        if (long_sum) {
+            const uint32_t sum = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+            for (int k = k0, part = 0; k < k1; k += PART_STAGES, ++part) {
+                const int acc = part % accs;
+                if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->part_full[acc]), (uint32_t)(part / accs) & 1u, wait))) break;
+                tc_fence_after();
+                add_sums(sum + SUM_COLS, sum + acc * (SUM_COLS / 2), p.rows, part == 0);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(k + PART_STAGES < k1 ? &sy->part_empty[acc] : &sy->done));
+            }
+        }
     } else {
         // ------------------------------------------------------ decoding
         // A stage's values are made before its slot is free.
@@ -280,10 +316,11 @@ weights_tmem_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             tc_fence_after();
             const int piece = row >> 2;
             uint8_t* at = smem + (row & 3) * 4;
+            const uint32_t sum = tmem_base + (long_sum ? SUM_COLS : 0);
 #pragma unroll 1
             for (int m = group * 32; m < p.rows; m += 32 * GROUPS) {
                 uint32_t r[32];
-                tmem_ld32(tmem_base + lanes + (uint32_t)m, r);
+                tmem_ld32(sum + lanes + (uint32_t)m, r);
                 tmem_wait_ld(r);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -317,10 +354,10 @@ cudaError_t launch(int M, int N, int K, const void* X, long ldx, const Mx4Operan
     p.gb = W.g;
     if (e == cudaSuccess) e = set_smem_limit_once<weights_tmem_kernel<FMT, TC>>(SMEM_LIMIT);
     unsigned long long fits = 0;
-    if (e == cudaSuccess) e = clusters_that_fit<weights_tmem_kernel<FMT, TC>>(THREADS, SMEM_LIMIT, &fits);
+    if (e == cudaSuccess) e = clusters_that_fit<weights_tmem_kernel<FMT, TC>>(THREADS<TC>, SMEM_LIMIT, &fits);
     if (e != cudaSuccess) return e;
     p.split = split_for(p.num_tiles, p.stages, fits, 3);
-    ClusterLaunch cfg(p.split * p.num_tiles, THREADS, smem_bytes<FMT>(p.rows), p.split, s);
+    ClusterLaunch cfg(p.split * p.num_tiles, THREADS<TC>, smem_bytes<FMT>(p.rows), p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_tmem_kernel<FMT, TC>, tmX, tmW, tmS, p);
 }
 
