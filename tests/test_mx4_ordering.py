@@ -1,0 +1,36 @@
+"""What the kernels of the 4-bit operators hand from one block or kernel to
+another, read from their sources (no GPU)."""
+import glob
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tiled_matrix_multiplication_sm_gb300", "csrc")
+
+
+def sources():
+    files = sorted(glob.glob(os.path.join(CSRC, "mx4_*")))
+    assert files
+    for path in files:
+        with open(path) as f:
+            yield os.path.basename(path), f.read()
+
+
+def test_arrivals_on_another_blocks_barrier_have_cluster_scope():
+    """Without a scope PTX takes the block's own, which orders nothing between two blocks."""
+    found = 0
+    for name, text in sources():
+        for arrival in re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster", text):
+            found += 1
+            assert re.search(r"\.(release|relaxed)\.cluster\.shared::cluster", arrival), (name, arrival)
+    assert found
+
+
+def test_relaxed_arrivals_come_after_a_fence():
+    for name, text in sources():
+        if "mbar_arrive_cluster(" not in text or name == "mx4_ptx.h":
+            continue
+        lines = text.split("\n")
+        for i, line in enumerate(lines):
+            if "mbar_arrive_cluster(" in line:
+                before = "\n".join(lines[max(0, i - 5):i])
+                assert "tc_fence_before()" in before or "release_smem()" in before, (name, i + 1)

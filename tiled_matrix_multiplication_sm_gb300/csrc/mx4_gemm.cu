@@ -147,7 +147,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int row = mb * S::TM + (int)rank * 128;
                 const int col = nb * S::TN + (int)rank * 128;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                    ok = __all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                     if (!ok) break;
                     if (!stall) {
                     if (elect_one()) {
@@ -171,7 +171,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (leader) {
                 for (int s = 0; s < STAGES; ++s)
                     if (armed & (1u << s))
-                        mbar_wait<false>(smem_u32(&sy->full[s]), (armed_parity >> s) & 1u, wait);
+                        mbar_wait<false, PAIR>(smem_u32(&sy->full[s]), (armed_parity >> s) & 1u, wait);
             } else if (*(volatile int*)&sy->abort) {
                 // After a timeout this block cannot observe its own copies;
                 // give any in flight time to land (a copy takes microseconds).
@@ -194,14 +194,14 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 // memory (and with them all of the tile before it). Single:
                 // the tile two before, which used this accumulator.
                 if (PAIR ? it >= 1 : it >= 2)
-                    if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
-                                                               (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait)))
+                    if (!__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
+                                                     (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait)))
                         break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + ((it & 1) ? S::ACC1 : 0);
                 const uint32_t sfa = tmem_base + S::SF, sfb = sfa + S::SF_TILES * 4;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
+                    ok = __all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -245,7 +245,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
             int mb, nb;
             tile_coords(t, p, mb, nb);
-            const bool ok = mbar_wait(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait);
+            const bool ok = mbar_wait<true, PAIR>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             auto release = [&]() {

@@ -35,13 +35,21 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-// On a barrier that may be in the pair's other block. What the arrival hands
-// over is read by the tensor cores (shared memory behind fence_async_smem,
-// tensor memory behind tcgen05 fences), not by the other block's threads, so
-// the default scope is enough; a release at cluster scope took about 1900
-// cycles in a block with copies and writes in flight.
+// On a barrier that may be in the pair's other block: at cluster scope, and
+// itself without order. What it hands over is ordered before it by tc_fence_before
+// (tensor memory), or by fence_async_smem and release_smem (shared memory that
+// the MMA reads), and after the wait by mbar_wait<.., CLUSTER> and tc_fence_after.
+// (A release of all memory at cluster scope took about 1900 cycles in a block
+// with copies and writes in flight: 8192 x 14336 x 4096 NVFP4 gemm_mx4 173 us.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+// Release and acquire at cluster scope, of shared memory alone.
+__device__ __forceinline__ void release_smem() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void acquire_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
@@ -51,11 +59,17 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 // that the other warps need (gemm_w4, 8192 x 14336 x 4096 MXFP4: 572 us, with
 // the default limit's polling 607).
 constexpr int SUSPEND_NS = 1000000;
+template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity), "n"(SUSPEND_NS) : "memory");
+    if constexpr (CLUSTER)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity), "n"(SUSPEND_NS) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity), "n"(SUSPEND_NS) : "memory");
     return ok != 0;
 }
 
@@ -69,16 +83,17 @@ struct Wait {
 
 // Wait for the phase of `bar` with parity `parity`. False when the block's
 // abort flag is raised (HONOUR) or the limit has passed, which raises the
-// flag and records the timeout.
-template <bool HONOUR>
+// flag and records the timeout. CLUSTER: a barrier that the pair's other block
+// arrives on, or its copies and MMAs.
+template <bool HONOUR, bool CLUSTER>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
     // The clock is read only once a wait is long: a read costs as much as
     // several polls.
     for (int i = 0; i < 32; ++i)
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<CLUSTER>(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<CLUSTER>(bar, parity)) return true;
         if ((it & 15u) == 0) {
             if (HONOUR && *(volatile int*)w.abort) return false;
             if (globaltimer() - t0 > w.limit_ns || it >= (1u << 30)) {
@@ -89,9 +104,11 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const
         }
     }
 }
-template <bool HONOUR = true>
+template <bool HONOUR = true, bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Wait& w) {
-    return mbar_try(bar, parity) || mbar_wait_slow<HONOUR>(bar, parity, w);
+    const bool ok = mbar_try<CLUSTER>(bar, parity) || mbar_wait_slow<HONOUR, CLUSTER>(bar, parity, w);
+    if constexpr (CLUSTER) acquire_smem();
+    return ok;
 }
 
 // ------------------------------------------------------- cluster of blocks

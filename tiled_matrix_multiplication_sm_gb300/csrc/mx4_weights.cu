@@ -147,7 +147,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tile_coords(t, p, mb, nb);
             const int row = mb * TM + (int)rank * 128;
             for (int kb = 0; kb < p.kblocks; ++kb) {
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
                 if (!stall) {
                     if (elect_one()) {
@@ -166,7 +166,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         if (leader) {
             for (int i = 0; i < STAGES; ++i)
                 if (armed & (1u << i))
-                    mbar_wait<false>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
+                    mbar_wait<false, true>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
         } else if (*(volatile int*)&sy->abort) {
             // After a timeout this block cannot observe its own copies; give
             // any in flight time to land (a copy takes microseconds).
@@ -187,13 +187,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (t >= p.num_tiles) break;
                 // What this accumulator held before is out.
                 const int acc = p.parts > 1 ? 1 : i & 1, turn = p.parts > 1 ? i : i >> 1;
-                ok = turn == 0 || __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[acc]), (uint32_t)(turn - 1) & 1u, wait));
+                ok = turn == 0 || __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_empty[acc]), (uint32_t)(turn - 1) & 1u, wait));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * TN);
                 const int first = part * p.part_blocks, last = min(first + p.part_blocks, p.kblocks) - 1;
                 for (int kb = first; kb <= last; ++kb) {
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
+                    ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -234,7 +234,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             if constexpr (sizeof(TC) == 4) {
                 if (p.parts > 1) {
                     for (int part = 0; ok && part < p.parts; ++part, ++it) {
-                        ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_full[1]), it & 1u, wait));
+                        ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_full[1]), it & 1u, wait));
                         if (!ok) break;
                         tc_fence_after();
                         add_sums(lanes, lanes + TN, TN, part == 0);
@@ -248,7 +248,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             if (!stored) {
                 const int acc = (int)(it & 1);
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_full[acc]), it >> 1 & 1u, wait));
+                ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_full[acc]), it >> 1 & 1u, wait));
                 if (!ok) break;
                 ++it;
                 tc_fence_after();
@@ -338,7 +338,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             decode_run<false>(v[i], w[i], f0, FMT == TGEMM_MXFP4 ? f0 : sy->factors[b1[i]]);
                         }
                     }
-                    ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), sph, wait));
+                    ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->empty[s]), sph, wait));
                     if (!ok) break;
                     uint8_t* dst = smem + s * STAGE_BYTES + A_BYTES;
 #pragma unroll
@@ -349,7 +349,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     fence_async_smem();          // the MMA reads through the async proxy
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full0 + (uint32_t)(s * sizeof(uint64_t)));
+                    if (lane == 0) {
+                        release_smem();
+                        mbar_arrive_cluster(full0 + (uint32_t)(s * sizeof(uint64_t)));
+                    }
                     next += GROUPS;
                     s += GROUPS;
                     if (s >= STAGES) { s -= STAGES; sph ^= 1u; }
