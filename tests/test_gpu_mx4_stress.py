@@ -35,3 +35,44 @@ def test_long_pair_products_give_the_same_bits_beside_other_work(tgemm, op, fmt,
             assert torch.equal(out, first)
     side.synchronize()
     assert tgemm.device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 20, 260])
+def test_operands_written_just_before_they_are_read(tgemm, M):
+    """Chains of calls whose operands (values, tensor scales, codes, bias) the
+    calls before them on the stream have just written, in the same buffers each
+    time, against the same chain with a wait after each call."""
+    N, K = 520, 1100
+    rng = torch.Generator(device="cuda").manual_seed(M)
+    X = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    W = torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    bias, g = torch.empty(N, device="cuda"), torch.empty(1, device="cuda")
+    back = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    seeds = [torch.randn(3, generator=rng, device="cuda") for _ in range(30)]
+    base = torch.randn(N, K, generator=rng, device="cuda"), torch.randn(M, K, generator=rng, device="cuda")
+
+    def chain(seed, wait):
+        def then(x):
+            if wait:
+                torch.cuda.synchronize()
+            return x
+
+        torch.mul(base[1], seed[0] * 30, out=X)
+        then(torch.mul(base[0], seed[1], out=W))
+        torch.mul(base[0][:, 0], seed[2], out=bias)
+        g.copy_(then(tgemm.mx4_tensor_scale(X)))
+        x = then(tgemm.mx4_quantize(X, "nvfp4", tensor_scale=g))
+        w, w_t = then(tgemm.mx4_quantize_both(W, "nvfp4"))
+        tgemm.mx4_dequantize(x, out=back)
+        then(None)
+        y = then(tgemm.gemm_w4(back, w, bias=bias))
+        z = then(tgemm.gemm_mx4(x, w, bias=bias, out_dtype=torch.bfloat16))
+        v = then(tgemm.mx4_dequantize(w_t, torch.bfloat16))
+        return y, z, v, back.clone()
+
+    fast = [chain(s, False) for s in seeds]
+    slow = [chain(s, True) for s in seeds]
+    for f, s in zip(fast, slow):
+        for a, b in zip(f, s):
+            assert torch.equal(a, b)
+    assert tgemm.device_status() == 0

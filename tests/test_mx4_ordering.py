@@ -34,3 +34,13 @@ def test_relaxed_arrivals_come_after_a_fence():
             if "mbar_arrive_cluster(" in line:
                 before = "\n".join(lines[max(0, i - 5):i])
                 assert "tc_fence_before()" in before or "release_smem()" in before, (name, i + 1)
+
+
+def test_operands_are_not_read_as_read_only():
+    """A kernel starts while the one before it still writes its operands
+    (programmatic dependent launch): loads for what nothing writes while the
+    kernel runs may not be used for them, and may move above the wait."""
+    for name, text in sources():
+        code = re.sub(r"//.*", "", text)
+        for what in ("__ldg", "ld.global.nc", "__restrict__"):
+            assert what not in code, (name, what)

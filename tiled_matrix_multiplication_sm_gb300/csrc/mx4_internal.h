@@ -71,7 +71,11 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return (c & 8) ? -v : v;
 }
 
-__device__ __forceinline__ float mx4_g(const float* g) { return g != nullptr ? __ldg(g) : 1.0f; }
+// (Operands are read by plain loads: the read-only path takes what nothing writes
+// while a kernel runs, and with programmatic dependent launch a kernel runs
+// while the one before it still writes them. Nor may such loads move above
+// pdl_wait, as read-only ones may.)
+__device__ __forceinline__ float mx4_g(const float* g) { return g != nullptr ? *g : 1.0f; }
 
 // One output under the rule; C_old is read only when beta != 0.
 template <typename T>

@@ -176,7 +176,7 @@ tensor_scale_kernel(long rows, long cols, const T* X, long ldx, bool vec, int sh
 #pragma unroll
             for (int j = 0; j < LOADS; ++j) {
                 const long r = r0 + j * dr, c = (p0 + j * dc) * V;
-                v[j] = r < rows && c + V <= cols ? __ldg(reinterpret_cast<const uint4*>(X + r * ldx + c)) : make_uint4(0, 0, 0, 0);
+                v[j] = r < rows && c + V <= cols ? *reinterpret_cast<const uint4*>(X + r * ldx + c) : make_uint4(0, 0, 0, 0);
             }
             uint32_t all = 0;
 #pragma unroll
@@ -525,9 +525,9 @@ dequantize_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales, con
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             if (i < n) {
-                w[i] = __ldg(reinterpret_cast<const uint32_t*>(code + (r + i) * pitch));
+                w[i] = *reinterpret_cast<const uint32_t*>(code + (r + i) * pitch);
                 // Eight rows from a multiple of 8 on lie in one column of a tile.
-                b[i] = __ldg(scale + (r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4);
+                b[i] = scale[(r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4];
             }
         }
 #pragma unroll
@@ -585,8 +585,8 @@ dequantize_any_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales,
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (r + i < R) {
-                w[i] = __ldg(code + (r + i) * pitch) >> (c & 1) * 4;
-                b[i] = __ldg(scale + (r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4);
+                w[i] = code[(r + i) * pitch] >> (c & 1) * 4;
+                b[i] = scale[(r >> 7) * row_of_tiles + ((r & 31) + i) * 16 + ((r & 127) >> 5) * 4];
             }
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)

@@ -87,7 +87,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (col + h * 32 + j < p.N)
-                            r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldg(o.bias + col + h * 32 + j));
+                            r[j] = __float_as_uint(__uint_as_float(r[j]) + o.bias[col + h * 32 + j]);
                 if constexpr (sizeof(TC) == 4) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -129,7 +129,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
                 if (c < p.N) {
                     TC* out = static_cast<TC*>(o.C) + (long)row0 * o.ldc + c;
                     const uint8_t* buf = bufs + (lane & 3) * 4;
-                    const float bias = o.bias != nullptr ? __ldg(o.bias + c) : 0.0f;
+                    const float bias = o.bias != nullptr ? o.bias[c] : 0.0f;
 #pragma unroll 1
                     for (int k = 0; k < rows; k += 8) {
                         float v[8], old[8];

@@ -180,7 +180,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) xs[j][i] = __ldg(reinterpret_cast<const uint4*>(x_row[i] + k0) + j);
+                for (int i = 0; i < NT; ++i) xs[j][i] = reinterpret_cast<const uint4*>(x_row[i] + k0)[j];
 #pragma unroll
             for (int j = 0; j < 4; ++j) step8(u, j, xs[j], f, std::false_type());
             return;
