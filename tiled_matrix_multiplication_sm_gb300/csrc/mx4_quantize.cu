@@ -50,52 +50,58 @@ __device__ __forceinline__ uint32_t e4m3_halves(uint32_t byte) {
 // What the scales of a matrix are made with.
 struct Scaling {
     float g, six_g, inv, cap;
+    float down, g_down;                                  // a power of two, and g times it
     __device__ __forceinline__ explicit Scaling(const float* gp) {
         g = mx4_g(gp);
         if (!(g >= kMinG && g <= kMaxG)) g = 0.0f;       // every scale NaN
         six_g = 6.0f * g;
         inv = __frcp_rn(six_g);
         cap = 896.0f * six_g;                            // quotients from 464 on all give 448
+        down = g >= 0x1p60f ? 0x1p-64f : 1.0f;
+        g_down = g * down;
     }
 };
 
 // The scale byte of a block whose largest |x| is m (an infinity or a NaN if
-// the block holds one), and what its values are divided with: 1 / d and -d (0
-// and 0: every code is 0). Quotients are q = x (1 / d) with one correction
-// step, q + (x - q d) (1 / d) (Markstein, 1990): a quotient that is the
-// midpoint of two codes, common for BF16 values over scales of 4 bits, comes
-// out exact, where x (1 / d) alone would fall to either side.
+// the block holds one), and what its values are multiplied with: a number just
+// below 1 / d and the rest of 1 / d (0 and 0: every code is 0). A quotient is
+// x inv + x rest in one rounding, so that one that is the midpoint of two codes,
+// common for BF16 values over scales of 4 bits, comes out exact, where x (1 / d)
+// alone would fall to either side. Both terms have x's sign: a quotient past
+// FP32's range (under a g far too small for x) is an infinity of that sign,
+// which the conversion makes the largest code. (A correction step
+// q + (x - q d) (1 / d) makes it NaN.) The rest is 2^-22 of 1 / d, a normal number
+// for d up to 2^100: under a large g, x and g are brought down by 2^64 first.
 template <int FMT>
-__device__ __forceinline__ uint32_t block_scale(float m, const Scaling& k, float& inv, float& neg_d) {
+__device__ __forceinline__ uint32_t block_scale(float m, const Scaling& k, float& inv, float& rest) {
     const bool bad = __float_as_uint(m) >= 0x7F800000u;
     if (FMT == TGEMM_MXFP4) {
         const int e = (int)(__float_as_uint(m) >> 23) - 2;     // biased floor(log2 m), minus 2
         const uint32_t byte = e > 0 ? (uint32_t)e : 0u;
         inv = bad ? 0.0f : __uint_as_float((254u - byte) << 23);       // 2^(127 - byte): exact
-        neg_d = 0.0f;
+        rest = 0.0f;
         return bad ? 0xFFu : byte;
     }
     const float c = fminf(m, k.cap);
     float q = c * k.inv;
     q = fmaf(fmaf(-q, k.six_g, c), k.inv, q);
     const uint32_t byte = e4m3(q);
-    const float d = e4m3_fast(byte) * k.g;
+    const float d = e4m3_fast(byte) * k.g_down;
     float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
-    y = fmaf(y, fmaf(-d, y, 1.0f), y);                         // Newton
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));      // within 2^-23 of itself
+    y = __uint_as_float(__float_as_uint(y) - 2u);
     const bool none = bad || byte == 0 || k.g == 0.0f;
     inv = none ? 0.0f : y;
-    neg_d = none ? 0.0f : -d;
+    rest = none ? 0.0f : fmaf(-d, y, 1.0f) * y;
     return bad || k.g == 0.0f ? 0x7Fu : byte;
 }
 
 // Two values over their divisors.
 template <int FMT>
-__device__ __forceinline__ float2 divide2(float x0, float x1, uint64_t inv2, uint64_t neg_d2) {
-    const uint64_t x = pack2(x0, x1);
-    uint64_t q = fma2(x, inv2, 0);
-    if (FMT == TGEMM_NVFP4) q = fma2(fma2(q, neg_d2, x), inv2, q);
-    return unpack2(q);
+__device__ __forceinline__ float2 divide2(float x0, float x1, uint64_t inv2, uint64_t rest2, uint64_t down2) {
+    uint64_t x = pack2(x0, x1);
+    if (FMT == TGEMM_NVFP4) x = fma2(x, down2, 0);
+    return unpack2(fma2(x, inv2, FMT == TGEMM_NVFP4 ? fma2(x, rest2, 0) : 0));
 }
 
 // Eight values to a word of codes, the first in the lowest bits.
@@ -266,18 +272,18 @@ __device__ __forceinline__ uint32_t quantize_row(const uint32_t* w, const Scalin
     uint32_t m = w[0];
 #pragma unroll
     for (int i = 1; i < WORDS; ++i) m = max_abs<T>(m, w[i]);
-    float inv, neg_d;
-    const uint32_t byte = block_scale<FMT>(__uint_as_float(magnitude<T>(m)), k, inv, neg_d);
-    const uint64_t inv2 = pack2(inv, inv), neg_d2 = pack2(neg_d, neg_d);
+    float inv, rest;
+    const uint32_t byte = block_scale<FMT>(__uint_as_float(magnitude<T>(m)), k, inv, rest);
+    const uint64_t inv2 = pack2(inv, inv), rest2 = pack2(rest, rest), down2 = pack2(k.down, k.down);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
         float2 q[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if constexpr (sizeof(T) == 2)
-                q[j] = divide2<FMT>(low_bf16(w[i * 4 + j]), high_bf16(w[i * 4 + j]), inv2, neg_d2);
+                q[j] = divide2<FMT>(low_bf16(w[i * 4 + j]), high_bf16(w[i * 4 + j]), inv2, rest2, down2);
             else
-                q[j] = divide2<FMT>(__uint_as_float(w[i * 8 + 2 * j]), __uint_as_float(w[i * 8 + 2 * j + 1]), inv2, neg_d2);
+                q[j] = divide2<FMT>(__uint_as_float(w[i * 8 + 2 * j]), __uint_as_float(w[i * 8 + 2 * j + 1]), inv2, rest2, down2);
         }
         codes[i] = e2m1x8(q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y);
     }
@@ -307,18 +313,18 @@ __device__ __forceinline__ uint32_t quantize_columns(const uint32_t* w, const Sc
         most[0] = fabsf(__uint_as_float(m[0]));
         most[1] = fabsf(__uint_as_float(m[1]));
     }
-    float inv[2], neg_d[2];
-    const uint32_t b0 = block_scale<FMT>(most[0], k, inv[0], neg_d[0]), b1 = block_scale<FMT>(most[1], k, inv[1], neg_d[1]);
-    const uint64_t inv2 = pack2(inv[0], inv[1]), neg_d2 = pack2(neg_d[0], neg_d[1]);
+    float inv[2], rest[2];
+    const uint32_t b0 = block_scale<FMT>(most[0], k, inv[0], rest[0]), b1 = block_scale<FMT>(most[1], k, inv[1], rest[1]);
+    const uint64_t inv2 = pack2(inv[0], inv[1]), rest2 = pack2(rest[0], rest[1]), down2 = pack2(k.down, k.down);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
         float2 q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if constexpr (sizeof(T) == 2)
-                q[j] = divide2<FMT>(low_bf16(w[i * 8 + j]), high_bf16(w[i * 8 + j]), inv2, neg_d2);
+                q[j] = divide2<FMT>(low_bf16(w[i * 8 + j]), high_bf16(w[i * 8 + j]), inv2, rest2, down2);
             else
-                q[j] = divide2<FMT>(__uint_as_float(w[i * 16 + 2 * j]), __uint_as_float(w[i * 16 + 2 * j + 1]), inv2, neg_d2);
+                q[j] = divide2<FMT>(__uint_as_float(w[i * 16 + 2 * j]), __uint_as_float(w[i * 16 + 2 * j + 1]), inv2, rest2, down2);
         }
         codes[0][i] = e2m1x8(q[0].x, q[1].x, q[2].x, q[3].x, q[4].x, q[5].x, q[6].x, q[7].x);
         codes[1][i] = e2m1x8(q[0].y, q[1].y, q[2].y, q[3].y, q[4].y, q[5].y, q[6].y, q[7].y);
