@@ -156,11 +156,11 @@ TGEMM_API int gemm_mx4(int M, int N, int K,
 /*
  * gemm_w4 — the same product with A in BF16 (M x K, lda >= K, any alignment
  * to 2 bytes) and B a kept 4-bit matrix: activations that stay in 16 bits
- * with weights in 4. Each weight's code x scale is a BF16 number exactly;
- * products are summed in FP32 and
+ * with weights in 4. Products of A with code x scale are exact; they are summed
+ * in FP32 and
  *     v = acc * gb * alpha, then beta and bias as in gemm_mx4.
- * With TGEMM_NVFP4 the sums are held times 2^-16, so that terms below 2^-110
- * may lose bits. With more than 24 rows an A whose rows do not start on
+ * The sums are held times 2^-16 (TGEMM_NVFP4) or 2^-2 (TGEMM_MXFP4), so that
+ * terms below 2^-110 or 2^-124 may lose bits. With more than 24 rows an A whose rows do not start on
  * 16-byte boundaries is copied first, to 2 M round_up(K, 64) bytes of
  * stream-ordered scratch from the library's pool (see tgemm.h).
  *

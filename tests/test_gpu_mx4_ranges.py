@@ -69,3 +69,22 @@ def test_quotients_one_step_from_the_midpoints(tgemm, power):
     want_codes, want = ref.quantize(x.astype(np.float64), "nvfp4", g)
     assert np.array_equal(got, want)
     assert np.array_equal(ref.e2m1(codes), ref.e2m1(want_codes))
+
+
+@pytest.mark.parametrize("M", [1, 12, 40, 2100])             # each kernel of gemm_w4
+@pytest.mark.parametrize("op", ["w4", "mx4"])
+def test_every_code_under_every_mxfp4_scale(tgemm, op, M):
+    """Weights up to 6 x 2^127, which no FP32 holds, times small activations."""
+    scales, codes = (v.ravel() for v in np.meshgrid(np.arange(255), np.arange(16)))
+    order = np.random.default_rng(2).permutation(len(scales))
+    scales, codes = scales[order], codes[order]
+    N, K = len(scales), 32
+    B = tgemm.mx4_pack(torch.from_numpy(ref.pack_codes(np.repeat(codes[:, None], K, axis=1))).cuda(),
+                       torch.from_numpy(scales[:, None].astype(np.uint8)).cuda(), "mxfp4", cols=K)
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    X[:, 5] = 3 * 2.0 ** -12
+    A = X if op == "w4" else tgemm.mx4_quantize(X, "mxfp4")
+    got = (tgemm.gemm_w4 if op == "w4" else tgemm.gemm_mx4)(A, B).double().cpu().numpy()
+    want = ref.e2m1(codes) * ref.scale_value(scales, "mxfp4") * (3 * 2.0 ** -12)
+    fine = (np.abs(want) >= 2.0 ** -120) | (want == 0)
+    assert fine.sum() > 0.9 * N and np.array_equal(got[:, fine], np.broadcast_to(want[fine], (M, fine.sum())))

@@ -170,7 +170,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
                 f[i][0] = factors[u.scales[i] & 0xFF];
                 f[i][1] = factors[u.scales[i] >> 8];
             } else {
-                f[i][0] = f[i][1] = (u.scales[i] + 126) * 0x00800080u;
+                f[i][0] = f[i][1] = (u.scales[i] + 124) * 0x00800080u;
                 w |= wide(u.scales[i]);
             }
         }
