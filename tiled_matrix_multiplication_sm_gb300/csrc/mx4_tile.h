@@ -152,14 +152,6 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
     }
 }
 
-// The tensor cores cut what does not fit into an FP32 sum off at every 16
-// columns of K, always towards zero: over 14336 columns BF16 products lose 8e-6 of the
-// result's norm, four times what an FP32 library product does. So where C
-// keeps 32 bits, a sum over more than SUM_K columns is made of sums over
-// SUM_K, added with rounding to nearest. (A BF16 C rounds by 2e-3 itself; sums of
-// products of 4-bit values lose 1e-7, their bits being few.)
-constexpr int SUM_K = 1024;
-
 // Adds `cols` columns of `part` to `total` (`first`: moves them there), both in
 // this warp's lanes of tensor memory.
 __device__ __forceinline__ void add_sums(uint32_t total, uint32_t part, int cols, bool first) {

@@ -10,7 +10,8 @@
 // Eight warps of a block take every eighth 128 columns; their sums meet in
 // shared memory, and those of up to eight blocks of a cluster, which split K
 // further when W has few rows, through distributed shared memory, always in
-// the same order.
+// the same order. Where C keeps 32 bits a warp's sum is made of sums over
+// SUM_K columns, as in the other kernels.
 
 #include "mx4_decode.h"
 
@@ -69,8 +70,9 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 }
 
 // BLOCKS: how many blocks are resident on an SM, 2 (up to 128 registers a
-// thread) or 3 (80).
-template <int FMT, int NT, int RW, int BLOCKS, typename TC>
+// thread) or 3 (80). LONG: a warp's sum is made of parts (for sums of one part,
+// 1 x 14336 x 4096 MXFP4 with FP32 C, the registers of a second sum cost 6 %).
+template <int FMT, int NT, int RW, int BLOCKS, bool LONG, typename TC>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
 weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool vec, Mx4Operand W,
                     Mx4Out out, int split) {
@@ -205,8 +207,22 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         }
     };
 
+    // The parts of a long sum are added with rounding to nearest.
+    float parts[RW][NT][4] = {};
+    auto end_part = [&]() {
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    parts[r][i][k] += acc[r][i][k];
+                    acc[r][i][k] = 0.0f;
+                }
+    };
+
     const int step = WARPS * split;
-    int unit = rank * WARPS + warp, slot = 0;
+    int unit = rank * WARPS + warp, slot = 0, in_part = 0;
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) fetch(unit + i * step, i);
 #pragma unroll 1
@@ -216,8 +232,13 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         take(u, slot);
         fetch(unit + DEPTH * step, slot);            // the lane's own slot, read just before
         run(u, unit);
+        if (LONG && ++in_part == SUM_K / UNIT_K) {
+            in_part = 0;
+            end_part();
+        }
         if (++slot == DEPTH) slot = 0;
     }
+    if (LONG) end_part();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 
@@ -227,7 +248,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                part[warp][r * 16 + (k >> 1) * 8 + g][i * 8 + 2 * t + (k & 1)] = acc[r][i][k];
+                part[warp][r * 16 + (k >> 1) * 8 + g][i * 8 + 2 * t + (k & 1)] = LONG ? parts[r][i][k] : acc[r][i][k];
     __syncthreads();
     const float gb = mx4_g(W.g);
     auto store = [&](int i, float v) {
@@ -260,8 +281,8 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int FMT, int NT, int RW, int BLOCKS, typename TC>
-cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
+template <int FMT, int NT, int RW, int BLOCKS, bool LONG, typename TC>
+cudaError_t launch_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
                    int split, cudaStream_t s) {
     const long tiles = ((long)N + 16 * RW - 1) / (16 * RW);
     cudaLaunchConfig_t cfg = {};
@@ -278,10 +299,19 @@ cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    const cudaError_t e = set_smem_limit_once<weights_rows_kernel<FMT, NT, RW, BLOCKS, TC>>(sizeof(Slots<RW>));
+    const cudaError_t e = set_smem_limit_once<weights_rows_kernel<FMT, NT, RW, BLOCKS, LONG, TC>>(sizeof(Slots<RW>));
     if (e != cudaSuccess) return e;
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
-    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, RW, BLOCKS, TC>, M, N, K, X, ldx, vec, W, out, split);
+    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, RW, BLOCKS, LONG, TC>, M, N, K, X, ldx, vec, W, out, split);
+}
+
+template <int FMT, int NT, int RW, int BLOCKS, typename TC>
+cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
+                   int split, cudaStream_t s) {
+    if constexpr (sizeof(TC) == 4)
+        if (((long)K + UNIT_K - 1) / UNIT_K > (long)WARPS * split * (SUM_K / UNIT_K))
+            return launch_kernel<FMT, NT, RW, BLOCKS, true, TC>(M, N, K, X, ldx, W, out, split, s);
+    return launch_kernel<FMT, NT, RW, BLOCKS, false, TC>(M, N, K, X, ldx, W, out, split, s);
 }
 
 // Resident blocks (2 or 3) and the blocks of a cluster that split K. The
