@@ -21,6 +21,8 @@
 //   single  128 x 128 tiles on one SM, for products with few tiles; of very
 //           few, a cluster's blocks split K and add their shares through
 //           distributed shared memory.
+// Long sums with an FP32 result (LONG) come in parts, accumulator by
+// accumulator; the epilogue's warps add them up in registers.
 //
 // Rows past M and N are read as zeros (TMA fill, zero scales) and not stored.
 // Waits are bounded as in the other tensor-core kernels.
@@ -41,17 +43,26 @@ constexpr int STAGE_K = MX4_SPAN;
 constexpr int OPERAND_BYTES = 128 * SW;       // 128 rows of codes
 constexpr int STAGES = 5;
 constexpr int EPI_BYTES = 8 * BUF_BYTES;
+constexpr int PART_STAGES = SUM_STEPS * 64 / STAGE_K;      // of a long sum
 
-template <int FMT, bool PAIR>
+template <int FMT, bool PAIR, bool LONG>
 struct Shape {
     static constexpr int TM = PAIR ? 256 : 128;           // rows of a tile
     static constexpr int TN = PAIR ? 256 : 128;           // columns
     // Epilogue: sets of four warps (one to a quarter of tensor memory's lanes)
     // with BUFS buffers a warp. A second set shortens the only tile's way out
     // (1024^3 MXFP4 8.5 -> 7.4 us); between tiles shared memory is the bound,
-    // and it costs (8192 x 14336 x 4096 NVFP4 155 -> 158 us).
-    static constexpr int SETS = PAIR ? 1 : 2, BUFS = 2 / SETS;
-    static constexpr int EPI_WARPS = 4 * SETS, THREADS = 64 + 32 * EPI_WARPS;
+    // and it costs (8192 x 14336 x 4096 NVFP4 155 -> 158 us). Long sums need two:
+    // a thread holds half a row of the tile, which for a pair takes more
+    // registers than 10 warps can have each: the first four (two of them idle)
+    // give theirs to the epilogue's. (14336 x 4096 x 8192 NVFP4: 171 us, with
+    // the sums spilled 226; in one part 164.)
+    static constexpr int SETS = PAIR && !LONG ? 1 : 2, BUFS = 2 / SETS;
+    static constexpr bool SHARED_REGS = PAIR && LONG;
+    static constexpr int EPI0 = SHARED_REGS ? 4 : 2;                  // the epilogue's first warp
+    static constexpr int EPI_WARPS = 4 * SETS, THREADS = 32 * (EPI0 + EPI_WARPS);
+    static constexpr int FEW_REGS = 40, MANY_REGS = 224;
+    static constexpr int REGS = SHARED_REGS ? (4 * FEW_REGS + EPI_WARPS * MANY_REGS) / (4 + EPI_WARPS) + 1 : 0;   // at launch, at least
     static constexpr int SF_TILES = STAGE_K / mx4_block(FMT) / 4;     // scale tiles of 128 rows a stage
     static constexpr int SFA_BYTES = SF_TILES * MX4_TILE_BYTES;
     static constexpr int SFB_BYTES = SFA_BYTES * (TN / 128);
@@ -79,12 +90,12 @@ struct Params : Tiling {
     const float *ga, *gb;
 };
 
-template <int FMT, bool PAIR, typename TC>
-__global__ void __launch_bounds__(Shape<FMT, PAIR>::THREADS, 1)
+template <int FMT, bool PAIR, bool LONG, typename TC>
+__global__ void __launch_bounds__(Shape<FMT, PAIR, LONG>::THREADS, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmC, const Params p) {
-    using S = Shape<FMT, PAIR>;
+    using S = Shape<FMT, PAIR, LONG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* epi = smem + STAGES * S::STAGE_BYTES;
@@ -133,6 +144,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t tmem_empty0 =
         PAIR ? map_to_rank(smem_u32(&sy->tmem_empty[0]), 0) : smem_u32(&sy->tmem_empty[0]);
 
+    if (warp < S::EPI0) {
+    if constexpr (S::SHARED_REGS) give_registers<S::FEW_REGS>();
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
         // The whole warp runs the loop (addresses stay uniform values), one
@@ -189,10 +202,12 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int it = 0, s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = unit; ok && t < p.num_tiles; t += p.units, ++it) {
-                // Pair: the previous tile's shared columns have left tensor
-                // memory (and with them all of the tile before it). Single:
-                // the tile two before, which used this accumulator.
+            // A tile's sum, or of LONG ones each part in turn: first to last - 1.
+            for (int t = unit, first = kb0; ok && t < p.num_tiles; ++it) {
+                const int last = LONG ? min(first + PART_STAGES, kb1) : kb1;
+                // Pair: the previous sum's shared columns have left tensor
+                // memory (and with them all of the sum before it). Single:
+                // the sum two before, which used this accumulator.
                 if (PAIR ? it >= 1 : it >= 2)
                     if (!__all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->tmem_empty[PAIR ? 0 : it & 1]),
                                                      (uint32_t)(PAIR ? it - 1 : (it >> 1) - 1) & 1u, wait)))
@@ -200,7 +215,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tc_fence_after();
                 const uint32_t d = tmem_base + ((it & 1) ? S::ACC1 : 0);
                 const uint32_t sfa = tmem_base + S::SF, sfb = sfa + S::SF_TILES * 4;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = first; kb < last; ++kb) {
                     ok = __all_sync(~0u, mbar_wait<true, PAIR>(smem_u32(&sy->full[s]), ph, wait));
                     if (!ok) break;
                     tc_fence_after();
@@ -222,40 +237,98 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         mma_mx4<FMT, PAIR>(d, smem_desc(a + k * 32, 16, 1024, 2),
                                            smem_desc(a + OPERAND_BYTES + k * 32, 16, 1024, 2),
                                            mx4_instr<FMT, S::TM, S::TN>(half), sfa + tile * 4,
-                                           sfb + tile * 4 * (S::TN / 128), kb != kb0 || k != 0);
+                                           sfb + tile * 4 * (S::TN / 128), kb != first || k != 0);
                     }
                     tc_commit<PAIR>(smem_u32(&sy->empty[s]));
-                    if (kb == kb1 - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
+                    if (kb == last - 1) tc_commit<PAIR>(smem_u32(&sy->tmem_full[it & 1]));
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+                first = last;
+                if (last == kb1) {
+                    first = kb0;
+                    t += p.units;
                 }
             }
             if (elect_one()) tc_commit<PAIR>(smem_u32(&sy->drain));
             mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
         __syncwarp();
+    }
     } else {
         // ------------------------------------------------------ epilogue
+        if constexpr (S::SHARED_REGS) take_registers<S::MANY_REGS>();
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
-        const int set = (warp - 2) >> 2;
-        uint8_t* bufs = epi + (warp - 2) * S::BUFS * BUF_BYTES;
+        const int set = (warp - S::EPI0) >> 2;
+        uint8_t* bufs = epi + (warp - S::EPI0) * S::BUFS * BUF_BYTES;
         const float ga = mx4_g(p.ga), gb = mx4_g(p.gb);
         int it = 0;
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 31) {
+                const uint32_t bar = tmem_empty0 + (uint32_t)((PAIR ? 0 : it & 1) * sizeof(uint64_t));
+                if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
+            }
+        };
+        if constexpr (LONG) {
+            // This set's half of the row, 64 columns a turn. The turn that may
+            // hold columns which the other accumulator shares -- a pair's first
+            // 64, set 0's, or last, set 1's -- comes first, and then the next
+            // part may start.
+            constexpr int HALF = S::TN / 2, TURNS = HALF / 64;
+            bool ok = true;
+            for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+                float sum[TURNS][2][32] = {};
+                #pragma unroll 1
+                for (int first = kb0; first < kb1; first += PART_STAGES, ++it) {
+                    ok = __all_sync(~0u, mbar_wait<true, PAIR, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem_base + ((it & 1) ? S::ACC1 : 0) + ((uint32_t)(q * 32) << 16) + set * HALF;
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const uint32_t from = acc + (i ^ (TURNS > 1 ? set : 0)) * 64;
+                        uint32_t r[2][32];
+                        tmem_ld32(from, r[0]);
+                        tmem_ld32(from + 32, r[1]);
+                        tmem_wait_ld(r[0]);
+                        tmem_wait_ld(r[1]);
+                        if (i == 0) release();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                sum[i][h][j] += __uint_as_float(r[h][j]);
+                    }
+                }
+                if (!ok) break;
+                if (!PAIR && p.split > 1) {
+                    // The tile's copies and MMAs are done: its stages hold the share.
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        share_columns(smem, q * 32 + lane, set * HALF + h * 32, reinterpret_cast<uint32_t (&)[32]>(sum[0][h]));
+                    break;
+                }
+                int mb, nb;
+                tile_coords(t, p, mb, nb);
+                const int row0 = mb * S::TM + (int)rank * 128 + q * 32;
+#pragma unroll
+                for (int i = 0; i < TURNS; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        store_half<S::BUFS, TC>(p, &tmC, bufs, i, h, row0, min(32, p.M - row0),
+                                                nb * S::TN + set * HALF + (i ^ (TURNS > 1 ? set : 0)) * 64, ga, gb,
+                                                reinterpret_cast<uint32_t (&)[32]>(sum[i][h]));
+            }
+        } else
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
             int mb, nb;
             tile_coords(t, p, mb, nb);
             const bool ok = mbar_wait<true, PAIR>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 31) {
-                    const uint32_t bar = tmem_empty0 + (uint32_t)((PAIR ? 0 : it & 1) * sizeof(uint64_t));
-                    if constexpr (PAIR) mbar_arrive_cluster(bar); else mbar_arrive(bar);
-                }
-            };
             if (!PAIR && p.split > 1) {
                 // The tile's copies and MMAs are done: its stages hold the share.
                 if (set == 0) store_share(smem, tmem_base + ((uint32_t)(q * 32) << 16), q);
@@ -293,10 +366,31 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(int M, int N, const Mx4O
         mx4_store(static_cast<TC*>(out.C) + r * out.ldc + c, 0.0f, 1.0f, 1.0f, out, (int)c);
 }
 
+template <int FMT, bool PAIR, bool LONG, typename TC>
+cudaError_t launch_kernel(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSA, const CUtensorMap& tmSB,
+                          const CUtensorMap& tmC, const Params& p, cudaStream_t s) {
+    using S = Shape<FMT, PAIR, LONG>;
+    cudaError_t e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, LONG, TC>>(S::SMEM);
+    if constexpr (S::SHARED_REGS) {
+        // A block that is launched with fewer registers than its warps are to
+        // have would wait for them without end.
+        static std::atomic<int> regs{0};
+        if (e == cudaSuccess && regs.load(std::memory_order_relaxed) == 0) {
+            cudaFuncAttributes a;
+            e = cudaFuncGetAttributes(&a, mx4_gemm_kernel<FMT, PAIR, LONG, TC>);
+            if (e == cudaSuccess) regs.store(a.numRegs, std::memory_order_relaxed);
+        }
+        if (e == cudaSuccess && regs.load(std::memory_order_relaxed) < S::REGS) return cudaErrorLaunchOutOfResources;
+    }
+    if (e != cudaSuccess) return e;
+    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, S::THREADS, S::SMEM, PAIR ? 2 : p.split, s);
+    return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, LONG, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
+}
+
 template <int FMT, bool PAIR, typename TC>
 cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B, const Mx4Out& out,
                    int num_sms, cudaStream_t s) {
-    using S = Shape<FMT, PAIR>;
+    using S = Shape<FMT, PAIR, false>;
     const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (enc == nullptr) return cudaErrorNotSupported;
     CUtensorMap tmA, tmB, tmSA, tmSB, tmC;
@@ -310,18 +404,20 @@ cudaError_t launch(int M, int N, int K, const Mx4Operand& A, const Mx4Operand& B
     p.kblocks = (int)(((long)K + STAGE_K - 1) / STAGE_K);
     p.ga = A.g; p.gb = B.g;
     p.tma_c = encode_c(enc, &tmC, out, M, N) ? 1 : 0;
-    if (e == cudaSuccess) e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, TC>>(S::SMEM);
     if (!PAIR && p.num_tiles * 2 <= num_sms) {
         // 10 steps: 128 x 2048 x 2048, 6 saved, whole 5.5 us and split 6.3;
         // x 4096, 12 saved, 7.8 and 6.9; 1024 x 1024 x 4096, 8 saved, 8.4 and 9.2.
         unsigned long long fits = 0;
-        if (e == cudaSuccess) e = clusters_that_fit<mx4_gemm_kernel<FMT, PAIR, TC>>(S::THREADS, S::SMEM, &fits);
+        if (e == cudaSuccess) e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, false, TC>>(S::SMEM);
+        if (e == cudaSuccess) e = clusters_that_fit<mx4_gemm_kernel<FMT, PAIR, false, TC>>(S::THREADS, S::SMEM, &fits);
         p.split = split_for(p.num_tiles, p.kblocks, fits, 10);
         p.units = p.num_tiles;
     }
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, S::THREADS, S::SMEM, PAIR ? 2 : p.split, s);
-    return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
+    if constexpr (sizeof(TC) == 4)
+        if ((p.kblocks + p.split - 1) / p.split > PART_STAGES)
+            return launch_kernel<FMT, PAIR, true, TC>(tmA, tmB, tmSA, tmSB, tmC, p, s);
+    return launch_kernel<FMT, PAIR, false, TC>(tmA, tmB, tmSA, tmSB, tmC, p, s);
 }
 
 template <int FMT, bool PAIR>

@@ -33,13 +33,16 @@ __host__ __device__ constexpr size_t mx4_scale_at(long r, long b, long tiles_k) 
            (size_t)(r % 128 / 32 * 4) + (size_t)(b % 4);
 }
 
-// The tensor cores cut what does not fit into an FP32 sum off at every 16
-// columns of K, always towards zero: over 14336 columns BF16 products lose 8e-6 of the
-// result's norm, four times what an FP32 library product does. So where C
-// keeps 32 bits, a sum over more than SUM_K columns is made of sums over
-// SUM_K, added with rounding to nearest. (A BF16 C rounds by 2e-3 itself; sums of
-// products of 4-bit values lose 1e-7, their bits being few.)
-constexpr int SUM_K = 1024;
+// The tensor cores cut what does not fit into an FP32 sum off at every step of
+// K, always towards zero: over 14336 columns BF16 products lose 8e-6 of the
+// result's norm, four times what an FP32 library product does; products of
+// two 4-bit matrices, whose steps are four times as long, nothing while all terms
+// are multiples of 2^-24 of the sum, but 5.5e-6 with NVFP4 scales over 16
+// octaves and 2.5e-5 over 65536 columns. So where C keeps 32 bits, a sum of more
+// than SUM_STEPS steps is made of sums over SUM_STEPS, added with rounding to
+// nearest. (A BF16 C rounds by 2e-3 itself.)
+constexpr int SUM_STEPS = 64;
+constexpr int SUM_K = 16 * SUM_STEPS;                 // of BF16 products
 
 // A 4-bit operand of a product.
 struct Mx4Operand {

@@ -84,9 +84,10 @@ struct Wait {
 // Wait for the phase of `bar` with parity `parity`. False when the block's
 // abort flag is raised (HONOUR) or the limit has passed, which raises the
 // flag and records the timeout. CLUSTER: a barrier that the pair's other block
-// arrives on, or its copies and MMAs.
+// arrives on, or its copies and MMAs. INLINE: in a warp whose registers are full
+// of values that a call would have to save.
 template <bool HONOUR, bool CLUSTER>
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const Wait& w) {
     // The clock is read only once a wait is long: a read costs as much as
     // several polls.
     for (int i = 0; i < 32; ++i)
@@ -104,12 +105,25 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const
         }
     }
 }
-template <bool HONOUR = true, bool CLUSTER = false>
+template <bool HONOUR, bool CLUSTER>
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
+    return mbar_poll<HONOUR, CLUSTER>(bar, parity, w);
+}
+template <bool HONOUR = true, bool CLUSTER = false, bool INLINE = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Wait& w) {
-    const bool ok = mbar_try<CLUSTER>(bar, parity) || mbar_wait_slow<HONOUR, CLUSTER>(bar, parity, w);
+    const bool ok = mbar_try<CLUSTER>(bar, parity) ||
+                    (INLINE ? mbar_poll<HONOUR, CLUSTER>(bar, parity, w) : mbar_wait_slow<HONOUR, CLUSTER>(bar, parity, w));
     if constexpr (CLUSTER) acquire_smem();
     return ok;
 }
+
+// ------------------------------------------------------------- registers
+// Four warps' registers a thread, from here on: fewer given to the block, or
+// more taken of what others gave (all four warps; waits until they are there).
+template <int REGS>
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REGS)); }
 
 // ------------------------------------------------------- cluster of blocks
 __device__ __forceinline__ uint32_t cluster_rank() {

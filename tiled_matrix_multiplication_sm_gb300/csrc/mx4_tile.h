@@ -37,6 +37,90 @@ __device__ __forceinline__ void tile_coords(int t, const Tiling& p, int& mb, int
 // Where 16-byte piece j of row r lies in a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint32_t swizzled(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
+// Stores 32 columns of this warp's 32 rows from registers, the accumulator's
+// values: half h of turn `turn`, whose 64 columns start at column `col` of C.
+template <int BUFS, typename TC>
+__device__ __forceinline__ void store_half(const Tiling& p, const CUtensorMap* tmC, uint8_t* bufs, int turn, int h,
+                                           int row0, int rows, int col, float ga, float gb, uint32_t (&r)[32]) {
+    constexpr int CW = 128 / (int)sizeof(TC);
+    const int lane = threadIdx.x & 31;
+    const Mx4Out& o = p.out;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ga * gb * o.alpha);
+    if (p.tma_c) {
+        // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16: one of 64 --
+        // through BUFS buffers in turn: the last box in this one has to have
+        // left it.
+        uint8_t* buf = bufs + (sizeof(TC) == 4 ? h : turn) % BUFS * BUF_BYTES;
+        if (sizeof(TC) == 4 || h == 0) {
+            if (lane == 0) tma_store_wait_read<BUFS - 1>();
+            __syncwarp();
+        }
+        if (o.bias != nullptr)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + h * 32 + j < p.N)
+                    r[j] = __float_as_uint(__uint_as_float(r[j]) + o.bias[col + h * 32 + j]);
+        if constexpr (sizeof(TC) == 4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(buf + swizzled(lane, j)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * k]),
+                                                                   __uint_as_float(r[8 * j + 2 * k + 1]));
+                    w[k] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                *reinterpret_cast<uint4*>(buf + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (sizeof(TC) == 4 || h == 1) {
+            fence_async_smem();
+            __syncwarp();
+            const int c = col + (sizeof(TC) == 4 ? h * CW : 0);
+            if (lane == 0) {
+                if (rows > 0 && c < p.N) tma_store_2d(tmC, c, row0, smem_u32(buf));
+                tma_store_commit();                       // counted even when there is none
+            }
+        }
+    } else {
+        // Any alignment, and beta: 32 x 32 FP32 blocks through shared memory,
+        // then whole row segments, a column a lane, eight rows' loads ahead of
+        // their stores.
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(bufs + swizzled(lane, j)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        __syncwarp();
+        const int c = col + h * 32 + lane;
+        if (c < p.N) {
+            TC* out = static_cast<TC*>(o.C) + (long)row0 * o.ldc + c;
+            const uint8_t* buf = bufs + (lane & 3) * 4;
+            const float bias = o.bias != nullptr ? o.bias[c] : 0.0f;
+#pragma unroll 1
+            for (int k = 0; k < rows; k += 8) {
+                float v[8], old[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = *reinterpret_cast<const float*>(buf + swizzled(k + j, lane >> 2));
+                    old[j] = o.beta != 0.0f && k + j < rows ? (float)out[j * o.ldc] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (o.beta != 0.0f) v[j] = fmaf(o.beta, old[j], v[j]);
+                    if (o.bias != nullptr) v[j] += bias;
+                    if (k + j < rows) out[j * o.ldc] = (TC)v[j];
+                }
+                out += 8 * o.ldc;
+            }
+        }
+    }
+}
+
 // Drains this warp's 32 rows of a tile, 64 columns a turn; of SETS sets of
 // epilogue warps, set `set` takes every SETS-th turn. `last_first`: the last
 // 64 columns, which the next tile's accumulator shares, are turn 0. release()
@@ -47,10 +131,8 @@ template <int TN, int SETS, bool BOTH, int BUFS, typename TC, typename Release>
 __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* tmC, uint32_t tmem,
                                            uint8_t* bufs, int row0, int col0, bool last_first, int set,
                                            int release_turn, float ga, float gb, Release release) {
-    constexpr int W = 64, CW = 128 / (int)sizeof(TC);
+    constexpr int W = 64;
     constexpr int TURNS = TN / W;
-    const int lane = threadIdx.x & 31;
-    const Mx4Out& o = p.out;
     const int rows = min(32, p.M - row0);
 #pragma unroll 1
     for (int i = set; i < TURNS; i += SETS) {
@@ -72,82 +154,7 @@ __device__ __forceinline__ void drain_tile(const Tiling& p, const CUtensorMap* t
                 tmem_wait_ld(r);
                 if (h == 1 && i == release_turn) release();
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ga * gb * o.alpha);
-            if (p.tma_c) {
-                // Boxes of 128-byte rows -- FP32: two of 32 columns, BF16:
-                // one of 64 -- through BUFS buffers in turn: the last box in
-                // this one has to have left it.
-                uint8_t* buf = bufs + (sizeof(TC) == 4 ? h : i / SETS) % BUFS * BUF_BYTES;
-                if (sizeof(TC) == 4 || h == 0) {
-                    if (lane == 0) tma_store_wait_read<BUFS - 1>();
-                    __syncwarp();
-                }
-                if (o.bias != nullptr)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + h * 32 + j < p.N)
-                            r[j] = __float_as_uint(__uint_as_float(r[j]) + o.bias[col + h * 32 + j]);
-                if constexpr (sizeof(TC) == 4) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(buf + swizzled(lane, j)) =
-                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * k]),
-                                                                           __uint_as_float(r[8 * j + 2 * k + 1]));
-                            w[k] = *reinterpret_cast<const uint32_t*>(&b);
-                        }
-                        *reinterpret_cast<uint4*>(buf + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                if (sizeof(TC) == 4 || h == 1) {
-                    fence_async_smem();
-                    __syncwarp();
-                    const int c = col + (sizeof(TC) == 4 ? h * CW : 0);
-                    if (lane == 0) {
-                        if (rows > 0 && c < p.N) tma_store_2d(tmC, c, row0, smem_u32(buf));
-                        tma_store_commit();                       // counted even when there is none
-                    }
-                }
-            } else {
-                // Any alignment, and beta: 32 x 32 FP32 blocks through shared
-                // memory, then whole row segments, a column a lane, eight
-                // rows' loads ahead of their stores.
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(bufs + swizzled(lane, j)) =
-                        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                __syncwarp();
-                const int c = col + h * 32 + lane;
-                if (c < p.N) {
-                    TC* out = static_cast<TC*>(o.C) + (long)row0 * o.ldc + c;
-                    const uint8_t* buf = bufs + (lane & 3) * 4;
-                    const float bias = o.bias != nullptr ? o.bias[c] : 0.0f;
-#pragma unroll 1
-                    for (int k = 0; k < rows; k += 8) {
-                        float v[8], old[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            v[j] = *reinterpret_cast<const float*>(buf + swizzled(k + j, lane >> 2));
-                            old[j] = o.beta != 0.0f && k + j < rows ? (float)out[j * o.ldc] : 0.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (o.beta != 0.0f) v[j] = fmaf(o.beta, old[j], v[j]);
-                            if (o.bias != nullptr) v[j] += bias;
-                            if (k + j < rows) out[j * o.ldc] = (TC)v[j];
-                        }
-                        out += 8 * o.ldc;
-                    }
-                }
-            }
+            store_half<BUFS, TC>(p, tmC, bufs, i / SETS, h, row0, rows, col, ga, gb, r);
         }
     }
 }
@@ -172,9 +179,16 @@ __device__ __forceinline__ void add_sums(uint32_t total, uint32_t part, int cols
     tmem_wait_st();
 }
 
-// A tile whose sum is split over a cluster: this warp's 32 rows of the block's
-// share, FP32, to `partial` (128 rows of 128 columns, 16-byte pieces permuted
-// by the row so that neither side's accesses conflict).
+// A tile whose sum is split over a cluster: the block's share, FP32, goes to
+// `partial` (128 rows of 128 columns, 16-byte pieces permuted by the row so that
+// neither side's accesses conflict). 32 columns of a row from registers, and this
+// warp's 32 rows from tensor memory.
+__device__ __forceinline__ void share_columns(uint8_t* partial, int row, int c, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(partial + row * 512 + (((c / 4 + j) ^ (row & 31)) << 4)) =
+            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+}
 __device__ __forceinline__ void store_share(uint8_t* partial, uint32_t tmem, int q) {
     const int row = q * 32 + (threadIdx.x & 31);
 #pragma unroll 1
@@ -182,10 +196,7 @@ __device__ __forceinline__ void store_share(uint8_t* partial, uint32_t tmem, int
         uint32_t r[32];
         tmem_ld32(tmem + (uint32_t)c, r);
         tmem_wait_ld(r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(partial + row * 512 + (((c / 4 + j) ^ (row & 31)) << 4)) =
-                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        share_columns(partial, row, c, r);
     }
 }
 
