@@ -162,9 +162,10 @@ TGEMM_API int gemm_mx4(int M, int N, int K,
  * in FP32 (with an FP32 C in parts of 1024 columns, as above) and
  *     v = acc * gb * alpha, then beta and bias as in gemm_mx4.
  * The sums are held times 2^-16 (TGEMM_NVFP4) or 2^-2 (TGEMM_MXFP4), so that
- * terms below 2^-110 or 2^-124 may lose bits. With more than 24 rows an A whose rows do not start on
+ * terms below 2^-110 or 2^-124 may lose bits. An A whose rows do not start on
  * 16-byte boundaries is copied first, to 2 M round_up(K, 64) bytes of
- * stream-ordered scratch from the library's pool (see tgemm.h).
+ * stream-ordered scratch from the library's pool (see tgemm.h), where M > 24,
+ * where M > 8 and N K >= 2^24, and where K >= 2^27.
  *
  * Errors as gemm_mx4, and TGEMM_ERR_INVALID_ARG for lda < K or A off 2 bytes.
  */

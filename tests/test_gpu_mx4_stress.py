@@ -76,3 +76,22 @@ def test_operands_written_just_before_they_are_read(tgemm, M):
         for a, b in zip(f, s):
             assert torch.equal(a, b)
     assert tgemm.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 4100, 4130), (20, 4100, 4130), (8, 4100, 4130), (16, 300, 4130), (40, 300, 1030)])
+def test_rows_off_16_bytes_of_either_route_in_a_graph(tgemm, M, N, K):
+    """9 to 24 rows of much weight: such an A is copied to scratch first."""
+    A, B, a, b = operands(tgemm, "w4", M, N, K, "mxfp4", "whole")
+    A = torch.cat([A, A[:, :3]], dim=1)[:, :K]
+    assert A.stride(0) % 8 != 0
+    want = torch.from_numpy(a @ b.T).float().cuda()
+    assert torch.equal(tgemm.gemm_w4(A, B), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tgemm.gemm_w4(A, B)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert tgemm.device_status() == 0
