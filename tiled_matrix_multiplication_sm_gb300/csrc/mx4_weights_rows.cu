@@ -1,8 +1,8 @@
 // Few BF16 rows times a kept 4-bit matrix, C = alpha X W^T + beta C + bias
 // with at most MX4_FEW_ROWS rows of X: bound by reading W once.
 //
-// A warp multiplies 16 RW rows of W (the 16-row side of mma.sync m16n8k16)
-// with 8 NT rows of X. A lane takes 16 bytes of codes of two rows -- 32
+// A warp multiplies 32 rows of W (RW times the 16-row side of mma.sync
+// m16n8k16) with 8 NT rows of X. A lane takes 16 bytes of codes of two rows -- 32
 // columns of K, four lanes side by side 128 -- and uses them as the K
 // positions that the instruction gives it: a sum over K may take its terms in
 // any order as long as X's fragments follow the same one. So codes go from
@@ -25,6 +25,7 @@ using namespace mx4_decode;
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
 constexpr int UNIT_K = 128;
+constexpr int RW = 2, TN = 16 * RW;                  // 16-row tiles of W a warp, and their rows
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -51,12 +52,10 @@ __device__ __forceinline__ uint4 load_x(const __nv_bfloat16* x, int left) {
 // slots of its own, DEPTH units ahead, so the copies need no registers and no
 // barrier.
 constexpr int DEPTH = 2;
-template <int RW>
 struct Unit {
     uint4 codes[2 * RW];
     uint32_t scales[2 * RW];
 };
-template <int RW>
 struct Slots {
     uint4 codes[WARPS][DEPTH][2 * RW][32];
     uint32_t scales[WARPS][DEPTH][2 * RW][32];
@@ -72,18 +71,18 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 // BLOCKS: how many blocks are resident on an SM, 2 (up to 128 registers a
 // thread) or 3 (80). LONG: a warp's sum is made of parts (for sums of one part,
 // 1 x 14336 x 4096 MXFP4 with FP32 C, the registers of a second sum cost 6 %).
-template <int FMT, int NT, int RW, int BLOCKS, bool LONG, typename TC>
+template <int FMT, int NT, int BLOCKS, bool LONG, typename TC>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
 weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool vec, Mx4Operand W,
                     Mx4Out out, int split) {
-    constexpr int TN = 16 * RW, TM = 8 * NT;
+    constexpr int TM = 8 * NT;
     __shared__ uint32_t factors[256];
     extern __shared__ __align__(16) uint8_t slots_raw[];
-    Slots<RW>& slots = *reinterpret_cast<Slots<RW>*>(slots_raw);
+    Slots& slots = *reinterpret_cast<Slots*>(slots_raw);
     // The sums, once every warp is done with its slots.
     float (&part)[WARPS][TN][TM + 1] = *reinterpret_cast<float (*)[WARPS][TN][TM + 1]>(slots_raw);
     __shared__ float total[TN * TM];
-    static_assert(sizeof(part) <= sizeof(Slots<RW>), "sums in place of the slots");
+    static_assert(sizeof(part) <= sizeof(Slots), "sums in place of the slots");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = split > 1 ? (int)(blockIdx.x % split) : 0;
     const long n0 = (long)(blockIdx.x / split) * TN;
@@ -103,15 +102,12 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
     for (int i = 0; i < 2 * RW; ++i) {
         const uint32_t r = (uint32_t)min((long)(i * 8 + g), N - 1 - n0);
         code_at[i] = r * pitch;
-        const uint32_t in = (uint32_t)(n0 % 32) + r;               // the block's rows lie in one tile
-        scale_at[i] = (in / 32 * 4 + in % 32 * 16) - (uint32_t)(n0 % 32 * 16) +
-                      (FMT == TGEMM_MXFP4 ? 0 : (t >> 1) * MX4_TILE_BYTES);
+        scale_at[i] = r * 16 + (FMT == TGEMM_MXFP4 ? 0 : (t >> 1) * MX4_TILE_BYTES);     // 32 rows in one column of a tile
     }
     const __nv_bfloat16* x_row[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) x_row[i] = X + (long)min(i * 8 + g, M - 1) * ldx + t * 32;
 
-    using U = Unit<RW>;
     // A unit's copies, one group; past the last unit an empty one.
     auto fetch = [&](int unit, int slot) {
         if (unit < units) {
@@ -126,7 +122,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto take = [&](U& u, int slot) {
+    auto take = [&](Unit& u, int slot) {
 #pragma unroll
         for (int i = 0; i < 2 * RW; ++i) {
             u.codes[i] = slots.codes[warp][slot][i][lane];
@@ -137,7 +133,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
 
     float acc[RW][NT][4] = {};
     // Columns j * 8 .. j * 8 + 7 of a lane's 32: X's fragments, and the product.
-    auto step8 = [&](const U& u, int j, const uint4 (&xs)[NT], const uint32_t (&f)[2 * RW][2], auto is_wide) {
+    auto step8 = [&](const Unit& u, int j, const uint4 (&xs)[NT], const uint32_t (&f)[2 * RW][2], auto is_wide) {
         uint32_t b[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -163,7 +159,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
         }
     };
     // X comes from the caches: loaded when its unit is due, not ahead.
-    auto run = [&](const U& u, int unit) {
+    auto run = [&](const Unit& u, int unit) {
         uint32_t f[2 * RW][2];                     // the factors of a row's first and last 16 codes
         bool w = false;
 #pragma unroll
@@ -228,7 +224,7 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
 #pragma unroll 1
     for (; unit < units; unit += step) {
         asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory");
-        U u;
+        Unit u;
         take(u, slot);
         fetch(unit + DEPTH * step, slot);            // the lane's own slot, read just before
         run(u, unit);
@@ -281,14 +277,14 @@ weights_rows_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, bool 
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int FMT, int NT, int RW, int BLOCKS, bool LONG, typename TC>
+template <int FMT, int NT, int BLOCKS, bool LONG, typename TC>
 cudaError_t launch_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
                    int split, cudaStream_t s) {
-    const long tiles = ((long)N + 16 * RW - 1) / (16 * RW);
+    const long tiles = ((long)N + TN - 1) / TN;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = sizeof(Slots<RW>);
+    cfg.dynamicSmemBytes = sizeof(Slots);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -299,19 +295,19 @@ cudaError_t launch_kernel(int M, int N, int K, const __nv_bfloat16* X, long ldx,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    const cudaError_t e = set_smem_limit_once<weights_rows_kernel<FMT, NT, RW, BLOCKS, LONG, TC>>(sizeof(Slots<RW>));
+    const cudaError_t e = set_smem_limit_once<weights_rows_kernel<FMT, NT, BLOCKS, LONG, TC>>(sizeof(Slots));
     if (e != cudaSuccess) return e;
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
-    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, RW, BLOCKS, LONG, TC>, M, N, K, X, ldx, vec, W, out, split);
+    return cudaLaunchKernelEx(&cfg, weights_rows_kernel<FMT, NT, BLOCKS, LONG, TC>, M, N, K, X, ldx, vec, W, out, split);
 }
 
-template <int FMT, int NT, int RW, int BLOCKS, typename TC>
+template <int FMT, int NT, int BLOCKS, typename TC>
 cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W, const Mx4Out& out,
                    int split, cudaStream_t s) {
     if constexpr (sizeof(TC) == 4)
         if (((long)K + UNIT_K - 1) / UNIT_K > (long)WARPS * split * (SUM_K / UNIT_K))
-            return launch_kernel<FMT, NT, RW, BLOCKS, true, TC>(M, N, K, X, ldx, W, out, split, s);
-    return launch_kernel<FMT, NT, RW, BLOCKS, false, TC>(M, N, K, X, ldx, W, out, split, s);
+            return launch_kernel<FMT, NT, BLOCKS, true, TC>(M, N, K, X, ldx, W, out, split, s);
+    return launch_kernel<FMT, NT, BLOCKS, false, TC>(M, N, K, X, ldx, W, out, split, s);
 }
 
 // Resident blocks (2 or 3) and the blocks of a cluster that split K. The
@@ -341,9 +337,9 @@ Choice choose(long tiles, int K, int num_sms, int most = 3) {
 template <int FMT, int NT, typename TC>
 cudaError_t launch_blocks(int M, int N, int K, const __nv_bfloat16* X, long ldx, const Mx4Operand& W,
                           const Mx4Out& out, int num_sms, cudaStream_t s) {
-    const Choice c = choose(((long)N + 31) / 32, K, num_sms);
-    return c.blocks == 2 ? launch<FMT, NT, 2, 2, TC>(M, N, K, X, ldx, W, out, c.split, s)
-                         : launch<FMT, NT, 2, 3, TC>(M, N, K, X, ldx, W, out, c.split, s);
+    const Choice c = choose(((long)N + TN - 1) / TN, K, num_sms);
+    return c.blocks == 2 ? launch<FMT, NT, 2, TC>(M, N, K, X, ldx, W, out, c.split, s)
+                         : launch<FMT, NT, 3, TC>(M, N, K, X, ldx, W, out, c.split, s);
 }
 
 template <int FMT, typename TC>
@@ -351,7 +347,7 @@ cudaError_t launch_rows(int M, int N, int K, const __nv_bfloat16* X, long ldx, c
                         const Mx4Out& out, int num_sms, cudaStream_t s) {
     if (M <= 8) return launch_blocks<FMT, 1, TC>(M, N, K, X, ldx, W, out, num_sms, s);
     if (M <= 16) return launch_blocks<FMT, 2, TC>(M, N, K, X, ldx, W, out, num_sms, s);
-    return launch<FMT, 3, 2, 2, TC>(M, N, K, X, ldx, W, out, choose(((long)N + 31) / 32, K, num_sms, 2).split, s);
+    return launch<FMT, 3, 2, TC>(M, N, K, X, ldx, W, out, choose(((long)N + TN - 1) / TN, K, num_sms, 2).split, s);
 }
 
 }  // namespace
