@@ -123,9 +123,14 @@ cudaError_t mx4_weights(int M, int N, int K, const void* A, long lda, const Mx4O
                         const Mx4Out& out, int num_sms, cudaStream_t s);
 
 // At most MX4_FEW_ROWS rows of A (mx4_weights_rows.cu): all products with up to
-// 8, and small ones with more, where its shorter start counts. 24 x 1024 x 1024
-// MXFP4 takes 3.9 us there and 4.6 in mx4_weights_tmem.cu; 24 x 4096 x 4096 NVFP4
-// 8.9 and 7.7; 16 x 4096 x 14336 16.6 and 16.0; 8 x 4096 x 14336 13.4 and 14.9.
+// 8, and small ones with more, where its shorter start counts. There, and in
+// mx4_weights_tmem.cu (us, BF16 C):
+//     MXFP4   8 x 1024 x 1024    2.4   4.3      NVFP4   9 x 1024 x 4096    5.3   5.5
+//             8 x 4096 x 14336  13.3  15.0             24 x 1024 x 4096    6.0   5.7
+//             8 x 65536 x 4096  48.9  59.6             16 x 4096 x 4096    7.3   7.3
+//            24 x 1024 x 1024    4.0   4.5             24 x 4096 x 4096    9.0   7.7
+//            16 x 14336 x 4096  14.6  15.2             16 x 14336 x 4096  16.1  14.8
+//            24 x 14336 x 4096  22.9  15.5             16 x 65536 x 4096  66.2  59.0
 constexpr int MX4_FEW_ROWS = 24;
 inline bool mx4_few_rows(int M, int N, int K) { return M <= 8 || (M <= MX4_FEW_ROWS && (long)N * K < 1L << 24); }
 cudaError_t mx4_weights_rows(int M, int N, int K, const void* A, long lda, const Mx4Operand& B, int fmt,

@@ -600,8 +600,7 @@ dequantize_any_kernel(int R, int C, const uint8_t* codes, const uint8_t* scales,
     }
 }
 
-// One thread moves 16 bytes of codes or, in the second part of the grid's
-// work, one scale byte.
+// A thread moves, of every row that it takes, a byte of codes and a scale byte.
 template <int FMT>
 __global__ void __launch_bounds__(256)
 pack_kernel(int R, int C, const uint8_t* sc, long ldc, const uint8_t* ss, long lds, uint8_t* codes,

@@ -310,11 +310,12 @@ cudaError_t launch(int M, int N, int K, const __nv_bfloat16* X, long ldx, const 
     return launch_kernel<FMT, NT, BLOCKS, false, TC>(M, N, K, X, ldx, W, out, split, s);
 }
 
-// Resident blocks (2 or 3) and the blocks of a cluster that split K. The
-// kernel is bound by instruction issue, so a round of resident blocks takes as
-// long as there are blocks on an SM, times a warp's units and about three
-// units' worth of start and end. Two against three: 16 x 4096 x 14336 NVFP4
-// 16.6 us (clusters of 2) and 19.4 (of 3), 16 x 14336 x 4096 19.2 and 15.6.
+// Resident blocks (2 or 3) and the blocks of a cluster that split K. A round of
+// resident blocks is taken to last as long as there are blocks on an SM, times a
+// warp's units and about three units' worth of start and end. Two against three,
+// MXFP4, us (* the choice): 1 x 1024 x 4096 3.9* and 4.5, 8 x 4096 x 4096 5.5* and 7.3,
+// 1 x 4096 x 14336 12.9* and 13.9, 8 x 14336 x 4096 14.8 and 11.5*, 8 x 8192 x 28672
+// 38.6* and 46.0; with many rounds it errs, 1 x 65536 x 4096 43.5* and 39.9.
 struct Choice {
     int blocks, split;
 };
