@@ -53,16 +53,11 @@ struct Shape {
     // with BUFS buffers a warp. A second set shortens the only tile's way out
     // (1024^3 MXFP4 8.5 -> 7.4 us); between tiles shared memory is the bound,
     // and it costs (8192 x 14336 x 4096 NVFP4 155 -> 158 us). Long sums need two:
-    // a thread holds half a row of the tile, which for a pair takes more
-    // registers than 10 warps can have each: the first four (two of them idle)
-    // give theirs to the epilogue's. (14336 x 4096 x 8192 NVFP4: 171 us, with
-    // the sums spilled 226; in one part 164.)
+    // a thread holds half a row of the tile, for a pair in 128 of its 168
+    // registers (14336 x 4096 x 8192 NVFP4: 170 us, in one part 164; with the
+    // sums spilled around the epilogue's waits 226).
     static constexpr int SETS = PAIR && !LONG ? 1 : 2, BUFS = 2 / SETS;
-    static constexpr bool SHARED_REGS = PAIR && LONG;
-    static constexpr int EPI0 = SHARED_REGS ? 4 : 2;                  // the epilogue's first warp
-    static constexpr int EPI_WARPS = 4 * SETS, THREADS = 32 * (EPI0 + EPI_WARPS);
-    static constexpr int FEW_REGS = 40, MANY_REGS = 224;
-    static constexpr int REGS = SHARED_REGS ? (4 * FEW_REGS + EPI_WARPS * MANY_REGS) / (4 + EPI_WARPS) + 1 : 0;   // at launch, at least
+    static constexpr int EPI_WARPS = 4 * SETS, THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int SF_TILES = STAGE_K / mx4_block(FMT) / 4;     // scale tiles of 128 rows a stage
     static constexpr int SFA_BYTES = SF_TILES * MX4_TILE_BYTES;
     static constexpr int SFB_BYTES = SFA_BYTES * (TN / 128);
@@ -144,8 +139,6 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t tmem_empty0 =
         PAIR ? map_to_rank(smem_u32(&sy->tmem_empty[0]), 0) : smem_u32(&sy->tmem_empty[0]);
 
-    if (warp < S::EPI0) {
-    if constexpr (S::SHARED_REGS) give_registers<S::FEW_REGS>();
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
         // The whole warp runs the loop (addresses stay uniform values), one
@@ -255,13 +248,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
         __syncwarp();
-    }
     } else {
         // ------------------------------------------------------ epilogue
-        if constexpr (S::SHARED_REGS) take_registers<S::MANY_REGS>();
         const int q = warp & 3;                            // tensor-memory lanes 32 q .. 32 q + 31
-        const int set = (warp - S::EPI0) >> 2;
-        uint8_t* bufs = epi + (warp - S::EPI0) * S::BUFS * BUF_BYTES;
+        const int set = (warp - 2) >> 2;
+        uint8_t* bufs = epi + (warp - 2) * S::BUFS * BUF_BYTES;
         const float ga = mx4_g(p.ga), gb = mx4_g(p.gb);
         int it = 0;
         auto release = [&]() {
@@ -280,7 +271,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             constexpr int HALF = S::TN / 2, TURNS = HALF / 64;
             bool ok = true;
             for (int t = unit; ok && t < p.num_tiles; t += p.units) {
-                float sum[TURNS][2][32] = {};
+                float sum[TURNS][2][32] = {};            // (a first part that is moved instead of added: more registers)
                 #pragma unroll 1
                 for (int first = kb0; first < kb1; first += PART_STAGES, ++it) {
                     ok = __all_sync(~0u, mbar_wait<true, PAIR, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
@@ -290,17 +281,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < TURNS; ++i) {
                         const uint32_t from = acc + (i ^ (TURNS > 1 ? set : 0)) * 64;
-                        uint32_t r[2][32];
-                        tmem_ld32(from, r[0]);
-                        tmem_ld32(from + 32, r[1]);
-                        tmem_wait_ld(r[0]);
-                        tmem_wait_ld(r[1]);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(from + c, r);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[i][c / 32][c % 32 + j] += __uint_as_float(r[j]);
+                        }
                         if (i == 0) release();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                sum[i][h][j] += __uint_as_float(r[h][j]);
                     }
                 }
                 if (!ok) break;
@@ -370,18 +359,7 @@ template <int FMT, bool PAIR, bool LONG, typename TC>
 cudaError_t launch_kernel(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSA, const CUtensorMap& tmSB,
                           const CUtensorMap& tmC, const Params& p, cudaStream_t s) {
     using S = Shape<FMT, PAIR, LONG>;
-    cudaError_t e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, LONG, TC>>(S::SMEM);
-    if constexpr (S::SHARED_REGS) {
-        // A block that is launched with fewer registers than its warps are to
-        // have would wait for them without end.
-        static std::atomic<int> regs{0};
-        if (e == cudaSuccess && regs.load(std::memory_order_relaxed) == 0) {
-            cudaFuncAttributes a;
-            e = cudaFuncGetAttributes(&a, mx4_gemm_kernel<FMT, PAIR, LONG, TC>);
-            if (e == cudaSuccess) regs.store(a.numRegs, std::memory_order_relaxed);
-        }
-        if (e == cudaSuccess && regs.load(std::memory_order_relaxed) < S::REGS) return cudaErrorLaunchOutOfResources;
-    }
+    const cudaError_t e = set_smem_limit_once<mx4_gemm_kernel<FMT, PAIR, LONG, TC>>(S::SMEM);
     if (e != cudaSuccess) return e;
     ClusterLaunch cfg((PAIR ? 2 : p.split) * p.units, S::THREADS, S::SMEM, PAIR ? 2 : p.split, s);
     return cudaLaunchKernelEx(&cfg.config, mx4_gemm_kernel<FMT, PAIR, LONG, TC>, tmA, tmB, tmSA, tmSB, tmC, p);
