@@ -44,3 +44,19 @@ def test_operands_are_not_read_as_read_only():
         code = re.sub(r"//.*", "", text)
         for what in ("__ldg", "ld.global.nc", "__restrict__"):
             assert what not in code, (name, what)
+
+
+def test_kernels_that_take_all_tensor_memory_have_an_sm_to_themselves():
+    """Their wait for it has no limit, and blocks of a cluster wait for each
+    other: two clusters on the same SMs could each hold what the other needs.
+    An SM has 228 KB of shared memory, 1 KB of it taken for each block."""
+    kb = 1024
+    text = dict(sources())
+    limit = int(re.search(r"SMEM_LIMIT = (\d+) \* 1024;", text["mx4_weights_tmem.cu"])[1]) * kb
+    assert re.search(r"ONE_BLOCK = SMEM_LIMIT / 2 \+ 1024;", text["mx4_weights_tmem.cu"])
+    assert re.search(r"smem_bytes<FMT>\(p\.rows\) > ONE_BLOCK \? smem_bytes<FMT>\(p\.rows\) : ONE_BLOCK;", text["mx4_weights_tmem.cu"])
+    assert 2 * (limit // 2 + kb + kb) > 228 * kb
+    # The others' stages alone, in bytes.
+    for name, stage in (("mx4_gemm.cu", 2 * 128 * 128), ("mx4_weights.cu", 2 * 128 * 128)):
+        stages = int(re.search(r"constexpr int STAGES = (\d+);", text[name])[1])
+        assert 2 * (stages * stage + kb) > 228 * kb, name

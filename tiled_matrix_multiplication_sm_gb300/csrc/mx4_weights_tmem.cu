@@ -75,6 +75,10 @@ constexpr int smem_bytes(int rows) {
     return 1024 + SLOTS * PARTS * rows * SW + CHUNKS * (CODES_BYTES + SF_BYTES<FMT>) + SYNC_BYTES;
 }
 static_assert(smem_bytes<TGEMM_NVFP4>(128) <= SMEM_LIMIT, "shared memory");
+// A block takes all of an SM's tensor memory and waits for it without a limit:
+// of two clusters that shared SMs, each could hold what the other waits for. A
+// launch asks for so much shared memory that no SM holds two blocks.
+constexpr int ONE_BLOCK = SMEM_LIMIT / 2 + 1024;
 
 struct Params : Tiling {
     int stages;                 // of K
@@ -357,7 +361,8 @@ cudaError_t launch(int M, int N, int K, const void* X, long ldx, const Mx4Operan
     if (e == cudaSuccess) e = clusters_that_fit<weights_tmem_kernel<FMT, TC>>(THREADS<TC>, SMEM_LIMIT, &fits);
     if (e != cudaSuccess) return e;
     p.split = split_for(p.num_tiles, p.stages, fits, 3);
-    ClusterLaunch cfg(p.split * p.num_tiles, THREADS<TC>, smem_bytes<FMT>(p.rows), p.split, s);
+    const int smem = smem_bytes<FMT>(p.rows) > ONE_BLOCK ? smem_bytes<FMT>(p.rows) : ONE_BLOCK;
+    ClusterLaunch cfg(p.split * p.num_tiles, THREADS<TC>, smem, p.split, s);
     return cudaLaunchKernelEx(&cfg.config, weights_tmem_kernel<FMT, TC>, tmX, tmW, tmS, p);
 }
 
