@@ -1,0 +1,119 @@
+// Activations and their slopes, in FP32.
+#pragma once
+
+#include "fused_internal.h"
+
+namespace tgemm {
+namespace fused_act {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float ROOT_HALF = 0.70710678118654752f;
+constexpr float ROOT_2_PI = 0.79788456080286536f;       // sqrt(2 / pi)
+constexpr float INV_ROOT_2PI = 0.39894228040143268f;    // 1 / sqrt(2 pi)
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-v)): relative error below 2^-20 where it is not near FP32's
+// smallest numbers (the product v log2(e) is rounded), far below BF16's rounding.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + exp2_fast(v * -LOG2E)); }
+
+// tanh's form of GELU is z sigmoid(2 u), without the cancellation of 1 + tanh
+// for negative z.
+__device__ __forceinline__ float tanh_arg(float z) { return 2.0f * ROOT_2_PI * z * fmaf(0.044715f * z, z, 1.0f); }
+
+template <int ACT>
+__device__ __forceinline__ float value(float z) {
+    if constexpr (ACT == TGEMM_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == TGEMM_ACT_GELU) return 0.5f * z * erfcf(-ROOT_HALF * z);
+    if constexpr (ACT == TGEMM_ACT_GELU_TANH) return z * sigmoid(tanh_arg(z));
+    if constexpr (ACT == TGEMM_ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+
+// act(z) and act'(z).
+template <int ACT>
+__device__ __forceinline__ void value_slope(float z, float& v, float& d) {
+    if constexpr (ACT == TGEMM_ACT_RELU) {
+        v = value<ACT>(z);
+        d = z > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (ACT == TGEMM_ACT_GELU) {
+        const float phi = 0.5f * erfcf(-ROOT_HALF * z);
+        v = z * phi;
+        d = fmaf(z * INV_ROOT_2PI, exp2_fast(z * z * (-0.5f * LOG2E)), phi);
+    } else if constexpr (ACT == TGEMM_ACT_GELU_TANH) {
+        const float s = sigmoid(tanh_arg(z));
+        v = z * s;
+        d = fmaf(v * (1.0f - s), 2.0f * ROOT_2_PI * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
+    } else if constexpr (ACT == TGEMM_ACT_SILU) {
+        const float s = sigmoid(z);
+        v = z * s;
+        d = fmaf(v, 1.0f - s, s);
+    } else {
+        v = z;
+        d = 1.0f;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void apply(int act, float (&v)[N]) {
+#define TGEMM_EACH(ACT)                                       \
+    case ACT:                                                 \
+        _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] = value<ACT>(v[j]); \
+        break
+    switch (act) {
+        TGEMM_EACH(TGEMM_ACT_RELU);
+        TGEMM_EACH(TGEMM_ACT_GELU);
+        TGEMM_EACH(TGEMM_ACT_GELU_TANH);
+        TGEMM_EACH(TGEMM_ACT_SILU);
+        default: break;
+    }
+#undef TGEMM_EACH
+}
+// d *= act'(z).
+template <int N>
+__device__ __forceinline__ void times_slope(int act, float (&d)[N], const float (&z)[N]) {
+#define TGEMM_EACH(ACT)                                       \
+    case ACT:                                                 \
+        _Pragma("unroll") for (int j = 0; j < N; ++j) {       \
+            float v, slope;                                   \
+            value_slope<ACT>(z[j], v, slope);                 \
+            d[j] *= slope;                                    \
+        }                                                     \
+        break
+    switch (act) {
+        TGEMM_EACH(TGEMM_ACT_RELU);
+        TGEMM_EACH(TGEMM_ACT_GELU);
+        TGEMM_EACH(TGEMM_ACT_GELU_TANH);
+        TGEMM_EACH(TGEMM_ACT_SILU);
+        default: break;
+    }
+#undef TGEMM_EACH
+}
+// Gated: g, u become d u act'(g), d act(g).
+template <int N>
+__device__ __forceinline__ void gated_grad(int act, const float (&d)[N], float (&g)[N], float (&u)[N]) {
+#define TGEMM_EACH(ACT)                                       \
+    case ACT:                                                 \
+        _Pragma("unroll") for (int j = 0; j < N; ++j) {       \
+            float v, slope;                                   \
+            value_slope<ACT>(g[j], v, slope);                 \
+            g[j] = d[j] * u[j] * slope;                       \
+            u[j] = d[j] * v;                                  \
+        }                                                     \
+        break
+    switch (act) {
+        TGEMM_EACH(TGEMM_ACT_RELU);
+        TGEMM_EACH(TGEMM_ACT_GELU);
+        TGEMM_EACH(TGEMM_ACT_GELU_TANH);
+        TGEMM_EACH(TGEMM_ACT_SILU);
+        default:
+            TGEMM_EACH(TGEMM_ACT_NONE);
+    }
+#undef TGEMM_EACH
+}
+
+}  // namespace fused_act
+}  // namespace tgemm

@@ -1,0 +1,867 @@
+// Products of BF16 matrices with what follows them in their epilogue: bias,
+// activation, gating and residual; an activation's gradient and its column sums;
+// the maxima and sums of a softmax cross entropy, and its gradient.
+//
+// The product is the tensor cores' (tcgen05, kind f16, FP32 accumulators): 256 x
+// 256 tiles on SM pairs (cta_group::2), persistent, one block on an SM. Ten
+// warps: 0 copies (TMA), 1 issues the MMAs, 2 to 9 are the epilogue, two sets
+// of four (one to a quarter of tensor memory's lanes), each set on half of the
+// tile's columns. Stages of 64 columns of K, two accumulators, so that a tile's
+// epilogue runs beside the next tile's MMAs. Either operand is read as it is
+// kept, K-major in boxes of 128 rows x 128 bytes or MN-major in two boxes of 64
+// rows of K x 128 bytes, both in the 128-byte swizzle.
+//
+// Gated products take 128 columns of g (the pair's first block) and the same 128
+// of u (its second) for a tile, so that a thread holds both of a row.
+//
+// Sums of more than SUM_K columns that end in 32 bits (LONG) come in parts,
+// accumulator by accumulator; the epilogue's warps add them up in registers
+// and put the total back where the last part lay.
+//
+// A thread has a row of the tile. Where C, R and Z allow TMA, boxes of 32 rows x
+// 128 bytes pass between its registers and memory through shared memory; where
+// they do not, 32 x 32 blocks of sums go through shared memory to a column a
+// lane, and the epilogue works on segments of rows.
+//
+// Rows past M and columns past N are read as zeros and not stored. Waits are
+// bounded as in the other tensor-core kernels.
+
+#include "fused_act.h"
+#include "mx4_tile.h"
+
+#include <cstring>
+
+namespace tgemm {
+namespace {
+
+using namespace mx4_tile;
+using namespace fused_act;
+typedef __nv_bfloat16 bf16;
+
+constexpr int TILE = 256;
+constexpr int STAGE_K = 64;
+constexpr int OPERAND_BYTES = 128 * SW;              // a block's 128 rows of A, or of B
+constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
+constexpr int STAGES = 5;
+constexpr int EPI_WARPS = 8;
+constexpr int WARP_BYTES = 2 * BUF_BYTES;            // two boxes a warp
+constexpr int EPI_BYTES = EPI_WARPS * WARP_BYTES;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 256;
+static_assert(SMEM <= 227 * 1024, "shared memory");
+constexpr int PART_BLOCKS = SUM_K / STAGE_K;
+
+struct Sync {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t tmem_full[2], tmem_empty[2];
+    uint64_t loaded[EPI_WARPS];                      // boxes of R or Z
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Sync) <= 256, "barrier block");
+
+struct Params {
+    int M, N, kblocks;
+    int tiles_n, num_tiles, units, group_m, tiles_m;
+    int a_mn, b_mn;
+    int rows;                   // C, R and Z pass by TMA
+    int bias4;                  // bias in pieces of 16 bytes
+    FusedEpilogue e;
+    unsigned long long wait_limit_ns;
+    int* status;
+    int debug_stall;
+};
+
+struct Maps {
+    CUtensorMap A, B, B2;       // B2: gated, u's
+    // ACT: C, R, Z, Z's second half. GRAD: C, Z, and the second halves of both.
+    CUtensorMap E[4];
+};
+
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// ------------------------------------------------- boxes in shared memory
+// This thread's row of a box: 32 FP32 or half h of 64 BF16.
+__device__ __forceinline__ void put_f32(uint8_t* buf, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(buf + swizzled(lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void put_bf16(uint8_t* buf, int h, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(buf + swizzled(lane, h * 4 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void get_f32(const uint8_t* buf, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float4 w = *reinterpret_cast<const float4*>(buf + swizzled(lane, j));
+        v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
+    }
+}
+__device__ __forceinline__ void get_bf16(const uint8_t* buf, int h, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(buf + swizzled(lane, h * 4 + j));
+        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[8 * j + 2 * k] = __uint_as_float(p[k] << 16);
+            v[8 * j + 2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
+        }
+    }
+}
+
+// 32 sums of this thread's lane (zeros where K is 0).
+__device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32], int kblocks) {
+    uint32_t r[32];
+    tmem_ld32(tmem, r);
+    tmem_wait_ld(r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = kblocks > 0 ? __uint_as_float(r[j]) : 0.0f;
+}
+
+// v += bias of columns `at`, .. (of `cols`, from `bias` on).
+__device__ __forceinline__ void add_bias(const Params& p, const float* bias, int at, float (&v)[32]) {
+    if (bias == nullptr) return;
+    if (p.bias4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at + 4 * j < p.N) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + at + 4 * j);
+                v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+            }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (at + j < p.N) v[j] += bias[at + j];
+    }
+}
+
+// Sums over the warp's 32 rows of 32 columns: lane j gets column j's. Each step
+// exchanges half of the columns that are left with the lane half as far away.
+__device__ __forceinline__ float column_sums(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+        const bool upper = lane & w;
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+            const float send = upper ? v[j] : v[j + w], keep = upper ? v[j + w] : v[j];
+            v[j] = keep + __shfl_xor_sync(~0u, send, w);
+        }
+    }
+    return v[0];
+}
+
+// --------------------------------------------- C in segments of its rows
+// 32 columns from column `col` of C of this warp's `rows` rows, from registers
+// (a row a lane) through `bufs` to a column a lane, any alignment, eight rows'
+// loads ahead of their stores. v2: gated ACT, u's sums.
+template <int KIND, bool GATED>
+__device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, int row0, int rows, int col, const float (&v)[32],
+                                              const float (&v2)[32]) {
+    const FusedEpilogue& e = p.e;
+    const int lane = threadIdx.x & 31;
+    constexpr bool TWO = KIND == FUSED_ACT && GATED;
+    __syncwarp();
+    put_f32(bufs, v);
+    if constexpr (TWO) put_f32(bufs + BUF_BYTES, v2);
+    __syncwarp();
+    const int c = col + lane;
+    if (c < p.N) {
+        const long N = p.N;
+        float b = 0.0f, b2 = 0.0f;
+        if (KIND == FUSED_ACT && e.bias != nullptr) {
+            b = e.bias[c];
+            if constexpr (TWO) b2 = e.bias[N + c];
+        }
+        float sum = 0.0f, sum2 = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < rows; k += 8) {
+            const long row = row0 + k;
+            float x[8], y[8], z[8];
+            bf16* Z = static_cast<bf16*>(e.Z) + row * e.ldz + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t at = swizzled(k + j, lane >> 2) + (lane & 3) * 4;
+                x[j] = *reinterpret_cast<const float*>(bufs + at) + b;
+                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(bufs + BUF_BYTES + at) + b2;
+            }
+            if constexpr (KIND == FUSED_ACT) {
+                if (e.Z != nullptr)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (k + j < rows) {
+                            Z[j * e.ldz] = __float2bfloat16(x[j]);
+                            if constexpr (TWO) Z[j * e.ldz + N] = __float2bfloat16(y[j]);
+                        }
+                apply(e.act, x);
+                if constexpr (TWO)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= y[j];
+                if (e.R != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        z[j] = k + j >= rows ? 0.0f
+                               : e.r_f32     ? static_cast<const float*>(e.R)[(row + j) * e.ldr + c]
+                                             : __bfloat162float(static_cast<const bf16*>(e.R)[(row + j) * e.ldr + c]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = fmaf(e.r_scale, z[j], x[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    z[j] = k + j < rows ? __bfloat162float(Z[j * e.ldz]) : 0.0f;
+                    if constexpr (GATED) y[j] = k + j < rows ? __bfloat162float(Z[j * e.ldz + N]) : 0.0f;
+                }
+                if constexpr (GATED) {
+                    gated_grad(e.act, x, z, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = z[j];
+                } else {
+                    times_slope(e.act, x, z);
+                }
+                if (e.sums != nullptr)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (k + j < rows) {
+                            sum += x[j];
+                            if constexpr (GATED) sum2 += y[j];
+                        }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < rows) {
+                    const long at = (row + j) * e.ldc + c;
+                    if (e.c_f32) static_cast<float*>(e.C)[at] = x[j];
+                    else static_cast<bf16*>(e.C)[at] = __float2bfloat16(x[j]);
+                    if constexpr (KIND == FUSED_GRAD && GATED) static_cast<bf16*>(e.C)[at + N] = __float2bfloat16(y[j]);
+                }
+        }
+        if (KIND == FUSED_GRAD && e.sums != nullptr) {
+            float* out = e.sums + (long)(row0 / FUSED_SUM_ROWS) * (GATED ? 2 * N : N) + c;
+            out[0] = sum;
+            if constexpr (GATED) out[N] = sum2;
+        }
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------- C by TMA, in boxes
+// One lane: a box from shared memory to C or Z, of columns from c on.
+__device__ __forceinline__ void store_box(const Params& p, const CUtensorMap* map, int c, int row0, uint8_t* buf) {
+    if (c < p.N) tma_store_2d(map, c, row0, smem_u32(buf));
+    tma_store_commit();                                  // counted even when there is none
+}
+
+// One lane: the boxes of R or Z that 64 columns from `col` on need, to the two
+// buffers as turn_boxes wants them.
+template <int KIND, bool GATED>
+__device__ __forceinline__ void load_boxes(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t bar, int row0, int col) {
+    const FusedEpilogue& e = p.e;
+    const uint32_t b0 = smem_u32(bufs), b1 = b0 + BUF_BYTES;
+    const bool wide = KIND == FUSED_ACT && e.r_f32, two = (KIND == FUSED_GRAD && GATED) || (wide && col + 32 < p.N);
+    mbar_arrive_expect_tx(bar, (two ? 2 : 1) * BUF_BYTES);
+    tma_load_2d<false>(!wide && !GATED && e.c_f32 ? b1 : b0, &maps->E[1], col, row0, bar);
+    if (two) tma_load_2d<false>(b1, wide ? &maps->E[1] : &maps->E[3], wide ? col + 32 : col, row0, bar);
+}
+
+// 64 columns of C from column `col` on. `acc`: their sums; acc2: gated ACT, u's.
+// The buffers are free; the boxes that load_boxes asked for are in them.
+template <int KIND, bool GATED, typename Release>
+__device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, uint32_t acc2,
+                                           int row0, int rows, int col, int& box, Release release) {
+    const FusedEpilogue& e = p.e;
+    const int lane = threadIdx.x & 31;
+    uint8_t *const b0 = bufs, *const b1 = bufs + BUF_BYTES;
+    const bool aux = KIND == FUSED_GRAD || (KIND == FUSED_ACT && (e.R != nullptr || e.Z != nullptr));
+    float v[32], w[32];
+    auto send = [&](int map, int c, uint8_t* buf) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) store_box(p, &maps->E[map], c, row0, buf);
+    };
+    auto wait_sent = [&]() {
+        if (lane == 0) tma_store_wait_read<0>();
+        __syncwarp();
+    };
+    if constexpr (KIND == FUSED_ACT && GATED) {
+        if (e.Z != nullptr) {
+            // Both halves of Z leave first, through both buffers.
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load_sums(acc + h * 32, v, p.kblocks);
+                add_bias(p, e.bias, col + h * 32, v);
+                put_bf16(b0, h, v);
+                load_sums(acc2 + h * 32, v, p.kblocks);
+                add_bias(p, e.bias != nullptr ? e.bias + p.N : nullptr, col + h * 32, v);
+                put_bf16(b1, h, v);
+            }
+            send(2, col, b0);
+            send(3, col, b1);
+            wait_sent();
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = col + h * 32;
+        load_sums(acc + h * 32, v, p.kblocks);
+        if constexpr (KIND == FUSED_ACT) {
+            add_bias(p, e.bias, c, v);
+            if constexpr (GATED) {
+                load_sums(acc2 + h * 32, w, p.kblocks);
+                add_bias(p, e.bias != nullptr ? e.bias + p.N : nullptr, c, w);
+            }
+        }
+        if (h == 1) release();
+        uint8_t* out = b0;                               // of this half's C
+        if constexpr (KIND == FUSED_ACT) {
+            if constexpr (GATED) {
+                apply(e.act, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= w[j];
+            }
+            if (e.R != nullptr) {
+                if (e.r_f32) get_f32(h == 0 ? b0 : b1, w);
+                else get_bf16(!GATED && e.c_f32 ? b1 : b0, h, w);
+            }
+            if constexpr (!GATED) {
+                if (e.Z != nullptr) put_bf16(b1, h, v);
+                apply(e.act, v);
+            }
+            if (e.R != nullptr)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(e.r_scale, w[j], v[j]);
+            if (e.c_f32 && e.Z == nullptr && h == 1) out = b1;
+        } else {
+            float g[32];
+            if constexpr (GATED) {
+                get_bf16(b0, h, g);
+                get_bf16(b1, h, w);
+                gated_grad(e.act, v, g, w);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = g[j];
+                put_bf16(b1, h, w);
+            } else {
+                get_bf16(e.c_f32 ? b1 : b0, h, w);
+                times_slope(e.act, v, w);
+                if (e.c_f32 && h == 1) out = b1;
+            }
+        }
+        if (!aux) {
+            // Boxes through the two buffers in turn.
+            out = bufs + (box & 1) * BUF_BYTES;
+            if (e.c_f32 || h == 0) {
+                if (lane == 0) tma_store_wait_read<1>();
+                __syncwarp();
+            }
+        } else if (KIND == FUSED_ACT && e.c_f32 && e.Z != nullptr && h == 1) {
+            wait_sent();
+        }
+        if (e.c_f32) {
+            put_f32(out, v);
+            send(0, c, out);
+            ++box;
+        } else {
+            put_bf16(out, h, v);
+        }
+        if constexpr (KIND == FUSED_GRAD) {
+            if (e.sums != nullptr) {
+                // (Rows past M may hold a NaN: 0 times an infinity of B's.)
+                float* to = e.sums + (long)(row0 / FUSED_SUM_ROWS) * (GATED ? 2L * p.N : p.N) + c + lane;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = lane < rows ? v[j] : 0.0f;
+                float sum = column_sums(v);
+                if (c + lane < p.N) to[0] = sum;
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) w[j] = lane < rows ? w[j] : 0.0f;
+                    sum = column_sums(w);
+                    if (c + lane < p.N) to[p.N] = sum;
+                }
+            }
+        }
+    }
+    if (!e.c_f32) {
+        send(0, col, aux ? b0 : bufs + (box & 1) * BUF_BYTES);
+        ++box;
+        if constexpr (KIND == FUSED_GRAD && GATED) send(2, col, b1);
+    }
+    if (KIND == FUSED_ACT && !GATED && e.Z != nullptr) send(2, col, b1);
+}
+
+// ------------------------------------------------------------ cross entropy
+// The maximum of this thread's row over the set's 128 columns and the sum of
+// exp(z - maximum); the target's logit where it is among them.
+__device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int row, int col) {
+    const FusedEpilogue& e = p.e;
+    const bool in = row < p.M;
+    const long long target = in ? e.target[row] - e.first : -1;
+    float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < FUSED_CE_COLS; i += 32) {
+        float v[32];
+        load_sums(acc + i, v, p.kblocks);
+        const int c = col + i;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= e.alpha;
+        if (c + 32 > p.N)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = c + j < p.N ? v[j] : -INFINITY;
+        const long long t = target - c;
+        const bool here = t >= 0 && t < 32 && target < p.N;
+        if (__any_sync(~0u, here)) {
+            float z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = t == j ? v[j] : z;
+            if (here) e.picked[row] = z;
+            __syncwarp();
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        s *= exp2_fast((m - base) * LOG2E);
+        float q[4] = {};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) q[j & 3] += exp2_fast((v[j] - base) * LOG2E);
+        s += (q[0] + q[1]) + (q[2] + q[3]);
+        m = top;
+    }
+    if (in && col < p.N) e.parts[(long)(col / FUSED_CE_COLS) * p.M + row] = make_float2(m, s);
+}
+
+// 64 columns of the logits' gradient.
+__device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
+                                             int& box, float lse, float scale, long long target, bool kept) {
+    const int lane = threadIdx.x & 31;
+    uint8_t* buf = bufs + (box++ & 1) * BUF_BYTES;
+    if (lane == 0) tma_store_wait_read<1>();
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[32];
+        load_sums(acc + h * 32, v, p.kblocks);
+        const long long t = target - (col + h * 32);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] * p.e.alpha - lse) * LOG2E);
+        if (__any_sync(~0u, t >= 0 && t < 32))
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] -= t == j ? 1.0f : 0.0f;
+        // (A row left out may hold infinities.)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = kept ? v[j] * scale : 0.0f;
+        put_bf16(buf, h, v);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) store_box(p, &maps->E[0], col, row0, buf);
+}
+
+// ------------------------------------------------------------------- kernel
+__device__ __forceinline__ void tile_at(int t, const Params& p, int& mb, int& nb) {
+    const int per_group = p.group_m * p.tiles_n;
+    const int first = t / per_group * p.group_m;
+    const int gm = min(p.tiles_m - first, p.group_m);
+    mb = first + t % per_group % gm;
+    nb = t % per_group / gm;
+}
+
+template <int KIND, bool GATED, bool LONG>
+__global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    constexpr bool TWO = KIND == FUSED_ACT && GATED;     // 128 columns of C a tile
+    constexpr int TC = TWO ? TILE / 2 : TILE;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* epi = smem + STAGES * STAGE_BYTES;
+    Sync* sy = reinterpret_cast<Sync*>(epi + EPI_BYTES);
+    const uint32_t stage0 = smem_u32(smem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int unit = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&sy->full[s]), 1);
+            mbar_init(smem_u32(&sy->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&sy->tmem_full[a]), 1);
+            mbar_init(smem_u32(&sy->tmem_empty[a]), 2 * EPI_WARPS);
+        }
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(smem_u32(&sy->loaded[w]), 1);
+        mbar_init(smem_u32(&sy->drain), 1);
+        sy->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        if (p.kblocks > 0) {
+            prefetch_map(&maps.A);
+            prefetch_map(&maps.B);
+        }
+    }
+    if (warp == 1) tmem_alloc<true, TMEM_COLS>(smem_u32(&sy->tmem_base));
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = sy->tmem_base;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const Wait wait{&sy->abort, p.status, p.wait_limit_ns};
+    // The leader's barriers, as cluster addresses.
+    const uint32_t full0 = map_to_rank(smem_u32(&sy->full[0]), 0);
+    const uint32_t tmem_empty0 = map_to_rank(smem_u32(&sy->tmem_empty[0]), 0);
+
+    if (warp == 0) {
+        // -------------------------------------------------- TMA producer
+        uint32_t armed = 0, armed_parity = 0, ph = 0;
+        int s = 0;
+        bool ok = true, stall = p.debug_stall != 0;            // test hook: the first stage is never filled
+        const CUtensorMap* mapB = TWO && !leader ? &maps.B2 : &maps.B;
+        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+            int mb, nb;
+            tile_at(t, p, mb, nb);
+            const int row = mb * TILE + (int)rank * 128;
+            const int col = nb * TC + (TWO ? 0 : (int)rank * 128);
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
+                if (!ok) break;
+                if (!stall) {
+                    if (elect_one()) {
+                        const uint32_t full = full0 + (uint32_t)(s * sizeof(uint64_t));
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&sy->full[s]), 2 * STAGE_BYTES);
+                        const uint32_t a = stage0 + s * STAGE_BYTES, b = a + OPERAND_BYTES;
+                        if (p.a_mn) {
+                            tma_load_2d<true>(a, &maps.A, row, kb * STAGE_K, full);
+                            tma_load_2d<true>(a + OPERAND_BYTES / 2, &maps.A, row + 64, kb * STAGE_K, full);
+                        } else {
+                            tma_load_2d<true>(a, &maps.A, kb * STAGE_K, row, full);
+                        }
+                        if (p.b_mn) {
+                            tma_load_2d<true>(b, mapB, col, kb * STAGE_K, full);
+                            tma_load_2d<true>(b + OPERAND_BYTES / 2, mapB, col + 64, kb * STAGE_K, full);
+                        } else {
+                            tma_load_2d<true>(b, mapB, kb * STAGE_K, col, full);
+                        }
+                    }
+                    armed |= 1u << s;
+                    armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                }
+                stall = false;
+                __syncwarp();
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+        if (leader) {
+            for (int i = 0; i < STAGES; ++i)
+                if (armed & (1u << i)) mbar_wait<false, true>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
+        } else if (*(volatile int*)&sy->abort) {
+            // After a timeout this block cannot observe its own copies; give
+            // any in flight time to land (a copy takes microseconds).
+            const unsigned long long t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        if (leader) {
+            const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
+                                   (uint32_t)(TILE >> 3) << 17 | (uint32_t)(TILE >> 4) << 24;
+            // A step of 16 columns of K: 32 bytes of a K-major row, 16 rows MN-major
+            // (whose 64-column halves are half an operand apart).
+            const uint32_t a_step = p.a_mn ? 16 * SW : 32, a_lead = p.a_mn ? OPERAND_BYTES / 2 : 16;
+            const uint32_t b_step = p.b_mn ? 16 * SW : 32, b_lead = p.b_mn ? OPERAND_BYTES / 2 : 16;
+            int it = 0, s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            // A tile's sum, or of LONG ones each part in turn: first to last - 1.
+            for (int t = unit, first = 0; ok && t < p.num_tiles; ++it) {
+                const int last = LONG ? min(first + PART_BLOCKS, p.kblocks) : p.kblocks;
+                if (it >= 2)
+                    if (!__all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait)))
+                        break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(it & 1) * TILE;
+                for (int kb = first; kb < last; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->full[s]), ph, wait));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t a = stage0 + s * STAGE_BYTES, b = a + OPERAND_BYTES;
+#pragma unroll
+                        for (int k = 0; k < STAGE_K / 16; ++k)
+                            mma_bf16(d, smem_desc(a + k * a_step, a_lead, 1024, 2), smem_desc(b + k * b_step, b_lead, 1024, 2),
+                                     idesc, kb != first || k != 0);
+                        tc_commit<true>(smem_u32(&sy->empty[s]));
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (ok && elect_one()) tc_commit<true>(smem_u32(&sy->tmem_full[it & 1]));
+                __syncwarp();
+                first = last;
+                if (last == p.kblocks) {
+                    first = 0;
+                    t += p.units;
+                }
+            }
+            if (elect_one()) tc_commit<true>(smem_u32(&sy->drain));
+            mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3;                                // tensor-memory lanes 32 q .. 32 q + 31
+        const int set = (warp - 2) >> 2;
+        uint8_t* bufs = epi + (warp - 2) * WARP_BYTES;
+        const uint32_t loaded = smem_u32(&sy->loaded[warp - 2]);
+        const bool loads = p.rows && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
+        constexpr int SET_COLS = TC / 2, TURNS = SET_COLS / 64;
+        int it = 0, box = 0;
+        uint32_t load_ph = 0;
+        bool loading = false;                                  // boxes asked for and not waited for
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 31) mbar_arrive_cluster(tmem_empty0 + (uint32_t)((it & 1) * sizeof(uint64_t)));
+        };
+        for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
+            int mb, nb;
+            tile_at(t, p, mb, nb);
+            const int row0 = mb * TILE + (int)rank * 128 + q * 32, rows = min(32, p.M - row0);
+            const int col0 = nb * TC + set * SET_COLS;
+            // R or Z of the first turn, while the sums are made. (Gated ACT with
+            // Z: the buffers carry Z out first.)
+            auto ask = [&](int col) {
+                if (lane == 0) {
+                    tma_store_wait_read<0>();
+                    load_boxes<KIND, GATED>(p, &maps, bufs, loaded, row0, col);
+                }
+                __syncwarp();
+                loading = true;
+            };
+            if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
+                if (loads && rows > 0 && col0 < p.N) ask(col0);
+
+            bool ok = true;
+            if constexpr (LONG) {
+                float sum[4][32] = {};
+                #pragma unroll 1
+                for (int first = 0; ok && first < p.kblocks; first += PART_BLOCKS) {
+                    ok = __all_sync(~0u, mbar_wait<true, true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * 128;
+                    const bool final = first + PART_BLOCKS >= p.kblocks;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(acc + i * 32 + c, r);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[i][c + j] += __uint_as_float(r[j]);
+                        }
+                        if (final) tmem_st32(acc + i * 32, reinterpret_cast<uint32_t (&)[32]>(sum[i]));
+                    }
+                    if (!final) {
+                        release();
+                        ++it;
+                    }
+                }
+                if (ok) tmem_wait_st();
+            } else {
+                ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
+                tc_fence_after();
+            }
+            if (!ok) break;
+            const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * SET_COLS;
+            if constexpr (KIND == FUSED_CE) {
+                ce_columns(p, acc, row0 + lane, col0);
+                release();
+            } else if constexpr (KIND == FUSED_CE_GRAD) {
+                const bool in = lane < rows;
+                const long long target = in ? p.e.target[row0 + lane] : -1;
+                const bool kept = target >= 0 && target < p.e.vocabulary;
+                const float lse = in ? p.e.lse[row0 + lane] : 0.0f;
+                const float scale = in ? p.e.alpha * p.e.dloss[row0 + lane] : 0.0f;
+#pragma unroll 1
+                for (int i = 0; i < TURNS; ++i) {
+                    if (rows > 0 && col0 + i * 64 < p.N)
+                        ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col0 + i * 64, box, lse, scale, target - p.e.first, kept);
+                }
+                release();
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < TURNS; ++i) {
+                    const int col = col0 + i * 64;
+                    const bool last = i == TURNS - 1;
+                    if (rows <= 0 || col >= p.N) {
+                        if (last) release();
+                        continue;
+                    }
+                    if (p.rows) {
+                        if (i > 0 && loads) ask(col);
+                        if (loading) {
+                            ok = __all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait));
+                            if (!ok) break;
+                            load_ph ^= 1u;
+                            loading = false;
+                        } else if (KIND == FUSED_ACT && p.e.Z != nullptr) {
+                            if (lane == 0) tma_store_wait_read<0>();
+                            __syncwarp();
+                        }
+                        turn_boxes<KIND, GATED>(p, &maps, bufs, acc + i * 64, acc + 128 + i * 64, row0, rows, col, box,
+                                                [&]() { if (last) release(); });
+                    } else {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            float v[32], w[32];
+                            load_sums(acc + i * 64 + h * 32, v, p.kblocks);
+                            if constexpr (TWO) load_sums(acc + 128 + i * 64 + h * 32, w, p.kblocks);
+                            if (last && h == 1) release();
+                            store_columns<KIND, GATED>(p, bufs, row0, rows, col + h * 32, v, w);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+        if (loading) mbar_wait<false>(loaded, load_ph, wait);
+        tma_store_wait_all();
+    }
+
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_free<true, TMEM_COLS>(tmem_base);
+}
+
+// ------------------------------------------------------------------- launch
+// An operand, K-major (rows x K) in boxes of 64 columns x 128 rows, or MN-major
+// (K x rows) in boxes of 64 columns x 64 rows.
+bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld, int rows, int K, bool mn) {
+    const cuuint64_t dims[2] = {(cuuint64_t)(mn ? rows : K), (cuuint64_t)(mn ? K : rows)}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, mn ? 64u : 128u};
+    return encode(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// C, R or Z in boxes of 32 rows x 128 bytes, where TMA takes them: base and rows
+// on 16 bytes, whole 16-byte pieces long (a store clipped inside such a
+// piece also writes the rest of it).
+bool boxable(const void* x, long ld, int N, bool f32) {
+    const int esz = f32 ? 4 : 2;
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * esz % 16 == 0 && (long)N * esz % 16 == 0;
+}
+bool encode_boxes(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld, int M, int N, bool f32) {
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+    return encode(enc, map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, dims, strides,
+                  box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+const void* second_half(const void* x, int N) { return static_cast<const bf16*>(x) + N; }
+
+template <int KIND, bool GATED, bool LONG>
+cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
+    const cudaError_t e = set_smem_limit_once<fused_kernel<KIND, GATED, LONG>>(SMEM);
+    if (e != cudaSuccess) return e;
+    ClusterLaunch cfg(2 * p.units, THREADS, SMEM, 2, s);
+    return cudaLaunchKernelEx(&cfg.config, fused_kernel<KIND, GATED, LONG>, maps, p);
+}
+
+}  // namespace
+
+cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogue& e, int num_sms, cudaStream_t s) {
+    const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const bool two = kind == FUSED_ACT && e.gated;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    Params p;
+    p.M = m.M;
+    p.N = m.N;
+    p.kblocks = (int)(((long)m.K + STAGE_K - 1) / STAGE_K);
+    const int cols = two ? TILE / 2 : TILE;
+    p.tiles_m = (int)(((long)m.M + TILE - 1) / TILE);
+    p.tiles_n = (int)(((long)m.N + cols - 1) / cols);
+    if ((long)p.tiles_m * p.tiles_n > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    p.num_tiles = p.tiles_m * p.tiles_n;
+    p.units = p.num_tiles < num_sms / 2 ? p.num_tiles : num_sms / 2;
+    p.group_m = p.tiles_m >= 32 ? 16 : 8;
+    p.a_mn = m.a_mn ? 1 : 0;
+    p.b_mn = m.b_mn ? 1 : 0;
+    p.e = e;
+    p.bias4 = reinterpret_cast<uintptr_t>(e.bias) % 16 == 0 && m.N % 4 == 0 ? 1 : 0;
+    p.wait_limit_ns = wait_limit_ns();
+    p.debug_stall = debug_stall();
+    const cudaError_t err = mx4_status_word(&p.status);
+    if (err != cudaSuccess) return err;
+    if (m.K > 0 && (!encode_operand(enc, &maps.A, m.A, m.lda, m.M, m.K, m.a_mn) ||
+                    !encode_operand(enc, &maps.B, m.B, m.ldb, m.N, m.K, m.b_mn) ||
+                    (two && !encode_operand(enc, &maps.B2, m.B2, m.ldb, m.N, m.K, m.b_mn))))
+        return cudaErrorInvalidValue;
+    // C, R and Z by TMA: all of them, and where two buffers hold them (an FP32 R
+    // takes both, and leaves none for Z).
+    // (The logits' gradient is scratch, its rows whole 64 columns long: what lies
+    // past N there, from rows past the vocabulary, is read by no product.)
+    const bool f32 = e.c_f32;
+    const int width = kind == FUSED_CE_GRAD ? (m.N + 7) / 8 * 8 : m.N;
+    bool rows = kind != FUSED_CE && boxable(e.C, e.ldc, width, f32);
+    if (kind == FUSED_ACT)
+        rows = rows && (e.R == nullptr || boxable(e.R, e.ldr, m.N, e.r_f32)) && (e.Z == nullptr || boxable(e.Z, e.ldz, m.N, false)) &&
+               !(e.Z != nullptr && (e.r_f32 || (two && e.R != nullptr)));
+    if (kind == FUSED_GRAD) rows = rows && boxable(e.Z, e.ldz, m.N, false);
+    if (rows) {
+        bool ok = encode_boxes(enc, &maps.E[0], e.C, e.ldc, m.M, width, f32);
+        if (kind == FUSED_ACT) {
+            if (e.R != nullptr) ok = ok && encode_boxes(enc, &maps.E[1], e.R, e.ldr, m.M, m.N, e.r_f32);
+            if (e.Z != nullptr) ok = ok && encode_boxes(enc, &maps.E[2], e.Z, e.ldz, m.M, m.N, false);
+            if (e.Z != nullptr && two) ok = ok && encode_boxes(enc, &maps.E[3], second_half(e.Z, m.N), e.ldz, m.M, m.N, false);
+        } else if (kind == FUSED_GRAD) {
+            ok = ok && encode_boxes(enc, &maps.E[1], e.Z, e.ldz, m.M, m.N, false);
+            if (e.gated)
+                ok = ok && encode_boxes(enc, &maps.E[2], second_half(e.C, m.N), e.ldc, m.M, m.N, false) &&
+                     encode_boxes(enc, &maps.E[3], second_half(e.Z, m.N), e.ldz, m.M, m.N, false);
+        }
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    p.rows = rows ? 1 : 0;
+    const bool parts = p.kblocks > PART_BLOCKS;
+    switch (kind) {
+        case FUSED_ACT:
+            if (two) return launch<FUSED_ACT, true, false>(maps, p, s);
+            return parts && f32 ? launch<FUSED_ACT, false, true>(maps, p, s) : launch<FUSED_ACT, false, false>(maps, p, s);
+        case FUSED_GRAD: {
+            const bool l = parts && (f32 || e.sums != nullptr);
+            if (e.gated) return l ? launch<FUSED_GRAD, true, true>(maps, p, s) : launch<FUSED_GRAD, true, false>(maps, p, s);
+            return l ? launch<FUSED_GRAD, false, true>(maps, p, s) : launch<FUSED_GRAD, false, false>(maps, p, s);
+        }
+        case FUSED_CE:
+            return parts ? launch<FUSED_CE, false, true>(maps, p, s) : launch<FUSED_CE, false, false>(maps, p, s);
+        default:
+            return rows ? launch<FUSED_CE_GRAD, false, false>(maps, p, s) : cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tgemm

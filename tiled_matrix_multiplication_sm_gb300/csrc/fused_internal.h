@@ -1,0 +1,76 @@
+// Internal interface of the products with what follows them in their epilogue.
+// The public contract is in include/tgemm_fused.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/tgemm_fused.h"
+#include "tgemm_internal.h"
+
+namespace tgemm {
+
+// The operands of a product, op(A) M x K and op(B) K x N, BF16.
+struct FusedProduct {
+    int M, N, K;
+    const void* A;
+    long lda;
+    bool a_mn;                  // kept K x M
+    const void* B;
+    long ldb;
+    bool b_mn;                  // kept K x N
+    const void* B2;             // gated: the second N columns of op(B), kept like B
+};
+
+// What the epilogue does with a sum.
+enum FusedKind {
+    FUSED_ACT,                  // C = act(z) + r_scale R, Z = z (gated: C = act(g) u + r_scale R)
+    FUSED_GRAD,                 // C = d act'(Z) (gated: the two halves), sums of its columns
+    FUSED_CE,                   // m, the maximum of 128 columns of logits, and the sum of exp(z - m); the target's logit
+    FUSED_CE_GRAD,              // C = scale dloss (softmax - one hot)
+};
+
+struct FusedEpilogue {
+    int act = TGEMM_ACT_NONE;
+    bool gated = false;
+    void* C = nullptr;
+    long ldc = 0;
+    bool c_f32 = false;
+    const float* bias = nullptr;
+    const void* R = nullptr;
+    long ldr = 0;
+    bool r_f32 = false;
+    float r_scale = 1.0f;
+    void* Z = nullptr;          // FUSED_ACT: written; FUSED_GRAD: read
+    long ldz = 0;
+    float* sums = nullptr;      // FUSED_GRAD: [blocks of 32 rows][columns of C]
+    // Cross entropy.
+    float alpha = 1.0f;
+    const long long* target = nullptr;
+    long first = 0;             // the vocabulary entry of column 0
+    long vocabulary = 0;
+    const float* lse = nullptr;
+    const float* dloss = nullptr;
+    float2* parts = nullptr;    // FUSED_CE: [blocks of 128 columns][M], m and sum of exp(z - m)
+    float* picked = nullptr;    // FUSED_CE: M logits of the targets
+};
+
+constexpr int FUSED_SUM_ROWS = 32;       // rows of C a partial column sum covers
+constexpr int FUSED_CE_COLS = 128;       // columns of logits a maximum and a sum cover
+
+// Operands on 16-byte boundaries, with rows on them.
+cudaError_t fused_gemm(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, cudaStream_t s);
+
+// ---- what joins the epilogues' shares (fused_join.cu)
+// db[c] = the sum of `blocks` rows of sums, `cols` wide.
+cudaError_t fused_join_sums(const float* sums, long blocks, long cols, float* db, cudaStream_t s);
+// loss and lse of T rows from their `blocks` maxima and sums.
+cudaError_t fused_join_ce(const float2* parts, const float* picked, const long long* target, int T, long V, long blocks,
+                          float* loss, float* lse, cudaStream_t s);
+// X to Y (ldy), rows whose target is not in 0 .. V - 1 as zeros.
+cudaError_t fused_keep_rows(const void* X, long ldx, void* Y, long ldy, int T, int D, const long long* target, long V,
+                            cudaStream_t s);
+
+}  // namespace tgemm
