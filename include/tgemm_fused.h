@@ -131,6 +131,14 @@ TGEMM_API int gemm_ce_grad(int T, int V, int D, const void* X, long ldx, const v
                            void* dX, long lddx, int dx_type, void* dW, long lddw, int dw_type, float beta,
                            cudaStream_t stream);
 
+/*
+ * gemm_set_fused_kernel — the kernel of these products, for tests and tuning:
+ * -1 by a model of their times (the default), 0 always 256 x 256 tiles on SM
+ * pairs, 1 always few tiles on one SM each. Process-wide, for calls made
+ * after it. Returns TGEMM_OK or TGEMM_ERR_INVALID_ARG.
+ */
+TGEMM_API int gemm_set_fused_kernel(int mode);
+
 #ifdef __cplusplus
 }
 #endif

@@ -89,6 +89,12 @@ def test_gemm_ce_grad_refuses(lib, change):
     assert lib.gemm_ce_grad(*{**CE_GRAD, **change}.values()) == INVALID
 
 
+def test_the_kernel_setter_validates(lib):
+    for mode in (-2, 2):
+        assert fused.set_fused_kernel(mode) == INVALID
+    assert fused.set_fused_kernel(0) == 0 and fused.set_fused_kernel(-1) == 0
+
+
 def test_empty_results_are_accepted_without_a_device(lib):
     for M, N in ((0, 4), (4, 0)):
         assert lib.gemm_act(*{**ACT, "M": M, "N": N, "A": 0, "B": 0, "C": 0}.values()) == 0

@@ -14,6 +14,14 @@ BF16, F32 = torch.bfloat16, torch.float32
 SENTINEL = -77.0
 
 
+@pytest.fixture(params=["pairs", "few"])
+def kernel(request, tgemm):
+    """Every test that takes it runs in both of the products' kernels."""
+    assert tgemm.fused.set_fused_kernel({"pairs": 0, "few": 1}[request.param]) == 0
+    yield request.param
+    tgemm.fused.set_fused_kernel(-1)
+
+
 def generator(*seed):
     return torch.Generator().manual_seed(zlib.crc32(repr(seed).encode()))
 
@@ -66,7 +74,7 @@ SIZES = [(1, 1, 1), (1, 264, 64), (5, 7, 3), (16, 96, 40), (31, 33, 65), (64, 12
 @pytest.mark.parametrize("way", ["packed", "padded", "odd"])
 @pytest.mark.parametrize("ta,tb", list(itertools.product([False, True], repeat=2)))
 @pytest.mark.parametrize("M,N,K", SIZES)
-def test_whole_numbers_are_exact(tgemm, M, N, K, ta, tb, way):
+def test_whole_numbers_are_exact(tgemm, kernel, M, N, K, ta, tb, way):
     """relu(a b + bias) + R, FP32, with every operand's storage; nothing around C is written."""
     g = generator(M, N, K, ta, tb, way)
     a, b, A, B = operands(g, M, N, K, ta, tb, way)
@@ -84,7 +92,7 @@ def test_whole_numbers_are_exact(tgemm, M, N, K, ta, tb, way):
 @pytest.mark.parametrize("c,r", list(itertools.product([BF16, F32], [None, BF16, F32])))
 @pytest.mark.parametrize("keep_z,bias", list(itertools.product([False, True], repeat=2)))
 @pytest.mark.parametrize("M,N,K", [(1, 40, 64), (40, 104, 96), (290, 600, 136)])
-def test_every_mix_of_types_and_extras(tgemm, M, N, K, c, r, keep_z, bias, way):
+def test_every_mix_of_types_and_extras(tgemm, kernel, M, N, K, c, r, keep_z, bias, way):
     g = generator(M, N, K, str(c), str(r), keep_z, bias, way)
     a, b, A, B = operands(g, M, N, K, False, True, way, most=1)
     z = a @ b
@@ -109,7 +117,7 @@ def test_every_mix_of_types_and_extras(tgemm, M, N, K, c, r, keep_z, bias, way):
 @pytest.mark.parametrize("tb", [False, True])
 @pytest.mark.parametrize("extras", ["", "bias", "residual", "keep_z", "bias residual keep_z"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 136, 64), (17, 100, 72), (130, 129, 200), (300, 392, 136), (260, 1000, 40)])
-def test_gated_whole_numbers_are_exact(tgemm, M, N, K, extras, tb, way):
+def test_gated_whole_numbers_are_exact(tgemm, kernel, M, N, K, extras, tb, way):
     g = generator(M, N, K, extras, tb, way)
     a, b, A, B = operands(g, M, N, K, False, tb, way, wide=2 * N, most=1)
     z = a @ b
@@ -131,7 +139,7 @@ def test_gated_whole_numbers_are_exact(tgemm, M, N, K, extras, tb, way):
 
 
 @pytest.mark.parametrize("gated,residual", [(False, None), (False, F32), (True, F32), (True, BF16)])
-def test_long_rows_and_many_tiles(tgemm, gated, residual):
+def test_long_rows_and_many_tiles(tgemm, kernel, gated, residual):
     """More tiles than SM pairs, sums of several parts, residuals of both types."""
     M, N, K = 1300, 5000, 1160
     g = generator(gated, str(residual))
@@ -151,7 +159,7 @@ def test_long_rows_and_many_tiles(tgemm, gated, residual):
 @pytest.mark.parametrize("act", ref.ACTS)
 @pytest.mark.parametrize("c", [BF16, F32])
 @pytest.mark.parametrize("M,N,K", [(3, 72, 64), (200, 300, 520), (300, 328, 2100), (40, 200, 4000)])
-def test_activations_are_within_their_bounds(tgemm, act, c, M, N, K):
+def test_activations_are_within_their_bounds(tgemm, kernel, act, c, M, N, K):
     g = generator(act, str(c), M)
     a = torch.randn(M, K, generator=g).to(BF16)
     b = (torch.randn(N, K, generator=g) * 2.5 / K ** 0.5).to(BF16)    # z as far as some 10
@@ -179,7 +187,7 @@ def test_activations_of_every_size_of_number(tgemm, act):
 @pytest.mark.parametrize("way", ["packed", "odd"])
 @pytest.mark.parametrize("c", [BF16, F32])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 72, 64), (33, 250, 40), (256, 256, 64), (290, 520, 136), (700, 264, 72)])
-def test_gradients_of_whole_numbers_are_exact(tgemm, M, N, K, c, way):
+def test_gradients_of_whole_numbers_are_exact(tgemm, kernel, M, N, K, c, way):
     """relu's: d where z > 0; db sums them exactly."""
     g = generator(M, N, K, str(c), way)
     a, b, A, B = operands(g, M, N, K, False, False, way, most=1)
@@ -198,7 +206,7 @@ def test_gradients_of_whole_numbers_are_exact(tgemm, M, N, K, c, way):
 
 @pytest.mark.parametrize("way", ["packed", "odd"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (5, 72, 64), (290, 130, 136), (300, 520, 200)])
-def test_gated_gradients_of_whole_numbers_are_exact(tgemm, M, N, K, way):
+def test_gated_gradients_of_whole_numbers_are_exact(tgemm, kernel, M, N, K, way):
     g = generator(M, N, K, way)
     a, b, A, B = operands(g, M, N, K, False, False, way, most=1)
     z = whole(g, M, 2 * N)
@@ -212,7 +220,7 @@ def test_gated_gradients_of_whole_numbers_are_exact(tgemm, M, N, K, way):
 
 
 @pytest.mark.parametrize("ta,tb", [(True, False), (False, True), (True, True)])
-def test_gradients_take_every_storage(tgemm, ta, tb):
+def test_gradients_take_every_storage(tgemm, kernel, ta, tb):
     M, N, K = 150, 300, 90
     g = generator(ta, tb)
     a, b, A, B = operands(g, M, N, K, ta, tb, "odd", most=1)
@@ -225,7 +233,7 @@ def test_gradients_take_every_storage(tgemm, ta, tb):
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("act", ref.ACTS)
 @pytest.mark.parametrize("M,N,K", [(3, 72, 64), (330, 200, 520), (300, 328, 2100)])
-def test_gradients_are_within_their_bounds(tgemm, act, gated, M, N, K):
+def test_gradients_are_within_their_bounds(tgemm, kernel, act, gated, M, N, K):
     g = generator(act, gated, M)
     a = torch.randn(M, K, generator=g).to(BF16)
     b = (torch.randn(K, N, generator=g) / K ** 0.5).to(BF16)
@@ -273,7 +281,7 @@ def test_a_gradient_is_a_difference_of_the_layer(tgemm):
             assert abs((f[0] - f[1]) / h - da[i, k]) <= third + 3 * 2.0 ** -8 * 1.13 * terms
 
 
-def test_in_place(tgemm):
+def test_in_place(tgemm, kernel):
     """R may be C, and dZ may be Z."""
     g = generator(4)
     for M, N, K in ((40, 104, 64), (290, 520, 136), (290, 521, 136)):
@@ -294,7 +302,7 @@ def test_in_place(tgemm):
 
 
 @pytest.mark.parametrize("M,N,K", [(4, 24, 0), (0, 24, 8), (4, 0, 8), (0, 0, 0), (300, 40, 0)])
-def test_sizes_of_zero(tgemm, M, N, K):
+def test_sizes_of_zero(tgemm, kernel, M, N, K):
     A, B = torch.ones(M, K, dtype=BF16, device="cuda"), torch.ones(N, K, dtype=BF16, device="cuda")
     bias = torch.arange(N, dtype=F32, device="cuda") - 5
     r = torch.full((M, N), 2.0, dtype=BF16, device="cuda")
@@ -308,7 +316,7 @@ def test_sizes_of_zero(tgemm, M, N, K):
     assert not dz.any()
 
 
-def test_infinities_and_nan_stay_in_their_rows_and_columns(tgemm):
+def test_infinities_and_nan_stay_in_their_rows_and_columns(tgemm, kernel):
     M, N, K = 300, 280, 96
     g = generator(5)
     a, b, A, B = operands(g, M, N, K, False, True, "packed", most=1)
@@ -325,7 +333,7 @@ def test_infinities_and_nan_stay_in_their_rows_and_columns(tgemm):
     assert torch.equal(db.double().cpu()[cols], (a[:130] @ b).sum(0)[cols])
 
 
-def test_calls_on_streams_and_in_graphs(tgemm):
+def test_calls_on_streams_and_in_graphs(tgemm, kernel):
     """Two calls at once on two streams, and two graphs that replay together, with
     scratch (operands off 16 bytes, column sums) in both."""
     g = generator(6)
@@ -364,7 +372,7 @@ def test_calls_on_streams_and_in_graphs(tgemm):
     assert tgemm.device_status() == 0
 
 
-def test_results_do_not_depend_on_timing(tgemm):
+def test_results_do_not_depend_on_timing(tgemm, kernel):
     g = generator(8)
     a, b = (torch.randn(s, generator=g).to(BF16).cuda() for s in ((1000, 1500), (1500, 900)))
     z = torch.randn(1000, 900, generator=g).to(BF16).cuda()
@@ -376,7 +384,7 @@ def test_results_do_not_depend_on_timing(tgemm):
 
 @pytest.mark.parametrize("M,N", [(4, 200), (300, 600)])
 @pytest.mark.parametrize("grad", [False, True])
-def test_a_stage_that_never_fills_is_reported(tgemm, grad, M, N):
+def test_a_stage_that_never_fills_is_reported(tgemm, kernel, grad, M, N):
     g = generator(7)
     a, b, A, B = operands(g, M, N, 512, False, True, "packed", most=1)
     z = whole(g, M, N)

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import fused_reference as ref
-from test_gpu_fused_act import BF16, F32, generator, place, room, untouched
+from test_gpu_fused_act import BF16, F32, generator, kernel, place, room, untouched  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -25,7 +25,7 @@ SIZES = [(1, 1, 1), (1, 300, 64), (5, 7, 9), (16, 1000, 72), (31, 33, 65), (130,
 @pytest.mark.parametrize("way", ["packed", "odd"])
 @pytest.mark.parametrize("alpha", [1.0, -0.4])
 @pytest.mark.parametrize("T,V,D", SIZES)
-def test_losses(tgemm, T, V, D, alpha, way):
+def test_losses(tgemm, kernel, T, V, D, alpha, way):
     g = generator(T, V, D, alpha, way)
     x, w, target = inputs(g, T, V, D)
     loss, lse = tgemm.gemm_ce(place(x, BF16, way), place(w, BF16, way), target.cuda(), alpha=alpha)
@@ -41,7 +41,7 @@ def test_losses(tgemm, T, V, D, alpha, way):
 @pytest.mark.parametrize("way", ["packed", "odd"])
 @pytest.mark.parametrize("dx,dw", [(BF16, BF16), (F32, F32), (BF16, F32)])
 @pytest.mark.parametrize("T,V,D", SIZES)
-def test_gradients(tgemm, T, V, D, dx, dw, way):
+def test_gradients(tgemm, kernel, T, V, D, dx, dw, way):
     alpha = 0.8
     g = generator(T, V, D, str(dx), str(dw), way)
     x, w, target = inputs(g, T, V, D)
@@ -104,7 +104,7 @@ def test_losses_over_several_turns_of_tokens(tgemm):
     ref.check(loss[rows.cuda()], want, e_loss, "loss")
 
 
-def test_dw_is_added_to_what_is_there(tgemm):
+def test_dw_is_added_to_what_is_there(tgemm, kernel):
     T, V, D = 140, 300, 72
     g = generator(11)
     x, w, target = inputs(g, T, V, D)
@@ -123,7 +123,7 @@ def test_dw_is_added_to_what_is_there(tgemm):
         assert torch.equal(out, dw.to(dtype))
 
 
-def test_rows_left_out_add_nothing_whatever_they_hold(tgemm):
+def test_rows_left_out_add_nothing_whatever_they_hold(tgemm, kernel):
     T, V, D = 290, 520, 100
     g = generator(12)
     x, w, target = inputs(g, T, V, D, left_out=0.3)
@@ -147,7 +147,7 @@ def test_rows_left_out_add_nothing_whatever_they_hold(tgemm):
     assert not l3.any() and not dx.any() and not dw.any()
 
 
-def test_a_sure_loss_keeps_its_digits(tgemm):
+def test_a_sure_loss_keeps_its_digits(tgemm, kernel):
     """A target 20 above two others: loss = log1p(2 exp(-20)), exactly representable sums."""
     D = 64
     w = torch.zeros(3, D)
@@ -161,7 +161,7 @@ def test_a_sure_loss_keeps_its_digits(tgemm):
     assert abs(loss[1].double().cpu() - (20 + small)) <= 20 * 2.0 ** -23
 
 
-def test_infinite_logits(tgemm):
+def test_infinite_logits(tgemm, kernel):
     """Logits of minus infinity count nothing; plus infinity makes NaN, in its row alone."""
     D, V, T = 64, 300, 5
     x = torch.zeros(T, D)
@@ -183,7 +183,7 @@ def test_infinite_logits(tgemm):
 
 
 @pytest.mark.parametrize("T,V,D", [(0, 10, 8), (4, 0, 8), (4, 10, 0), (0, 0, 8)])
-def test_sizes_of_zero(tgemm, T, V, D):
+def test_sizes_of_zero(tgemm, kernel, T, V, D):
     X, W = torch.ones(T, D, dtype=BF16, device="cuda"), torch.ones(V, D, dtype=BF16, device="cuda")
     t = torch.zeros(T, dtype=torch.int64, device="cuda")
     loss, lse = tgemm.gemm_ce(X, W, t)
@@ -229,7 +229,7 @@ def test_gradients_are_differences_of_the_loss(tgemm):
             assert abs(f / h - grad[i, j].double().cpu()) <= bound
 
 
-def test_calls_on_streams_and_in_graphs(tgemm):
+def test_calls_on_streams_and_in_graphs(tgemm, kernel):
     g = generator(14)
     cases = []
     for i in range(2):
@@ -269,7 +269,7 @@ def test_calls_on_streams_and_in_graphs(tgemm):
 
 
 @pytest.mark.parametrize("T", [4, 300])
-def test_a_stage_that_never_fills_is_reported(tgemm, T):
+def test_a_stage_that_never_fills_is_reported(tgemm, kernel, T):
     g = generator(15)
     x, w, target = inputs(g, T, 600, 512)
     X, W, t = x.cuda(), w.cuda(), target.cuda()

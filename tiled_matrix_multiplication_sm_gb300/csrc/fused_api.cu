@@ -87,13 +87,18 @@ struct Operands {
     }
 };
 
-// The product of checked operands that is not empty. `more` bytes of scratch
-// beside the operands' go to epilogue(), which gives the epilogue, and to
+// The product of checked operands that is not empty. With `sums`, scratch for
+// the column sums' shares goes to epilogue(), which gives the epilogue, and to
 // after(), which joins what it left there.
 template <typename Epilogue, typename After>
-cudaError_t run(const Operands& o, tgemm::FusedKind kind, size_t more, Epilogue epilogue, After after, int sms, cudaStream_t s) {
+cudaError_t run(const Operands& o, tgemm::FusedKind kind, bool gated, bool sums, Epilogue epilogue, After after, int sms,
+                cudaStream_t s) {
     Scratch scratch(s);
     const bool a_mn = (o.flags & TGEMM_TRANS_A) != 0, b_mn = (o.flags & TGEMM_TRANS_B) == 0;
+    tgemm::FusedPlan plan;
+    cudaError_t e = tgemm::fused_plan(kind, FusedProduct{o.M, o.N, o.K, nullptr, 0, a_mn, nullptr, 0, b_mn, nullptr}, gated, sms, &plan);
+    if (e != cudaSuccess) return e;
+    const size_t more = sums ? (size_t)plan.sum_blocks * (gated ? 2 : 1) * o.N * sizeof(float) : 0;
     Operand a(o.A, o.lda, o.K == 0 ? 0 : a_mn ? o.K : o.M, a_mn ? o.M : o.K, scratch);
     // Two halves side by side in a row (K x 2 N) start on 16 bytes only where N
     // is a multiple of 8 and are two matrices otherwise.
@@ -108,7 +113,7 @@ cudaError_t run(const Operands& o, tgemm::FusedKind kind, size_t more, Epilogue 
         other.at = scratch.add((size_t)other.rows * other.padded() * 2);
     }
     const size_t extra = scratch.add(more);
-    cudaError_t e = scratch.take();
+    e = scratch.take();
     if (e != cudaSuccess) return e;
     e = a.lay(scratch, s);
     if (e == cudaSuccess) e = b.lay(scratch, s);
@@ -117,9 +122,9 @@ cudaError_t run(const Operands& o, tgemm::FusedKind kind, size_t more, Epilogue 
         b2.x = static_cast<const __nv_bfloat16*>(b.x) + (b_mn ? (long)o.N : (long)o.N * b.ld);
     if (e == cudaSuccess) {
         const FusedProduct p{o.M, o.N, o.K, a.x, a.ld, a_mn, b.x, b.ld, b_mn, b2.x};
-        e = tgemm::fused_gemm(kind, p, epilogue(scratch.at(extra)), sms, s);
+        e = tgemm::fused_gemm(kind, p, epilogue(scratch.at(extra)), plan, sms, s);
     }
-    if (e == cudaSuccess) e = after(scratch.at(extra));
+    if (e == cudaSuccess) e = after(scratch.at(extra), plan.sum_blocks);
     return scratch.give(e);
 }
 
@@ -138,7 +143,11 @@ int check_ce(int T, int V, int D, const void* X, long ldx, const void* W, long l
 
 cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long ldw, float alpha, const long long* target,
                float* loss, float* lse, int sms, cudaStream_t s) {
-    const long blocks = ((long)V + tgemm::FUSED_CE_COLS - 1) / tgemm::FUSED_CE_COLS;
+    tgemm::FusedPlan plan;
+    cudaError_t e = tgemm::fused_plan(tgemm::FUSED_CE, FusedProduct{T, V, D, nullptr, 0, false, nullptr, 0, false, nullptr}, false,
+                                      sms, &plan);
+    if (e != cudaSuccess) return e;
+    const long blocks = plan.ce_blocks;
     // Tokens a turn: whole tiles, as many as the maxima and sums leave room for.
     long turn = T;
     if (blocks > 0 && (size_t)T * blocks * sizeof(float2) > PIECE_BYTES) {
@@ -148,7 +157,7 @@ cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long
     Scratch scratch(s);
     Operand x(X, ldx, V == 0 || D == 0 ? 0 : T, D, scratch), w(W, ldw, D == 0 ? 0 : V, D, scratch);
     const size_t parts = scratch.add((size_t)turn * blocks * sizeof(float2)), picked = scratch.add((size_t)turn * sizeof(float));
-    cudaError_t e = scratch.take();
+    e = scratch.take();
     if (e != cudaSuccess) return e;
     e = x.lay(scratch, s);
     if (e == cudaSuccess) e = w.lay(scratch, s);
@@ -161,7 +170,7 @@ cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long
         ep.parts = static_cast<float2*>(scratch.at(parts));
         ep.picked = static_cast<float*>(scratch.at(picked));
         const FusedProduct p{n, V, D, static_cast<const __nv_bfloat16*>(x.x) + t * x.ld, x.ld, false, w.x, w.ld, false, nullptr};
-        if (V > 0) e = tgemm::fused_gemm(tgemm::FUSED_CE, p, ep, sms, s);
+        if (V > 0) e = tgemm::fused_gemm(tgemm::FUSED_CE, p, ep, plan, sms, s);
         if (e == cudaSuccess) e = tgemm::fused_join_ce(ep.parts, ep.picked, ep.target, n, V, blocks, loss + t, lse + t, s);
     }
     return scratch.give(e);
@@ -172,6 +181,13 @@ struct Gradient {
     long ld;
     int type;
 };
+
+// A product as its plan has it.
+cudaError_t product(tgemm::FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int sms, cudaStream_t s) {
+    tgemm::FusedPlan plan;
+    const cudaError_t err = tgemm::fused_plan(kind, p, false, sms, &plan);
+    return err != cudaSuccess ? err : tgemm::fused_gemm(kind, p, e, plan, sms, s);
+}
 
 cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W, long ldw, float alpha, const long long* target,
                     const float* lse, const float* dloss, const Gradient& dX, const Gradient& dW, float beta, int sms,
@@ -207,7 +223,7 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
             ep.lse = lse;
             ep.dloss = dloss;
             const FusedProduct p{T, n, D, x.x, x.ld, false, wv, w.ld, false, nullptr};
-            e = tgemm::fused_gemm(tgemm::FUSED_CE_GRAD, p, ep, sms, s);
+            e = product(tgemm::FUSED_CE_GRAD, p, ep, sms, s);
         }
         if (e == cudaSuccess && dX.x != nullptr && T > 0) {
             const bool last = v + piece >= V;
@@ -221,7 +237,7 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
                 ep.r_f32 = true;
             }
             const FusedProduct p{T, D, n, z, ldz, false, wv, w.ld, true, nullptr};
-            e = tgemm::fused_gemm(tgemm::FUSED_ACT, p, ep, sms, s);
+            e = product(tgemm::FUSED_ACT, p, ep, sms, s);
         }
         if (e == cudaSuccess && dW.x != nullptr && n > 0) {
             FusedEpilogue ep;
@@ -235,7 +251,7 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
                 ep.r_scale = beta;
             }
             const FusedProduct p{n, D, T, z, ldz, true, kept, ldk, true, nullptr};
-            e = tgemm::fused_gemm(tgemm::FUSED_ACT, p, ep, sms, s);
+            e = product(tgemm::FUSED_ACT, p, ep, sms, s);
         }
     }
     return scratch.give(e);
@@ -274,7 +290,7 @@ int gemm_act(int M, int N, int K, const void* A, long lda, const void* B, long l
     e.r_f32 = r_type == TGEMM_TYPE_F32;
     e.Z = Z;
     e.ldz = ldz;
-    return done(run(o, tgemm::FUSED_ACT, 0, [&](void*) { return e; }, [](void*) { return cudaSuccess; }, sms, stream));
+    return done(run(o, tgemm::FUSED_ACT, gated, false, [&](void*) { return e; }, [](void*, long) { return cudaSuccess; }, sms, stream));
 }
 
 int gemm_act_grad(int M, int N, int K, const void* A, long lda, const void* B, long ldb, int flags, int act, const void* Z,
@@ -303,14 +319,12 @@ int gemm_act_grad(int M, int N, int K, const void* A, long lda, const void* B, l
     e.c_f32 = dz_type == TGEMM_TYPE_F32;
     e.Z = const_cast<void*>(Z);
     e.ldz = ldz;
-    const long blocks = ((long)M + tgemm::FUSED_SUM_ROWS - 1) / tgemm::FUSED_SUM_ROWS;
-    const size_t more = db != nullptr ? (size_t)blocks * wide * sizeof(float) : 0;
-    return done(run(o, tgemm::FUSED_GRAD, more,
+    return done(run(o, tgemm::FUSED_GRAD, gated, db != nullptr,
                     [&](void* sums) {
                         if (db != nullptr) e.sums = static_cast<float*>(sums);
                         return e;
                     },
-                    [&](void* sums) {
+                    [&](void* sums, long blocks) {
                         return db == nullptr ? cudaSuccess
                                              : tgemm::fused_join_sums(static_cast<const float*>(sums), blocks, wide, db, stream);
                     },

@@ -26,8 +26,7 @@
 // Rows past M and columns past N are read as zeros and not stored. Waits are
 // bounded as in the other tensor-core kernels.
 
-#include "fused_act.h"
-#include "mx4_tile.h"
+#include "fused_column.h"
 
 #include <cstring>
 
@@ -36,8 +35,7 @@ namespace {
 
 using namespace mx4_tile;
 using namespace fused_act;
-typedef __nv_bfloat16 bf16;
-
+using namespace fused_column;
 constexpr int TILE = 256;
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // a block's 128 rows of A, or of B
@@ -78,12 +76,6 @@ struct Maps {
     // ACT: C, R, Z, Z's second half. GRAD: C, Z, and the second halves of both.
     CUtensorMap E[4];
 };
-
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
 
 // ------------------------------------------------- boxes in shared memory
 // This thread's row of a box: 32 FP32 or half h of 64 BF16.
@@ -128,15 +120,6 @@ __device__ __forceinline__ void get_bf16(const uint8_t* buf, int h, float (&v)[3
     }
 }
 
-// 32 sums of this thread's lane (zeros where K is 0).
-__device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32], int kblocks) {
-    uint32_t r[32];
-    tmem_ld32(tmem, r);
-    tmem_wait_ld(r);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = kblocks > 0 ? __uint_as_float(r[j]) : 0.0f;
-}
-
 // v += bias of columns `at`, .. (of `cols`, from `bias` on).
 __device__ __forceinline__ void add_bias(const Params& p, const float* bias, int at, float (&v)[32]) {
     if (bias == nullptr) return;
@@ -171,95 +154,32 @@ __device__ __forceinline__ float column_sums(float (&v)[32]) {
 }
 
 // --------------------------------------------- C in segments of its rows
-// 32 columns from column `col` of C of this warp's `rows` rows, from registers
-// (a row a lane) through `bufs` to a column a lane, any alignment, eight rows'
-// loads ahead of their stores. v2: gated ACT, u's sums.
+// 32 columns from column `col` on of C of this warp's `rows` rows, from registers
+// (a row a lane) through `bufs` to a column a lane. v2: gated ACT, u's sums.
 template <int KIND, bool GATED>
 __device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, int row0, int rows, int col, const float (&v)[32],
                                               const float (&v2)[32]) {
     const FusedEpilogue& e = p.e;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = col + lane;
     constexpr bool TWO = KIND == FUSED_ACT && GATED;
     __syncwarp();
     put_f32(bufs, v);
     if constexpr (TWO) put_f32(bufs + BUF_BYTES, v2);
     __syncwarp();
-    const int c = col + lane;
     if (c < p.N) {
-        const long N = p.N;
-        float b = 0.0f, b2 = 0.0f;
-        if (KIND == FUSED_ACT && e.bias != nullptr) {
-            b = e.bias[c];
-            if constexpr (TWO) b2 = e.bias[N + c];
-        }
-        float sum = 0.0f, sum2 = 0.0f;
+        Column<KIND, GATED> column(e, p.N, c);
 #pragma unroll 1
         for (int k = 0; k < rows; k += 8) {
-            const long row = row0 + k;
-            float x[8], y[8], z[8];
-            bf16* Z = static_cast<bf16*>(e.Z) + row * e.ldz + c;
+            float x[8], y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t at = swizzled(k + j, lane >> 2) + (lane & 3) * 4;
-                x[j] = *reinterpret_cast<const float*>(bufs + at) + b;
-                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(bufs + BUF_BYTES + at) + b2;
+                x[j] = *reinterpret_cast<const float*>(bufs + at);
+                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(bufs + BUF_BYTES + at);
             }
-            if constexpr (KIND == FUSED_ACT) {
-                if (e.Z != nullptr)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (k + j < rows) {
-                            Z[j * e.ldz] = __float2bfloat16(x[j]);
-                            if constexpr (TWO) Z[j * e.ldz + N] = __float2bfloat16(y[j]);
-                        }
-                apply(e.act, x);
-                if constexpr (TWO)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] *= y[j];
-                if (e.R != nullptr) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        z[j] = k + j >= rows ? 0.0f
-                               : e.r_f32     ? static_cast<const float*>(e.R)[(row + j) * e.ldr + c]
-                                             : __bfloat162float(static_cast<const bf16*>(e.R)[(row + j) * e.ldr + c]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fmaf(e.r_scale, z[j], x[j]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    z[j] = k + j < rows ? __bfloat162float(Z[j * e.ldz]) : 0.0f;
-                    if constexpr (GATED) y[j] = k + j < rows ? __bfloat162float(Z[j * e.ldz + N]) : 0.0f;
-                }
-                if constexpr (GATED) {
-                    gated_grad(e.act, x, z, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = z[j];
-                } else {
-                    times_slope(e.act, x, z);
-                }
-                if (e.sums != nullptr)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (k + j < rows) {
-                            sum += x[j];
-                            if constexpr (GATED) sum2 += y[j];
-                        }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (k + j < rows) {
-                    const long at = (row + j) * e.ldc + c;
-                    if (e.c_f32) static_cast<float*>(e.C)[at] = x[j];
-                    else static_cast<bf16*>(e.C)[at] = __float2bfloat16(x[j]);
-                    if constexpr (KIND == FUSED_GRAD && GATED) static_cast<bf16*>(e.C)[at + N] = __float2bfloat16(y[j]);
-                }
+            column.finish(row0 + k, rows - k, x, y);
         }
-        if (KIND == FUSED_GRAD && e.sums != nullptr) {
-            float* out = e.sums + (long)(row0 / FUSED_SUM_ROWS) * (GATED ? 2 * N : N) + c;
-            out[0] = sum;
-            if constexpr (GATED) out[N] = sum2;
-        }
+        column.leave(row0 / FUSED_SUM_ROWS);
     }
     __syncwarp();
 }
@@ -610,7 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
                         const uint32_t a = stage0 + s * STAGE_BYTES, b = a + OPERAND_BYTES;
 #pragma unroll
                         for (int k = 0; k < STAGE_K / 16; ++k)
-                            mma_bf16(d, smem_desc(a + k * a_step, a_lead, 1024, 2), smem_desc(b + k * b_step, b_lead, 1024, 2),
+                            mma_bf16<true>(d, smem_desc(a + k * a_step, a_lead, 1024, 2), smem_desc(b + k * b_step, b_lead, 1024, 2),
                                      idesc, kb != first || k != 0);
                         tc_commit<true>(smem_u32(&sy->empty[s]));
                     }
@@ -792,7 +712,9 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogue& e, int num_sms, cudaStream_t s) {
+cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogue& e, const FusedPlan& plan, int num_sms,
+                       cudaStream_t s) {
+    if (plan.few) return fused_few(kind, m, e, plan, num_sms, s);
     const auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (enc == nullptr) return cudaErrorNotSupported;
     const bool two = kind == FUSED_ACT && e.gated;

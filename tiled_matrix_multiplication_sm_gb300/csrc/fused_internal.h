@@ -28,7 +28,7 @@ struct FusedProduct {
 enum FusedKind {
     FUSED_ACT,                  // C = act(z) + r_scale R, Z = z (gated: C = act(g) u + r_scale R)
     FUSED_GRAD,                 // C = d act'(Z) (gated: the two halves), sums of its columns
-    FUSED_CE,                   // m, the maximum of 128 columns of logits, and the sum of exp(z - m); the target's logit
+    FUSED_CE,                   // m, the maximum of a block of logits, and the sum of exp(z - m); the target's logit
     FUSED_CE_GRAD,              // C = scale dloss (softmax - one hot)
 };
 
@@ -45,7 +45,7 @@ struct FusedEpilogue {
     float r_scale = 1.0f;
     void* Z = nullptr;          // FUSED_ACT: written; FUSED_GRAD: read
     long ldz = 0;
-    float* sums = nullptr;      // FUSED_GRAD: [blocks of 32 rows][columns of C]
+    float* sums = nullptr;      // FUSED_GRAD: [blocks of rows][columns of C]
     // Cross entropy.
     float alpha = 1.0f;
     const long long* target = nullptr;
@@ -53,15 +53,36 @@ struct FusedEpilogue {
     long vocabulary = 0;
     const float* lse = nullptr;
     const float* dloss = nullptr;
-    float2* parts = nullptr;    // FUSED_CE: [blocks of 128 columns][M], m and sum of exp(z - m)
+    float2* parts = nullptr;    // FUSED_CE: [blocks of columns][M], m and sum of exp(z - m)
     float* picked = nullptr;    // FUSED_CE: M logits of the targets
 };
 
-constexpr int FUSED_SUM_ROWS = 32;       // rows of C a partial column sum covers
-constexpr int FUSED_CE_COLS = 128;       // columns of logits a maximum and a sum cover
+// In fused_gemm.cu: rows of C a partial column sum covers, columns of logits a
+// maximum and a sum cover.
+constexpr int FUSED_SUM_ROWS = 32;
+constexpr int FUSED_CE_COLS = 128;
+
+// In fused_few.cu: sets of epilogue warps, each with its sums of columns; bytes of
+// shared memory for stages.
+constexpr int FUSED_FEW_SETS = 4;
+constexpr int FUSED_FEW_RING = 209 * 1024;
+
+// How a product runs: on SM pairs (fused_gemm.cu), or as few tiles (fused_few.cu).
+struct FusedPlan {
+    bool few;
+    int height, tokens, split, chunks;   // few: columns and rows of C a tile, blocks that share its sum, 64s of K a stage
+    long sum_blocks;                     // rows of FusedEpilogue::sums
+    long ce_blocks;                      // of FusedEpilogue::parts
+};
+// Only the sizes and storage of the operands are read.
+cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, bool gated, int num_sms, FusedPlan* plan);
 
 // Operands on 16-byte boundaries, with rows on them.
-cudaError_t fused_gemm(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, cudaStream_t s);
+cudaError_t fused_gemm(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, const FusedPlan& plan, int num_sms,
+                       cudaStream_t s);
+cudaError_t fused_few(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, const FusedPlan& plan, int num_sms,
+                      cudaStream_t s);
+cudaError_t fused_few_clusters(unsigned long long* fits);
 
 // ---- what joins the epilogues' shares (fused_join.cu)
 // db[c] = the sum of `blocks` rows of sums, `cols` wide.

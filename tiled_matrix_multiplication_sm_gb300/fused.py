@@ -30,6 +30,7 @@ _SIZES = [_INT, _INT, _INT, _VP, _LONG, _VP, _LONG]
 _SIGNATURES = {
     "gemm_act": (_INT, _SIZES + [_INT, _INT, _VP, _VP, _LONG, _INT, _VP, _LONG, _VP, _LONG, _INT, _VP]),
     "gemm_act_grad": (_INT, _SIZES + [_INT, _INT, _VP, _LONG, _VP, _LONG, _INT, _VP, _VP]),
+    "gemm_set_fused_kernel": (_INT, [_INT]),
     "gemm_ce": (_INT, _SIZES + [_FLT, _VP, _VP, _VP, _VP]),
     "gemm_ce_grad": (_INT, _SIZES + [_FLT, _VP, _VP, _VP, _VP, _LONG, _INT, _VP, _LONG, _INT, _FLT, _VP]),
 }
@@ -244,3 +245,9 @@ def gemm_ce_grad(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: to
     _call("gemm_ce_grad", device, stream, T, V, D, X.data_ptr(), ldx, W.data_ptr(), ldw, alpha, t, lse_ptr, dloss_ptr,
           dx.data_ptr() if x_grad else 0, lddx, x_kind, dw.data_ptr() if w_grad else 0, lddw, w_kind, beta)
     return dx, dw
+
+
+def set_fused_kernel(mode: int) -> int:
+    """-1: by a model of the kernels' times; 0: 256 x 256 tiles on SM pairs; 1: few
+    tiles, on one SM each."""
+    return int(load().gemm_set_fused_kernel(int(mode)))
