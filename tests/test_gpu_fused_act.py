@@ -219,6 +219,39 @@ def test_gated_gradients_of_whole_numbers_are_exact(tgemm, kernel, M, N, K, way)
     assert untouched(out, around)
 
 
+@pytest.mark.parametrize("gated,in_place", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("M,N,K", [(1300, 5000, 200), (1100, 2200, 72)])
+def test_gradients_of_many_tiles(tgemm, kernel, M, N, K, gated, in_place):
+    """Tiles of fewer than 256 columns, whose last turn is short."""
+    g = generator(M, gated, in_place)
+    a, b, A, B = operands(g, M, N, K, False, False, "packed", most=1)
+    z = whole(g, M, 2 * N if gated else N)
+    Z = z.to(BF16).cuda()
+    d = (a.float() @ b.float()).double()
+    want = torch.cat((d * z[:, N:] * (z[:, :N] > 0), d * z[:, :N].clamp(min=0)), dim=1) if gated else d * (z > 0)
+    dz, db = tgemm.gemm_act_grad(A, B, Z, "relu", gated=gated, out=Z if in_place else None)
+    assert torch.equal(dz.cpu(), want.bfloat16()) and torch.equal(db.double().cpu(), want.sum(dim=0))
+
+
+@pytest.mark.parametrize("M,N", [(1300, 5000), (700, 2208), (700, 2207), (2400, 1500)])
+@pytest.mark.parametrize("c,r", [(BF16, None), (BF16, BF16), (F32, F32), (BF16, F32)])
+def test_residuals_of_many_tiles(tgemm, kernel, M, N, c, r):
+    """The same, C in place of R where the types agree, and Z beside it."""
+    K = 200
+    g = generator(M, N, str(c), str(r))
+    a, b, A, B = operands(g, M, N, K, False, True, "packed", most=1)
+    z = (a.float() @ b.float()).double()
+    assert z.abs().max() <= 256
+    res = whole(g, M, N) if r is not None else torch.zeros(M, N).double()
+    R = None if r is None else res.to(r).cuda()
+    out = R if c == r else None
+    C, Z = tgemm.gemm_act(A, B, "relu", trans_b=True, residual=R, keep_z=True, out_dtype=c, out=out)
+    assert torch.equal(C.cpu(), (z.clamp(min=0) + res).to(c)) and torch.equal(Z.double().cpu(), z)
+    R = None if r is None else res.to(r).cuda()
+    C = tgemm.gemm_act(A, B, trans_b=True, residual=R, out_dtype=c, out=R if c == r else None)
+    assert torch.equal(C.cpu(), (z + res).to(c))
+
+
 @pytest.mark.parametrize("ta,tb", [(True, False), (False, True), (True, True)])
 def test_gradients_take_every_storage(tgemm, kernel, ta, tb):
     M, N, K = 150, 300, 90

@@ -19,7 +19,7 @@ def inputs(g, T, V, D, left_out=0.2, scale=1.0):
 
 
 SIZES = [(1, 1, 1), (1, 300, 64), (5, 7, 9), (16, 1000, 72), (31, 33, 65), (130, 257, 40), (256, 256, 64), (300, 1037, 136),
-         (600, 5000, 200), (64, 128, 1100), (270, 515, 2061)]
+         (600, 5000, 200), (64, 128, 1100), (270, 515, 2061), (1300, 4999, 72)]
 
 
 @pytest.mark.parametrize("way", ["packed", "odd"])

@@ -87,18 +87,15 @@ struct Operands {
     }
 };
 
-// The product of checked operands that is not empty. With `sums`, scratch for
-// the column sums' shares goes to epilogue(), which gives the epilogue, and to
-// after(), which joins what it left there.
-template <typename Epilogue, typename After>
-cudaError_t run(const Operands& o, tgemm::FusedKind kind, bool gated, bool sums, Epilogue epilogue, After after, int sms,
-                cudaStream_t s) {
+// The product of checked operands that is not empty. db: the column sums of a
+// gradient's result, or NULL; e.sums is set here.
+cudaError_t run(const Operands& o, tgemm::FusedKind kind, FusedEpilogue& e, float* db, int sms, cudaStream_t s) {
     Scratch scratch(s);
     const bool a_mn = (o.flags & TGEMM_TRANS_A) != 0, b_mn = (o.flags & TGEMM_TRANS_B) == 0;
+    FusedProduct p{o.M, o.N, o.K, nullptr, 0, a_mn, nullptr, 0, b_mn, nullptr};
     tgemm::FusedPlan plan;
-    cudaError_t e = tgemm::fused_plan(kind, FusedProduct{o.M, o.N, o.K, nullptr, 0, a_mn, nullptr, 0, b_mn, nullptr}, gated, sms, &plan);
-    if (e != cudaSuccess) return e;
-    const size_t more = sums ? (size_t)plan.sum_blocks * (gated ? 2 : 1) * o.N * sizeof(float) : 0;
+    cudaError_t err = tgemm::fused_plan(kind, p, e, sms, &plan);
+    if (err != cudaSuccess) return err;
     Operand a(o.A, o.lda, o.K == 0 ? 0 : a_mn ? o.K : o.M, a_mn ? o.M : o.K, scratch);
     // Two halves side by side in a row (K x 2 N) start on 16 bytes only where N
     // is a multiple of 8 and are two matrices otherwise.
@@ -112,20 +109,24 @@ cudaError_t run(const Operands& o, tgemm::FusedKind kind, bool gated, bool sums,
         other.copied = true;
         other.at = scratch.add((size_t)other.rows * other.padded() * 2);
     }
-    const size_t extra = scratch.add(more);
-    e = scratch.take();
-    if (e != cudaSuccess) return e;
-    e = a.lay(scratch, s);
-    if (e == cudaSuccess) e = b.lay(scratch, s);
-    if (e == cudaSuccess && apart) e = b2.lay(scratch, s);
+    const long wide = (e.gated ? 2L : 1L) * o.N;
+    const size_t sums = scratch.add(db != nullptr ? (size_t)plan.sum_blocks * wide * sizeof(float) : 0);
+    err = scratch.take();
+    if (err != cudaSuccess) return err;
+    err = a.lay(scratch, s);
+    if (err == cudaSuccess) err = b.lay(scratch, s);
+    if (err == cudaSuccess && apart) err = b2.lay(scratch, s);
     if (o.halves == 2 && !apart)
         b2.x = static_cast<const __nv_bfloat16*>(b.x) + (b_mn ? (long)o.N : (long)o.N * b.ld);
-    if (e == cudaSuccess) {
-        const FusedProduct p{o.M, o.N, o.K, a.x, a.ld, a_mn, b.x, b.ld, b_mn, b2.x};
-        e = tgemm::fused_gemm(kind, p, epilogue(scratch.at(extra)), plan, sms, s);
-    }
-    if (e == cudaSuccess) e = after(scratch.at(extra), plan.sum_blocks);
-    return scratch.give(e);
+    if (db != nullptr) e.sums = static_cast<float*>(scratch.at(sums));
+    p.A = a.x;
+    p.lda = a.ld;
+    p.B = b.x;
+    p.ldb = b.ld;
+    p.B2 = b2.x;
+    if (err == cudaSuccess) err = tgemm::fused_gemm(kind, p, e, plan, sms, s);
+    if (err == cudaSuccess && db != nullptr) err = tgemm::fused_join_sums(e.sums, plan.sum_blocks, wide, db, s);
+    return scratch.give(err);
 }
 
 // ------------------------------------------------------------ cross entropy
@@ -144,8 +145,8 @@ int check_ce(int T, int V, int D, const void* X, long ldx, const void* W, long l
 cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long ldw, float alpha, const long long* target,
                float* loss, float* lse, int sms, cudaStream_t s) {
     tgemm::FusedPlan plan;
-    cudaError_t e = tgemm::fused_plan(tgemm::FUSED_CE, FusedProduct{T, V, D, nullptr, 0, false, nullptr, 0, false, nullptr}, false,
-                                      sms, &plan);
+    cudaError_t e = tgemm::fused_plan(tgemm::FUSED_CE, FusedProduct{T, V, D, nullptr, 0, false, nullptr, 0, false, nullptr},
+                                      FusedEpilogue(), sms, &plan);
     if (e != cudaSuccess) return e;
     const long blocks = plan.ce_blocks;
     // Tokens a turn: whole tiles, as many as the maxima and sums leave room for.
@@ -185,7 +186,7 @@ struct Gradient {
 // A product as its plan has it.
 cudaError_t product(tgemm::FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int sms, cudaStream_t s) {
     tgemm::FusedPlan plan;
-    const cudaError_t err = tgemm::fused_plan(kind, p, false, sms, &plan);
+    const cudaError_t err = tgemm::fused_plan(kind, p, e, sms, &plan);
     return err != cudaSuccess ? err : tgemm::fused_gemm(kind, p, e, plan, sms, s);
 }
 
@@ -290,7 +291,7 @@ int gemm_act(int M, int N, int K, const void* A, long lda, const void* B, long l
     e.r_f32 = r_type == TGEMM_TYPE_F32;
     e.Z = Z;
     e.ldz = ldz;
-    return done(run(o, tgemm::FUSED_ACT, gated, false, [&](void*) { return e; }, [](void*, long) { return cudaSuccess; }, sms, stream));
+    return done(run(o, tgemm::FUSED_ACT, e, nullptr, sms, stream));
 }
 
 int gemm_act_grad(int M, int N, int K, const void* A, long lda, const void* B, long ldb, int flags, int act, const void* Z,
@@ -319,16 +320,7 @@ int gemm_act_grad(int M, int N, int K, const void* A, long lda, const void* B, l
     e.c_f32 = dz_type == TGEMM_TYPE_F32;
     e.Z = const_cast<void*>(Z);
     e.ldz = ldz;
-    return done(run(o, tgemm::FUSED_GRAD, gated, db != nullptr,
-                    [&](void* sums) {
-                        if (db != nullptr) e.sums = static_cast<float*>(sums);
-                        return e;
-                    },
-                    [&](void* sums, long blocks) {
-                        return db == nullptr ? cudaSuccess
-                                             : tgemm::fused_join_sums(static_cast<const float*>(sums), blocks, wide, db, stream);
-                    },
-                    sms, stream));
+    return done(run(o, tgemm::FUSED_GRAD, e, db, sms, stream));
 }
 
 int gemm_ce(int T, int V, int D, const void* X, long ldx, const void* W, long ldw, float alpha, const long long* target,

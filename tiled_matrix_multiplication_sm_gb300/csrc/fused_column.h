@@ -72,29 +72,49 @@ struct Column {
         }
     }
 
-    // Rows row .. row + 7, of which the first n are C's, from their sums x (TWO: g's, y u's).
-    __device__ __forceinline__ void finish(long row, int n, float (&x)[8], float (&y)[8]) {
-        float z[8];
-        bf16* Z = static_cast<bf16*>(e.Z) + row * e.ldz + c;
+    // What rows row .. row + 7, of which the first n are C's (FULL: all), take beside
+    // their sums: R, or Z (gated: and its second half).
+    template <bool FULL>
+    __device__ __forceinline__ void load(long row, int n, float (&z)[8], float (&w)[8]) const {
+        if (KIND == FUSED_ACT && e.R != nullptr) {
+            if (e.r_f32) {
+                const float* R = static_cast<const float*>(e.R) + row * e.ldr + c;
+#pragma unroll
+                for (int j = 0; j < 8; ++j, R += e.ldr) z[j] = FULL || j < n ? *R : 0.0f;
+            } else {
+                const bf16* R = static_cast<const bf16*>(e.R) + row * e.ldr + c;
+#pragma unroll
+                for (int j = 0; j < 8; ++j, R += e.ldr) z[j] = FULL || j < n ? __bfloat162float(*R) : 0.0f;
+            }
+        }
+        if (KIND == FUSED_GRAD) {
+            const bf16* Z = static_cast<const bf16*>(e.Z) + row * e.ldz + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j, Z += e.ldz) {
+                z[j] = FULL || j < n ? __bfloat162float(*Z) : 0.0f;
+                if constexpr (GATED) w[j] = FULL || j < n ? __bfloat162float(Z[N]) : 0.0f;
+            }
+        }
+    }
+
+    // Those rows, from their sums x (TWO: g's, y u's) and what load gave.
+    template <bool FULL>
+    __device__ __forceinline__ void finish(long row, int n, float (&x)[8], float (&y)[8], float (&z)[8], float (&w)[8]) {
         if constexpr (KIND == FUSED_ACT) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] += b;
                 if constexpr (TWO) y[j] += b2;
             }
-            if (e.R != nullptr)
+            if (e.Z != nullptr) {
+                bf16* Z = static_cast<bf16*>(e.Z) + row * e.ldz + c;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    z[j] = j >= n      ? 0.0f
-                           : e.r_f32 ? static_cast<const float*>(e.R)[(row + j) * e.ldr + c]
-                                     : __bfloat162float(static_cast<const bf16*>(e.R)[(row + j) * e.ldr + c]);
-            if (e.Z != nullptr)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) {
-                        Z[j * e.ldz] = __float2bfloat16(x[j]);
-                        if constexpr (TWO) Z[j * e.ldz + N] = __float2bfloat16(y[j]);
+                for (int j = 0; j < 8; ++j, Z += e.ldz)
+                    if (FULL || j < n) {
+                        Z[0] = __float2bfloat16(x[j]);
+                        if constexpr (TWO) Z[N] = __float2bfloat16(y[j]);
                     }
+            }
             apply(e.act, x);
             if constexpr (TWO)
 #pragma unroll
@@ -103,43 +123,73 @@ struct Column {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = fmaf(e.r_scale, z[j], x[j]);
         } else if constexpr (KIND == FUSED_GRAD) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                z[j] = j < n ? __bfloat162float(Z[j * e.ldz]) : 0.0f;
-                if constexpr (GATED) y[j] = j < n ? __bfloat162float(Z[j * e.ldz + N]) : 0.0f;
-            }
             if constexpr (GATED) {
-                gated_grad(e.act, x, z, y);
+                gated_grad(e.act, x, z, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = z[j];
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = z[j];
+                    y[j] = w[j];
+                }
             } else {
                 times_slope(e.act, x, z);
             }
             if (e.sums != nullptr)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (j < n) {
+                    if (FULL || j < n) {
                         sum += x[j];
                         if constexpr (GATED) sum2 += y[j];
                     }
         } else if constexpr (KIND == FUSED_CE_GRAD) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < n) {
+                if (FULL || j < n) {
                     const long long t = e.target[row + j];
                     const float p = exp2_fast((x[j] * e.alpha - e.lse[row + j]) * LOG2E) - (t - e.first == c ? 1.0f : 0.0f);
                     // (A row left out may hold infinities.)
                     x[j] = t >= 0 && t < e.vocabulary ? p * (e.alpha * e.dloss[row + j]) : 0.0f;
                 }
         }
+        const long at = row * e.ldc + c;
+        if (e.c_f32) {
+            float* C = static_cast<float*>(e.C) + at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) {
-                const long at = (row + j) * e.ldc + c;
-                if (e.c_f32) static_cast<float*>(e.C)[at] = x[j];
-                else static_cast<bf16*>(e.C)[at] = __float2bfloat16(x[j]);
-                if constexpr (KIND == FUSED_GRAD && GATED) static_cast<bf16*>(e.C)[at + N] = __float2bfloat16(y[j]);
+            for (int j = 0; j < 8; ++j, C += e.ldc)
+                if (FULL || j < n) *C = x[j];
+        } else {
+            bf16* C = static_cast<bf16*>(e.C) + at;
+#pragma unroll
+            for (int j = 0; j < 8; ++j, C += e.ldc)
+                if (FULL || j < n) {
+                    C[0] = __float2bfloat16(x[j]);
+                    if constexpr (KIND == FUSED_GRAD && GATED) C[N] = __float2bfloat16(y[j]);
+                }
+        }
+    }
+
+    // Rows row + first, row + first + step, .. below row + end in groups of eight, sums
+    // by sums(k, x, y); a group's loads are on their way while the one before is
+    // finished. All lanes of a warp (`in`: this one has a column).
+    template <typename Sums>
+    __device__ __forceinline__ void rows(long row, int first, int end, int step, bool in, Sums sums) {
+        float z[8], w[8];
+        if (in && first < end) load<false>(row + first, end - first, z, w);
+#pragma unroll 1
+        for (int k = first; k < end; k += step) {
+            float x[8], y[8], next_z[8], next_w[8];
+            const int left = end - k - step;
+            if (in && left >= 8) load<true>(row + k + step, 8, next_z, next_w);
+            else if (in && left > 0) load<false>(row + k + step, left, next_z, next_w);
+            sums(k, x, y);
+            if (in && end - k >= 8) finish<true>(row + k, 8, x, y, z, w);
+            else if (in) finish<false>(row + k, end - k, x, y, z, w);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                z[j] = next_z[j];
+                w[j] = next_w[j];
             }
+        }
     }
 
     // The sums, as entry `block` of what fused_join_sums adds up.

@@ -359,14 +359,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     for (int k = begin; k < end && row + k < p.M; k += 32)
                         ce_tokens(p, acc + k, row + k, min(end - k, p.M - row - k), c, in, (long)(t / p.tiles_m) * ((p.height + 31) / 32) + q);
             } else {
-#pragma unroll 1
-                for (int k = begin; k < end && row + k < p.M; k += 8) {
-                    float x[8], y[8];
+                column.rows(row, begin, min(end, p.M - row), 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
                     load_sums8(acc + k, x, p.kblocks);
                     if constexpr (TWO) load_sums8(acc + p.acc + k, y, p.kblocks);
-                    if (in) column.finish(row + k, p.M - row - k, x, y);
-                    __syncwarp();
-                }
+                });
                 if (in) column.leave((long)(t % p.tiles_m) * SETS + set);
                 __syncwarp();
             }
@@ -378,24 +374,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         cluster_sync_all();
         const int row = unit % p.tiles_m * p.tokens, col = unit / p.tiles_m * p.height;
         const int q = warp & 3, set = (warp - 2) >> 2, c = col + q * 32 + lane;
-        if (warp >= 2 && q * 32 + lane < p.height && c < p.N) {
+        if (warp >= 2) {
             // Groups of eight tokens, in turn to the cluster's blocks and their sets.
-            Column<KIND, GATED> column(p.e, p.N, c);
-#pragma unroll 1
-            for (int k = (part * SETS + set) * 8; k < p.tokens && row + k < p.M; k += SETS * 8 * p.split) {
-                float x[8] = {}, y[8] = {};
-#pragma unroll 4
-                for (int i = 0; i < p.split; ++i) {
-                    const uint32_t from = map_to_rank(stage0, (uint32_t)i) + (uint32_t)((k * 128 + q * 32 + lane) * 4);
+            const bool in = q * 32 + lane < p.height && c < p.N;
+            Column<KIND, GATED> column(p.e, p.N, in ? c : 0);
+            column.rows(row, (part * SETS + set) * 8, min(p.tokens, p.M - row), SETS * 8 * p.split, in,
+                        [&](int k, float (&x)[8], float (&y)[8]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        x[j] += ld_cluster(from + j * 512);
-                        if constexpr (TWO) y[j] += ld_cluster(from + (p.tokens + j) * 512);
-                    }
-                }
-                column.finish(row + k, p.M - row - k, x, y);
-            }
-            column.leave(((long)(unit % p.tiles_m) * p.split + part) * SETS + set);
+                            for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+#pragma unroll 4
+                            for (int i = 0; i < p.split; ++i) {
+                                const uint32_t from = map_to_rank(stage0, (uint32_t)i) + (uint32_t)((k * 128 + q * 32 + lane) * 4);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    x[j] += ld_cluster(from + j * 512);
+                                    if constexpr (TWO) y[j] += ld_cluster(from + (p.tokens + j) * 512);
+                                }
+                            }
+                        });
+            if (in) column.leave(((long)(unit % p.tiles_m) * p.split + part) * SETS + set);
         }
         __syncwarp();
         cluster_sync_all();           // no block leaves while another reads its share
@@ -451,7 +448,7 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     p.M = m.M;
     p.N = m.N;
     p.chunks = plan.chunks;
-    p.part_blocks = SUM_K / CHUNK_K / p.chunks;
+    p.part_blocks = fused_part_k(kind, e.c_f32) / CHUNK_K / p.chunks;
     p.kblocks = (int)(((long)m.K + p.chunks * CHUNK_K - 1) / (p.chunks * CHUNK_K));
     p.height = plan.height;
     p.tokens = plan.tokens;

@@ -36,7 +36,7 @@ namespace {
 using namespace mx4_tile;
 using namespace fused_act;
 using namespace fused_column;
-constexpr int TILE = 256;
+constexpr int TILE = 256;                            // rows of a tile, and columns of an accumulator
 constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // a block's 128 rows of A, or of B
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
@@ -47,7 +47,6 @@ constexpr int EPI_BYTES = EPI_WARPS * WARP_BYTES;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 256;
 static_assert(SMEM <= 227 * 1024, "shared memory");
-constexpr int PART_BLOCKS = SUM_K / STAGE_K;
 
 struct Sync {
     uint64_t full[STAGES], empty[STAGES];
@@ -62,8 +61,8 @@ static_assert(sizeof(Sync) <= 256, "barrier block");
 struct Params {
     int M, N, kblocks;
     int tiles_n, num_tiles, units, group_m, tiles_m;
+    int part_blocks;            // stages a part of a long sum
     int a_mn, b_mn;
-    int rows;                   // C, R and Z pass by TMA
     int bias4;                  // bias in pieces of 16 bytes
     FusedEpilogue e;
     unsigned long long wait_limit_ns;
@@ -166,22 +165,43 @@ __device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, in
     put_f32(bufs, v);
     if constexpr (TWO) put_f32(bufs + BUF_BYTES, v2);
     __syncwarp();
-    if (c < p.N) {
-        Column<KIND, GATED> column(e, p.N, c);
-#pragma unroll 1
-        for (int k = 0; k < rows; k += 8) {
-            float x[8], y[8];
+    {
+        const bool in = c < p.N;
+        Column<KIND, GATED> column(e, p.N, in ? c : 0);
+        // Where this lane's column lies in the rows of a group of eight.
+        uint32_t at[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) at[j] = swizzled(j, lane >> 2) + (lane & 3) * 4;
+        column.rows(row0, 0, rows, 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
+            const uint8_t* group = bufs + k * SW;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t at = swizzled(k + j, lane >> 2) + (lane & 3) * 4;
-                x[j] = *reinterpret_cast<const float*>(bufs + at);
-                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(bufs + BUF_BYTES + at);
+                x[j] = *reinterpret_cast<const float*>(group + at[j]);
+                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(group + BUF_BYTES + at[j]);
             }
-            column.finish(row0 + k, rows - k, x, y);
-        }
-        column.leave(row0 / FUSED_SUM_ROWS);
+        });
+        if (in) column.leave(row0 / FUSED_SUM_ROWS);
     }
     __syncwarp();
+}
+
+// One row's columns col .. end - 1 of R or Z on their way to L2.
+__device__ __forceinline__ void ask_bytes(const void* x, long from, long to) {
+    const char* at = static_cast<const char*>(x);
+    for (long b = from; b < to; b += 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(at + b));
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(at + to - 1));
+}
+template <int KIND, bool GATED>
+__device__ __forceinline__ void ask_columns(const Params& p, long row, long col, long end) {
+    const FusedEpilogue& e = p.e;
+    if (col >= end) return;
+    if (KIND == FUSED_GRAD) {
+        ask_bytes(e.Z, (row * e.ldz + col) * 2, (row * e.ldz + end) * 2);
+        if (GATED) ask_bytes(e.Z, (row * e.ldz + p.N + col) * 2, (row * e.ldz + p.N + end) * 2);
+    } else if (e.R != nullptr) {
+        const long size = e.r_f32 ? 4 : 2;
+        ask_bytes(e.R, (row * e.ldr + col) * size, (row * e.ldr + end) * size);
+    }
 }
 
 // ------------------------------------------------------- C by TMA, in boxes
@@ -404,10 +424,11 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& mb, int& nb
     nb = t % per_group / gm;
 }
 
-template <int KIND, bool GATED, bool LONG>
+// BOXES: C, R and Z pass by TMA (fused_boxes).
+template <int KIND, bool GATED, bool LONG, bool BOXES>
 __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-    constexpr bool TWO = KIND == FUSED_ACT && GATED;     // 128 columns of C a tile
-    constexpr int TC = TWO ? TILE / 2 : TILE;
+    constexpr bool TWO = KIND == FUSED_ACT && GATED;
+    constexpr int TC = TWO ? TILE / 2 : TILE;            // columns of C a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* epi = smem + STAGES * STAGE_BYTES;
@@ -516,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
             bool ok = true;
             // A tile's sum, or of LONG ones each part in turn: first to last - 1.
             for (int t = unit, first = 0; ok && t < p.num_tiles; ++it) {
-                const int last = LONG ? min(first + PART_BLOCKS, p.kblocks) : p.kblocks;
+                const int last = LONG ? min(first + p.part_blocks, p.kblocks) : p.kblocks;
                 if (it >= 2)
                     if (!__all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait)))
                         break;
@@ -555,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
         const int set = (warp - 2) >> 2;
         uint8_t* bufs = epi + (warp - 2) * WARP_BYTES;
         const uint32_t loaded = smem_u32(&sy->loaded[warp - 2]);
-        const bool loads = p.rows && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
+        const bool loads = BOXES && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
         constexpr int SET_COLS = TC / 2, TURNS = SET_COLS / 64;
         int it = 0, box = 0;
         uint32_t load_ph = 0;
@@ -580,19 +601,21 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
                 __syncwarp();
                 loading = true;
             };
-            if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
+            if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD) {
                 if (loads && rows > 0 && col0 < p.N) ask(col0);
+                if (!BOXES && lane < rows) ask_columns<KIND, GATED>(p, row0 + lane, col0, min(col0 + SET_COLS, p.N));
+            }
 
             bool ok = true;
             if constexpr (LONG) {
                 float sum[4][32] = {};
                 #pragma unroll 1
-                for (int first = 0; ok && first < p.kblocks; first += PART_BLOCKS) {
+                for (int first = 0; ok && first < p.kblocks; first += p.part_blocks) {
                     ok = __all_sync(~0u, mbar_wait<true, true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * 128;
-                    const bool final = first + PART_BLOCKS >= p.kblocks;
+                    const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * SET_COLS;
+                    const bool final = first + p.part_blocks >= p.kblocks;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -620,19 +643,15 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
             if constexpr (KIND == FUSED_CE) {
                 ce_columns(p, acc, row0 + lane, col0);
                 release();
-            } else if constexpr (KIND == FUSED_CE_GRAD) {
-                const bool in = lane < rows;
-                const long long target = in ? p.e.target[row0 + lane] : -1;
-                const bool kept = target >= 0 && target < p.e.vocabulary;
-                const float lse = in ? p.e.lse[row0 + lane] : 0.0f;
-                const float scale = in ? p.e.alpha * p.e.dloss[row0 + lane] : 0.0f;
-#pragma unroll 1
-                for (int i = 0; i < TURNS; ++i) {
-                    if (rows > 0 && col0 + i * 64 < p.N)
-                        ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col0 + i * 64, box, lse, scale, target - p.e.first, kept);
-                }
-                release();
             } else {
+                // Of this thread's row (CE_GRAD).
+                long long target = -1;
+                float lse = 0.0f, scale = 0.0f;
+                if (KIND == FUSED_CE_GRAD && lane < rows) {
+                    target = p.e.target[row0 + lane];
+                    lse = p.e.lse[row0 + lane];
+                    scale = p.e.alpha * p.e.dloss[row0 + lane];
+                }
 #pragma unroll 1
                 for (int i = 0; i < TURNS; ++i) {
                     const int col = col0 + i * 64;
@@ -641,19 +660,25 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
                         if (last) release();
                         continue;
                     }
-                    if (p.rows) {
-                        if (i > 0 && loads) ask(col);
-                        if (loading) {
-                            ok = __all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait));
-                            if (!ok) break;
-                            load_ph ^= 1u;
-                            loading = false;
-                        } else if (KIND == FUSED_ACT && p.e.Z != nullptr) {
-                            if (lane == 0) tma_store_wait_read<0>();
-                            __syncwarp();
+                    if constexpr (BOXES) {
+                        if constexpr (KIND == FUSED_CE_GRAD) {
+                            ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col, box, lse, scale, target - p.e.first,
+                                         target >= 0 && target < p.e.vocabulary);
+                            if (last) release();
+                        } else {
+                            if (i > 0 && loads) ask(col);
+                            if (loading) {
+                                ok = __all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait));
+                                if (!ok) break;
+                                load_ph ^= 1u;
+                                loading = false;
+                            } else if (KIND == FUSED_ACT && p.e.Z != nullptr) {
+                                if (lane == 0) tma_store_wait_read<0>();
+                                __syncwarp();
+                            }
+                            turn_boxes<KIND, GATED>(p, &maps, bufs, acc + i * 64, acc + 128 + i * 64, row0, rows, col, box,
+                                                    [&]() { if (last) release(); });
                         }
-                        turn_boxes<KIND, GATED>(p, &maps, bufs, acc + i * 64, acc + 128 + i * 64, row0, rows, col, box,
-                                                [&]() { if (last) release(); });
                     } else {
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
@@ -687,13 +712,7 @@ bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld,
     return encode(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// C, R or Z in boxes of 32 rows x 128 bytes, where TMA takes them: base and rows
-// on 16 bytes, whole 16-byte pieces long (a store clipped inside such a
-// piece also writes the rest of it).
-bool boxable(const void* x, long ld, int N, bool f32) {
-    const int esz = f32 ? 4 : 2;
-    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * esz % 16 == 0 && (long)N * esz % 16 == 0;
-}
+// C, R or Z in boxes of 32 rows x 128 bytes.
 bool encode_boxes(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld, int M, int N, bool f32) {
     const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
     const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
@@ -702,12 +721,16 @@ bool encode_boxes(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld, i
 }
 const void* second_half(const void* x, int N) { return static_cast<const bf16*>(x) + N; }
 
-template <int KIND, bool GATED, bool LONG>
-cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
-    const cudaError_t e = set_smem_limit_once<fused_kernel<KIND, GATED, LONG>>(SMEM);
+template <int KIND, bool GATED, bool LONG, bool BOXES>
+cudaError_t launch_kernel(const Maps& maps, const Params& p, cudaStream_t s) {
+    const cudaError_t e = set_smem_limit_once<fused_kernel<KIND, GATED, LONG, BOXES>>(SMEM);
     if (e != cudaSuccess) return e;
     ClusterLaunch cfg(2 * p.units, THREADS, SMEM, 2, s);
-    return cudaLaunchKernelEx(&cfg.config, fused_kernel<KIND, GATED, LONG>, maps, p);
+    return cudaLaunchKernelEx(&cfg.config, fused_kernel<KIND, GATED, LONG, BOXES>, maps, p);
+}
+template <int KIND, bool GATED, bool LONG>
+cudaError_t launch(const Maps& maps, const Params& p, bool boxes, cudaStream_t s) {
+    return boxes ? launch_kernel<KIND, GATED, LONG, true>(maps, p, s) : launch_kernel<KIND, GATED, LONG, false>(maps, p, s);
 }
 
 }  // namespace
@@ -724,6 +747,7 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
     p.M = m.M;
     p.N = m.N;
     p.kblocks = (int)(((long)m.K + STAGE_K - 1) / STAGE_K);
+    p.part_blocks = fused_part_k(kind, e.c_f32) / STAGE_K;
     const int cols = two ? TILE / 2 : TILE;
     p.tiles_m = (int)(((long)m.M + TILE - 1) / TILE);
     p.tiles_n = (int)(((long)m.N + cols - 1) / cols);
@@ -743,19 +767,11 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
                     !encode_operand(enc, &maps.B, m.B, m.ldb, m.N, m.K, m.b_mn) ||
                     (two && !encode_operand(enc, &maps.B2, m.B2, m.ldb, m.N, m.K, m.b_mn))))
         return cudaErrorInvalidValue;
-    // C, R and Z by TMA: all of them, and where two buffers hold them (an FP32 R
-    // takes both, and leaves none for Z).
-    // (The logits' gradient is scratch, its rows whole 64 columns long: what lies
-    // past N there, from rows past the vocabulary, is read by no product.)
-    const bool f32 = e.c_f32;
-    const int width = kind == FUSED_CE_GRAD ? (m.N + 7) / 8 * 8 : m.N;
-    bool rows = kind != FUSED_CE && boxable(e.C, e.ldc, width, f32);
-    if (kind == FUSED_ACT)
-        rows = rows && (e.R == nullptr || boxable(e.R, e.ldr, m.N, e.r_f32)) && (e.Z == nullptr || boxable(e.Z, e.ldz, m.N, false)) &&
-               !(e.Z != nullptr && (e.r_f32 || (two && e.R != nullptr)));
-    if (kind == FUSED_GRAD) rows = rows && boxable(e.Z, e.ldz, m.N, false);
-    if (rows) {
-        bool ok = encode_boxes(enc, &maps.E[0], e.C, e.ldc, m.M, width, f32);
+    const bool boxes = plan.boxes;
+    if (boxes) {
+        // (The logits' gradient is scratch, its rows whole 64 columns long: what lies
+        // past N there, from rows past the vocabulary, is read by no product.)
+        bool ok = encode_boxes(enc, &maps.E[0], e.C, e.ldc, m.M, kind == FUSED_CE_GRAD ? (m.N + 7) / 8 * 8 : m.N, e.c_f32);
         if (kind == FUSED_ACT) {
             if (e.R != nullptr) ok = ok && encode_boxes(enc, &maps.E[1], e.R, e.ldr, m.M, m.N, e.r_f32);
             if (e.Z != nullptr) ok = ok && encode_boxes(enc, &maps.E[2], e.Z, e.ldz, m.M, m.N, false);
@@ -768,21 +784,21 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
         }
         if (!ok) return cudaErrorInvalidValue;
     }
-    p.rows = rows ? 1 : 0;
-    const bool parts = p.kblocks > PART_BLOCKS;
+    const bool parts = p.kblocks > p.part_blocks;
     switch (kind) {
         case FUSED_ACT:
-            if (two) return launch<FUSED_ACT, true, false>(maps, p, s);
-            return parts && f32 ? launch<FUSED_ACT, false, true>(maps, p, s) : launch<FUSED_ACT, false, false>(maps, p, s);
+            if (two) return launch<FUSED_ACT, true, false>(maps, p, boxes, s);
+            return parts && e.c_f32 ? launch<FUSED_ACT, false, true>(maps, p, boxes, s)
+                                    : launch<FUSED_ACT, false, false>(maps, p, boxes, s);
         case FUSED_GRAD: {
-            const bool l = parts && (f32 || e.sums != nullptr);
-            if (e.gated) return l ? launch<FUSED_GRAD, true, true>(maps, p, s) : launch<FUSED_GRAD, true, false>(maps, p, s);
-            return l ? launch<FUSED_GRAD, false, true>(maps, p, s) : launch<FUSED_GRAD, false, false>(maps, p, s);
+            const bool l = parts && (e.c_f32 || e.sums != nullptr);
+            if (e.gated) return l ? launch<FUSED_GRAD, true, true>(maps, p, boxes, s) : launch<FUSED_GRAD, true, false>(maps, p, boxes, s);
+            return l ? launch<FUSED_GRAD, false, true>(maps, p, boxes, s) : launch<FUSED_GRAD, false, false>(maps, p, boxes, s);
         }
         case FUSED_CE:
-            return parts ? launch<FUSED_CE, false, true>(maps, p, s) : launch<FUSED_CE, false, false>(maps, p, s);
-        default:
-            return rows ? launch<FUSED_CE_GRAD, false, false>(maps, p, s) : cudaErrorInvalidValue;
+            return parts ? launch_kernel<FUSED_CE, false, true, false>(maps, p, s)
+                         : launch_kernel<FUSED_CE, false, false, false>(maps, p, s);
+        default: return launch_kernel<FUSED_CE_GRAD, false, false, true>(maps, p, s);
     }
 }
 

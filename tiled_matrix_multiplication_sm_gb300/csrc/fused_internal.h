@@ -67,15 +67,29 @@ constexpr int FUSED_CE_COLS = 128;
 constexpr int FUSED_FEW_SETS = 4;
 constexpr int FUSED_FEW_RING = 209 * 1024;
 
+// Columns of K a part of a long sum covers. (A gradient's own result is BF16 and
+// only its column sums keep 32 bits: 2048. 8192 x 14336 x 4096 gated: 641 us, with
+// 1024 690, with one part 624; of db's norm it loses 1.2e-6, 0.7e-6, 2.2e-6.)
+inline int fused_part_k(FusedKind kind, bool c_f32) { return kind == FUSED_GRAD && !c_f32 ? 2048 : 1024; }
+
 // How a product runs: on SM pairs (fused_gemm.cu), or as few tiles (fused_few.cu).
 struct FusedPlan {
     bool few;
+    bool boxes;                          // pairs: fused_boxes
     int height, tokens, split, chunks;   // few: columns and rows of C a tile, blocks that share its sum, 64s of K a stage
     long sum_blocks;                     // rows of FusedEpilogue::sums
     long ce_blocks;                      // of FusedEpilogue::parts
 };
-// Only the sizes and storage of the operands are read.
-cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, bool gated, int num_sms, FusedPlan* plan);
+// Only the sizes and storage of the operands are read, and of the epilogue what
+// decides whether its matrices pass by TMA.
+cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan);
+
+// Whether C, R and Z pass by TMA on pairs, in boxes of 32 rows x 128 bytes: bases
+// and rows on 16 bytes, whole 16-byte pieces long (a store clipped inside such a
+// piece also writes the rest of it), and two boxes of shared memory for all of a
+// turn's (an FP32 R takes both and leaves none for Z). The logits' gradient is scratch
+// laid out for it.
+bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e);
 
 // Operands on 16-byte boundaries, with rows on them.
 cudaError_t fused_gemm(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, const FusedPlan& plan, int num_sms,

@@ -59,10 +59,26 @@ double pair_us(int M, long N, int K, int halves, int pairs) {
 
 }  // namespace
 
-cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, bool gated, int num_sms, FusedPlan* plan) {
-    const int halves = kind == FUSED_ACT && gated ? 2 : 1;
+bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e) {
+    auto fits = [&](const void* x, long ld, bool f32) {
+        const int size = f32 ? 4 : 2;
+        return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * size % 16 == 0 && (long)N * size % 16 == 0;
+    };
+    switch (kind) {
+        case FUSED_ACT:
+            return fits(e.C, e.ldc, e.c_f32) && (e.R == nullptr || fits(e.R, e.ldr, e.r_f32)) &&
+                   (e.Z == nullptr || (fits(e.Z, e.ldz, false) && !(e.R != nullptr && (e.r_f32 || e.gated))));
+        case FUSED_GRAD: return fits(e.C, e.ldc, e.c_f32) && fits(e.Z, e.ldz, false);
+        case FUSED_CE_GRAD: return true;
+        default: return false;
+    }
+}
+
+cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan) {
+    const int halves = kind == FUSED_ACT && e.gated ? 2 : 1;
     plan->few = false;
     plan->height = plan->tokens = plan->split = plan->chunks = 0;
+    plan->boxes = fused_boxes(kind, p.N, e);
     plan->sum_blocks = up(p.M, FUSED_SUM_ROWS);
     plan->ce_blocks = up(p.N, FUSED_CE_COLS);
     // Two rounds of pair tiles and more: always on pairs.
@@ -71,8 +87,8 @@ cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, bool gated, int nu
         (forced < 0 && up(p.M, 256) * up((long)p.N * halves, 256) >= num_sms))
         return cudaSuccess;
     unsigned long long fits = 0;
-    const cudaError_t e = fused_few_clusters(&fits);
-    if (e != cudaSuccess) return e;
+    const cudaError_t err = fused_few_clusters(&fits);
+    if (err != cudaSuccess) return err;
     double best = forced == 1 ? 1e300 : pair_us(p.M, p.N, p.K, halves, num_sms / 2);
     const int most = halves == 2 ? 128 : 256, whole = (int)up(p.M, 16) * 16;
     const int tokens[5] = {whole, 32, 64, 128, 256};

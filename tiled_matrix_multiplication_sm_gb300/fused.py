@@ -19,7 +19,7 @@ import torch
 
 from . import binding
 from .binding import TGEMM_OK, TGEMM_TRANS_A, TGEMM_TRANS_B, TgemmError, _stream_handle
-from .mx4 import _check_matrix, _check_values, _empty, _type
+from .mx4 import TGEMM_TYPE_BF16, _check_matrix, _check_values, _empty, _type
 
 TGEMM_GATED = 4
 
@@ -51,12 +51,11 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-def _call(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
-    """Run entry point ``name`` with ``args`` and the stream on ``device``;
+def _call(name: str, index: int, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Run entry point ``name`` with ``args`` and the stream on device ``index``;
     switches devices only when another one is current."""
     fn = getattr(_lib or load(), name)
-    index = device.index
-    if index is None or index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         status = fn(*args, _stream_handle(stream, index))
     else:
         with torch.cuda.device(index):
@@ -71,40 +70,56 @@ def _activation(act: str) -> int:
     return _ACTIVATIONS[act]
 
 
+def _bf16(x, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, leading dimension) of a bfloat16 operand. The checks in
+    one place and few steps (they are most of a small call's host time); what
+    fails them goes to _check_matrix for its error."""
+    if isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.is_cuda:
+        shape = x.shape
+        if len(shape) == 2:
+            rows, cols = shape
+            ld, step = x.stride()
+            if (step == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+                return rows, cols, max(ld, cols, 1)
+    ld = _check_matrix(x, name, torch.bfloat16)
+    return x.shape[0], x.shape[1], ld
+
+
 def _operands(A, B, trans_a: bool, trans_b: bool, halves: int):
-    """(M, N, K, lda, ldb, flags) of op(A) op(B), whose columns come in ``halves`` halves."""
-    lda = _check_matrix(A, "A", torch.bfloat16)
-    ldb = _check_matrix(B, "B", torch.bfloat16)
-    if A.device != B.device:
+    """(M, N, K, lda, ldb, flags, device index) of op(A) op(B), whose columns come in ``halves`` halves."""
+    rows, cols, lda = _bf16(A, "A")
+    M, K = (cols, rows) if trans_a else (rows, cols)
+    rows, cols, ldb = _bf16(B, "B")
+    K2, wide = (cols, rows) if trans_b else (rows, cols)
+    index = A.get_device()
+    if index != B.get_device():
         raise ValueError(f"A is on {A.device}, B on {B.device}")
-    M, K = (A.shape[1], A.shape[0]) if trans_a else A.shape
-    K2, wide = (B.shape[1], B.shape[0]) if trans_b else B.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} / {tuple(B.shape)}")
     if wide % halves != 0:
         raise ValueError(f"a gated product needs an even number of columns, got {wide}")
-    return M, wide // halves, K, lda, ldb, (TGEMM_TRANS_A if trans_a else 0) | (TGEMM_TRANS_B if trans_b else 0)
+    return M, wide // halves, K, lda, ldb, (TGEMM_TRANS_A if trans_a else 0) | (TGEMM_TRANS_B if trans_b else 0), index
 
 
-def _like(x, name: str, shape, device) -> Tuple[int, int]:
+def _like(x, name: str, rows: int, cols: int, index: int) -> Tuple[int, int]:
     """(leading dimension, TGEMM_TYPE_*) of a matrix of this shape on this device."""
     ld, kind = _check_values(x, name)
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, the operands on {device}")
+    if tuple(x.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(rows, cols)}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, the operands on cuda:{index}")
     return ld, kind
 
 
-def _vector(x, name: str, n: int, dtype: torch.dtype, device) -> int:
+def _vector(x, name: str, n: int, dtype: torch.dtype, index: int) -> int:
     """The pointer of a contiguous vector of n elements."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if tuple(x.shape) != (n,):
+    if x.shape != (n,):
         raise ValueError(f"{name} must have {n} elements, got shape {tuple(x.shape)}")
-    if x.device != device or (n > 1 and x.stride(0) != 1):
+    if not x.is_cuda or x.get_device() != index or (n > 1 and x.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous and on the operands' device")
     return x.data_ptr()
 
@@ -126,21 +141,20 @@ def gemm_act(A: torch.Tensor, B: torch.Tensor, act: str = "none", trans_a: bool 
     float32, and may be ``out`` itself. With ``keep_z`` (C, Z) comes back, Z the
     bfloat16 z that :func:`gemm_act_grad` takes."""
     code = _activation(act)
-    M, N, K, lda, ldb, flags = _operands(A, B, trans_a, trans_b, 2 if gated else 1)
-    device = A.device
+    M, N, K, lda, ldb, flags, device = _operands(A, B, trans_a, trans_b, 2 if gated else 1)
     wide = 2 * N if gated else N
     if out is None:
         ldc, kind = max(N, 1), _type(out_dtype, "out_dtype")
     else:
-        ldc, kind = _like(out, "out", (M, N), device)
+        ldc, kind = _like(out, "out", M, N, device)
     if gated:
         flags |= TGEMM_GATED
-        if kind != _type(torch.bfloat16, ""):
+        if kind != TGEMM_TYPE_BF16:
             raise TypeError("a gated product's result is bfloat16")
     b = 0 if bias is None else _vector(bias, "bias", wide, torch.float32, device)
     r, ldr, r_kind = 0, 0, 0
     if residual is not None:
-        ldr, r_kind = _like(residual, "residual", (M, N), device)
+        ldr, r_kind = _like(residual, "residual", M, N, device)
         r = residual.data_ptr()
     if out is None:
         out = _empty(stream, M, N, dtype=out_dtype, device=device)
@@ -163,16 +177,15 @@ def gemm_act_grad(A: torch.Tensor, B: torch.Tensor, Z: torch.Tensor, act: str = 
     act'(g), d * act(g)] have 2 N columns. dZ goes to ``out`` (which may be Z) or
     a new ``out_dtype`` matrix; without ``bias_grad`` only dZ comes back."""
     code = _activation(act)
-    M, N, K, lda, ldb, flags = _operands(A, B, trans_a, trans_b, 1)
-    device = A.device
+    M, N, K, lda, ldb, flags, device = _operands(A, B, trans_a, trans_b, 1)
     wide = 2 * N if gated else N
-    ldz, z_kind = _like(Z, "Z", (M, wide), device)
-    if z_kind != _type(torch.bfloat16, ""):
+    ldz, z_kind = _like(Z, "Z", M, wide, device)
+    if z_kind != TGEMM_TYPE_BF16:
         raise TypeError("Z must be bfloat16")
     if out is None:
         ldc, kind = max(wide, 1), _type(out_dtype, "out_dtype")
     else:
-        ldc, kind = _like(out, "out", (M, wide), device)
+        ldc, kind = _like(out, "out", M, wide, device)
     if gated:
         flags |= TGEMM_GATED
         if kind != z_kind:
@@ -186,15 +199,15 @@ def gemm_act_grad(A: torch.Tensor, B: torch.Tensor, Z: torch.Tensor, act: str = 
 
 
 def _head(X, W, target):
-    """(T, V, D, ldx, ldw, target's pointer) of a head's product."""
-    ldx = _check_matrix(X, "X", torch.bfloat16)
-    ldw = _check_matrix(W, "W", torch.bfloat16)
-    if X.device != W.device:
+    """(T, V, D, ldx, ldw, target's pointer, device index) of a head's product."""
+    T, D, ldx = _bf16(X, "X")
+    V, D2, ldw = _bf16(W, "W")
+    index = X.get_device()
+    if index != W.get_device():
         raise ValueError(f"X is on {X.device}, W on {W.device}")
-    if X.shape[1] != W.shape[1]:
+    if D != D2:
         raise ValueError(f"inner dimensions differ: {tuple(X.shape)} / {tuple(W.shape)}")
-    T = X.shape[0]
-    return T, W.shape[0], X.shape[1], ldx, ldw, _vector(target, "target", T, torch.int64, X.device)
+    return T, V, D, ldx, ldw, _vector(target, "target", T, torch.int64, index), index
 
 
 def gemm_ce(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, alpha: float = 1.0,
@@ -204,10 +217,10 @@ def gemm_ce(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, alpha: float
     z[target]. X (T x D) and W (V x D) are bfloat16, target int64; a row whose
     target is not in 0 .. V - 1 is left out, with a loss of 0. The logits are
     not kept."""
-    T, V, D, ldx, ldw, t = _head(X, W, target)
-    loss = _empty(stream, T, dtype=torch.float32, device=X.device)
-    lse = _empty(stream, T, dtype=torch.float32, device=X.device)
-    _call("gemm_ce", X.device, stream, T, V, D, X.data_ptr(), ldx, W.data_ptr(), ldw, alpha, t, loss.data_ptr(),
+    T, V, D, ldx, ldw, t, device = _head(X, W, target)
+    loss = _empty(stream, T, dtype=torch.float32, device=device)
+    lse = _empty(stream, T, dtype=torch.float32, device=device)
+    _call("gemm_ce", device, stream, T, V, D, X.data_ptr(), ldx, W.data_ptr(), ldw, alpha, t, loss.data_ptr(),
           lse.data_ptr())
     return loss, lse
 
@@ -222,8 +235,7 @@ def gemm_ce_grad(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: to
     (``dloss`` float32, one entry a token). ``x_grad``/``w_grad`` say which are
     wanted (the other is None). dW goes to ``dw_out``, plus ``beta`` times what
     is there (a sum over micro-batches), or to a new ``dw_dtype`` matrix."""
-    T, V, D, ldx, ldw, t = _head(X, W, target)
-    device = X.device
+    T, V, D, ldx, ldw, t, device = _head(X, W, target)
     lse_ptr = _vector(lse, "lse", T, torch.float32, device)
     dloss_ptr = _vector(dloss, "dloss", T, torch.float32, device)
     dx, dw, x_kind, w_kind, lddx, lddw = None, None, 0, 0, D, D
@@ -236,7 +248,7 @@ def gemm_ce_grad(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: to
     if w_grad and dw_out is None:
         w_kind = _type(dw_dtype, "dw_dtype")
     elif w_grad:
-        lddw, w_kind = _like(dw_out, "dw_out", (V, D), device)
+        lddw, w_kind = _like(dw_out, "dw_out", V, D, device)
         dw = dw_out
     if x_grad:
         dx = _empty(stream, T, D, dtype=dx_dtype, device=device)
