@@ -15,7 +15,7 @@
  * but for what an entry says.
  *
  * Sums of products are FP32: on the tensor cores, which cut low bits off at
- * every step, up to 1024 columns of K where a result keeps 32 bits (an FP32 C,
+ * every step, up to 2048 columns of K where a result keeps 32 bits (an FP32 C,
  * db, loss and lse); longer ones are then made of such parts, added with
  * rounding to nearest. Values go from the sum to the result in FP32 and are
  * rounded once, to nearest even, where the result is BF16.
@@ -101,7 +101,7 @@ TGEMM_API int gemm_act_grad(int M, int N, int K, const void* A, long lda, const 
  * X is T x D, W is V x D; target (T entries of 64 bits), loss and lse (T floats
  * each) are in device memory. A row whose target is not in 0 .. V - 1 is left
  * out: its loss is 0 whatever X holds there. Each 128 columns of the
- * vocabulary leave a maximum and a sum for each token (scratch: 8 bytes for
+ * vocabulary or so leave a maximum and a sum for each token (scratch: 8 bytes for
  * each of them; tokens are taken in turns of 256 MB of it).
  *
  * T == 0 is a no-op. Errors as gemm_act, and TGEMM_ERR_INVALID_ARG for an

@@ -61,15 +61,22 @@ struct Operand {
         if (copied) at = scratch.add((size_t)rows * padded() * 2);
     }
     long padded() const { return ((long)cols + 63) / 64 * 64; }
-    cudaError_t lay(const Scratch& scratch, cudaStream_t s) {
-        if (!copied) return cudaSuccess;
-        void* to = scratch.at(at);
-        const cudaError_t e = tgemm::repack_rows(x, ld, to, padded(), rows, cols, 2, s);
-        x = to;
+    // The copy that lays it in its scratch (none: an empty one).
+    tgemm::RepackJob lay(const Scratch& scratch) {
+        tgemm::RepackJob job;
+        if (!copied) return job;
+        job = {x, ld, scratch.at(at), padded(), rows, cols};
+        x = job.dst;
         ld = padded();
-        return e;
+        return job;
     }
 };
+
+// Two operands' copies in one launch.
+cudaError_t lay(Operand& a, Operand& b, const Scratch& scratch, cudaStream_t s) {
+    if (!a.copied && !b.copied) return cudaSuccess;
+    return tgemm::repack_rows2(a.lay(scratch), b.lay(scratch), 2, s);
+}
 
 // A product's operands, checked; op(B) has `wide` columns, in `halves` halves.
 struct Operands {
@@ -113,9 +120,9 @@ cudaError_t run(const Operands& o, tgemm::FusedKind kind, FusedEpilogue& e, floa
     const size_t sums = scratch.add(db != nullptr ? (size_t)plan.sum_blocks * wide * sizeof(float) : 0);
     err = scratch.take();
     if (err != cudaSuccess) return err;
-    err = a.lay(scratch, s);
-    if (err == cudaSuccess) err = b.lay(scratch, s);
-    if (err == cudaSuccess && apart) err = b2.lay(scratch, s);
+    err = lay(a, b, scratch, s);
+    Operand none(nullptr, 0, 0, 0, scratch);
+    if (err == cudaSuccess && apart) err = lay(b2, none, scratch, s);
     if (o.halves == 2 && !apart)
         b2.x = static_cast<const __nv_bfloat16*>(b.x) + (b_mn ? (long)o.N : (long)o.N * b.ld);
     if (db != nullptr) e.sums = static_cast<float*>(scratch.at(sums));
@@ -160,8 +167,7 @@ cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long
     const size_t parts = scratch.add((size_t)turn * blocks * sizeof(float2)), picked = scratch.add((size_t)turn * sizeof(float));
     e = scratch.take();
     if (e != cudaSuccess) return e;
-    e = x.lay(scratch, s);
-    if (e == cudaSuccess) e = w.lay(scratch, s);
+    e = lay(x, w, scratch, s);
     for (long t = 0; e == cudaSuccess && t < T; t += turn) {
         const int n = (int)(T - t < turn ? T - t : turn);
         FusedEpilogue ep;
@@ -206,8 +212,7 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     const size_t sum_at = scratch.add(sums ? (size_t)T * ldk * 4 : 0);
     cudaError_t e = scratch.take();
     if (e != cudaSuccess) return e;
-    e = x.lay(scratch, s);
-    if (e == cudaSuccess) e = w.lay(scratch, s);
+    e = lay(x, w, scratch, s);
     void *const z = scratch.at(z_at), *const kept = scratch.at(kept_at), *const sum = scratch.at(sum_at);
     if (e == cudaSuccess && dW.x != nullptr && T > 0 && V > 0) e = tgemm::fused_keep_rows(X, ldx, kept, ldk, T, D, target, V, s);
     for (long v = 0; e == cudaSuccess && (v < V || v == 0); v += piece > 0 ? piece : 1) {

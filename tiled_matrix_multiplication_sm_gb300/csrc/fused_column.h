@@ -30,7 +30,10 @@ __device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32], int kbl
     tmem_ld32(tmem, r);
     tmem_wait_ld(r);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = kblocks > 0 ? __uint_as_float(r[j]) : 0.0f;
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (kblocks == 0)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
 }
 
 // Column c of C, below N columns (gated: and column N + c of what has 2 N), rows

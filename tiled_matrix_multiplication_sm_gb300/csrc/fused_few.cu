@@ -448,7 +448,7 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     p.M = m.M;
     p.N = m.N;
     p.chunks = plan.chunks;
-    p.part_blocks = fused_part_k(kind, e.c_f32) / CHUNK_K / p.chunks;
+    p.part_blocks = FUSED_PART_K / CHUNK_K / p.chunks;
     p.kblocks = (int)(((long)m.K + p.chunks * CHUNK_K - 1) / (p.chunks * CHUNK_K));
     p.height = plan.height;
     p.tokens = plan.tokens;

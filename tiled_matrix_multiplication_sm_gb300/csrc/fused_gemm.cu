@@ -3,10 +3,10 @@
 // the maxima and sums of a softmax cross entropy, and its gradient.
 //
 // The product is the tensor cores' (tcgen05, kind f16, FP32 accumulators): 256 x
-// 256 tiles on SM pairs (cta_group::2), persistent, one block on an SM. Ten
-// warps: 0 copies (TMA), 1 issues the MMAs, 2 to 9 are the epilogue, two sets
-// of four (one to a quarter of tensor memory's lanes), each set on half of the
-// tile's columns. Stages of 64 columns of K, two accumulators, so that a tile's
+// 256 tiles on SM pairs (cta_group::2), persistent, one block on an SM.
+// Warp 0 copies (TMA), 1 issues the MMAs, the others are the epilogue, two
+// or four sets of four (one to a quarter of tensor memory's lanes), each set on its
+// share of the tile's columns. Stages of 64 columns of K, two accumulators, so that a tile's
 // epilogue runs beside the next tile's MMAs. Either operand is read as it is
 // kept, K-major in boxes of 128 rows x 128 bytes or MN-major in two boxes of 64
 // rows of K x 128 bytes, both in the 128-byte swizzle.
@@ -14,7 +14,7 @@
 // Gated products take 128 columns of g (the pair's first block) and the same 128
 // of u (its second) for a tile, so that a thread holds both of a row.
 //
-// Sums of more than SUM_K columns that end in 32 bits (LONG) come in parts,
+// Sums of more than FUSED_PART_K columns that end in 32 bits (LONG) come in parts,
 // accumulator by accumulator; the epilogue's warps add them up in registers
 // and put the total back where the last part lay.
 //
@@ -41,22 +41,29 @@ constexpr int STAGE_K = 64;
 constexpr int OPERAND_BYTES = 128 * SW;              // a block's 128 rows of A, or of B
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr int STAGES = 5;
-constexpr int EPI_WARPS = 8;
-constexpr int WARP_BYTES = 2 * BUF_BYTES;            // two boxes a warp
-constexpr int EPI_BYTES = EPI_WARPS * WARP_BYTES;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 256;
+constexpr int EPI_BYTES = 16 * BUF_BYTES;
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 512;
 static_assert(SMEM <= 227 * 1024, "shared memory");
+// The epilogue: sets of four warps, each on its share of a tile's columns. Boxes
+// and gated sums take two buffers a warp; a column a lane takes one, and more
+// warps hide its latencies (3000 x 5001 x 1537 with R and Z: 99 us with two sets).
+template <int KIND, bool GATED, bool BOXES>
+struct Shape {
+    static constexpr bool TWO = KIND == FUSED_ACT && GATED;      // 128 columns of C a tile
+    static constexpr int SETS = BOXES || TWO || KIND == FUSED_CE ? 2 : 4, WARPS = 4 * SETS;
+    static constexpr int WARP_BYTES = EPI_BYTES / WARPS;
+    static constexpr int THREADS = 64 + 32 * WARPS;
+};
 
 struct Sync {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t tmem_full[2], tmem_empty[2];
-    uint64_t loaded[EPI_WARPS];                      // boxes of R or Z
+    uint64_t loaded[8];                              // boxes of R or Z
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
-static_assert(sizeof(Sync) <= 256, "barrier block");
+static_assert(sizeof(Sync) <= 512, "barrier block");
 
 struct Params {
     int M, N, kblocks;
@@ -183,25 +190,6 @@ __device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, in
         if (in) column.leave(row0 / FUSED_SUM_ROWS);
     }
     __syncwarp();
-}
-
-// One row's columns col .. end - 1 of R or Z on their way to L2.
-__device__ __forceinline__ void ask_bytes(const void* x, long from, long to) {
-    const char* at = static_cast<const char*>(x);
-    for (long b = from; b < to; b += 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(at + b));
-    asm volatile("prefetch.global.L2 [%0];" :: "l"(at + to - 1));
-}
-template <int KIND, bool GATED>
-__device__ __forceinline__ void ask_columns(const Params& p, long row, long col, long end) {
-    const FusedEpilogue& e = p.e;
-    if (col >= end) return;
-    if (KIND == FUSED_GRAD) {
-        ask_bytes(e.Z, (row * e.ldz + col) * 2, (row * e.ldz + end) * 2);
-        if (GATED) ask_bytes(e.Z, (row * e.ldz + p.N + col) * 2, (row * e.ldz + p.N + end) * 2);
-    } else if (e.R != nullptr) {
-        const long size = e.r_f32 ? 4 : 2;
-        ask_bytes(e.R, (row * e.ldr + col) * size, (row * e.ldr + end) * size);
-    }
 }
 
 // ------------------------------------------------------- C by TMA, in boxes
@@ -426,8 +414,9 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& mb, int& nb
 
 // BOXES: C, R and Z pass by TMA (fused_boxes).
 template <int KIND, bool GATED, bool LONG, bool BOXES>
-__global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-    constexpr bool TWO = KIND == FUSED_ACT && GATED;
+__global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    using S = Shape<KIND, GATED, BOXES>;
+    constexpr bool TWO = S::TWO;
     constexpr int TC = TWO ? TILE / 2 : TILE;            // columns of C a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -447,9 +436,9 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&sy->tmem_full[a]), 1);
-            mbar_init(smem_u32(&sy->tmem_empty[a]), 2 * EPI_WARPS);
+            mbar_init(smem_u32(&sy->tmem_empty[a]), 2 * S::WARPS);
         }
-        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(smem_u32(&sy->loaded[w]), 1);
+        for (int w = 0; w < 8; ++w) mbar_init(smem_u32(&sy->loaded[w]), 1);
         mbar_init(smem_u32(&sy->drain), 1);
         sy->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -574,10 +563,10 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                                // tensor-memory lanes 32 q .. 32 q + 31
         const int set = (warp - 2) >> 2;
-        uint8_t* bufs = epi + (warp - 2) * WARP_BYTES;
-        const uint32_t loaded = smem_u32(&sy->loaded[warp - 2]);
+        uint8_t* bufs = epi + (warp - 2) * S::WARP_BYTES;
+        const uint32_t loaded = smem_u32(&sy->loaded[(warp - 2) & 7]);
         const bool loads = BOXES && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
-        constexpr int SET_COLS = TC / 2, TURNS = SET_COLS / 64;
+        constexpr int SET_COLS = TC / S::SETS, TURNS = SET_COLS / 64;
         int it = 0, box = 0;
         uint32_t load_ph = 0;
         bool loading = false;                                  // boxes asked for and not waited for
@@ -601,14 +590,12 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
                 __syncwarp();
                 loading = true;
             };
-            if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD) {
+            if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
                 if (loads && rows > 0 && col0 < p.N) ask(col0);
-                if (!BOXES && lane < rows) ask_columns<KIND, GATED>(p, row0 + lane, col0, min(col0 + SET_COLS, p.N));
-            }
 
             bool ok = true;
             if constexpr (LONG) {
-                float sum[4][32] = {};
+                float sum[SET_COLS / 32][32] = {};
                 #pragma unroll 1
                 for (int first = 0; ok && first < p.kblocks; first += p.part_blocks) {
                     ok = __all_sync(~0u, mbar_wait<true, true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
@@ -617,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1) fused_kernel(const __grid_constant
                     const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * SET_COLS;
                     const bool final = first + p.part_blocks >= p.kblocks;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < SET_COLS / 32; ++i) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 16) {
                             uint32_t r[16];
@@ -725,7 +712,7 @@ template <int KIND, bool GATED, bool LONG, bool BOXES>
 cudaError_t launch_kernel(const Maps& maps, const Params& p, cudaStream_t s) {
     const cudaError_t e = set_smem_limit_once<fused_kernel<KIND, GATED, LONG, BOXES>>(SMEM);
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg(2 * p.units, THREADS, SMEM, 2, s);
+    ClusterLaunch cfg(2 * p.units, Shape<KIND, GATED, BOXES>::THREADS, SMEM, 2, s);
     return cudaLaunchKernelEx(&cfg.config, fused_kernel<KIND, GATED, LONG, BOXES>, maps, p);
 }
 template <int KIND, bool GATED, bool LONG>
@@ -747,7 +734,7 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
     p.M = m.M;
     p.N = m.N;
     p.kblocks = (int)(((long)m.K + STAGE_K - 1) / STAGE_K);
-    p.part_blocks = fused_part_k(kind, e.c_f32) / STAGE_K;
+    p.part_blocks = FUSED_PART_K / STAGE_K;
     const int cols = two ? TILE / 2 : TILE;
     p.tiles_m = (int)(((long)m.M + TILE - 1) / TILE);
     p.tiles_n = (int)(((long)m.N + cols - 1) / cols);

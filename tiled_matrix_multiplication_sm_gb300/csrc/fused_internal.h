@@ -67,10 +67,12 @@ constexpr int FUSED_CE_COLS = 128;
 constexpr int FUSED_FEW_SETS = 4;
 constexpr int FUSED_FEW_RING = 209 * 1024;
 
-// Columns of K a part of a long sum covers. (A gradient's own result is BF16 and
-// only its column sums keep 32 bits: 2048. 8192 x 14336 x 4096 gated: 641 us, with
-// 1024 690, with one part 624; of db's norm it loses 1.2e-6, 0.7e-6, 2.2e-6.)
-inline int fused_part_k(FusedKind kind, bool c_f32) { return kind == FUSED_GRAD && !c_f32 ? 2048 : 1024; }
+// Columns of K a part of a long sum covers. A tile's last part holds its accumulator
+// until the epilogue is done, and the next tile's last part waits for it: 8192 x 14336 x
+// 4096 gated gradient 641 us, with parts of 1024 690, with one part 624. (Errors of
+// the FP32 result's norm: one part 0.55e-6 a 1024 columns, parts of 1024 0.7e-6, of 2048
+// 1.2e-6; an FP32 product in torch 0.2e-6 to 0.7e-6.)
+constexpr int FUSED_PART_K = 2048;
 
 // How a product runs: on SM pairs (fused_gemm.cu), or as few tiles (fused_few.cu).
 struct FusedPlan {

@@ -19,7 +19,7 @@ import torch
 
 from . import binding
 from .binding import TGEMM_OK, TGEMM_TRANS_A, TGEMM_TRANS_B, TgemmError, _stream_handle
-from .mx4 import TGEMM_TYPE_BF16, _check_matrix, _check_values, _empty, _type
+from .mx4 import TGEMM_TYPE_BF16, _TYPES, _check_matrix, _check_values, _empty, _type
 
 TGEMM_GATED = 4
 
@@ -103,6 +103,10 @@ def _operands(A, B, trans_a: bool, trans_b: bool, halves: int):
 
 def _like(x, name: str, rows: int, cols: int, index: int) -> Tuple[int, int]:
     """(leading dimension, TGEMM_TYPE_*) of a matrix of this shape on this device."""
+    if isinstance(x, torch.Tensor) and x.dtype in _TYPES and x.is_cuda and x.shape == (rows, cols) and x.get_device() == index:
+        ld, step = x.stride()                 # few steps, as in _bf16
+        if (step == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+            return max(ld, cols, 1), _TYPES[x.dtype]
     ld, kind = _check_values(x, name)
     if tuple(x.shape) != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(rows, cols)}")
