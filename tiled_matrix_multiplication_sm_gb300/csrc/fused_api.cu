@@ -62,21 +62,14 @@ struct Operand {
     }
     long padded() const { return ((long)cols + 63) / 64 * 64; }
     // The copy that lays it in its scratch (none: an empty one).
-    tgemm::RepackJob lay(const Scratch& scratch) {
-        tgemm::RepackJob job;
-        if (!copied) return job;
-        job = {x, ld, scratch.at(at), padded(), rows, cols};
+    tgemm::CopyJob lay(const Scratch& scratch) {
+        if (!copied) return tgemm::CopyJob{};
+        const tgemm::CopyJob job{x, ld, scratch.at(at), padded(), rows, cols, nullptr, 0, false};
         x = job.dst;
         ld = padded();
         return job;
     }
 };
-
-// Two operands' copies in one launch.
-cudaError_t lay(Operand& a, Operand& b, const Scratch& scratch, cudaStream_t s) {
-    if (!a.copied && !b.copied) return cudaSuccess;
-    return tgemm::repack_rows2(a.lay(scratch), b.lay(scratch), 2, s);
-}
 
 // A product's operands, checked; op(B) has `wide` columns, in `halves` halves.
 struct Operands {
@@ -120,9 +113,8 @@ cudaError_t run(const Operands& o, tgemm::FusedKind kind, FusedEpilogue& e, floa
     const size_t sums = scratch.add(db != nullptr ? (size_t)plan.sum_blocks * wide * sizeof(float) : 0);
     err = scratch.take();
     if (err != cudaSuccess) return err;
-    err = lay(a, b, scratch, s);
-    Operand none(nullptr, 0, 0, 0, scratch);
-    if (err == cudaSuccess && apart) err = lay(b2, none, scratch, s);
+    const tgemm::CopyJob jobs[3] = {a.lay(scratch), b.lay(scratch), b2.lay(scratch)};
+    err = tgemm::fused_copy_rows(jobs, 3, s);
     if (o.halves == 2 && !apart)
         b2.x = static_cast<const __nv_bfloat16*>(b.x) + (b_mn ? (long)o.N : (long)o.N * b.ld);
     if (db != nullptr) e.sums = static_cast<float*>(scratch.at(sums));
@@ -167,7 +159,8 @@ cudaError_t ce(int T, int V, int D, const void* X, long ldx, const void* W, long
     const size_t parts = scratch.add((size_t)turn * blocks * sizeof(float2)), picked = scratch.add((size_t)turn * sizeof(float));
     e = scratch.take();
     if (e != cudaSuccess) return e;
-    e = lay(x, w, scratch, s);
+    const tgemm::CopyJob jobs[2] = {x.lay(scratch), w.lay(scratch)};
+    e = tgemm::fused_copy_rows(jobs, 2, s);
     for (long t = 0; e == cudaSuccess && t < T; t += turn) {
         const int n = (int)(T - t < turn ? T - t : turn);
         FusedEpilogue ep;
@@ -206,15 +199,28 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     const bool sums = dX.x != nullptr && piece < V;          // dX over several pieces
     const long ldz = (piece + 63) / 64 * 64, ldk = ((long)D + 63) / 64 * 64;
     Scratch scratch(s);
-    Operand x(X, ldx, V == 0 ? 0 : T, D, scratch), w(W, ldw, T == 0 ? 0 : V, D, scratch);
+    // A dW takes X with the rows left out as zeros; the logits may take it too.
+    const bool keep = dW.x != nullptr && T > 0 && V > 0;
+    Operand x(X, ldx, V == 0 || keep ? 0 : T, D, scratch), w(W, ldw, T == 0 ? 0 : V, D, scratch);
     const size_t z_at = scratch.add((size_t)T * ldz * 2);
-    const size_t kept_at = scratch.add(dW.x != nullptr ? (size_t)T * ldk * 2 : 0);
-    const size_t sum_at = scratch.add(sums ? (size_t)T * ldk * 4 : 0);
-    cudaError_t e = scratch.take();
+    const size_t kept_at = scratch.add(keep ? (size_t)T * ldk * 2 : 0);
+    // Few tokens: dX, a sum over all of the vocabulary, in slices.
+    tgemm::FusedPlan slice{};
+    slice.slices = 1;
+    cudaError_t e = cudaSuccess;
+    if (dX.x != nullptr && T > 0 && piece == V && V > 0)
+        e = tgemm::fused_plan_slices(FusedProduct{T, D, V, nullptr, 0, false, nullptr, 0, true, nullptr}, sms, &slice);
     if (e != cudaSuccess) return e;
-    e = lay(x, w, scratch, s);
+    const size_t sum_at = scratch.add(sums ? (size_t)T * ldk * 4 : slice.slices > 1 ? (size_t)slice.slices * T * D * 4 : 0);
+    e = scratch.take();
+    if (e != cudaSuccess) return e;
     void *const z = scratch.at(z_at), *const kept = scratch.at(kept_at), *const sum = scratch.at(sum_at);
-    if (e == cudaSuccess && dW.x != nullptr && T > 0 && V > 0) e = tgemm::fused_keep_rows(X, ldx, kept, ldk, T, D, target, V, s);
+    const tgemm::CopyJob jobs[3] = {x.lay(scratch), w.lay(scratch), {X, ldx, kept, ldk, keep ? T : 0, D, target, V, false}};
+    e = tgemm::fused_copy_rows(jobs, 3, s);
+    if (keep) {
+        x.x = kept;
+        x.ld = ldk;
+    }
     for (long v = 0; e == cudaSuccess && (v < V || v == 0); v += piece > 0 ? piece : 1) {
         const int n = (int)(V - v < piece ? V - v : piece);
         const __nv_bfloat16* wv = static_cast<const __nv_bfloat16*>(w.x) + v * w.ld;
@@ -231,7 +237,17 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
             const FusedProduct p{T, n, D, x.x, x.ld, false, wv, w.ld, false, nullptr};
             e = product(tgemm::FUSED_CE_GRAD, p, ep, sms, s);
         }
-        if (e == cudaSuccess && dX.x != nullptr && T > 0) {
+        if (e == cudaSuccess && slice.slices > 1) {
+            FusedEpilogue ep;
+            ep.C = sum;
+            ep.ldc = D;
+            ep.c_f32 = true;
+            const FusedProduct p{T, D, n, z, ldz, false, wv, w.ld, true, nullptr};
+            e = tgemm::fused_gemm(tgemm::FUSED_ACT, p, ep, slice, sms, s);
+            if (e == cudaSuccess)
+                e = tgemm::fused_join_slices(static_cast<const float*>(sum), slice.slices, T, D, dX.x, dX.ld,
+                                             dX.type == TGEMM_TYPE_F32, s);
+        } else if (e == cudaSuccess && dX.x != nullptr && T > 0) {
             const bool last = v + piece >= V;
             FusedEpilogue ep;
             ep.C = last ? dX.x : sum;

@@ -47,7 +47,10 @@ struct Column {
     float b = 0.0f, b2 = 0.0f;                                   // bias
     float sum = 0.0f, sum2 = 0.0f;                               // GRAD: of this thread's rows
 
-    __device__ __forceinline__ Column(const FusedEpilogue& e_, long N_, int c_) : e(e_), N(N_), c(c_) {
+    const long shift;                                            // ACT: of C, in elements
+
+    __device__ __forceinline__ Column(const FusedEpilogue& e_, long N_, int c_, long shift_ = 0)
+        : e(e_), N(N_), c(c_), shift(shift_) {
         if (KIND == FUSED_ACT && e.bias != nullptr) {
             b = e.bias[c];
             if constexpr (TWO) b2 = e.bias[N + c];
@@ -153,7 +156,7 @@ struct Column {
                     x[j] = t >= 0 && t < e.vocabulary ? p * (e.alpha * e.dloss[row + j]) : 0.0f;
                 }
         }
-        const long at = row * e.ldc + c;
+        const long at = row * e.ldc + c + (KIND == FUSED_ACT && !GATED ? shift : 0);
         if (e.c_f32) {
             float* C = static_cast<float*>(e.C) + at;
 #pragma unroll

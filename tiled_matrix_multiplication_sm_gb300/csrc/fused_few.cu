@@ -11,7 +11,8 @@
 // SMs (14336 columns: 150 tiles of 96); the MMA's other rows multiply what lies
 // behind them in shared memory, and nobody reads them. Where that is not
 // enough, a cluster's blocks split K and add their shares through distributed
-// shared memory, in the order of their ranks.
+// shared memory, in the order of their ranks; a sum over a vocabulary, longer than that,
+// comes in slices, each to an FP32 matrix of its own.
 //
 // Eighteen warps: 0 copies (TMA, as many stages as fit), 1 issues the MMAs, the
 // others are the epilogue, four sets of four on a quarter of the tokens each. Two accumulators (gated: of two halves each). Long sums that end in
@@ -52,6 +53,7 @@ struct Params {
     int M, N, kblocks;
     int height, tokens;                              // of a tile: columns and rows of C
     int tiles_m, num_tiles, units, split;
+    int slices;                                      // of a tile's sum: num_tiles counts each
     int chunks, part_blocks;                         // chunks of K a stage, stages a part of a long sum
     int stages, half_bytes, stage_bytes;             // of a stage: one half of the weights, all
     int w_box, x_box;                                // K-major: a stage's chunks in one box
@@ -166,7 +168,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x % p.split, unit = blockIdx.x / p.split;
-    const int kb0 = (int)((long)p.kblocks * part / p.split), kb1 = (int)((long)p.kblocks * (part + 1) / p.split);
+    // A tile's row and column in C, and this block's stages of its sum: its share of
+    // the cluster's, or the tile's slice.
+    auto tile = [&](int t, int& row, int& col, int& kb0, int& kb1) {
+        const int n = p.split > 1 ? p.split : p.slices, i = p.split > 1 ? part : t % p.slices;
+        kb0 = (int)((long)p.kblocks * i / n);
+        kb1 = (int)((long)p.kblocks * (i + 1) / n);
+        t /= p.slices;
+        row = t % p.tiles_m * p.tokens;
+        col = t / p.tiles_m * p.height;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -202,7 +213,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         int s = 0;
         bool ok = true, stall = p.debug_stall != 0;            // test hook: the first stage is never filled
         for (int t = unit; ok && t < p.num_tiles; t += p.units) {
-            const int row = t % p.tiles_m * p.tokens, col = t / p.tiles_m * p.height;
+            int row, col, kb0, kb1;
+            tile(t, row, col, kb0, kb1);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
@@ -244,6 +256,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         int it = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
+        int row, col, kb0, kb1;
+        tile(unit, row, col, kb0, kb1);
         for (int t = unit, first = kb0; ok && t < p.num_tiles; ++it) {
             const int last = LONG ? min(first + p.part_blocks, kb1) : kb1;
             if (it >= 2)
@@ -277,8 +291,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             __syncwarp();
             first = last;
             if (last == kb1) {
-                first = kb0;
                 t += p.units;
+                tile(t, row, col, kb0, kb1);
+                first = kb0;
             }
         }
         if (elect_one()) tc_commit<false>(smem_u32(&sy->drain));
@@ -299,11 +314,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             if (lane == 31) mbar_arrive(smem_u32(&sy->tmem_empty[it & 1]));
         };
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
-            const int row = t % p.tiles_m * p.tokens, col = t / p.tiles_m * p.height;
+            int row, col, kb0, kb1;
+            tile(t, row, col, kb0, kb1);
             const int c = col + q * 32 + lane;
             const bool in = q * 32 + lane < p.height && c < p.N;
             // What the epilogue reads, while the sums are made: bias, and R or Z into L2.
-            Column<KIND, GATED> column(p.e, p.N, in ? c : 0);
+            Column<KIND, GATED> column(p.e, p.N, in ? c : 0, (long)(t % p.slices) * p.M * p.e.ldc);
             if (in) column.ask(row + begin + lane, min(p.M, row + end));
             bool ok = true;
             if constexpr (LONG) {
@@ -357,13 +373,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (q * 32 < p.height)
 #pragma unroll 1
                     for (int k = begin; k < end && row + k < p.M; k += 32)
-                        ce_tokens(p, acc + k, row + k, min(end - k, p.M - row - k), c, in, (long)(t / p.tiles_m) * ((p.height + 31) / 32) + q);
+                        ce_tokens(p, acc + k, row + k, min(end - k, p.M - row - k), c, in, (long)(col / p.height) * ((p.height + 31) / 32) + q);
             } else {
                 column.rows(row, begin, min(end, p.M - row), 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
-                    load_sums8(acc + k, x, p.kblocks);
-                    if constexpr (TWO) load_sums8(acc + p.acc + k, y, p.kblocks);
+                    load_sums8(acc + k, x, kb1 - kb0);
+                    if constexpr (TWO) load_sums8(acc + p.acc + k, y, kb1 - kb0);
                 });
-                if (in) column.leave((long)(t % p.tiles_m) * SETS + set);
+                if (in) column.leave((long)(row / p.tokens) * SETS + set);
                 __syncwarp();
             }
             release();
@@ -372,7 +388,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
     if (KIND != FUSED_CE && p.split > 1) {
         cluster_sync_all();
-        const int row = unit % p.tiles_m * p.tokens, col = unit / p.tiles_m * p.height;
+        int row, col, kb0, kb1;
+        tile(unit, row, col, kb0, kb1);
         const int q = warp & 3, set = (warp - 2) >> 2, c = col + q * 32 + lane;
         if (warp >= 2) {
             // Groups of eight tokens, in turn to the cluster's blocks and their sets.
@@ -392,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                 }
                             }
                         });
-            if (in) column.leave(((long)(unit % p.tiles_m) * p.split + part) * SETS + set);
+            if (in) column.leave(((long)(row / p.tokens) * p.split + part) * SETS + set);
         }
         __syncwarp();
         cluster_sync_all();           // no block leaves while another reads its share
@@ -454,7 +471,8 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     p.tokens = plan.tokens;
     p.split = plan.split;
     p.tiles_m = (m.M + p.tokens - 1) / p.tokens;
-    p.num_tiles = p.tiles_m * ((m.N + p.height - 1) / p.height);
+    p.slices = plan.slices;
+    p.num_tiles = p.tiles_m * ((m.N + p.height - 1) / p.height) * p.slices;
     p.units = p.split > 1 || p.num_tiles < num_sms ? p.num_tiles : num_sms;
     p.half_bytes = p.chunks * p.height * SW;
     p.stage_bytes = (two ? 2 : 1) * p.half_bytes + p.chunks * p.tokens * SW;
@@ -472,7 +490,7 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
                     !encode_operand(enc, &maps.W, m.B, m.ldb, m.N, m.K, m.b_mn, p.height, p.chunks, &p.w_box) ||
                     (two && !encode_operand(enc, &maps.W2, m.B2, m.ldb, m.N, m.K, m.b_mn, p.height, p.chunks, &p.w_box))))
         return cudaErrorInvalidValue;
-    const bool parts = p.kblocks > p.part_blocks * p.split;
+    const bool parts = p.kblocks > p.part_blocks * p.split * p.slices;
     switch (kind) {
         case FUSED_ACT:
             if (two) return launch<FUSED_ACT, true, false>(maps, p, s);

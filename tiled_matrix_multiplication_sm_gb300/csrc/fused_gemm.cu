@@ -348,8 +348,9 @@ __device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int ro
         float v[32];
         load_sums(acc + i, v, p.kblocks);
         const int c = col + i;
+        if (e.alpha != 1.0f)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= e.alpha;
+            for (int j = 0; j < 32; ++j) v[j] *= e.alpha;
         if (c + 32 > p.N)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = c + j < p.N ? v[j] : -INFINITY;
@@ -365,12 +366,14 @@ __device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int ro
         float top = m;
 #pragma unroll
         for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-        const float base = top == -INFINITY ? 0.0f : top;
+        // exp(v - top) as 2^(v L - c), c = top L rounded: one multiply-add each. What c is
+        // off by, exactly the remainder of that product, goes back into the sum.
+        const float base = top == -INFINITY ? 0.0f : top, at = base * LOG2E, off = fmaf(base, LOG2E, -at);
         s *= exp2_fast((m - base) * LOG2E);
         float q[4] = {};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) q[j & 3] += exp2_fast((v[j] - base) * LOG2E);
-        s += (q[0] + q[1]) + (q[2] + q[3]);
+        for (int j = 0; j < 32; ++j) q[j & 3] += exp2_fast(fmaf(v[j], LOG2E, -at));
+        s += ((q[0] + q[1]) + (q[2] + q[3])) * exp2_fast(-off);
         m = top;
     }
     if (in && col < p.N) e.parts[(long)(col / FUSED_CE_COLS) * p.M + row] = make_float2(m, s);
@@ -379,6 +382,8 @@ __device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int ro
 // 64 columns of the logits' gradient.
 __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
                                              int& box, float lse, float scale, long long target, bool kept) {
+    // (Rounded once a row: 2^-24 of the logit, far below BF16's rounding of the result.)
+    const float by = p.e.alpha * LOG2E, less = lse * LOG2E;
     const int lane = threadIdx.x & 31;
     uint8_t* buf = bufs + (box++ & 1) * BUF_BYTES;
     if (lane == 0) tma_store_wait_read<1>();
@@ -389,7 +394,7 @@ __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, 
         load_sums(acc + h * 32, v, p.kblocks);
         const long long t = target - (col + h * 32);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] * p.e.alpha - lse) * LOG2E);
+        for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], by, -less));
         if (__any_sync(~0u, t >= 0 && t < 32))
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] -= t == j ? 1.0f : 0.0f;

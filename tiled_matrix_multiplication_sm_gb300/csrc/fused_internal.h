@@ -79,12 +79,17 @@ struct FusedPlan {
     bool few;
     bool boxes;                          // pairs: fused_boxes
     int height, tokens, split, chunks;   // few: columns and rows of C a tile, blocks that share its sum, 64s of K a stage
+    int slices;                          // few: C comes as so many FP32 matrices of M x N, to be added up (1: as it is)
     long sum_blocks;                     // rows of FusedEpilogue::sums
     long ce_blocks;                      // of FusedEpilogue::parts
 };
 // Only the sizes and storage of the operands are read, and of the epilogue what
 // decides whether its matrices pass by TMA.
 cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan);
+
+// The plan of a plain FUSED_ACT product whose sum may come in slices (a long one, of
+// a C with few tiles).
+cudaError_t fused_plan_slices(const FusedProduct& p, int num_sms, FusedPlan* plan);
 
 // Whether C, R and Z pass by TMA on pairs, in boxes of 32 rows x 128 bytes: bases
 // and rows on 16 bytes, whole 16-byte pieces long (a store clipped inside such a
@@ -106,8 +111,20 @@ cudaError_t fused_join_sums(const float* sums, long blocks, long cols, float* db
 // loss and lse of T rows from their `blocks` maxima and sums.
 cudaError_t fused_join_ce(const float2* parts, const float* picked, const long long* target, int T, long V, long blocks,
                           float* loss, float* lse, cudaStream_t s);
-// X to Y (ldy), rows whose target is not in 0 .. V - 1 as zeros.
-cudaError_t fused_keep_rows(const void* X, long ldx, void* Y, long ldy, int T, int D, const long long* target, long V,
-                            cudaStream_t s);
+// out (ld, FP32 or BF16) = the sum of `slices` matrices, rows x cols each, FP32.
+cudaError_t fused_join_slices(const float* parts, int slices, int rows, int cols, void* out, long ld, bool f32, cudaStream_t s);
+// Copies of up to three BF16 matrices in one launch, to rows of whole 64 columns;
+// with `target`, rows whose target is not in 0 .. V - 1 as zeros.
+struct CopyJob {
+    const void* src;
+    long ld_src;
+    void* dst;
+    long ld_dst;
+    int rows, cols;
+    const long long* target;
+    long V;
+    bool wide;                    // set by fused_copy_rows
+};
+cudaError_t fused_copy_rows(const CopyJob* jobs, int count, cudaStream_t s);
 
 }  // namespace tgemm

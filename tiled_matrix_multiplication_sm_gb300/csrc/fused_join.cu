@@ -1,5 +1,5 @@
-// The small kernels beside the fused products: joining column sums and the
-// cross entropy's maxima and sums, and keeping the rows that count.
+// The small kernels beside the fused products: joining column sums, slices of a
+// sum and the cross entropy's maxima and sums; copies of operands.
 
 #include "fused_act.h"
 
@@ -87,22 +87,92 @@ join_ce_kernel(const float2* parts, const float* picked, const long long* target
     }
 }
 
+// out[i][j] = the sum of `slices` matrices of rows x cols. A block takes 32 elements;
+// its 8 warps take every eighth slice each and are added in their order (76 slices
+// of 56 x 170: 11 us a thread an element).
+template <typename T>
 __global__ void __launch_bounds__(256)
-keep_rows_kernel(const __nv_bfloat16* X, long ldx, __nv_bfloat16* Y, long ldy, int T, int D, const long long* target,
-                 long V, int wide) {
+join_slices_kernel(const float* parts, int slices, long size, int cols, T* out, long ld) {
     pdl_launch_dependents();
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long i = (long)blockIdx.x * 32 + lane;
     pdl_wait();
-    for (long row = blockIdx.x; row < T; row += gridDim.x) {
-        const long long t = target[row];
-        const bool kept = t >= 0 && t < V;
-        const __nv_bfloat16* x = X + row * ldx;
-        __nv_bfloat16* y = Y + row * ldy;
-        if (wide) {
-            for (int c = threadIdx.x * 8; c < D; c += 256 * 8)
-                *reinterpret_cast<uint4*>(y + c) = kept ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
-        } else {
-            for (int c = threadIdx.x; c < D; c += 256) y[c] = kept ? x[c] : __float2bfloat16(0.0f);
+    float v = 0.0f;
+    if (i < size)
+#pragma unroll 8
+        for (int s = warp; s < slices; s += 8) v += parts[s * size + i];
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && i < size) {
+#pragma unroll
+        for (int w = 1; w < 8; ++w) v += part[w][lane];
+        const long row = i / cols;
+        out[row * ld + (i - row * cols)] = (T)v;
+    }
+}
+
+// Copies of matrices with rows off 16 bytes, and of rows that count. A warp takes
+// four rows at a time, so that narrow ones keep it as busy as wide ones (59871 x 170:
+// 34 us a row at a time), of 512 columns at most, two columns a lane; rows on 16 bytes
+// go eight columns a lane.
+struct Copies {
+    CopyJob job[3];
+    long blocks[3];               // up to and with each job's
+};
+constexpr int COPY_ROWS = 4, COPY_WARPS = 8, COPY_COLS = 512;
+
+__global__ void __launch_bounds__(32 * COPY_WARPS) copy_rows_kernel(const Copies c) {
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int which = (long)blockIdx.x < c.blocks[0] ? 0 : (long)blockIdx.x < c.blocks[1] ? 1 : 2;
+    const CopyJob j = c.job[which];
+    const long block = (long)blockIdx.x - (which > 0 ? c.blocks[which - 1] : 0);
+    const long across = (j.cols + COPY_COLS - 1) / COPY_COLS;
+    const long row0 = (block / across * COPY_WARPS + (threadIdx.x >> 5)) * COPY_ROWS;
+    const int first = (int)(block % across) * COPY_COLS, cols = min(j.cols, first + COPY_COLS);
+    const __nv_bfloat16 zero = __float2bfloat16(0.0f);
+    pdl_wait();
+    const __nv_bfloat16* from[COPY_ROWS];
+    bool kept[COPY_ROWS];
+#pragma unroll
+    for (int r = 0; r < COPY_ROWS; ++r) {
+        const long row = row0 + r;
+        kept[r] = row < j.rows;
+        if (kept[r] && j.target != nullptr) {
+            const long long t = j.target[row];
+            kept[r] = t >= 0 && t < j.V;
         }
+        from[r] = static_cast<const __nv_bfloat16*>(j.src) + row * j.ld_src;
+    }
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(j.dst) + row0 * j.ld_dst;
+    if (j.wide) {
+        for (int c0 = first + lane * 8; c0 < cols; c0 += 256) {
+            uint4 v[COPY_ROWS];
+#pragma unroll
+            for (int r = 0; r < COPY_ROWS; ++r)
+                v[r] = kept[r] ? *reinterpret_cast<const uint4*>(from[r] + c0) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < COPY_ROWS; ++r)
+                if (row0 + r < j.rows) *reinterpret_cast<uint4*>(to + r * j.ld_dst + c0) = v[r];
+        }
+        return;
+    }
+    for (int c0 = first + lane * 2; c0 < cols; c0 += 128) {
+        __nv_bfloat16 v[COPY_ROWS][2][2];
+#pragma unroll
+        for (int r = 0; r < COPY_ROWS; ++r)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) v[r][u][k] = kept[r] && c0 + u * 64 + k < cols ? from[r][c0 + u * 64 + k] : zero;
+        // (Rows of the copy hold whole 64 columns.)
+#pragma unroll
+        for (int r = 0; r < COPY_ROWS; ++r)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (row0 + r < j.rows && c0 + u * 64 < cols)
+                    *reinterpret_cast<__nv_bfloat162*>(to + r * j.ld_dst + c0 + u * 64) = __nv_bfloat162(v[r][u][0], v[r][u][1]);
     }
 }
 
@@ -122,12 +192,30 @@ cudaError_t fused_join_ce(const float2* parts, const float* picked, const long l
                       blocks, rows, loss, lse);
 }
 
-cudaError_t fused_keep_rows(const void* X, long ldx, void* Y, long ldy, int T, int D, const long long* target, long V,
-                            cudaStream_t s) {
-    // Whole 16-byte pieces of both rows.
-    const int wide = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldy % 8 == 0 && D % 8 == 0 ? 1 : 0;
-    return launch_pdl(keep_rows_kernel, dim3((unsigned)(T < 4096 ? T : 4096)), dim3(256), 0, s,
-                      static_cast<const __nv_bfloat16*>(X), ldx, static_cast<__nv_bfloat16*>(Y), ldy, T, D, target, V, wide);
+cudaError_t fused_join_slices(const float* parts, int slices, int rows, int cols, void* out, long ld, bool f32, cudaStream_t s) {
+    const long size = (long)rows * cols;
+    const dim3 grid((unsigned)((size + 31) / 32));
+    return f32 ? launch_pdl(join_slices_kernel<float>, grid, dim3(256), 0, s, parts, slices, size, cols, static_cast<float*>(out), ld)
+               : launch_pdl(join_slices_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, parts, slices, size, cols,
+                            static_cast<__nv_bfloat16*>(out), ld);
+}
+
+cudaError_t fused_copy_rows(const CopyJob* jobs, int count, cudaStream_t s) {
+    Copies c = {};
+    long blocks = 0;
+    int n = 0;
+    for (int i = 0; i < count; ++i) {
+        if (jobs[i].rows <= 0 || jobs[i].cols <= 0) continue;
+        c.job[n] = jobs[i];
+        c.job[n].wide = reinterpret_cast<uintptr_t>(jobs[i].src) % 16 == 0 && jobs[i].ld_src % 8 == 0 && jobs[i].cols % 8 == 0;
+        blocks += ((long)jobs[i].rows + COPY_ROWS * COPY_WARPS - 1) / (COPY_ROWS * COPY_WARPS) *
+                  (((long)jobs[i].cols + COPY_COLS - 1) / COPY_COLS);
+        c.blocks[n++] = blocks;
+    }
+    if (n == 0) return cudaSuccess;
+    if (blocks > 2147483647L) return cudaErrorInvalidValue;
+    for (int i = n; i < 3; ++i) c.blocks[i] = blocks;
+    return launch_pdl(copy_rows_kernel, dim3((unsigned)blocks), dim3(32 * COPY_WARPS), 0, s, c);
 }
 
 }  // namespace tgemm

@@ -74,10 +74,15 @@ bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e) {
     }
 }
 
-cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan) {
+namespace {
+
+// fused_plan, with its estimate of the time (0: not made).
+cudaError_t make_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan, double* us) {
+    *us = 0.0;
     const int halves = kind == FUSED_ACT && e.gated ? 2 : 1;
     plan->few = false;
     plan->height = plan->tokens = plan->split = plan->chunks = 0;
+    plan->slices = 1;
     plan->boxes = fused_boxes(kind, p.N, e);
     plan->sum_blocks = up(p.M, FUSED_SUM_ROWS);
     plan->ce_blocks = up(p.N, FUSED_CE_COLS);
@@ -114,9 +119,9 @@ cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogu
                 if (p.b_mn) height = up(height, 64) * 64;
                 if (c > 1 && tiles_m * up(p.N, height) > units) continue;
                 const Tiles tiles{(int)height, t, c, chunks_for(height * halves + t, p.K)};
-                const double us = few_us(p.M, p.N, p.K, halves, tiles, (int)units);
-                if (us < best) {
-                    best = us;
+                const double t_us = few_us(p.M, p.N, p.K, halves, tiles, (int)units);
+                if (t_us < best) {
+                    best = t_us;
                     plan->few = true;
                     plan->height = tiles.height;
                     plan->tokens = tiles.tokens;
@@ -126,9 +131,43 @@ cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogu
             }
         }
     }
+    *us = best;
     if (plan->few) {
         plan->sum_blocks = up(p.M, plan->tokens) * plan->split * FUSED_FEW_SETS;
         plan->ce_blocks = up(p.N, plan->height) * up(plan->height, 32);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t fused_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue& e, int num_sms, FusedPlan* plan) {
+    double us;
+    return make_plan(kind, p, e, num_sms, plan, &us);
+}
+
+cudaError_t fused_plan_slices(const FusedProduct& p, int num_sms, FusedPlan* plan) {
+    double best;
+    const cudaError_t err = make_plan(FUSED_ACT, p, FusedEpilogue(), num_sms, plan, &best);
+    if (err != cudaSuccess || best == 0.0) return err;
+    const int whole = (int)up(p.M, 16) * 16, tokens[3] = {64, 128, 256};
+    for (int t : tokens) {
+        if (!p.a_mn && t > whole) t = whole;
+        const int height = p.b_mn && p.N <= 64 ? 64 : 128;
+        const long tiles = up(p.M, t) * up(p.N, height);
+        const long slices = num_sms / tiles < up(p.K, 1024) ? num_sms / tiles : up(p.K, 1024);
+        if (slices < 2) continue;
+        const Tiles shape{height, t, 1, chunks_for(height + t, p.K)};
+        // A slice's time, and adding them up: a launch, and their bytes twice.
+        const double us = few_us(p.M, p.N, (int)up(p.K, slices), 1, shape, (int)tiles) + 4.0 + 8.0 * slices * p.M * p.N / HBM;
+        if (us > 0.95 * best) continue;
+        best = us;
+        plan->few = true;
+        plan->height = height;
+        plan->tokens = t;
+        plan->split = 1;
+        plan->slices = (int)slices;
+        plan->chunks = shape.chunks;
     }
     return cudaSuccess;
 }
