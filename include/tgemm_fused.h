@@ -15,10 +15,11 @@
  * but for what an entry says.
  *
  * Sums of products are FP32: on the tensor cores, which cut low bits off at
- * every step, up to 2048 columns of K where a result keeps 32 bits (an FP32 C,
- * db, loss and lse); longer ones are then made of such parts, added with
- * rounding to nearest. Values go from the sum to the result in FP32 and are
- * rounded once, to nearest even, where the result is BF16.
+ * every step. Where a result keeps 32 bits long sums are made of parts, added
+ * with rounding to nearest, so that it is off by 1e-6 of its norm or less (an
+ * FP32 C: parts of up to 1664 columns of K; db: 1152; loss and lse: 448). Values
+ * go from the sum to the result in FP32 and are rounded once, to nearest even,
+ * where the result is BF16.
  *
  * Activations, act(z):
  *   TGEMM_ACT_NONE       z

@@ -464,8 +464,8 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     Params p;
     p.M = m.M;
     p.N = m.N;
-    p.chunks = plan.chunks;
-    p.part_blocks = FUSED_PART_K / CHUNK_K / p.chunks;
+    p.chunks = kind == FUSED_CE && plan.chunks > 2 ? 2 : plan.chunks;     // (a part's 128 columns)
+    p.part_blocks = fused_parts(kind, true, (m.K - 1) / (plan.split * plan.slices) + 1, CHUNK_K * p.chunks).rest;
     p.kblocks = (int)(((long)m.K + p.chunks * CHUNK_K - 1) / (p.chunks * CHUNK_K));
     p.height = plan.height;
     p.tokens = plan.tokens;

@@ -14,9 +14,10 @@
 // Gated products take 128 columns of g (the pair's first block) and the same 128
 // of u (its second) for a tile, so that a thread holds both of a row.
 //
-// Sums of more than FUSED_PART_K columns that end in 32 bits (LONG) come in parts,
-// accumulator by accumulator; the epilogue's warps add them up in registers
-// and put the total back where the last part lay.
+// Sums of more than a part's columns that end in 32 bits (LONG) come in parts,
+// accumulator by accumulator; the epilogue's warps add them up in registers and
+// work from there where they can, so that accumulators are free as soon as they
+// are read.
 //
 // A thread has a row of the tile. Where C, R and Z allow TMA, boxes of 32 rows x
 // 128 bytes pass between its registers and memory through shared memory; where
@@ -68,7 +69,7 @@ static_assert(sizeof(Sync) <= 512, "barrier block");
 struct Params {
     int M, N, kblocks;
     int tiles_n, num_tiles, units, group_m, tiles_m;
-    int part_blocks;            // stages a part of a long sum
+    FusedParts part;
     int a_mn, b_mn;
     int bias4;                  // bias in pieces of 16 bytes
     FusedEpilogue e;
@@ -211,10 +212,11 @@ __device__ __forceinline__ void load_boxes(const Params& p, const Maps* maps, ui
     if (two) tma_load_2d<false>(b1, wide ? &maps->E[1] : &maps->E[3], wide ? col + 32 : col, row0, bar);
 }
 
-// 64 columns of C from column `col` on. `acc`: their sums; acc2: gated ACT, u's.
-// The buffers are free; the boxes that load_boxes asked for are in them.
-template <int KIND, bool GATED, typename Release>
-__device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, uint32_t acc2,
+// 64 columns of C from column `col` on. sums(h, v) gives half h's sums; acc2: gated
+// ACT, u's in tensor memory. The buffers are free; the boxes that load_boxes asked
+// for are in them.
+template <int KIND, bool GATED, typename Sums, typename Release>
+__device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, uint8_t* bufs, Sums sums, uint32_t acc2,
                                            int row0, int rows, int col, int& box, Release release) {
     const FusedEpilogue& e = p.e;
     const int lane = threadIdx.x & 31;
@@ -235,7 +237,7 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
             // Both halves of Z leave first, through both buffers.
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                load_sums(acc + h * 32, v, p.kblocks);
+                sums(h, v);
                 add_bias(p, e.bias, col + h * 32, v);
                 put_bf16(b0, h, v);
                 load_sums(acc2 + h * 32, v, p.kblocks);
@@ -250,7 +252,7 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int c = col + h * 32;
-        load_sums(acc + h * 32, v, p.kblocks);
+        sums(h, v);
         if constexpr (KIND == FUSED_ACT) {
             add_bias(p, e.bias, c, v);
             if constexpr (GATED) {
@@ -336,18 +338,21 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
 }
 
 // ------------------------------------------------------------ cross entropy
-// The maximum of this thread's row over the set's 128 columns and the sum of
-// exp(z - maximum); the target's logit where it is among them.
-__device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int row, int col) {
-    const FusedEpilogue& e = p.e;
-    const bool in = row < p.M;
-    const long long target = in ? e.target[row] - e.first : -1;
+// The maximum of this thread's row over its set's columns and the sum of exp(z -
+// maximum), taken 32 columns at a time; the target's logit where it is among them.
+struct CeRow {
+    const Params& p;
+    const int row;
+    const bool in;
+    const long long target;
     float m = -INFINITY, s = 0.0f;
-#pragma unroll 1
-    for (int i = 0; i < FUSED_CE_COLS; i += 32) {
-        float v[32];
-        load_sums(acc + i, v, p.kblocks);
-        const int c = col + i;
+
+    __device__ __forceinline__ CeRow(const Params& p_, int row_)
+        : p(p_), row(row_), in(row_ < p_.M), target(row_ < p_.M ? p_.e.target[row_] - p_.e.first : -1) {}
+
+    // The logits of columns c .. c + 31.
+    __device__ __forceinline__ void add(int c, float (&v)[32]) {
+        const FusedEpilogue& e = p.e;
         if (e.alpha != 1.0f)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= e.alpha;
@@ -366,7 +371,7 @@ __device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int ro
         float top = m;
 #pragma unroll
         for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-        // exp(v - top) as 2^(v L - c), c = top L rounded: one multiply-add each. What c is
+        // exp(v - top) as 2^(v L - at), at = top L rounded: one multiply-add each. What at is
         // off by, exactly the remainder of that product, goes back into the sum.
         const float base = top == -INFINITY ? 0.0f : top, at = base * LOG2E, off = fmaf(base, LOG2E, -at);
         s *= exp2_fast((m - base) * LOG2E);
@@ -376,8 +381,11 @@ __device__ __forceinline__ void ce_columns(const Params& p, uint32_t acc, int ro
         s += ((q[0] + q[1]) + (q[2] + q[3])) * exp2_fast(-off);
         m = top;
     }
-    if (in && col < p.N) e.parts[(long)(col / FUSED_CE_COLS) * p.M + row] = make_float2(m, s);
-}
+
+    __device__ __forceinline__ void leave(int col) const {
+        if (in && col < p.N) p.e.parts[(long)(col / FUSED_CE_COLS) * p.M + row] = make_float2(m, s);
+    }
+};
 
 // 64 columns of the logits' gradient.
 __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
@@ -415,6 +423,11 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& mb, int& nb
     const int gm = min(p.tiles_m - first, p.group_m);
     mb = first + t % per_group % gm;
     nb = t % per_group / gm;
+}
+
+// The end of the part that begins at stage `first`.
+__device__ __forceinline__ int part_end(const Params& p, int first) {
+    return min(first + (first < 2 * p.part.first ? p.part.first : p.part.rest), p.kblocks);
 }
 
 // BOXES: C, R and Z pass by TMA (fused_boxes).
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             bool ok = true;
             // A tile's sum, or of LONG ones each part in turn: first to last - 1.
             for (int t = unit, first = 0; ok && t < p.num_tiles; ++it) {
-                const int last = LONG ? min(first + p.part_blocks, p.kblocks) : p.kblocks;
+                const int last = LONG ? part_end(p, first) : p.kblocks;
                 if (it >= 2)
                     if (!__all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait)))
                         break;
@@ -572,6 +585,10 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
         const uint32_t loaded = smem_u32(&sy->loaded[(warp - 2) & 7]);
         const bool loads = BOXES && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
         constexpr int SET_COLS = TC / S::SETS, TURNS = SET_COLS / 64;
+        // A long sum's total stays in registers (HELD), or goes back to where its last
+        // part lay (BACK): with a column a lane a warp's registers are few, and a copy of the
+        // epilogue for each 32 of them cost more (3000 x 5001 x 1537 in two parts 121 us for 95).
+        constexpr bool BACK = LONG && !BOXES && KIND != FUSED_CE, HELD = LONG && !BACK;
         int it = 0, box = 0;
         uint32_t load_ph = 0;
         bool loading = false;                                  // boxes asked for and not waited for
@@ -598,16 +615,19 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
                 if (loads && rows > 0 && col0 < p.N) ask(col0);
 
+            const uint32_t lanes = (uint32_t)(q * 32) << 16;
+            auto accumulator = [&]() { return tmem_base + (uint32_t)(it & 1) * TILE + lanes + set * SET_COLS; };
             bool ok = true;
+            float sum[LONG ? SET_COLS / 32 : 1][32] = {};
             if constexpr (LONG) {
-                float sum[SET_COLS / 32][32] = {};
                 #pragma unroll 1
-                for (int first = 0; ok && first < p.kblocks; first += p.part_blocks) {
+                for (int first = 0; first < p.kblocks;) {
                     ok = __all_sync(~0u, mbar_wait<true, true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * SET_COLS;
-                    const bool final = first + p.part_blocks >= p.kblocks;
+                    const uint32_t acc = accumulator();
+                    first = part_end(p, first);
+                    const bool final = first == p.kblocks;
 #pragma unroll
                     for (int i = 0; i < SET_COLS / 32; ++i) {
 #pragma unroll
@@ -618,23 +638,42 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
 #pragma unroll
                             for (int j = 0; j < 16; ++j) sum[i][c + j] += __uint_as_float(r[j]);
                         }
-                        if (final) tmem_st32(acc + i * 32, reinterpret_cast<uint32_t (&)[32]>(sum[i]));
+                        if (BACK && final) tmem_st32(acc + i * 32, reinterpret_cast<uint32_t (&)[32]>(sum[i]));
                     }
-                    if (!final) {
-                        release();
-                        ++it;
-                    }
+                    if (!BACK || !final) release();
+                    if (!final) ++it;
                 }
-                if (ok) tmem_wait_st();
+                if (BACK && ok) tmem_wait_st();
             } else {
                 ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
                 tc_fence_after();
             }
             if (!ok) break;
-            const uint32_t acc = tmem_base + (uint32_t)(it & 1) * TILE + ((uint32_t)(q * 32) << 16) + set * SET_COLS;
+            const uint32_t acc = accumulator();
+            // Columns 32 i .. 32 i + 31 of the set's.
+            auto sums = [&](int i, float (&v)[32]) {
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = sum[i][j];
+                } else {
+                    load_sums(acc + i * 32, v, p.kblocks);
+                }
+            };
             if constexpr (KIND == FUSED_CE) {
-                ce_columns(p, acc, row0 + lane, col0);
-                release();
+                CeRow ce(p, row0 + lane);
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int i = 0; i < SET_COLS / 32; ++i) ce.add(col0 + i * 32, sum[i]);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < SET_COLS / 32; ++i) {
+                        float v[32];
+                        sums(i, v);
+                        ce.add(col0 + i * 32, v);
+                    }
+                    release();
+                }
+                ce.leave(col0);
             } else {
                 // Of this thread's row (CE_GRAD).
                 long long target = -1;
@@ -644,43 +683,51 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                     lse = p.e.lse[row0 + lane];
                     scale = p.e.alpha * p.e.dloss[row0 + lane];
                 }
-#pragma unroll 1
-                for (int i = 0; i < TURNS; ++i) {
+                // 64 columns of the set's; false: a wait ran out.
+                auto turn = [&](int i) {
                     const int col = col0 + i * 64;
-                    const bool last = i == TURNS - 1;
+                    auto done = [&]() {
+                        if (!HELD && i == TURNS - 1) release();
+                    };
                     if (rows <= 0 || col >= p.N) {
-                        if (last) release();
-                        continue;
+                        done();
+                        return true;
                     }
-                    if constexpr (BOXES) {
-                        if constexpr (KIND == FUSED_CE_GRAD) {
-                            ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col, box, lse, scale, target - p.e.first,
-                                         target >= 0 && target < p.e.vocabulary);
-                            if (last) release();
-                        } else {
-                            if (i > 0 && loads) ask(col);
-                            if (loading) {
-                                ok = __all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait));
-                                if (!ok) break;
-                                load_ph ^= 1u;
-                                loading = false;
-                            } else if (KIND == FUSED_ACT && p.e.Z != nullptr) {
-                                if (lane == 0) tma_store_wait_read<0>();
-                                __syncwarp();
-                            }
-                            turn_boxes<KIND, GATED>(p, &maps, bufs, acc + i * 64, acc + 128 + i * 64, row0, rows, col, box,
-                                                    [&]() { if (last) release(); });
+                    if constexpr (KIND == FUSED_CE_GRAD) {
+                        ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col, box, lse, scale, target - p.e.first,
+                                     target >= 0 && target < p.e.vocabulary);
+                        done();
+                    } else if constexpr (BOXES) {
+                        if (i > 0 && loads) ask(col);
+                        if (loading) {
+                            if (!__all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait))) return false;
+                            load_ph ^= 1u;
+                            loading = false;
+                        } else if (KIND == FUSED_ACT && p.e.Z != nullptr) {
+                            if (lane == 0) tma_store_wait_read<0>();
+                            __syncwarp();
                         }
+                        turn_boxes<KIND, GATED>(p, &maps, bufs, [&](int h, float (&v)[32]) { sums(i * 2 + h, v); }, acc + 128 + i * 64,
+                                                row0, rows, col, box, done);
                     } else {
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
+                        auto half = [&](int h) {
                             float v[32], w[32];
-                            load_sums(acc + i * 64 + h * 32, v, p.kblocks);
+                            sums(i * 2 + h, v);
                             if constexpr (TWO) load_sums(acc + 128 + i * 64 + h * 32, w, p.kblocks);
-                            if (last && h == 1) release();
+                            if (h == 1) done();
                             store_columns<KIND, GATED>(p, bufs, row0, rows, col + h * 32, v, w);
-                        }
+                        };
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) half(h);
                     }
+                    return true;
+                };
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) ok = ok && turn(i);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; ok && i < TURNS; ++i) ok = turn(i);
                 }
                 if (!ok) break;
             }
@@ -739,7 +786,7 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
     p.M = m.M;
     p.N = m.N;
     p.kblocks = (int)(((long)m.K + STAGE_K - 1) / STAGE_K);
-    p.part_blocks = FUSED_PART_K / STAGE_K;
+    p.part = fused_parts(kind, false, m.K, STAGE_K);
     const int cols = two ? TILE / 2 : TILE;
     p.tiles_m = (int)(((long)m.M + TILE - 1) / TILE);
     p.tiles_n = (int)(((long)m.N + cols - 1) / cols);
@@ -776,7 +823,7 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
         }
         if (!ok) return cudaErrorInvalidValue;
     }
-    const bool parts = p.kblocks > p.part_blocks;
+    const bool parts = p.kblocks > p.part.first;
     switch (kind) {
         case FUSED_ACT:
             if (two) return launch<FUSED_ACT, true, false>(maps, p, boxes, s);

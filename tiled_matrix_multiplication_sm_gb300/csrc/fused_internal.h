@@ -67,12 +67,22 @@ constexpr int FUSED_CE_COLS = 128;
 constexpr int FUSED_FEW_SETS = 4;
 constexpr int FUSED_FEW_RING = 209 * 1024;
 
-// Columns of K a part of a long sum covers. A tile's last part holds its accumulator
-// until the epilogue is done, and the next tile's last part waits for it: 8192 x 14336 x
-// 4096 gated gradient 641 us, with parts of 1024 690, with one part 624. (Errors of
-// the FP32 result's norm: one part 0.55e-6 a 1024 columns, parts of 1024 0.7e-6, of 2048
-// 1.2e-6; an FP32 product in torch 0.2e-6 to 0.7e-6.)
-constexpr int FUSED_PART_K = 2048;
+// Long sums come in parts where the result keeps 32 bits, in stages of so many
+// columns of K: `first` stages for the first two parts, `rest` for the others.
+//
+// A part of n stages of 64 loses n / 16 x 0.55e-6 of an FP32 C's norm, 0.99e-6 of a
+// gradient's column sums; parts of n_i, the mean of n_i weighted by n_i. An FP32
+// product in torch loses 0.2e-6 to 0.7e-6 in all. So C comes in parts of 21 (one of
+// up to 26: 0.96e-6), column sums in a weighted mean of 14.5. A loss is a small
+// difference of large logits: parts of 7, for few tokens of 2 (0.8e-6, 0.3e-6).
+//
+// On pairs the MMAs are two parts ahead of the epilogue at most, and that of a
+// gated gradient takes 9 us, the time of 34 stages: the first two parts are
+// longer (8192 x 14336 x 4096: 711 us in parts of 13, one part 618).
+struct FusedParts {
+    int first, rest;
+};
+FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k);
 
 // How a product runs: on SM pairs (fused_gemm.cu), or as few tiles (fused_few.cu).
 struct FusedPlan {

@@ -59,6 +59,29 @@ double pair_us(int M, long N, int K, int halves, int pairs) {
 
 }  // namespace
 
+FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
+    const int stages = (int)up(K, chunk_k), scale = chunk_k / 64 > 0 ? chunk_k / 64 : 1;
+    auto even = [&](int most) {
+        most = most / scale > 0 ? most / scale : 1;
+        const int n = stages > 0 ? (int)up(stages, up(stages, most)) : 1;
+        return FusedParts{n, n};
+    };
+    if (kind == FUSED_CE) return even(few ? 2 : 7);
+    if (kind != FUSED_GRAD) return stages * scale <= 26 ? FusedParts{stages, stages} : even(21);
+    if (few || stages <= 28) return even(14);
+    for (int first = 18; first > 14; --first) {
+        const int left = stages - 2 * first;
+        if (left < 1) continue;
+        for (int most = 14; most >= 8; --most) {
+            const int parts = (int)up(left, most), rest = (int)up(left, parts);
+            const double squares = 2.0 * first * first + (double)rest * rest * (parts - 1) +
+                                   (double)(left - rest * (parts - 1)) * (left - rest * (parts - 1));
+            if (squares <= 14.5 * stages) return {first, rest};
+        }
+    }
+    return even(14);
+}
+
 bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e) {
     auto fits = [&](const void* x, long ld, bool f32) {
         const int size = f32 ? 4 : 2;
