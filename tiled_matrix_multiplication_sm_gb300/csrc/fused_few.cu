@@ -130,14 +130,15 @@ __device__ __forceinline__ float across(const float (&from)[32], Op op) {
     return v[0];
 }
 
-// `n` (up to 32) tokens from `row` on against this warp's vocabulary entries, `c` this lane's
+// `n` (up to 32) tokens from `row` on, whose sums sums(v) gives, against this warp's vocabulary entries, `c` this lane's
 // (`in`: it is one): the maximum and the sum of exp(z - maximum) of each token, as
 // entry `block` of what fused_join_ce joins, and the target's logit.
-__device__ __forceinline__ void ce_tokens(const Params& p, uint32_t acc, int row, int n, int c, bool in, long block) {
+template <typename Sums>
+__device__ __forceinline__ void ce_tokens(const Params& p, Sums sums, int row, int n, int c, bool in, long block) {
     const FusedEpilogue& e = p.e;
     const int lane = threadIdx.x & 31;
     float v[32];
-    load_sums(acc, v, p.kblocks);
+    sums(v);
     const bool token = lane < n;
     // Where the target of token `lane` is among the warp's entries: its lane.
     const long long t = token ? e.target[row + lane] - (c - lane) : -1;
@@ -322,7 +323,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             Column<KIND, GATED> column(p.e, p.N, in ? c : 0, (long)(t % p.slices) * p.M * p.e.ldc);
             if (in) column.ask(row + begin + lane, min(p.M, row + end));
             bool ok = true;
+            const uint32_t lanes = (uint32_t)(q * 32) << 16;
             if constexpr (LONG) {
+                // (The total aside, in columns of its own, so that the last part's are free at
+                // once: no gain.)
                 constexpr int MOST = 256 / SETS / 8;
                 float sum[MOST][8] = {};
                 #pragma unroll 1
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     ok = __all_sync(~0u, mbar_wait<true, false, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t acc = tmem_base + (uint32_t)((it & 1) * p.acc) + ((uint32_t)(q * 32) << 16) + begin;
+                    const uint32_t acc = tmem_base + (uint32_t)((it & 1) * p.acc) + lanes + begin;
                     const bool final = first + p.part_blocks >= kb1;
 #pragma unroll
                     for (int i = 0; i < MOST; ++i)
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 tc_fence_after();
             }
             if (!ok) break;
-            const uint32_t acc = tmem_base + (uint32_t)((it & 1) * HALVES * p.acc) + ((uint32_t)(q * 32) << 16);
+            const uint32_t acc = tmem_base + (uint32_t)((it & 1) * HALVES * p.acc) + lanes;
             if (p.split > 1) {
                 // The tile's copies and MMAs are done: its stages hold the share,
                 // a row of 128 columns a token.
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (q * 32 < p.height)
 #pragma unroll 1
                     for (int k = begin; k < end && row + k < p.M; k += 32)
-                        ce_tokens(p, acc + k, row + k, min(end - k, p.M - row - k), c, in, (long)(col / p.height) * ((p.height + 31) / 32) + q);
+                        ce_tokens(p, [&](float (&v)[32]) { load_sums(acc + k, v, p.kblocks); }, row + k, min(end - k, p.M - row - k), c, in, (long)(col / p.height) * ((p.height + 31) / 32) + q);
             } else {
                 column.rows(row, begin, min(end, p.M - row), 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
                     load_sums8(acc + k, x, kb1 - kb0);
@@ -386,12 +390,32 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
     }
 
-    if (KIND != FUSED_CE && p.split > 1) {
+    if (p.split > 1) {
         cluster_sync_all();
         int row, col, kb0, kb1;
         tile(unit, row, col, kb0, kb1);
         const int q = warp & 3, set = (warp - 2) >> 2, c = col + q * 32 + lane;
-        if (warp >= 2) {
+        // A column's share of token k, from block i.
+        auto share = [&](int i, int k) { return map_to_rank(stage0, (uint32_t)i) + (uint32_t)((k * 128 + q * 32 + lane) * 4); };
+        if (KIND == FUSED_CE && warp >= 2 && q * 32 < p.height) {
+            // Groups of 32 tokens, in turn to the cluster's blocks and their sets. (Rows
+            // past the tile's are other memory of the stages, and not used.)
+#pragma unroll 1
+            for (int k = (part * SETS + set) * 32; k < p.tokens && row + k < p.M; k += SETS * 32 * p.split)
+                ce_tokens(p,
+                          [&](float (&v)[32]) {
+#pragma unroll
+                              for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll 1
+                              for (int i = 0; i < p.split; ++i) {
+                                  const uint32_t from = share(i, k);
+#pragma unroll
+                                  for (int j = 0; j < 32; ++j) v[j] += ld_cluster(from + j * 512);
+                              }
+                          },
+                          row + k, min(p.tokens - k, p.M - row - k), c, q * 32 + lane < p.height && c < p.N,
+                          (long)(col / p.height) * ((p.height + 31) / 32) + q);
+        } else if (KIND != FUSED_CE && warp >= 2) {
             // Groups of eight tokens, in turn to the cluster's blocks and their sets.
             const bool in = q * 32 + lane < p.height && c < p.N;
             Column<KIND, GATED> column(p.e, p.N, in ? c : 0);
@@ -401,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
 #pragma unroll 4
                             for (int i = 0; i < p.split; ++i) {
-                                const uint32_t from = map_to_rank(stage0, (uint32_t)i) + (uint32_t)((k * 128 + q * 32 + lane) * 4);
+                                const uint32_t from = share(i, k);
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) {
                                     x[j] += ld_cluster(from + j * 512);

@@ -125,9 +125,7 @@ cudaError_t make_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue
         if (p.a_mn) t = (int)up(t, 64) * 64;                     // MN-major boxes: 64 columns
         if (t > most || (i > 0 && t >= whole)) continue;
         const long tiles_m = up(p.M, t);
-        // (The cross entropy's maxima are not shared.)
-        const int splits = kind == FUSED_CE ? 1 : 8;
-        for (int c = 1; c <= splits; ++c) {
+        for (int c = 1; c <= 8; ++c) {
             const long units = c == 1 ? num_sms : (long)(fits >> 8 * (c - 1) & 255);
             if (units < 1 || up(p.K, 64) < c) continue;
             // Heights: whole MMAs, and those that fill one or two rounds of units.
