@@ -123,8 +123,9 @@ def test_dw_is_added_to_what_is_there(tgemm, kernel):
         assert torch.equal(out, dw.to(dtype))
 
 
-def test_rows_left_out_add_nothing_whatever_they_hold(tgemm, kernel):
-    T, V, D = 290, 520, 100
+@pytest.mark.parametrize("D", [100, 104, 1000])
+def test_rows_left_out_add_nothing_whatever_they_hold(tgemm, kernel, D):
+    T, V = 290, 520
     g = generator(12)
     x, w, target = inputs(g, T, V, D, left_out=0.3)
     out = (target < 0) | (target >= V)

@@ -199,9 +199,11 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     const bool sums = dX.x != nullptr && piece < V;          // dX over several pieces
     const long ldz = (piece + 63) / 64 * 64, ldk = ((long)D + 63) / 64 * 64;
     Scratch scratch(s);
-    // A dW takes X with the rows left out as zeros; the logits may take it too.
+    // A dW takes X with the rows left out as zeros: copied by the logits' product where
+    // that reads X as it is, else before it, and then the logits take it, too.
     const bool keep = dW.x != nullptr && T > 0 && V > 0;
-    Operand x(X, ldx, V == 0 || keep ? 0 : T, D, scratch), w(W, ldw, T == 0 ? 0 : V, D, scratch);
+    const bool inside = keep && !off(X, 16) && ldx % 8 == 0 && D % 8 == 0, before = keep && !inside;
+    Operand x(X, ldx, V == 0 || before ? 0 : T, D, scratch), w(W, ldw, T == 0 ? 0 : V, D, scratch);
     const size_t z_at = scratch.add((size_t)T * ldz * 2);
     const size_t kept_at = scratch.add(keep ? (size_t)T * ldk * 2 : 0);
     // Few tokens: dX, a sum over all of the vocabulary, in slices.
@@ -215,9 +217,9 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     e = scratch.take();
     if (e != cudaSuccess) return e;
     void *const z = scratch.at(z_at), *const kept = scratch.at(kept_at), *const sum = scratch.at(sum_at);
-    const tgemm::CopyJob jobs[3] = {x.lay(scratch), w.lay(scratch), {X, ldx, kept, ldk, keep ? T : 0, D, target, V, false}};
+    const tgemm::CopyJob jobs[3] = {x.lay(scratch), w.lay(scratch), {X, ldx, kept, ldk, before ? T : 0, D, target, V, false}};
     e = tgemm::fused_copy_rows(jobs, 3, s);
-    if (keep) {
+    if (before) {
         x.x = kept;
         x.ld = ldk;
     }
@@ -234,6 +236,13 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
             ep.vocabulary = V;
             ep.lse = lse;
             ep.dloss = dloss;
+            if (inside && v == 0) {
+                ep.keep = X;
+                ep.ld_keep = ldx;
+                ep.kept = kept;
+                ep.ld_kept = ldk;
+                ep.keep_cols = D;
+            }
             const FusedProduct p{T, n, D, x.x, x.ld, false, wv, w.ld, false, nullptr};
             e = product(tgemm::FUSED_CE_GRAD, p, ep, sms, s);
         }

@@ -36,6 +36,22 @@ __device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32], int kbl
         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
 }
 
+// The rows that count (FusedEpilogue::keep), by warp `mine` of `warps`: while the
+// first tile's sums are made (a kernel of its own before the product: 10 us on 4096 x
+// 4096, and a launch).
+__device__ __forceinline__ void keep_rows(const FusedEpilogue& e, long rows, long mine, long warps) {
+    const int lane = threadIdx.x & 31;
+    for (long row = mine; row < rows; row += warps) {
+        const long long t = e.target[row];
+        const bool counts = t >= 0 && t < e.vocabulary;
+        const bf16* from = static_cast<const bf16*>(e.keep) + row * e.ld_keep;
+        bf16* to = static_cast<bf16*>(e.kept) + row * e.ld_kept;
+#pragma unroll 4
+        for (int c = lane * 8; c < e.keep_cols; c += 256)
+            *reinterpret_cast<uint4*>(to + c) = counts ? *reinterpret_cast<const uint4*>(from + c) : make_uint4(0, 0, 0, 0);
+    }
+}
+
 // Column c of C, below N columns (gated: and column N + c of what has 2 N), rows
 // in groups of eight, whose loads come before their stores.
 template <int KIND, bool GATED>

@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             __syncwarp();
             if (lane == 31) mbar_arrive(smem_u32(&sy->tmem_empty[it & 1]));
         };
+        if (KIND == FUSED_CE_GRAD && p.e.kept != nullptr)
+            keep_rows(p.e, p.M, (long)blockIdx.x * EPI_WARPS + warp - 2, (long)gridDim.x * EPI_WARPS);
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
             int row, col, kb0, kb1;
             tile(t, row, col, kb0, kb1);

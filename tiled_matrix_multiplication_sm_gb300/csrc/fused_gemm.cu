@@ -597,6 +597,8 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             __syncwarp();
             if (lane == 31) mbar_arrive_cluster(tmem_empty0 + (uint32_t)((it & 1) * sizeof(uint64_t)));
         };
+        if (KIND == FUSED_CE_GRAD && p.e.kept != nullptr)
+            keep_rows(p.e, p.M, (long)blockIdx.x * S::WARPS + warp - 2, (long)gridDim.x * S::WARPS);
         for (int t = unit; t < p.num_tiles; t += p.units, ++it) {
             int mb, nb;
             tile_at(t, p, mb, nb);

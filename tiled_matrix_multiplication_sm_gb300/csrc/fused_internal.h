@@ -55,6 +55,13 @@ struct FusedEpilogue {
     const float* dloss = nullptr;
     float2* parts = nullptr;    // FUSED_CE: [blocks of columns][M], m and sum of exp(z - m)
     float* picked = nullptr;    // FUSED_CE: M logits of the targets
+    // FUSED_CE_GRAD: X's rows (whole 16 bytes, `keep_cols` BF16) to `kept`, those whose
+    // target is not in the vocabulary as zeros; NULL: none.
+    const void* keep = nullptr;
+    long ld_keep = 0;
+    void* kept = nullptr;
+    long ld_kept = 0;
+    int keep_cols = 0;
 };
 
 // In fused_gemm.cu: rows of C a partial column sum covers, columns of logits a
