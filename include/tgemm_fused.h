@@ -38,8 +38,9 @@
 extern "C" {
 #endif
 
-/* Largest M, N, K, T, V or D: two halves of a gated operand stay in an int. */
-#define TGEMM_FUSED_MAX_DIM 1073741824
+/* Largest M, N, K, T, V or D: two halves of a gated operand, and tiles' ends, stay in
+ * an int. */
+#define TGEMM_FUSED_MAX_DIM 1073741312
 
 #define TGEMM_ACT_NONE      0
 #define TGEMM_ACT_RELU      1

@@ -14,7 +14,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "tg
 FAKE = 0x10000           # never dereferenced: every call below is rejected first
 F32, BF16 = 0, 1
 INVALID = 1
-MOST = 1 << 30
+MOST = 1073741312
 
 
 @pytest.fixture(scope="module")

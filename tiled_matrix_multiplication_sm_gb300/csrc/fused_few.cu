@@ -498,7 +498,9 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     p.split = plan.split;
     p.tiles_m = (m.M + p.tokens - 1) / p.tokens;
     p.slices = plan.slices;
-    p.num_tiles = p.tiles_m * ((m.N + p.height - 1) / p.height) * p.slices;
+    const long tiles = (long)p.tiles_m * (((long)m.N + p.height - 1) / p.height) * p.slices;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    p.num_tiles = (int)tiles;
     p.units = p.split > 1 || p.num_tiles < num_sms ? p.num_tiles : num_sms;
     p.half_bytes = p.chunks * p.height * SW;
     p.stage_bytes = (two ? 2 : 1) * p.half_bytes + p.chunks * p.tokens * SW;

@@ -109,10 +109,11 @@ cudaError_t make_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue
     plan->boxes = fused_boxes(kind, p.N, e);
     plan->sum_blocks = up(p.M, FUSED_SUM_ROWS);
     plan->ce_blocks = up(p.N, FUSED_CE_COLS);
-    // Two rounds of pair tiles and more: always on pairs.
+    // Many rows, and two rounds of pair tiles or more: always on pairs. (Few rows of many
+    // columns are a stream of weights: 16 x 65536 x 4096 103 us on pairs, 85 as few.)
     const int forced = g_forced.load(std::memory_order_relaxed);
     if (p.M == 0 || p.N == 0 || p.K == 0 || forced == 0 ||
-        (forced < 0 && up(p.M, 256) * up((long)p.N * halves, 256) >= num_sms))
+        (forced < 0 && p.M > 512 && up(p.M, 256) * up((long)p.N * halves, 256) >= num_sms))
         return cudaSuccess;
     unsigned long long fits = 0;
     const cudaError_t err = fused_few_clusters(&fits);
