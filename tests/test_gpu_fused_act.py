@@ -366,6 +366,27 @@ def test_infinities_and_nan_stay_in_their_rows_and_columns(tgemm, kernel):
     assert torch.equal(db.double().cpu()[cols], (a[:130] @ b).sum(0)[cols])
 
 
+@pytest.mark.parametrize("N", [40000, 40001])
+def test_offsets_past_32_bits(tgemm, N):
+    """C, R and Z of more than 2^31 elements; rows at both ends and across the middle."""
+    M, K = 70000, 16
+    g = generator(N)
+    a, b = whole(g, M, K, most=1), whole(g, K, N, most=1)
+    A, B = a.to(BF16).cuda(), b.to(BF16).cuda()
+    rows = torch.tensor([0, 53686, 53687, 53688, 69000, M - 1])
+    R = torch.zeros(M, N, dtype=BF16, device="cuda")
+    r = whole(g, len(rows), N)
+    R[rows.cuda()] = r.to(BF16).cuda()
+    C, Z = tgemm.gemm_act(A, B, "relu", residual=R, keep_z=True)
+    z = a[rows] @ b
+    assert torch.equal(C[rows.cuda()].double().cpu(), z.clamp(min=0) + r)
+    assert torch.equal(Z[rows.cuda()].double().cpu(), z)
+    del C, R
+    dz, db = tgemm.gemm_act_grad(A, B, Z, "relu", out=Z)
+    assert torch.equal(dz[rows.cuda()].double().cpu(), z.clamp(min=0))
+    assert tgemm.device_status() == 0
+
+
 def test_calls_on_streams_and_in_graphs(tgemm, kernel):
     """Two calls at once on two streams, and two graphs that replay together, with
     scratch (operands off 16 bytes, column sums) in both."""

@@ -148,6 +148,38 @@ def test_rows_left_out_add_nothing_whatever_they_hold(tgemm, kernel, D):
     assert not l3.any() and not dx.any() and not dw.any()
 
 
+def test_a_vocabulary_past_32_bits(tgemm):
+    """W and dW of more than 2^31 elements; targets and checked rows at both ends."""
+    T, V, D = 6, 1100000, 2048
+    g = torch.Generator(device="cuda").manual_seed(21)
+    W = torch.empty(V, D, dtype=BF16, device="cuda")
+    for part in W.split(100000):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * D ** -0.5)
+    target = torch.tensor([0, 1048575, 1048577, V - 1, 7, -1])
+    X = (torch.randn(T, D, generator=g, device="cuda") + 12 * W[target.clamp(min=0).cuda()].float()).to(BF16)
+    z = torch.cat([(X.double() @ part.double().t()) for part in W.split(100000)], dim=1)
+    size = torch.cat([(X.double().abs() @ part.double().abs().t()).max(dim=1, keepdim=True).values for part in W.split(100000)], 1)
+    want_lse = torch.logsumexp(z, dim=1)
+    loss, lse = tgemm.gemm_ce(X, W, target.cuda())
+    tol = (D / 16 + 4) * 2.0 ** -22 * size.max(dim=1).values + 2.0 ** -18 + 2.0 ** -21 * want_lse.abs()
+    want = torch.where(target.cuda() >= 0, want_lse - z.gather(1, target.clamp(min=0).cuda()[:, None])[:, 0], want_lse * 0)
+    assert ((lse.double() - want_lse).abs() <= tol).all() and ((loss.double() - want).abs() <= 2 * tol).all()
+    dloss = torch.rand(T, generator=g, device="cuda")
+    dx, dw = tgemm.gemm_ce_grad(X, W, target.cuda(), lse, dloss)
+    rows = torch.tensor([0, 7, 1048574, 1048575, 1048576, 1048577, V - 2, V - 1])
+    p = torch.exp(z.cpu() - lse.double().cpu()[:, None])
+    p[target >= 0, target[target >= 0]] -= 1
+    dz = torch.where((target >= 0)[:, None], p * dloss.double().cpu()[:, None], torch.zeros_like(p))
+    x = X.double().cpu()
+    err = 2.0 ** -8 * dz.abs() + torch.where((target >= 0)[:, None], (p.abs() + 1e-30) * tol.cpu()[:, None] * 2, torch.zeros_like(p))
+    want_w = dz[:, rows].t() @ x
+    ref.check(dw[rows.cuda()], want_w, ref.rounded(want_w, (err[:, rows].t() + 2.0 ** -18 * dz[:, rows].abs().t()) @ x.abs() + 1e-12, BF16), "dW")
+    want_x = sum(dz[:, i:i + 100000].cuda() @ W[i:i + 100000].double() for i in range(0, V, 100000)).cpu()
+    mag = sum((err + 2.0 ** -14 * dz.abs())[:, i:i + 100000].cuda() @ W[i:i + 100000].double().abs() for i in range(0, V, 100000)).cpu()
+    ref.check(dx, want_x, ref.rounded(want_x, mag, BF16), "dX")
+    assert tgemm.device_status() == 0
+
+
 def test_a_sure_loss_keeps_its_digits(tgemm, kernel):
     """A target 20 above two others: loss = log1p(2 exp(-20)), exactly representable sums."""
     D = 64
