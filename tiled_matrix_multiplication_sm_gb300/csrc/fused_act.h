@@ -15,9 +15,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Of denormal results: 0. (__fdividef's care for large divisors costs as much as the
+// rest of a sigmoid.)
+__device__ __forceinline__ float inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 1 / (1 + exp(-v)): relative error below 2^-20 where it is not near FP32's
 // smallest numbers (the product v log2(e) is rounded), far below BF16's rounding.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + exp2_fast(v * -LOG2E)); }
+__device__ __forceinline__ float sigmoid(float v) { return inverse(1.0f + exp2_fast(v * -LOG2E)); }
 
 // tanh's form of GELU is z sigmoid(2 u), without the cancellation of 1 + tanh
 // for negative z.
@@ -30,7 +37,7 @@ __device__ __forceinline__ float tanh_arg(float z) { return 2.0f * ROOT_2_PI * z
 // instructions: 3000 x 5001 x 1537 with R and Z spent more on it than on the product.
 __device__ __forceinline__ float phi(float z, float& e) {
     e = exp2_fast(z * z * (-0.5f * LOG2E));
-    const float t = __fdividef(1.0f, fmaf(0.31112698372208f, fabsf(z), 1.0f));
+    const float t = inverse(fmaf(0.31112698372208f, fabsf(z), 1.0f));
     float p = 0.035613206675f;
     p = fmaf(p, t, -0.138980170652f);
     p = fmaf(p, t, 0.148354368869f);

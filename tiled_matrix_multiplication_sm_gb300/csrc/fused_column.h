@@ -191,11 +191,14 @@ struct Column {
 
     // Rows row + first, row + first + step, .. below row + end in groups of eight, sums
     // by sums(k, x, y); a group's loads are on their way while the one before is
-    // finished. All lanes of a warp (`in`: this one has a column).
-    template <typename Sums>
-    __device__ __forceinline__ void rows(long row, int first, int end, int step, bool in, Sums sums) {
+    // finished, the first group's while before() runs. All lanes of a warp (`in`: this
+    // one has a column).
+    template <typename Before, typename Sums>
+    __device__ __forceinline__ void rows(long row, int first, int end, int step, bool in, Before before, Sums sums) {
         float z[8], w[8];
-        if (in && first < end) load<false>(row + first, end - first, z, w);
+        if (in && end - first >= 8) load<true>(row + first, 8, z, w);
+        else if (in && first < end) load<false>(row + first, end - first, z, w);
+        before();
 #pragma unroll 1
         for (int k = first; k < end; k += step) {
             float x[8], y[8], next_z[8], next_w[8];

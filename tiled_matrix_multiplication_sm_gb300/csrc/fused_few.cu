@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     for (int k = begin; k < end && row + k < p.M; k += 32)
                         ce_tokens(p, [&](float (&v)[32]) { load_sums(acc + k, v, p.kblocks); }, row + k, min(end - k, p.M - row - k), c, in, (long)(col / p.height) * ((p.height + 31) / 32) + q);
             } else {
-                column.rows(row, begin, min(end, p.M - row), 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
+                column.rows(row, begin, min(end, p.M - row), 8, in, [] {}, [&](int k, float (&x)[8], float (&y)[8]) {
                     load_sums8(acc + k, x, kb1 - kb0);
                     if constexpr (TWO) load_sums8(acc + p.acc + k, y, kb1 - kb0);
                 });
@@ -393,12 +393,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     }
 
     if (p.split > 1) {
-        cluster_sync_all();
         int row, col, kb0, kb1;
         tile(unit, row, col, kb0, kb1);
         const int q = warp & 3, set = (warp - 2) >> 2, c = col + q * 32 + lane;
         // A column's share of token k, from block i.
         auto share = [&](int i, int k) { return map_to_rank(stage0, (uint32_t)i) + (uint32_t)((k * 128 + q * 32 + lane) * 4); };
+        if (KIND == FUSED_CE || warp < 2) cluster_sync_all();
         if (KIND == FUSED_CE && warp >= 2 && q * 32 < p.height) {
             // Groups of 32 tokens, in turn to the cluster's blocks and their sets. (Rows
             // past the tile's are other memory of the stages, and not used.)
@@ -422,6 +422,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const bool in = q * 32 + lane < p.height && c < p.N;
             Column<KIND, GATED> column(p.e, p.N, in ? c : 0);
             column.rows(row, (part * SETS + set) * 8, min(p.tokens, p.M - row), SETS * 8 * p.split, in,
+                        [&] {
+                            __syncwarp();
+                            cluster_sync_all();
+                        },
                         [&](int k, float (&x)[8], float (&y)[8]) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;

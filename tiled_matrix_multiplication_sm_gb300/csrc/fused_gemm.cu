@@ -162,34 +162,35 @@ __device__ __forceinline__ float column_sums(float (&v)[32]) {
 
 // --------------------------------------------- C in segments of its rows
 // 32 columns from column `col` on of C of this warp's `rows` rows, from registers
-// (a row a lane) through `bufs` to a column a lane. v2: gated ACT, u's sums.
-template <int KIND, bool GATED>
-__device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, int row0, int rows, int col, const float (&v)[32],
-                                              const float (&v2)[32]) {
+// (a row a lane, by sums(v, v2); v2: gated ACT, u's sums) through `bufs` to a column a
+// lane.
+template <int KIND, bool GATED, typename Sums>
+__device__ __forceinline__ void store_columns(const Params& p, uint8_t* bufs, int row0, int rows, int col, Sums sums) {
     const FusedEpilogue& e = p.e;
     const int lane = threadIdx.x & 31, c = col + lane;
     constexpr bool TWO = KIND == FUSED_ACT && GATED;
-    __syncwarp();
-    put_f32(bufs, v);
-    if constexpr (TWO) put_f32(bufs + BUF_BYTES, v2);
-    __syncwarp();
-    {
-        const bool in = c < p.N;
-        Column<KIND, GATED> column(e, p.N, in ? c : 0);
-        // Where this lane's column lies in the rows of a group of eight.
-        uint32_t at[8];
+    const bool in = c < p.N;
+    Column<KIND, GATED> column(e, p.N, in ? c : 0);
+    // Where this lane's column lies in the rows of a group of eight.
+    uint32_t at[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) at[j] = swizzled(j, lane >> 2) + (lane & 3) * 4;
-        column.rows(row0, 0, rows, 8, in, [&](int k, float (&x)[8], float (&y)[8]) {
-            const uint8_t* group = bufs + k * SW;
+    for (int j = 0; j < 8; ++j) at[j] = swizzled(j, lane >> 2) + (lane & 3) * 4;
+    column.rows(row0, 0, rows, 8, in, [&]() {
+        float v[32], v2[32];
+        sums(v, v2);
+        __syncwarp();
+        put_f32(bufs, v);
+        if constexpr (TWO) put_f32(bufs + BUF_BYTES, v2);
+        __syncwarp();
+    }, [&](int k, float (&x)[8], float (&y)[8]) {
+        const uint8_t* group = bufs + k * SW;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = *reinterpret_cast<const float*>(group + at[j]);
-                if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(group + BUF_BYTES + at[j]);
-            }
-        });
-        if (in) column.leave(row0 / FUSED_SUM_ROWS);
-    }
+        for (int j = 0; j < 8; ++j) {
+            x[j] = *reinterpret_cast<const float*>(group + at[j]);
+            if constexpr (TWO) y[j] = *reinterpret_cast<const float*>(group + BUF_BYTES + at[j]);
+        }
+    });
+    if (in) column.leave(row0 / FUSED_SUM_ROWS);
     __syncwarp();
 }
 
@@ -316,13 +317,15 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
             if (e.sums != nullptr) {
                 // (Rows past M may hold a NaN: 0 times an infinity of B's.)
                 float* to = e.sums + (long)(row0 / FUSED_SUM_ROWS) * (GATED ? 2L * p.N : p.N) + c + lane;
+                if (rows < 32)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = lane < rows ? v[j] : 0.0f;
+                    for (int j = 0; j < 32; ++j) v[j] = lane < rows ? v[j] : 0.0f;
                 float sum = column_sums(v);
                 if (c + lane < p.N) to[0] = sum;
                 if constexpr (GATED) {
+                    if (rows < 32)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) w[j] = lane < rows ? w[j] : 0.0f;
+                        for (int j = 0; j < 32; ++j) w[j] = lane < rows ? w[j] : 0.0f;
                     sum = column_sums(w);
                     if (c + lane < p.N) to[p.N] = sum;
                 }
@@ -616,6 +619,9 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             };
             if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
                 if (loads && rows > 0 && col0 < p.N) ask(col0);
+            // A column a lane: on their way to L2 only. (A tile ahead of that: 3 % slower.)
+            if constexpr (!BOXES && (KIND == FUSED_ACT || KIND == FUSED_GRAD))
+                for (int c = col0; c < min(p.N, col0 + SET_COLS); c += 32) Column<KIND, GATED>(p.e, p.N, c).ask(row0 + lane, row0 + rows);
 
             const uint32_t lanes = (uint32_t)(q * 32) << 16;
             auto accumulator = [&]() { return tmem_base + (uint32_t)(it & 1) * TILE + lanes + set * SET_COLS; };
@@ -713,11 +719,11 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                                                 row0, rows, col, box, done);
                     } else {
                         auto half = [&](int h) {
-                            float v[32], w[32];
-                            sums(i * 2 + h, v);
-                            if constexpr (TWO) load_sums(acc + 128 + i * 64 + h * 32, w, p.kblocks);
-                            if (h == 1) done();
-                            store_columns<KIND, GATED>(p, bufs, row0, rows, col + h * 32, v, w);
+                            store_columns<KIND, GATED>(p, bufs, row0, rows, col + h * 32, [&](float (&v)[32], float (&w)[32]) {
+                                sums(i * 2 + h, v);
+                                if constexpr (TWO) load_sums(acc + 128 + i * 64 + h * 32, w, p.kblocks);
+                                if (h == 1) done();
+                            });
                         };
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) half(h);
