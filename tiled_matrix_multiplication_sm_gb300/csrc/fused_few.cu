@@ -98,15 +98,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// One thread: `rows` rows of an operand, from `row` on, of stage kb.
-__device__ __forceinline__ void load_stage(const CUtensorMap* map, uint32_t to, int row, int rows, int kb, int chunks, int mn,
+// One thread: `rows` rows of an operand, from `row` on, of `chunks` chunks of K from `chunk` on.
+__device__ __forceinline__ void load_stage(const CUtensorMap* map, uint32_t to, int row, int rows, int chunk, int chunks, int mn,
                                            int box, uint32_t full) {
-    if (mn) {
-        for (int i = 0; i < rows; i += 64) tma_load_2d<false>(to + i * chunks * SW, map, row + i, kb * chunks * CHUNK_K, full);
-    } else if (box) {
-        tma_load_3d<false>(to, map, 0, row, kb * chunks, full);
+    if (box) {
+        tma_load_3d<false>(to, map, 0, row, chunk, full);
+    } else if (mn) {
+        for (int i = 0; i < rows; i += 64) tma_load_2d<false>(to + i * chunks * SW, map, row + i, chunk * CHUNK_K, full);
     } else {
-        for (int c = 0; c < chunks; ++c) tma_load_2d<false>(to + c * rows * SW, map, (kb * chunks + c) * CHUNK_K, row, full);
+        for (int c = 0; c < chunks; ++c) tma_load_2d<false>(to + c * rows * SW, map, (chunk + c) * CHUNK_K, row, full);
     }
 }
 
@@ -210,37 +210,41 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
-        uint32_t armed = 0, armed_parity = 0, ph = 0;
-        int s = 0;
-        bool ok = true, stall = p.debug_stall != 0;            // test hook: the first stage is never filled
-        for (int t = unit; ok && t < p.num_tiles; t += p.units) {
-            int row, col, kb0, kb1;
-            tile(t, row, col, kb0, kb1);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
-                if (!ok) break;
-                if (!stall) {
-                    if (elect_one()) {
+        // (One thread has the whole loop: with the warp in step a stage took 750 cycles.)
+        if (elect_one()) {
+            uint32_t armed = 0, armed_parity = 0, ph = 0, to = stage0;
+            int s = 0;
+            bool ok = true, stall = p.debug_stall != 0;        // test hook: the first stage is never filled
+            for (int t = unit; ok && t < p.num_tiles; t += p.units) {
+                int row, col, kb0, kb1;
+                tile(t, row, col, kb0, kb1);
+                int chunk = kb0 * p.chunks;
+                for (int kb = kb0; kb < kb1; ++kb, chunk += p.chunks) {
+                    ok = mbar_wait(smem_u32(&sy->empty[s]), ph ^ 1u, wait);
+                    if (!ok) break;
+                    if (!stall) {
                         const uint32_t full = smem_u32(&sy->full[s]);
-                        uint32_t to = stage0 + s * p.stage_bytes;
                         mbar_arrive_expect_tx(full, p.stage_bytes);
 #pragma unroll
-                        for (int h = 0; h < HALVES; ++h) {
-                            load_stage(h == 0 ? &maps.W : &maps.W2, to, col, p.height, kb, p.chunks, p.w_mn, p.w_box, full);
-                            to += p.half_bytes;
-                        }
-                        load_stage(&maps.X, to, row, p.tokens, kb, p.chunks, p.x_mn, p.x_box, full);
+                        for (int h = 0; h < HALVES; ++h)
+                            load_stage(h == 0 ? &maps.W : &maps.W2, to + h * p.half_bytes, col, p.height, chunk, p.chunks, p.w_mn,
+                                       p.w_box, full);
+                        load_stage(&maps.X, to + HALVES * p.half_bytes, row, p.tokens, chunk, p.chunks, p.x_mn, p.x_box, full);
+                        armed |= 1u << s;
+                        armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
                     }
-                    armed |= 1u << s;
-                    armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                    stall = false;
+                    to += p.stage_bytes;
+                    if (++s == p.stages) {
+                        s = 0;
+                        ph ^= 1u;
+                        to = stage0;
+                    }
                 }
-                stall = false;
-                __syncwarp();
-                if (++s == p.stages) { s = 0; ph ^= 1u; }
             }
+            for (int i = 0; i < p.stages; ++i)
+                if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
         }
-        for (int i = 0; i < p.stages; ++i)
-            if (armed & (1u << i)) mbar_wait<false>(smem_u32(&sy->full[i]), (armed_parity >> i) & 1u, wait);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
@@ -254,24 +258,23 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         const uint64_t w0 = smem_desc(stage0, p.w_mn ? p.chunks * CHUNK_K * SW : 16, 1024, 2);
         const uint64_t x0 = smem_desc(stage0 + HALVES * p.half_bytes, p.x_mn ? p.chunks * CHUNK_K * SW : 16, 1024, 2);
         const uint32_t upper = (uint32_t)(w0 >> 32);
-        int it = 0, s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        int row, col, kb0, kb1;
-        tile(unit, row, col, kb0, kb1);
-        for (int t = unit, first = kb0; ok && t < p.num_tiles; ++it) {
-            const int last = LONG ? min(first + p.part_blocks, kb1) : kb1;
-            if (it >= 2)
-                if (!__all_sync(~0u, mbar_wait(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait))) break;
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)((it & 1) * HALVES * p.acc);
-            for (int kb = first; kb < last; ++kb) {
-                ok = __all_sync(~0u, mbar_wait(smem_u32(&sy->full[s]), ph, wait));
-                if (!ok) break;
+        if (elect_one()) {
+            int it = 0, s = 0;
+            uint32_t ph = 0, at = 0;                           // (at: the stage, in descriptors' units)
+            bool ok = true;
+            int row, col, kb0, kb1;
+            tile(unit, row, col, kb0, kb1);
+            for (int t = unit, first = kb0; ok && t < p.num_tiles; ++it) {
+                const int last = LONG ? min(first + p.part_blocks, kb1) : kb1;
+                if (it >= 2 && !mbar_wait(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait)) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    uint32_t w = (uint32_t)w0 + (uint32_t)(s * p.stage_bytes >> 4), x = (uint32_t)x0 + (uint32_t)(s * p.stage_bytes >> 4);
-                    uint32_t more = kb != first;
+                const uint32_t d = tmem_base + (uint32_t)((it & 1) * HALVES * p.acc);
+                uint32_t more = 0;
+                for (int kb = first; kb < last; ++kb) {
+                    ok = mbar_wait(smem_u32(&sy->full[s]), ph, wait);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t w = (uint32_t)w0 + at, x = (uint32_t)x0 + at;
 #pragma unroll 1
                     for (int c = 0; c < p.chunks; ++c, w += w_chunk, x += x_chunk)
 #pragma unroll
@@ -284,21 +287,24 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             more = 1;
                         }
                     tc_commit<false>(smem_u32(&sy->empty[s]));
+                    at += (uint32_t)p.stage_bytes >> 4;
+                    if (++s == p.stages) {
+                        s = 0;
+                        ph ^= 1u;
+                        at = 0;
+                    }
                 }
-                __syncwarp();
-                if (++s == p.stages) { s = 0; ph ^= 1u; }
+                if (ok) tc_commit<false>(smem_u32(&sy->tmem_full[it & 1]));
+                first = last;
+                if (last == kb1) {
+                    t += p.units;
+                    tile(t, row, col, kb0, kb1);
+                    first = kb0;
+                }
             }
-            if (ok && elect_one()) tc_commit<false>(smem_u32(&sy->tmem_full[it & 1]));
-            __syncwarp();
-            first = last;
-            if (last == kb1) {
-                t += p.units;
-                tile(t, row, col, kb0, kb1);
-                first = kb0;
-            }
+            tc_commit<false>(smem_u32(&sy->drain));
+            mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
-        if (elect_one()) tc_commit<false>(smem_u32(&sy->drain));
-        mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue
@@ -464,7 +470,7 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
 bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* x, long ld, int rows, int K, bool mn, int box_rows, int chunks,
                     int* whole) {
     const cuuint64_t pitch = (cuuint64_t)ld * 2;
-    *whole = !mn && chunks > 1 && K % CHUNK_K == 0 ? 1 : 0;
+    *whole = !mn && K % CHUNK_K == 0 ? 1 : 0;
     if (*whole) {
         const cuuint64_t dims[3] = {CHUNK_K, (cuuint64_t)rows, (cuuint64_t)(K / CHUNK_K)}, strides[2] = {pitch, SW};
         const cuuint32_t box[3] = {CHUNK_K, (cuuint32_t)box_rows, (cuuint32_t)chunks};
