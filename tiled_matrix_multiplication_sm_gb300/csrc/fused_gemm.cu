@@ -19,6 +19,13 @@
 // work from there where they can, so that accumulators are free as soon as they
 // are read.
 //
+// Where tiles are few and sums long, a cluster's two, three or four pairs share a tile's K (one
+// tile a cluster). Each pair leaves its sums in its stages' shared memory, a turn of 64
+// columns falls to one of them, which adds up all shares, in the pairs' order, through
+// distributed shared memory, and goes on from there: 512 x 4096 x 14336 73 -> 45 us.
+// (Not for a gated gradient, whose totals in registers leave no room for it, nor for
+// what is as wide as a vocabulary.)
+//
 // A thread has a row of the tile. Where C, R and Z allow TMA, boxes of 32 rows x
 // 128 bytes pass between its registers and memory through shared memory; where
 // they do not, 32 x 32 blocks of sums go through shared memory to a column a
@@ -69,6 +76,7 @@ static_assert(sizeof(Sync) <= 512, "barrier block");
 struct Params {
     int M, N, kblocks;
     int tiles_n, num_tiles, units, group_m, tiles_m;
+    int split;                  // ACT and GRAD (not gated): pairs that share a tile's sum
     FusedParts part;
     int a_mn, b_mn;
     int bias4;                  // bias in pieces of 16 bytes
@@ -428,9 +436,36 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& mb, int& nb
     nb = t % per_group / gm;
 }
 
-// The end of the part that begins at stage `first`.
-__device__ __forceinline__ int part_end(const Params& p, int first) {
-    return min(first + (first < 2 * p.part.first ? p.part.first : p.part.rest), p.kblocks);
+// The end of the part that begins at stage `first` of a pair's `stages`.
+__device__ __forceinline__ int part_end(const Params& p, int first, int stages) {
+    return min(first + (first < 2 * p.part.first ? p.part.first : p.part.rest), stages);
+}
+
+// A pair's share of a tile's sums, in its stages' place: of a block, four columns of
+// its 128 rows after the other. 32 columns from `col` on of row `row`.
+__device__ __forceinline__ uint32_t share_at(int col, int row) { return (uint32_t)(col * 128 + row * 4) * 4; }
+__device__ __forceinline__ void leave_share(uint8_t* share, int col, int row, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(share + share_at(col + j, row)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+}
+// All pairs' shares of them, added up in the pairs' order.
+__device__ __forceinline__ void gather_shares(uint32_t share, int split, uint32_t rank, int col, int row, float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < split; ++i) {
+        const uint32_t from = map_to_rank(share, 2u * i + rank);
+        float4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[j].x), "=f"(x[j].y), "=f"(x[j].z), "=f"(x[j].w) : "r"(from + share_at(col + 4 * j, row)) : "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[4 * j] += x[j].x; v[4 * j + 1] += x[j].y; v[4 * j + 2] += x[j].z; v[4 * j + 3] += x[j].w;
+        }
+    }
 }
 
 // BOXES: C, R and Z pass by TMA (fused_boxes).
@@ -446,9 +481,15 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
     const uint32_t stage0 = smem_u32(smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    // The cluster's pair, and the block's place in it.
+    constexpr bool SPLITS = KIND == FUSED_ACT || (KIND == FUSED_GRAD && !GATED);
+    const uint32_t block = cluster_rank(), rank = block & 1u, pair0 = block - rank;
     const bool leader = rank == 0;
-    const int unit = blockIdx.x >> 1;
+    const int split = SPLITS ? p.split : 1, part = SPLITS ? (int)(block >> 1) : 0;
+    const int unit = SPLITS ? blockIdx.x / (2 * split) : blockIdx.x >> 1;
+    // This pair's stages of a tile's sum.
+    const int kb0 = (int)((long)p.kblocks * part / split), stages = (int)((long)p.kblocks * (part + 1) / split) - kb0;
+    bool met = false;                                    // the cluster's pairs, over their shares
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -479,8 +520,8 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
 
     const Wait wait{&sy->abort, p.status, p.wait_limit_ns};
     // The leader's barriers, as cluster addresses.
-    const uint32_t full0 = map_to_rank(smem_u32(&sy->full[0]), 0);
-    const uint32_t tmem_empty0 = map_to_rank(smem_u32(&sy->tmem_empty[0]), 0);
+    const uint32_t full0 = map_to_rank(smem_u32(&sy->full[0]), pair0);
+    const uint32_t tmem_empty0 = map_to_rank(smem_u32(&sy->tmem_empty[0]), pair0);
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
@@ -493,7 +534,7 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             tile_at(t, p, mb, nb);
             const int row = mb * TILE + (int)rank * 128;
             const int col = nb * TC + (TWO ? 0 : (int)rank * 128);
-            for (int kb = 0; kb < p.kblocks; ++kb) {
+            for (int kb = kb0; kb < kb0 + stages; ++kb) {
                 ok = __all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->empty[s]), ph ^ 1u, wait));
                 if (!ok) break;
                 if (!stall) {
@@ -547,7 +588,7 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             bool ok = true;
             // A tile's sum, or of LONG ones each part in turn: first to last - 1.
             for (int t = unit, first = 0; ok && t < p.num_tiles; ++it) {
-                const int last = LONG ? part_end(p, first) : p.kblocks;
+                const int last = LONG ? part_end(p, first, stages) : stages;
                 if (it >= 2)
                     if (!__all_sync(~0u, mbar_wait<true, true>(smem_u32(&sy->tmem_empty[it & 1]), (uint32_t)((it >> 1) - 1) & 1u, wait)))
                         break;
@@ -563,20 +604,20 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                         for (int k = 0; k < STAGE_K / 16; ++k)
                             mma_bf16<true>(d, smem_desc(a + k * a_step, a_lead, 1024, 2), smem_desc(b + k * b_step, b_lead, 1024, 2),
                                      idesc, kb != first || k != 0);
-                        tc_commit<true>(smem_u32(&sy->empty[s]));
+                        tc_commit<true>(smem_u32(&sy->empty[s]), pair0);
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
-                if (ok && elect_one()) tc_commit<true>(smem_u32(&sy->tmem_full[it & 1]));
+                if (ok && elect_one()) tc_commit<true>(smem_u32(&sy->tmem_full[it & 1]), pair0);
                 __syncwarp();
                 first = last;
-                if (last == p.kblocks) {
+                if (last == stages) {
                     first = 0;
                     t += p.units;
                 }
             }
-            if (elect_one()) tc_commit<true>(smem_u32(&sy->drain));
+            if (elect_one()) tc_commit<true>(smem_u32(&sy->drain), pair0);
             mbar_wait<false>(smem_u32(&sy->drain), 0, wait);
         }
         __syncwarp();
@@ -587,7 +628,7 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
         uint8_t* bufs = epi + (warp - 2) * S::WARP_BYTES;
         const uint32_t loaded = smem_u32(&sy->loaded[(warp - 2) & 7]);
         const bool loads = BOXES && (KIND == FUSED_GRAD || (KIND == FUSED_ACT && p.e.R != nullptr));
-        constexpr int SET_COLS = TC / S::SETS, TURNS = SET_COLS / 64;
+        constexpr int SET_COLS = TC / S::SETS, TURNS = SET_COLS / 64, HALVES = TWO ? 2 : 1;
         // A long sum's total stays in registers (HELD), or goes back to where its last
         // part lay (BACK): with a column a lane a warp's registers are few, and a copy of the
         // epilogue for each 32 of them cost more (3000 x 5001 x 1537 in two parts 121 us for 95).
@@ -617,11 +658,17 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                 __syncwarp();
                 loading = true;
             };
+            // The set's turns that are this pair's: each in turn to one of the cluster's.
+            auto owns = [&](int i) { return split == 1 || (set * TURNS + i) % split == part; };
+            bool asked = false;
             if constexpr (KIND == FUSED_ACT || KIND == FUSED_GRAD)
-                if (loads && rows > 0 && col0 < p.N) ask(col0);
+                if (loads && rows > 0 && col0 < p.N && owns(0)) {
+                    ask(col0);
+                    asked = true;
+                }
             // A column a lane: on their way to L2 only. (A tile ahead of that: 3 % slower.)
             if constexpr (!BOXES && (KIND == FUSED_ACT || KIND == FUSED_GRAD))
-                for (int c = col0; c < min(p.N, col0 + SET_COLS); c += 32) Column<KIND, GATED>(p.e, p.N, c).ask(row0 + lane, row0 + rows);
+                for (int c = col0; owns(0) && c < min(p.N, col0 + SET_COLS); c += 32) Column<KIND, GATED>(p.e, p.N, c).ask(row0 + lane, row0 + rows);
 
             const uint32_t lanes = (uint32_t)(q * 32) << 16;
             auto accumulator = [&]() { return tmem_base + (uint32_t)(it & 1) * TILE + lanes + set * SET_COLS; };
@@ -629,13 +676,13 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             float sum[LONG ? SET_COLS / 32 : 1][32] = {};
             if constexpr (LONG) {
                 #pragma unroll 1
-                for (int first = 0; first < p.kblocks;) {
+                for (int first = 0; first < stages;) {
                     ok = __all_sync(~0u, mbar_wait<true, true, true>(smem_u32(&sy->tmem_full[it & 1]), (uint32_t)(it >> 1) & 1u, wait));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t acc = accumulator();
-                    first = part_end(p, first);
-                    const bool final = first == p.kblocks;
+                    first = part_end(p, first, stages);
+                    const bool final = first == stages;
 #pragma unroll
                     for (int i = 0; i < SET_COLS / 32; ++i) {
 #pragma unroll
@@ -658,6 +705,42 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
             }
             if (!ok) break;
             const uint32_t acc = accumulator();
+            if (SPLITS && split > 1) {
+                // The tile's copies and MMAs are done: the stages hold the pair's share. What all
+                // shares add up to goes where the sums were.
+                const int mine = q * 32 + lane;
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int i = 0; i < SET_COLS / 32; ++i) leave_share(smem, set * SET_COLS + i * 32, mine, sum[i]);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < SET_COLS / 32 * HALVES; ++i) {
+                        const int at = i % HALVES * 128 + i / HALVES * 32;
+                        float v[32];
+                        load_sums(acc + at, v, stages);
+                        leave_share(smem, set * SET_COLS + at, mine, v);
+                    }
+                }
+                __syncwarp();
+                cluster_sync_all();
+                met = true;
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int i = 0; i < SET_COLS / 32; ++i)
+                        if (owns(i / 2)) gather_shares(stage0, split, rank, set * SET_COLS + i * 32, mine, sum[i]);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < SET_COLS / 32 * HALVES; ++i) {
+                        const int at = i % HALVES * 128 + i / HALVES * 32;
+                        float v[32];
+                        if (!owns(i / HALVES / 2)) continue;
+                        gather_shares(stage0, split, rank, set * SET_COLS + at, mine, v);
+                        __syncwarp();
+                        tmem_st32(acc + at, reinterpret_cast<uint32_t (&)[32]>(v));
+                    }
+                    tmem_wait_st();
+                }
+            }
             // Columns 32 i .. 32 i + 31 of the set's.
             auto sums = [&](int i, float (&v)[32]) {
                 if constexpr (HELD) {
@@ -697,7 +780,7 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                     auto done = [&]() {
                         if (!HELD && i == TURNS - 1) release();
                     };
-                    if (rows <= 0 || col >= p.N) {
+                    if (rows <= 0 || col >= p.N || !owns(i)) {
                         done();
                         return true;
                     }
@@ -706,7 +789,8 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                                      target >= 0 && target < p.e.vocabulary);
                         done();
                     } else if constexpr (BOXES) {
-                        if (i > 0 && loads) ask(col);
+                        if (loads && !asked) ask(col);
+                        asked = false;
                         if (loading) {
                             if (!__all_sync(~0u, mbar_wait<true>(loaded, load_ph, wait))) return false;
                             load_ph ^= 1u;
@@ -715,8 +799,8 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                             if (lane == 0) tma_store_wait_read<0>();
                             __syncwarp();
                         }
-                        turn_boxes<KIND, GATED>(p, &maps, bufs, [&](int h, float (&v)[32]) { sums(i * 2 + h, v); }, acc + 128 + i * 64,
-                                                row0, rows, col, box, done);
+                        turn_boxes<KIND, GATED>(p, &maps, bufs, [&](int h, float (&v)[32]) { sums(i * 2 + h, v); },
+                                                acc + 128 + i * 64, row0, rows, col, box, done);
                     } else {
                         auto half = [&](int h) {
                             store_columns<KIND, GATED>(p, bufs, row0, rows, col + h * 32, [&](float (&v)[32], float (&w)[32]) {
@@ -744,8 +828,13 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
         tma_store_wait_all();
     }
 
+    if (SPLITS && split > 1 && !met) {
+        __syncwarp();
+        cluster_sync_all();
+    }
+    __syncwarp();
     tc_fence_before();
-    cluster_sync_all();
+    cluster_sync_all();                                  // no block leaves while another reads its share
     tc_fence_after();
     if (warp == 1) tmem_free<true, TMEM_COLS>(tmem_base);
 }
@@ -772,7 +861,7 @@ template <int KIND, bool GATED, bool LONG, bool BOXES>
 cudaError_t launch_kernel(const Maps& maps, const Params& p, cudaStream_t s) {
     const cudaError_t e = set_smem_limit_once<fused_kernel<KIND, GATED, LONG, BOXES>>(SMEM);
     if (e != cudaSuccess) return e;
-    ClusterLaunch cfg(2 * p.units, Shape<KIND, GATED, BOXES>::THREADS, SMEM, 2, s);
+    ClusterLaunch cfg(2 * p.split * p.units, Shape<KIND, GATED, BOXES>::THREADS, SMEM, 2 * p.split, s);
     return cudaLaunchKernelEx(&cfg.config, fused_kernel<KIND, GATED, LONG, BOXES>, maps, p);
 }
 template <int KIND, bool GATED, bool LONG>
@@ -794,13 +883,14 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
     p.M = m.M;
     p.N = m.N;
     p.kblocks = (int)(((long)m.K + STAGE_K - 1) / STAGE_K);
-    p.part = fused_parts(kind, false, m.K, STAGE_K);
+    p.split = plan.split;
+    p.part = fused_parts(kind, false, (m.K - 1) / p.split + 1, STAGE_K);
     const int cols = two ? TILE / 2 : TILE;
     p.tiles_m = (int)(((long)m.M + TILE - 1) / TILE);
     p.tiles_n = (int)(((long)m.N + cols - 1) / cols);
     if ((long)p.tiles_m * p.tiles_n > 0x3FFFFFFF) return cudaErrorInvalidValue;
     p.num_tiles = p.tiles_m * p.tiles_n;
-    p.units = p.num_tiles < num_sms / 2 ? p.num_tiles : num_sms / 2;
+    p.units = p.split > 1 || p.num_tiles < num_sms / 2 ? p.num_tiles : num_sms / 2;
     p.group_m = p.tiles_m >= 32 ? 16 : 8;
     p.a_mn = m.a_mn ? 1 : 0;
     p.b_mn = m.b_mn ? 1 : 0;
@@ -831,7 +921,7 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
         }
         if (!ok) return cudaErrorInvalidValue;
     }
-    const bool parts = p.kblocks > p.part.first;
+    const bool parts = p.kblocks > p.part.first * p.split;
     switch (kind) {
         case FUSED_ACT:
             if (two) return launch<FUSED_ACT, true, false>(maps, p, boxes, s);

@@ -95,7 +95,8 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k);
 struct FusedPlan {
     bool few;
     bool boxes;                          // pairs: fused_boxes
-    int height, tokens, split, chunks;   // few: columns and rows of C a tile, blocks that share its sum, 64s of K a stage
+    int height, tokens, chunks;          // few: columns and rows of C a tile, 64s of K a stage
+    int split;                           // blocks (few) or pairs that share a tile's sum
     int slices;                          // few: C comes as so many FP32 matrices of M x N, to be added up (1: as it is)
     long sum_blocks;                     // rows of FusedEpilogue::sums
     long ce_blocks;                      // of FusedEpilogue::parts

@@ -1,14 +1,17 @@
-// Which kernel a fused product runs in, and the tiles of few.
+// Which kernel a fused product runs in, how many pairs share a tile's sum, and the
+// tiles of few.
 //
-// By a model of both kernels' times in microseconds, fitted to 1800 measured runs of
+// By a model of the kernels' times in microseconds, fitted to 1800 measured runs of
 // fused_few.cu's tiles (1 to 1024 tokens, 256 x 256 to 65536 x 4096 weights, plain,
-// gated, gradients and cross entropy) and of fused_gemm.cu's: what it picks takes
-// 1.7 % more than the best of them on average, 27 % at most. A few of them (us: tokens
-// x columns x K, on pairs, and as few tiles: best measured):
-//        1 x 14336 x 4096   42.9   21.4        256 x 1024 x 1024    12.6    5.7
-//       16 x 4096 x 14336   72.2   23.0        256 x 14336 x 4096   32.5   39.6
-//       64 x 4096 x 4096    26.5   11.2        512 x 4096 x 4096    27.7   22.0
-//      128 x 14336 x 4096   31.9   28.2       1024 x 4096 x 4096    28.5   34.7
+// gated, gradients and cross entropy) and 2600 of fused_gemm.cu's. Over 4600 others what
+// it picks takes 0.2 % more than the better of both kernels on average, 36 % at most; over
+// 2600 of 150 to 2048 tokens that could share sums 1 % more than the best sharing. A few
+// of them (us: tokens x columns x K, on pairs, and as few tiles):
+//        1 x 14336 x 4096   47.1   22.1        256 x 14336 x 4096   31.9   36.6
+//       16 x 4096 x 14336   34.4   23.6        512 x 4096 x 4096    20.0   20.0
+//       64 x 4096 x 4096    17.4   11.5        512 x 4096 x 14336   45.0   51.6
+//      128 x 14336 x 4096   31.4   26.0       1024 x 4096 x 4096    27.6   31.1
+//      256 x 1024 x 1024    10.8    5.8       1024 x 2048 x 8192    28.8   32.3
 
 #include "fused_internal.h"
 
@@ -32,10 +35,11 @@ struct Tiles {
     int height, tokens, split, chunks;
 };
 
-// Stages of as many chunks as leave room for three (a row's pieces next to each
-// other in memory: 16 x 14336 x 4096 29.1, 23.0, 22.4 us with 1, 2, 4 chunks).
+// Stages of as many chunks as leave room for four (a stage's waits and copies take the
+// same time whatever it holds: 140 tiles of 32 columns x 16 tokens, K = 14336, 46.6, 29.7,
+// 27.4 us with 1, 2, 4 chunks; of 96 x 128, K = 4096, in 7 stages of one 24.7, in 3 of two 26.4).
 int chunks_for(long rows, int K) {
-    int chunks = rows * 128 * 4 * 3 <= FUSED_FEW_RING ? 4 : rows * 128 * 2 * 3 <= FUSED_FEW_RING ? 2 : 1;
+    int chunks = rows * 128 * 4 * 4 <= FUSED_FEW_RING ? 4 : rows * 128 * 2 * 4 <= FUSED_FEW_RING ? 2 : 1;
     while (chunks > 1 && K <= 64 * (chunks / 2)) chunks /= 2;
     return chunks;
 }
@@ -51,10 +55,12 @@ double few_us(int M, long N, int K, int halves, const Tiles& t, int fits) {
            (t.split > 1 ? 1.5 + 0.013 * t.tokens : 0.0);
 }
 
-double pair_us(int M, long N, int K, int halves, int pairs) {
-    const double rounds = (double)up(up(M, 256) * up(N * halves, 256), pairs);
-    const double sm = rounds * (double)up(K, 64) * 0.388, hbm = 2.0 * K * ((double)N * halves + M) / HBM;
-    return 5.4 + (sm > hbm ? sm : hbm);
+// `split`: pairs that share a tile's sum (what they take longer: leaving and adding up
+// the shares).
+double pair_us(int M, long N, int K, int halves, int pairs, int split) {
+    const double rounds = split > 1 ? 1.0 : (double)up(up(M, 256) * up(N * halves, 256), pairs);
+    const double sm = rounds * (double)up(up(K, 64), split) * 0.285, hbm = 2.0 * K * ((double)N * halves + M) / HBM;
+    return (split > 1 ? 8.0 + 0.55 * split : 7.5) + std::sqrt(std::sqrt(power4(sm) + power4(hbm)));
 }
 
 }  // namespace
@@ -104,21 +110,33 @@ cudaError_t make_plan(FusedKind kind, const FusedProduct& p, const FusedEpilogue
     *us = 0.0;
     const int halves = kind == FUSED_ACT && e.gated ? 2 : 1;
     plan->few = false;
-    plan->height = plan->tokens = plan->split = plan->chunks = 0;
-    plan->slices = 1;
+    plan->height = plan->tokens = plan->chunks = 0;
+    plan->split = plan->slices = 1;
     plan->boxes = fused_boxes(kind, p.N, e);
     plan->sum_blocks = up(p.M, FUSED_SUM_ROWS);
     plan->ce_blocks = up(p.N, FUSED_CE_COLS);
     // Many rows, and two rounds of pair tiles or more: always on pairs. (Few rows of many
     // columns are a stream of weights: 16 x 65536 x 4096 103 us on pairs, 85 as few.)
     const int forced = g_forced.load(std::memory_order_relaxed);
-    if (p.M == 0 || p.N == 0 || p.K == 0 || forced == 0 ||
+    if (p.M == 0 || p.N == 0 || p.K == 0 ||
         (forced < 0 && p.M > 512 && up(p.M, 256) * up((long)p.N * halves, 256) >= num_sms))
         return cudaSuccess;
     unsigned long long fits = 0;
     const cudaError_t err = fused_few_clusters(&fits);
     if (err != cudaSuccess) return err;
-    double best = forced == 1 ? 1e300 : pair_us(p.M, p.N, p.K, halves, num_sms / 2);
+    double best = forced == 1 ? 1e300 : pair_us(p.M, p.N, p.K, halves, num_sms / 2, 1);
+    // Pairs that share a tile's sum, in clusters that the GPU holds all at once, two stages
+    // each at least (512 x 4096 x 14336 73 us alone, 45 with two pairs a tile).
+    const long pair_tiles = up(p.M, 256) * up((long)p.N * halves, 256);
+    for (int c = 2; forced != 1 && (kind == FUSED_ACT || (kind == FUSED_GRAD && !e.gated)) && c <= 4 / halves; ++c) {
+        if (pair_tiles > (long)(fits >> 8 * (2 * c - 1) & 255) || up(p.K, 64) < 2 * c) continue;
+        const double us_c = pair_us(p.M, p.N, p.K, halves, num_sms / 2, c);
+        if (us_c < best) {
+            best = us_c;
+            plan->split = c;
+        }
+    }
+    if (forced == 0) return cudaSuccess;
     const int most = halves == 2 ? 128 : 256, whole = (int)up(p.M, 16) * 16;
     const int tokens[5] = {whole, 32, 64, 128, 256};
     for (int i = 0; i < 5; ++i) {

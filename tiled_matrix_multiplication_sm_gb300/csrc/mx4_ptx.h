@@ -209,11 +209,11 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "n"(COLS) : "memory");
 }
 // Arrive on `bar` once the MMAs and copies issued so far are complete; PAIR:
-// in both blocks of the pair.
+// in both blocks of the pair, whose first has rank `first` in the cluster.
 template <bool PAIR>
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t first = 0) {
     if constexpr (PAIR) {
-        const uint16_t both = 0x3;
+        const uint16_t both = (uint16_t)(0x3u << first);
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
             " [%0], %1;" :: "r"(bar), "h"(both) : "memory");
