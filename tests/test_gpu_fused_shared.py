@@ -124,3 +124,24 @@ def test_the_same_call_gives_the_same_bits_alone_and_in_a_graph(tgemm):
     torch.cuda.synchronize()
     assert all(torch.equal(first, x) for xs in results for x in xs)
     assert tgemm.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N", [(300, 256), (1500, 1500)])
+@pytest.mark.parametrize("c", [BF16, F32])
+def test_a_stage_that_never_fills_is_reported(tgemm, M, N, c):
+    """Every pair's waits run out, and the cluster's blocks meet all the same."""
+    K = 2100
+    g = generator("stall", M, N)
+    a, b = whole(g, M, K), whole(g, N, K)
+    A, B = a.to(BF16).cuda(), b.to(BF16).cuda()
+    assert tgemm.device_status() == 0
+    tgemm.binding.set_wait_limit_ns(20_000_000)
+    tgemm.binding.set_debug_stall(True)
+    try:
+        tgemm.gemm_act(A, B, "relu", trans_b=True, out_dtype=c)
+        assert tgemm.device_status() == tgemm.binding.TGEMM_ERR_DEVICE_TIMEOUT
+    finally:
+        tgemm.binding.set_debug_stall(False)
+        tgemm.binding.set_wait_limit_ns(2_000_000_000)
+    assert tgemm.device_status() == 0
+    assert torch.equal(tgemm.gemm_act(A, B, "relu", trans_b=True, out_dtype=c).cpu(), product(a, b.t()).clamp(min=0).to(c))
