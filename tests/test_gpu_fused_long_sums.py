@@ -1,0 +1,66 @@
+"""What results of 32 bits of the fused products keep of long sums, against 64 bits:
+the header's bounds, relative to the result's norm.
+
+A tensor-core step of 16 columns of K adds to an FP32 sum with low bits cut off,
+which takes some 1.5e-8 of the sum from it each time where terms have random signs
+(6e-8 a stage of 64), and up to 2^-23 of it where all have one: a part of 13 stages
+loses 0.8e-6 and 1.5e-6 in the norm, however many parts there are, and activations
+make at most 1.2 of it (the largest ratio of z act'(z) to act(z) in the norm, z normal).
+"""
+import pytest
+import torch
+
+import fused_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+KERNELS = {"auto": -1, "pairs": 0, "few": 1}
+
+
+@pytest.fixture(autouse=True)
+def by_the_model(tgemm):
+    yield
+    tgemm.fused.set_fused_kernel(-1)
+
+
+def normal(seed, *size, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(size, generator=g, device="cuda") * scale).to(BF16)
+
+
+def off(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+# Boxes and a column a lane (513), pairs that share sums (tiles few, sums long) and that do
+# not, few tiles alone and in clusters; sums of a little over one part, of several, of many.
+SIZES = [("pairs", 300, 512, 1040), ("pairs", 4096, 2560, 1664), ("pairs", 4096, 2565, 1664), ("pairs", 300, 512, 2100),
+         ("pairs", 300, 512, 4096), ("pairs", 300, 513, 4096), ("pairs", 1500, 1500, 4096), ("pairs", 300, 512, 14336),
+         ("pairs", 300, 513, 14336), ("pairs", 2600, 4096, 14336), ("few", 300, 512, 1040), ("few", 40, 512, 1664),
+         ("few", 300, 512, 2100), ("few", 1500, 1500, 4096), ("few", 8, 513, 4096), ("few", 300, 512, 14336), ("few", 8, 512, 65536),
+         ("auto", 300, 512, 1024), ("auto", 16, 4096, 14336), ("auto", 3000, 5001, 1537)]
+
+
+@pytest.mark.parametrize("kernel,M,N,K", SIZES)
+def test_fp32_results_of_long_sums(tgemm, kernel, M, N, K):
+    A, B = normal(M + K, M, K), normal(N + K, N, K, scale=K ** -0.5)
+    z = A.double() @ B.double().t()
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    for act in ref.ACTS:
+        got, want = tgemm.gemm_act(A, B, act, trans_b=True, out_dtype=F32), ref.act(act, z)[0]
+        bound = 1e-6
+        if M == N:
+            # One seed: B is A's numbers, and terms on the diagonal are squares, of one sign: 2e-6 of
+            # them (the next test's), 1e-6 of the others; errors of different entries add in squares.
+            squares, all_of_it = want.diagonal().norm() ** 2, want.norm() ** 2
+            bound = (((1e-6) ** 2 * (all_of_it - squares) + (2e-6) ** 2 * squares) / all_of_it).sqrt().item()
+        assert off(got, want) <= bound, act
+
+
+@pytest.mark.parametrize("kernel,M,N,K", [s for s in SIZES if s[3] >= 1537])
+def test_fp32_results_of_long_sums_of_one_sign(tgemm, kernel, M, N, K):
+    A, B = normal(M + K, M, K).abs(), normal(N + K, N, K, scale=1 / K).abs()
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    got = tgemm.gemm_act(A, B, trans_b=True, out_dtype=F32)
+    assert off(got, A.double() @ B.double().t()) <= 2e-6

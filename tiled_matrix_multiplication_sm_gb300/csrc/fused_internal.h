@@ -77,11 +77,14 @@ constexpr int FUSED_FEW_RING = 209 * 1024;
 // Long sums come in parts where the result keeps 32 bits, in stages of so many
 // columns of K: `first` stages for the first two parts, `rest` for the others.
 //
-// A part of n stages of 64 loses n / 16 x 0.55e-6 of an FP32 C's norm, 0.99e-6 of a
-// gradient's column sums; parts of n_i, the mean of n_i weighted by n_i. An FP32
-// product in torch loses 0.2e-6 to 0.7e-6 in all. So C comes in parts of 21 (one of
-// up to 26: 0.96e-6), column sums in a weighted mean of 14.5. A loss is a small
-// difference of large logits: parts of 7, for few tokens of 2 (0.8e-6, 0.3e-6).
+// A part of n stages of 64 loses 6.2e-8 n of its sums' norm where terms have random
+// signs, nearly all of it in proportion to each sum, and 1.2e-7 n where all have one;
+// parts of n_i, the mean of n_i weighted by n_i: their number does not matter. An FP32
+// product in torch loses 0.2e-6 to 0.7e-6 in all. So C comes in parts of 13 at most: 0.8e-6,
+// 0.95e-6 once SiLU is taken of it (in parts of 21, 1.5e-6: 14336 x 4096 x 8192 with R 583 us
+// for 578; a column a lane, 3000 x 5001 x 1537 with R and Z in two parts 118 for 99 in one of
+// 1.6e-6), column sums in a weighted mean of 14.5: 0.9e-6. A loss is a small difference
+// of large logits: parts of 7, for few tokens of 2.
 //
 // On pairs the MMAs are two parts ahead of the epilogue at most, and that of a
 // gated gradient takes 9 us, the time of 34 stages: the first two parts are

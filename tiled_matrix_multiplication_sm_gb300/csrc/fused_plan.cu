@@ -73,7 +73,7 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
         return FusedParts{n, n};
     };
     if (kind == FUSED_CE) return even(few ? 2 : 7);
-    if (kind != FUSED_GRAD) return stages * scale <= 26 ? FusedParts{stages, stages} : even(21);
+    if (kind != FUSED_GRAD) return even(13);
     if (few || stages <= 28) return even(14);
     for (int first = 18; first > 14; --first) {
         const int left = stages - 2 * first;
