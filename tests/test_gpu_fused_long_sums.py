@@ -64,3 +64,23 @@ def test_fp32_results_of_long_sums_of_one_sign(tgemm, kernel, M, N, K):
     tgemm.fused.set_fused_kernel(KERNELS[kernel])
     got = tgemm.gemm_act(A, B, trans_b=True, out_dtype=F32)
     assert off(got, A.double() @ B.double().t()) <= 2e-6
+
+
+@pytest.mark.parametrize("kernel,T,V,D", [("pairs", 300, 5000, 1024), ("pairs", 300, 5001, 4096), ("pairs", 300, 5000, 14336),
+                                          ("pairs", 300, 20000, 4096), ("pairs", 2000, 20000, 4096), ("pairs", 300, 50000, 1024),
+                                          ("pairs", 40, 30000, 14336), ("few", 300, 20000, 4096), ("few", 8, 30000, 4096),
+                                          ("auto", 4, 30000, 2048), ("auto", 1300, 20001, 2049)])
+def test_losses_of_long_sums(tgemm, kernel, T, V, D):
+    """Targets some 8 above logits of spread 1, as a trained head's are. With every logit z losing c z a loss is
+    off by c (1 - p) z_t, p the target's probability: 4 c of the loss at V = 5000 (p = 0.27, loss 1.3), 3 c at 20000
+    (0.08, 2.5), less at larger V; c is 2.5e-7 in parts of 4 stages. lse is dominated by the largest logits: c of itself."""
+    W = normal(D, V, D, scale=D ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = (torch.randn((T, D), generator=g, device="cuda") + 8 * W[target].float()).to(BF16)
+    z = X.double() @ W.double().t()
+    want = torch.logsumexp(z, dim=1)
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    loss, lse = tgemm.gemm_ce(X, W, target)
+    assert off(lse, want) <= 2.5e-7
+    assert off(loss, want - z.gather(1, target[:, None])[:, 0]) <= 1e-6

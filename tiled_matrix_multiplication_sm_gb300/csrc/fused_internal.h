@@ -84,7 +84,8 @@ constexpr int FUSED_FEW_RING = 209 * 1024;
 // 0.95e-6 once SiLU is taken of it (in parts of 21, 1.5e-6: 14336 x 4096 x 8192 with R 583 us
 // for 578; a column a lane, 3000 x 5001 x 1537 with R and Z in two parts 118 for 99 in one of
 // 1.6e-6), column sums in a weighted mean of 14.5: 0.9e-6. A loss is a small difference
-// of large logits: parts of 7, for few tokens of 2.
+// of large logits, off by what its target's loses: parts of 4, for few tokens of 2 (8192 x
+// 65536 x 4096, us, in parts of 7, 5, 4, 3: 2206, 2203, 2213, 2287).
 //
 // On pairs the MMAs are two parts ahead of the epilogue at most, and that of a
 // gated gradient takes 9 us, the time of 34 stages: the first two parts are

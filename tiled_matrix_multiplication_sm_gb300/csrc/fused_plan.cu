@@ -72,7 +72,7 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
         const int n = stages > 0 ? (int)up(stages, up(stages, most)) : 1;
         return FusedParts{n, n};
     };
-    if (kind == FUSED_CE) return even(few ? 2 : 7);
+    if (kind == FUSED_CE) return even(few ? 2 : 4);
     if (kind != FUSED_GRAD) return even(13);
     if (few || stages <= 28) return even(14);
     for (int first = 18; first > 14; --first) {
