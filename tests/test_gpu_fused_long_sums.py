@@ -84,3 +84,49 @@ def test_losses_of_long_sums(tgemm, kernel, T, V, D):
     loss, lse = tgemm.gemm_ce(X, W, target)
     assert off(lse, want) <= 2.5e-7
     assert off(loss, want - z.gather(1, target[:, None])[:, 0]) <= 1e-6
+
+
+@pytest.mark.parametrize("kernel,M,N,K", [("pairs", 300, 512, 1152), ("pairs", 300, 513, 2100), ("pairs", 1500, 1500, 4096),
+                                          ("pairs", 8192, 512, 4096), ("pairs", 300, 512, 14336), ("few", 300, 512, 1152),
+                                          ("few", 1500, 1504, 4096), ("few", 40, 513, 4096), ("few", 300, 512, 14336),
+                                          ("auto", 256, 1024, 1024), ("auto", 2000, 4099, 2048)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_bias_gradients_of_long_sums(tgemm, kernel, M, N, K, gated):
+    """db, and dZ in 32 bits: slopes leave the sums' relative error as it is."""
+    A, B, Z = normal(M + 1, M, K, scale=1e-3), normal(N + 2, K, N, scale=K ** -0.5), normal(K + 3, M, 2 * N if gated else N)
+    d, z = A.double() @ B.double(), Z.double()
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    for act in ref.ACTS:
+        if gated:
+            v, s = ref.act(act, z[:, :N])
+            want = torch.cat((d * z[:, N:] * s, d * v), dim=1)
+        else:
+            want = d * ref.act(act, z)[1]
+        got, db = tgemm.gemm_act_grad(A, B, Z, act, gated=gated, out_dtype=BF16 if gated else F32)
+        assert off(db, want.sum(dim=0)) <= 1e-6, act
+        if not gated:
+            assert off(got, want) <= 1e-6, act
+
+
+@pytest.mark.parametrize("kernel,M,N,K", [("pairs", 300, 512, 1152), ("pairs", 2048, 513, 4096), ("few", 300, 512, 4096)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_bias_gradients_of_long_sums_of_one_sign(tgemm, kernel, M, N, K, gated):
+    A, B = normal(M + 1, M, K).abs(), normal(N + 2, K, N, scale=1 / K).abs()
+    Z = normal(K + 3, M, 2 * N if gated else N).abs() + 1
+    d, z = A.double() @ B.double(), Z.double()
+    want = (torch.cat((d * z[:, N:], d * z[:, :N]), dim=1) if gated else d).sum(dim=0)
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    assert off(tgemm.gemm_act_grad(A, B, Z, "relu", gated=gated)[1], want) <= 2e-6
+
+
+@pytest.mark.parametrize("kernel", ["pairs", "few"])
+@pytest.mark.parametrize("N", [64, 61])
+def test_bias_gradients_of_a_million_rows(tgemm, kernel, N):
+    """One stage of K: 0.7e-7 of the norm. What is left is the sum over the rows: one of n terms takes n additions of
+    2^-25 of the sum so far each, as an error's standard deviation at most, and the sum grows as the root of its terms:
+    (n / 2)^(1/2) 2^-25 of it. A block of 32 or 64 rows, 64 blocks, 64 such sums to a warp, and 8 warps: below 5e-7."""
+    M, K = 2 ** 20 + 77, 64
+    A, B, Z = normal(1, M, K), normal(2, K, N, scale=K ** -0.5), normal(3, M, N)
+    want = ((A.double() @ B.double()) * ref.act("silu", Z.double())[1]).sum(dim=0)
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    assert off(tgemm.gemm_act_grad(A, B, Z, "silu")[1], want) <= 5e-7

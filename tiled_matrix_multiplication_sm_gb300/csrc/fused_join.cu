@@ -9,8 +9,9 @@ namespace {
 using fused_act::exp2_fast;
 using fused_act::LOG2E;
 
-// A block takes 32 columns; its 8 warps take every eighth block of rows each
-// and are added in their order.
+// A block takes 32 columns; its 8 warps take every eighth block of rows each, add
+// them up 64 at a time, and are added in their order. (One after the other the roundings
+// of a million rows' additions took 1.0e-6 of db's norm.)
 __global__ void __launch_bounds__(256) join_sums_kernel(const float* sums, long blocks, long cols, float* db) {
     pdl_launch_dependents();
     __shared__ float part[8][32];
@@ -19,8 +20,13 @@ __global__ void __launch_bounds__(256) join_sums_kernel(const float* sums, long 
     pdl_wait();
     float v = 0.0f;
     if (c < cols)
+        for (long b = warp; b < blocks;) {
+            const long end = b + 8 * 64 < blocks ? b + 8 * 64 : blocks;
+            float some = 0.0f;
 #pragma unroll 4
-        for (long b = warp; b < blocks; b += 8) v += sums[b * cols + c];
+            for (; b < end; b += 8) some += sums[b * cols + c];
+            v += some;
+        }
     part[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < cols) {
