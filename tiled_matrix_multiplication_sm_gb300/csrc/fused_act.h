@@ -76,7 +76,10 @@ __device__ __forceinline__ void value_slope(float z, float& v, float& d) {
     } else if constexpr (ACT == TGEMM_ACT_GELU_TANH) {
         const float s = sigmoid(tanh_arg(z));
         v = z * s;
-        d = fmaf(v * (1.0f - s), 2.0f * ROOT_2_PI * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
+        // (A square past FP32's range, from |z| of 4e19 on, would be an infinity times 0: s or 1 - s
+        // is 0 long before.)
+        const float a = fminf(fabsf(z), 1e18f);
+        d = fmaf(v * (1.0f - s), 2.0f * ROOT_2_PI * fmaf(3.0f * 0.044715f * a, a, 1.0f), s);
     } else if constexpr (ACT == TGEMM_ACT_SILU) {
         const float s = sigmoid(z);
         v = z * s;
