@@ -27,3 +27,30 @@ def test_activations_and_slopes_far_out(tgemm, kernel, act):
     got = tgemm.gemm_act_grad(rows, one.cuda(), both.cuda(), act, gated=True, bias_grad=False)
     want, e = torch.cat((s, v), dim=1), torch.cat((es, ev), dim=1)
     ref.check(got, want, ref.rounded(want, e, BF16), "gated")
+
+
+def far_logits(V, other):
+    """(X, W, z): rows all of whose logits, or whose largest and least, are near the ends of FP32's range; z in 64 bits."""
+    x = torch.tensor([1.0, -1.0, 0.5, 2.0 ** -130, 0.0])[:, None] * 2.0 ** 64
+    w = torch.full((V, 1), other * 2.0 ** 63)
+    w[3] = w[V - 2] = 1.75 * 2.0 ** 63
+    z = x.double() @ w.double().t()
+    assert z.isfinite().all() and z[0].max() > 2.4e38 and z[1].max().abs() > 2.4e38
+    return x.to(BF16), w.to(BF16), z
+
+
+@pytest.mark.parametrize("V,other", [(40, 1.5), (300, 1.5), (40, -1.625), (300, -1.625)])
+def test_losses_of_logits_far_out(tgemm, kernel, V, other):
+    X, W, z = far_logits(V, other)
+    # Each row's largest logit (one of two or more), and its least.
+    target = torch.cat((z.argmax(dim=1), z.argmin(dim=1)))
+    X, z = torch.cat((X, X)), torch.cat((z, z))
+    top = z.max(dim=1).values
+    more = torch.log(torch.exp(z - top[:, None]).sum(dim=1))
+    # (From the maximum: lse itself has no bits left for log 2.) Losses past FP32's range are infinities.
+    loss = (more + (top - z.gather(1, target[:, None])[:, 0])).float().double()
+    got, lse = tgemm.gemm_ce(X.cuda(), W.cuda(), target.cuda())
+    got, finite = got.double().cpu(), loss.isfinite()
+    assert torch.equal(got[~finite], loss[~finite])
+    ref.check(got[finite], loss[finite], 2.0 ** -18 + 2.0 ** -20 * loss[finite].abs(), "loss")
+    ref.check(lse, top + more, 2.0 ** -18 + 2.0 ** -20 * top.abs(), "lse")

@@ -349,6 +349,11 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
 }
 
 // ------------------------------------------------------------ cross entropy
+// Past this a row's differences from its maximum, or lse, are taken before their product with
+// log2(e): rounded, that product is off by as much as its bits are apart (128 and more from
+// 2^31 on: 2^128 is an infinity), and from 2.36e38 on an infinity itself.
+constexpr float FAR = 1024.0f;
+
 // The maximum of this thread's row over its set's columns and the sum of exp(z -
 // maximum), taken 32 columns at a time; the target's logit where it is among them.
 struct CeRow {
@@ -384,7 +389,14 @@ struct CeRow {
         for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
         // exp(v - top) as 2^(v L - at), at = top L rounded: one multiply-add each. What at is
         // off by, exactly the remainder of that product, goes back into the sum.
-        const float base = top == -INFINITY ? 0.0f : top, at = base * LOG2E, off = fmaf(base, LOG2E, -at);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float from = base;
+        if (fabsf(base) > FAR) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] -= base;
+            from = 0.0f;
+        }
+        const float at = from * LOG2E, off = fmaf(from, LOG2E, -at);
         s *= exp2_fast((m - base) * LOG2E);
         float q[4] = {};
 #pragma unroll
