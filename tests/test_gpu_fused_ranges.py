@@ -54,3 +54,72 @@ def test_losses_of_logits_far_out(tgemm, kernel, V, other):
     assert torch.equal(got[~finite], loss[~finite])
     ref.check(got[finite], loss[finite], 2.0 ** -18 + 2.0 ** -20 * loss[finite].abs(), "loss")
     ref.check(lse, top + more, 2.0 ** -18 + 2.0 ** -20 * top.abs(), "lse")
+
+
+@pytest.mark.parametrize("V,other", [(40, 1.5), (300, 1.5), (40, -1.625), (300, -1.625)])
+def test_gradients_of_logits_far_out(tgemm, kernel, V, other):
+    """lse in FP32 is the largest logit itself, exp(z - lse) 1 or 0: sums of whole multiples of W's numbers, exact."""
+    X, W, z = far_logits(V, other)
+    target = z.argmax(dim=1)
+    lse = torch.logsumexp(z, dim=1).float()
+    p = torch.exp(z - lse.double()[:, None])
+    p[torch.arange(len(X)), target] -= 1
+    dloss = torch.full((len(X),), 2.0 ** -6)
+    dx, dw = tgemm.gemm_ce_grad(X.cuda(), W.cuda(), target.cuda(), lse.cuda(), dloss.cuda(), dx_dtype=F32, dw_dtype=F32)
+    assert torch.equal(dx.double().cpu()[:3], ((p * 2.0 ** -6) @ W.double())[:3])
+    assert dw.isfinite().all()
+
+
+@pytest.mark.parametrize("T,V", [(7, 100), (300, 1000)])
+@pytest.mark.parametrize("scale", [6, 12, 20, 28, 31, 34, 40, 80])
+def test_large_logits(tgemm, kernel, scale, T, V):
+    """Whole numbers times 2^scale: exact logits, and a loss of their exact differences and the logarithm of a small number."""
+    g = torch.Generator().manual_seed(scale + V)
+    x, w = torch.randint(-3, 4, (T, 8), generator=g).double(), torch.randint(-3, 4, (V, 8), generator=g).double()
+    target = torch.randint(0, V, (T,), generator=g)
+    z = x @ w.t() * 2.0 ** scale
+    target[::2] = z.argmax(dim=1)[::2]
+    X, W = (x * 2.0 ** scale).to(BF16), w.to(BF16)
+    top = z.max(dim=1).values
+    more = torch.log(torch.exp(z - top[:, None]).sum(dim=1))
+    loss = more + (top - z.gather(1, target[:, None])[:, 0])
+    got, lse = tgemm.gemm_ce(X.cuda(), W.cuda(), target.cuda())
+    # Exponentials and their sums to 2^-19, additions to 2^-24 of their sum.
+    ref.check(got, loss, 2.0 ** -18 + 2.0 ** -23 * loss, "loss")
+    ref.check(lse, top + more, 2.0 ** -18 + 2.0 ** -23 * top.abs(), "lse")
+    # Under the lse that FP32 holds: a difference rounded once, an exponential, and dz's rounding to BF16.
+    lse = lse.double().cpu()
+    p = torch.exp(z - lse[:, None])
+    ep = p * torch.expm1(2.0 ** -23 * (z - lse[:, None]).abs().clamp(max=200) + 2.0 ** -18)
+    if scale == 6:
+        ep = ep + p * torch.expm1(2.0 ** -22 * (z.abs() + lse.abs()[:, None]))
+    p[torch.arange(T), target] -= 1
+    # (FP32's and BF16's normal numbers end at 2^-126: an exponential below is 0.)
+    edz = ep + 2.0 ** -8 * (p.abs() + ep) + 2.0 ** -126
+    dx, dw = tgemm.gemm_ce_grad(X.cuda(), W.cuda(), target.cuda(), lse.float().cuda(), torch.ones(T, device="cuda"),
+                                dx_dtype=F32, dw_dtype=F32)
+    for got, a, b, e in ((dx, p, w, edz), (dw, p.t(), x * 2.0 ** scale, edz.t())):
+        want, tol = ref.sums(a, b)
+        ref.check(got, want, tol + e @ b.abs(), "gradient")
+
+
+@pytest.mark.parametrize("V", [40, 300])
+def test_gradients_under_an_alpha_far_out(tgemm, kernel, V):
+    """alpha past FP32's range over log2(e), logits of ordinary size."""
+    alpha = 1.5 * 2.0 ** 127
+    g = torch.Generator().manual_seed(V)
+    X = torch.randint(-3, 4, (33, 8), generator=g) * 2.0 ** -64
+    W = torch.randint(-3, 4, (V, 8), generator=g) * 2.0 ** -64
+    X, W = X.to(BF16), W.to(BF16)
+    target = torch.randint(0, V, (33,), generator=g)
+    loss, lse, z, ez = ref.ce(X.double(), W.double(), target, alpha)
+    assert z.abs().max() < 100
+    got, got_lse = tgemm.gemm_ce(X.cuda(), W.cuda(), target.cuda(), alpha)
+    e_lse, e_loss = ref.ce_bounds(z, ez, lse)
+    ref.check(got, loss, e_loss, "loss")
+    ref.check(got_lse, lse, e_lse, "lse")
+    dloss = torch.full((33,), 2.0 ** -60)
+    want_x, want_w, ex, ew = ref.ce_grad(X.double(), W.double(), target, got_lse.double().cpu(), dloss.double(), alpha)
+    dx, dw = tgemm.gemm_ce_grad(X.cuda(), W.cuda(), target.cuda(), got_lse, dloss.cuda(), alpha, dx_dtype=F32, dw_dtype=F32)
+    ref.check(dx, want_x, ref.rounded(want_x, ex, F32), "dX")
+    ref.check(dw, want_w, ref.rounded(want_w, ew, F32), "dW")

@@ -413,8 +413,9 @@ struct CeRow {
 // 64 columns of the logits' gradient.
 __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
                                              int& box, float lse, float scale, long long target, bool kept) {
-    // (Rounded once a row: 2^-24 of the logit, far below BF16's rounding of the result.)
-    const float by = p.e.alpha * LOG2E, less = lse * LOG2E;
+    // (Rounded once a row: 2^-24 of the logit, below BF16's rounding of the result by far up to FAR.)
+    const bool far = fabsf(lse) > FAR || fabsf(p.e.alpha) > FAR;
+    const float by = far ? LOG2E : p.e.alpha * LOG2E, less = far ? 0.0f : lse * LOG2E;
     const int lane = threadIdx.x & 31;
     uint8_t* buf = bufs + (box++ & 1) * BUF_BYTES;
     if (lane == 0) tma_store_wait_read<1>();
@@ -424,6 +425,9 @@ __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, 
         float v[32];
         load_sums(acc + h * 32, v, p.kblocks);
         const long long t = target - (col + h * 32);
+        if (far)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], p.e.alpha, -lse);
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], by, -less));
         if (__any_sync(~0u, t >= 0 && t < 32))
