@@ -7,7 +7,7 @@
 // fill the MMA whatever the number of tokens, and a lane has a column of C: its
 // 32 lanes' loads and stores are segments of rows, of any alignment.
 //
-// A tile takes `height` columns of C, 8 to 128, so that tiles are about as many as
+// A tile takes `height` columns of C, 16 to 128, so that tiles are about as many as
 // SMs (14336 columns: 150 tiles of 96); the MMA's other rows multiply what lies
 // behind them in shared memory, and nobody reads them. Where that is not
 // enough, a cluster's blocks split K and add their shares through distributed
@@ -33,12 +33,44 @@ constexpr int CHUNK_K = 64;                          // columns of K in a swizzl
 constexpr int MAX_STAGES = 24;
 constexpr int SETS = FUSED_FEW_SETS, EPI_WARPS = 4 * SETS;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-// The MMA reads 128 rows from an operand's start on: the last stage's reach past it.
+// The MMA reads 128 rows of the weights whatever the height: the last stage's reach past the ring.
 constexpr int GUARD_BYTES = 128 * SW;
 constexpr int SYNC_BYTES = 512;
 constexpr int SMEM = 227 * 1024;
 constexpr int RING_BYTES = FUSED_FEW_RING;
 static_assert(1024 + RING_BYTES + GUARD_BYTES + SYNC_BYTES <= SMEM, "shared memory");
+
+// A stage's bytes: chunks of K of `halves` times `height` rows of weights and of `tokens` rows.
+constexpr int stage_bytes_of(int height, int tokens, int chunks, int halves) { return chunks * (halves * height + tokens) * SW; }
+// What the MMA reads from a stage's start on: of the last half, 128 rows behind its last
+// chunk's start, or, MN-major, two boxes of 64, the second behind all of the first's chunks.
+constexpr int reach_of(int height, int chunks, int halves, bool w_mn) {
+    return (halves - 1) * chunks * height * SW + (w_mn ? 2 * chunks * CHUNK_K * SW : ((chunks - 1) * height + 128) * SW);
+}
+// As many stages as fit, with what the MMA reads from the last one on.
+constexpr int stages_of(int height, int tokens, int chunks, int halves, bool w_mn) {
+    const int bytes = stage_bytes_of(height, tokens, chunks, halves);
+    int n = RING_BYTES / bytes < MAX_STAGES ? RING_BYTES / bytes : MAX_STAGES;
+    while (n > 0 && (n - 1) * bytes + reach_of(height, chunks, halves, w_mn) > RING_BYTES + GUARD_BYTES) --n;
+    return n;
+}
+// Of all shapes that a plan may have: fewest stages.
+constexpr int fewest_stages() {
+    int fewest = MAX_STAGES;
+    for (int halves = 1; halves <= 2; ++halves)
+        for (int height = 16; height <= 128; height += 8)
+            for (int tokens = 16; tokens <= 256 / halves; tokens += 16)
+                for (int chunks = 1; chunks <= 4; chunks *= 2) {
+                    if (chunks > 1 && 4 * stage_bytes_of(height, tokens, chunks, halves) > RING_BYTES) continue;
+                    for (int mn = 0; mn < 2; ++mn) {
+                        if (mn && height % 64 != 0) continue;
+                        const int n = stages_of(height, tokens, chunks, halves, mn != 0);
+                        fewest = n < fewest ? n : fewest;
+                    }
+                }
+    return fewest;
+}
+static_assert(fewest_stages() >= 4, "every plan's tiles run four stages deep");
 
 struct Sync {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
@@ -513,8 +545,9 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     p.num_tiles = (int)tiles;
     p.units = p.split > 1 || p.num_tiles < num_sms ? p.num_tiles : num_sms;
     p.half_bytes = p.chunks * p.height * SW;
-    p.stage_bytes = (two ? 2 : 1) * p.half_bytes + p.chunks * p.tokens * SW;
-    p.stages = RING_BYTES / p.stage_bytes < MAX_STAGES ? RING_BYTES / p.stage_bytes : MAX_STAGES;
+    p.stage_bytes = stage_bytes_of(p.height, p.tokens, p.chunks, two ? 2 : 1);
+    p.stages = stages_of(p.height, p.tokens, p.chunks, two ? 2 : 1, m.b_mn);
+    if (p.stages < 1) return cudaErrorInvalidValue;
     p.acc = (p.tokens + 31) / 32 * 32;
     p.x_mn = m.a_mn ? 1 : 0;
     p.w_mn = m.b_mn ? 1 : 0;
