@@ -124,7 +124,8 @@ TGEMM_API int gemm_ce(int T, int V, int D, const void* X, long ldx, const void* 
  *
  * dz is made from X and W again, in BF16 scratch, for as many columns at a time
  * as 256 MB hold (1024 at least), so that memory does not grow with the
- * vocabulary; over more than one such piece dX is summed in FP32 scratch. dX
+ * vocabulary; over more than one such piece dX is summed in FP32, in scratch or, one
+ * of FP32 with rows on 16 bytes and D a multiple of 4, where it is. dX
  * (T x D) and dW (V x D) are BF16 or FP32; either may be NULL. dW is not read
  * when beta == 0. Rows left out (see gemm_ce) get a dX of 0 and add nothing to
  * dW, whatever X, lse and dloss hold there (with a finite W).

@@ -197,6 +197,9 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     if (piece < PIECE_COLS) piece = PIECE_COLS;
     if (piece > V) piece = V;
     const bool sums = dX.x != nullptr && piece < V;          // dX over several pieces
+    // An FP32 dX holds its own sum, where the products before the last can pass it by TMA
+    // as they pass scratch (131072 x 2048: 1 GB less of that).
+    const bool inside_x = sums && dX.type == TGEMM_TYPE_F32 && !off(dX.x, 16) && dX.ld % 4 == 0 && D % 4 == 0;
     const long ldz = (piece + 63) / 64 * 64, ldk = ((long)D + 63) / 64 * 64;
     Scratch scratch(s);
     // A dW takes X with the rows left out as zeros: copied by the logits' product where
@@ -213,10 +216,12 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
     if (dX.x != nullptr && T > 0 && piece == V && V > 0)
         e = tgemm::fused_plan_slices(FusedProduct{T, D, V, nullptr, 0, false, nullptr, 0, true, nullptr}, sms, &slice);
     if (e != cudaSuccess) return e;
-    const size_t sum_at = scratch.add(sums ? (size_t)T * ldk * 4 : slice.slices > 1 ? (size_t)slice.slices * T * D * 4 : 0);
+    const size_t sum_at = scratch.add(sums && !inside_x ? (size_t)T * ldk * 4 : slice.slices > 1 ? (size_t)slice.slices * T * D * 4 : 0);
     e = scratch.take();
     if (e != cudaSuccess) return e;
-    void *const z = scratch.at(z_at), *const kept = scratch.at(kept_at), *const sum = scratch.at(sum_at);
+    void *const z = scratch.at(z_at), *const kept = scratch.at(kept_at);
+    void *const sum = inside_x ? dX.x : scratch.at(sum_at);
+    const long ld_sum = inside_x ? dX.ld : ldk;
     const tgemm::CopyJob jobs[3] = {x.lay(scratch), w.lay(scratch), {X, ldx, kept, ldk, before ? T : 0, D, target, V, false}};
     e = tgemm::fused_copy_rows(jobs, 3, s);
     if (before) {
@@ -260,11 +265,11 @@ cudaError_t ce_grad(int T, int V, int D, const void* X, long ldx, const void* W,
             const bool last = v + piece >= V;
             FusedEpilogue ep;
             ep.C = last ? dX.x : sum;
-            ep.ldc = last ? dX.ld : ldk;
+            ep.ldc = last ? dX.ld : ld_sum;
             ep.c_f32 = !last || dX.type == TGEMM_TYPE_F32;
             if (v > 0) {
                 ep.R = sum;
-                ep.ldr = ldk;
+                ep.ldr = ld_sum;
                 ep.r_f32 = true;
             }
             const FusedProduct p{T, D, n, z, ldz, false, wv, w.ld, true, nullptr};
