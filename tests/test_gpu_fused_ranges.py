@@ -123,3 +123,23 @@ def test_gradients_under_an_alpha_far_out(tgemm, kernel, V):
     dx, dw = tgemm.gemm_ce_grad(X.cuda(), W.cuda(), target.cuda(), got_lse, dloss.cuda(), alpha, dx_dtype=F32, dw_dtype=F32)
     ref.check(dx, want_x, ref.rounded(want_x, ex, F32), "dX")
     ref.check(dw, want_w, ref.rounded(want_w, ew, F32), "dW")
+
+
+@pytest.mark.parametrize("act", ref.ACTS[2:])
+def test_tails_of_activations_keep_their_digits(tgemm, kernel, act):
+    """The relative error alone, down to values of 2^-100. An exponential of y (in units of its exponent) is off by
+    the rounding of y: 2^-24 y a rounding, of one product (silu: y = |z|), of the square and its product (gelu: z^2 / 2),
+    of the cubic's four and the factor (gelu_tanh: 2 u), each with the 2^-26 of y that log2(e) is off by; beside it
+    2^-22 of the exponential, 2^-22 of the reciprocal, their sum's 2^-24, gelu's fit (1.9e-7) and the roundings of
+    its polynomial, of degree 7: 2^-19 holds them."""
+    z = torch.cat([torch.linspace(-60, 12, 6001), torch.linspace(-8, 8, 4001), torch.linspace(-0.1, 0.1, 401)]).to(BF16).unique()
+    zd = z.double()
+    want = ref.act(act, zd)[0]
+    z, zd, want = (x[want.abs() >= 2.0 ** -100] for x in (z, zd, want))
+    y = {"silu": zd.abs(), "gelu": zd * zd / 2, "gelu_tanh": 2 * ref.R2PI * zd.abs() * (1 + 0.044715 * zd * zd)}[act]
+    roundings = {"silu": 1, "gelu": 2, "gelu_tanh": 5}[act]
+    got = tgemm.gemm_act(z[:, None].cuda(), torch.ones(1, 40, dtype=BF16, device="cuda"), act, out_dtype=F32)
+    off = (got.double().cpu() - want[:, None]).abs() / want.abs()[:, None]
+    # (Above zero the exponential is below one and goes into 1 + it, or 1 - it: what it is off by shrinks with it.)
+    bound = 2.0 ** -19 + (roundings + 0.25) * 2.0 ** -24 * y * torch.where(zd > 0, torch.exp(-y), torch.ones_like(y))
+    assert (off <= bound[:, None]).all(), (zd[(off > bound[:, None]).any(dim=1)], off.max())
