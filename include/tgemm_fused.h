@@ -17,7 +17,7 @@
  * Sums of products are FP32: on the tensor cores, which cut low bits off at
  * every step. Where a result keeps 32 bits long sums are made of parts, added
  * with rounding to nearest, so that it is off by 1e-6 of its norm or less where
- * terms have random signs, 2e-6 where all have one (an FP32 C: parts of up to 832
+ * terms have random signs, 2e-6 where all have one (an FP32 C: parts of up to 1088
  * columns of K; db: 1152; loss and lse: 256; a bias or residual that cancels
  * most of the sums leaves that much of the sums' norm, and a loss far below its
  * logits is off by 3e-7 of them). Values

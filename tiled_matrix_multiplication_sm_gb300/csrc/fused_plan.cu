@@ -73,19 +73,25 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
         return FusedParts{n, n};
     };
     if (kind == FUSED_CE) return even(few ? 2 : 4);
-    if (kind != FUSED_GRAD) return even(13);
-    if (few || stages <= 28) return even(14);
-    for (int first = 18; first > 14; --first) {
-        const int left = stages - 2 * first;
-        if (left < 1) continue;
-        for (int most = 14; most >= 8; --most) {
+    // On pairs: the first two parts up to `longest`, as long as the mean allows it, the others even.
+    const bool grad = kind == FUSED_GRAD;
+    const int most_even = grad ? 14 : 13, longest = grad ? 18 : 17;
+    const double mean = grad ? 14.5 : 13.0;
+    if (few || stages <= (grad ? 28 : 13)) return even(most_even);
+    for (int first = longest; first > most_even; --first) {
+        const int left = stages - 2 * first, second = stages - first;
+        if (left < 1) {
+            if (second > 0 && first * first + second * second <= mean * stages) return {first, second};
+            continue;
+        }
+        for (int most = most_even; most >= 8; --most) {
             const int parts = (int)up(left, most), rest = (int)up(left, parts);
             const double squares = 2.0 * first * first + (double)rest * rest * (parts - 1) +
                                    (double)(left - rest * (parts - 1)) * (left - rest * (parts - 1));
-            if (squares <= 14.5 * stages) return {first, rest};
+            if (squares <= mean * stages) return {first, rest};
         }
     }
-    return even(14);
+    return even(most_even);
 }
 
 bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e) {
