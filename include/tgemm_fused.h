@@ -17,8 +17,8 @@
  * Sums of products are FP32: on the tensor cores, which cut low bits off at
  * every step. Where a result keeps 32 bits long sums are made of parts, added
  * with rounding to nearest, so that it is off by 1e-6 of its norm or less where
- * terms have random signs, 2e-6 where all have one (an FP32 C: parts of up to 1088
- * columns of K; db: 1152; loss and lse: 256; a bias or residual that cancels
+ * terms have random signs, 2e-6 where all have one (an FP32 C and db: parts of up to
+ * 1152 columns of K; loss and lse: 256; a bias or residual that cancels
  * most of the sums leaves that much of the sums' norm, and a loss far below its
  * logits is off by 3e-7 of them). Values
  * go from the sum to the result in FP32 and are rounded once, to nearest even,

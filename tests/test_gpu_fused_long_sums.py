@@ -119,6 +119,15 @@ def test_bias_gradients_of_long_sums_of_one_sign(tgemm, kernel, M, N, K, gated):
     assert off(tgemm.gemm_act_grad(A, B, Z, "relu", gated=gated)[1], want) <= 2e-6
 
 
+def test_bias_gradients_of_many_rows_of_long_sums(tgemm):
+    """The dZ's errors add up over the rows as they themselves do: db is off by as much of its norm."""
+    M, N, K = 65536, 256, 4096
+    A, B, Z = normal(3, M, K, scale=1e-3), normal(4, K, N, scale=K ** -0.5), normal(5, M, N)
+    d = A.double() @ B.double()
+    for act in ref.ACTS:
+        assert off(tgemm.gemm_act_grad(A, B, Z, act)[1], (d * ref.act(act, Z.double())[1]).sum(dim=0)) <= 1e-6, act
+
+
 @pytest.mark.parametrize("kernel", ["pairs", "few"])
 @pytest.mark.parametrize("N", [64, 61])
 def test_bias_gradients_of_a_million_rows(tgemm, kernel, N):

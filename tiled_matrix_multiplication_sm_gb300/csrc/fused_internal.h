@@ -80,11 +80,12 @@ constexpr int FUSED_FEW_RING = 209 * 1024;
 // A part of n stages of 64 loses 6.2e-8 n of its sums' norm where terms have random
 // signs, nearly all of it in proportion to each sum, and 1.2e-7 n where all have one;
 // parts of n_i, the mean of n_i weighted by n_i: their number does not matter. An FP32
-// product in torch loses 0.2e-6 to 0.7e-6 in all. So C comes in parts of a weighted mean of
-// 13: 0.8e-6, 0.95e-6 once SiLU is taken of it (a column a lane, 3000 x 5001 x 1537 with R
-// and Z in two parts 93 us for 76 in one of 1.6e-6), column sums of 14.5: 0.9e-6. A loss is a small
-// difference of large logits, off by what its target's loses: parts of 4, for few tokens of 2
-// (8192 x 65536 x 4096, us, in parts of 7, 5, 4, 3: 2206, 2203, 2213, 2287).
+// product in torch loses 0.2e-6 to 0.7e-6 in all. So an FP32 C and column sums come in parts of
+// a weighted mean of 13: 0.8e-6, 0.95e-6 once SiLU is taken of it (a column a lane, 3000 x
+// 5001 x 1537 with R and Z in two parts 93 us for 76 in one of 1.6e-6; column sums of 65536 rows,
+// K = 4096, in parts of a mean of 14.5 1.04e-6). A loss is a small difference of large logits,
+// off by what its target's loses: parts of 4, for few tokens of 2 (8192 x 65536 x 4096, us, in
+// parts of 7, 5, 4, 3: 2206, 2203, 2213, 2287).
 //
 // On pairs the MMAs are two parts ahead of the epilogue at most, and that of a
 // gated gradient takes 9 us, the time of 34 stages: the first two parts are

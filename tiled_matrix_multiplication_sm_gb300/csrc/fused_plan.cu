@@ -73,25 +73,22 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
         return FusedParts{n, n};
     };
     if (kind == FUSED_CE) return even(few ? 2 : 4);
-    // On pairs: the first two parts up to `longest`, as long as the mean allows it, the others even.
-    const bool grad = kind == FUSED_GRAD;
-    const int most_even = grad ? 14 : 13, longest = grad ? 18 : 17;
-    const double mean = grad ? 14.5 : 13.0;
-    if (few || stages <= (grad ? 28 : 13)) return even(most_even);
-    for (int first = longest; first > most_even; --first) {
+    // On pairs: the first two parts up to 18, as long as a mean of 13 allows it, the others even.
+    constexpr int EVEN = 13;
+    if (few || stages <= EVEN) return even(EVEN);
+    for (int first = 18; first > EVEN; --first) {
         const int left = stages - 2 * first, second = stages - first;
         if (left < 1) {
-            if (second > 0 && first * first + second * second <= mean * stages) return {first, second};
+            if (second > 0 && first * first + second * second <= EVEN * stages) return {first, second};
             continue;
         }
-        for (int most = most_even; most >= 8; --most) {
+        for (int most = EVEN; most >= 8; --most) {
             const int parts = (int)up(left, most), rest = (int)up(left, parts);
-            const double squares = 2.0 * first * first + (double)rest * rest * (parts - 1) +
-                                   (double)(left - rest * (parts - 1)) * (left - rest * (parts - 1));
-            if (squares <= mean * stages) return {first, rest};
+            const double last = left - rest * (parts - 1), squares = 2.0 * first * first + (double)rest * rest * (parts - 1) + last * last;
+            if (squares <= (double)EVEN * stages) return {first, rest};
         }
     }
-    return even(most_even);
+    return even(EVEN);
 }
 
 bool fused_boxes(FusedKind kind, int N, const FusedEpilogue& e) {
