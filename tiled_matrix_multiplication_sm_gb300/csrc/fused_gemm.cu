@@ -410,7 +410,8 @@ struct CeRow {
     }
 };
 
-// 64 columns of the logits' gradient.
+// 64 columns of the logits' gradient, rounded to BF16: operands of the two products that
+// follow. (In two BF16 numbers each those products, two thirds of the call's, would be twice as long.)
 __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
                                              int& box, float lse, float scale, long long target, bool kept) {
     // (Rounded once a row: 2^-24 of the logit, below BF16's rounding of the result by far up to FAR.)

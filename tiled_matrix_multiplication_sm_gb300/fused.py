@@ -8,7 +8,9 @@ without keeping the logits, :func:`gemm_ce_grad` its gradients. Matrices are
 bfloat16 and row-major (any leading dimension), results bfloat16 or float32.
 Argument marshalling only, as in :mod:`.binding`; every call is asynchronous on
 ``stream`` (default: the current one), and what a call allocates belongs to
-that stream.
+that stream. Results have no autograd history, whatever ``requires_grad`` their
+operands have: the gradients are calls of their own, for a
+``torch.autograd.Function`` to make (``examples/fused_ffn.py`` has a layer's and a head's).
 """
 from __future__ import annotations
 
@@ -236,7 +238,8 @@ def gemm_ce_grad(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: to
                  stream: Optional[torch.cuda.Stream] = None
                  ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """(dX, dW), the gradients of sum(dloss * loss) of :func:`gemm_ce` with its lse
-    (``dloss`` float32, one entry a token). ``x_grad``/``w_grad`` say which are
+    (``dloss`` float32, one entry a token). The logits' gradient is rounded to bfloat16
+    between the products, for float32 results too. ``x_grad``/``w_grad`` say which are
     wanted (the other is None). dW goes to ``dw_out``, plus ``beta`` times what
     is there (a sum over micro-batches), or to a new ``dw_dtype`` matrix."""
     T, V, D, ldx, ldw, t, device = _head(X, W, target)
