@@ -131,8 +131,10 @@ TGEMM_API int gemm_ce(int T, int V, int D, const void* X, long ldx, const void* 
  * vocabulary; over more than one such piece dX is summed in FP32, in scratch or, one
  * of FP32 with rows on 16 bytes and D a multiple of 4, where it is. dX
  * (T x D) and dW (V x D) are BF16 or FP32; either may be NULL. In either type
- * they carry dz's rounding (half a step of BF16, 2^-8 of each at most): 1.5e-3 to
- * 2.3e-3 of their norm, beside the 1.7e-3 of a BF16 result's own. dW is not read
+ * they carry dz's rounding (half a step of BF16, 2^-8 of each at most): up to 2.3e-3
+ * of their norm, beside the 1.7e-3 of a BF16 result's own. z is summed as in gemm_ce,
+ * and dz of the target is a difference that keeps its digits: of a sure token it is as
+ * exact as its lse, off by 2^-23 of lse over 1 - p (p the target's probability). dW is not read
  * when beta == 0. Rows left out (see gemm_ce) get a dX of 0 and add nothing to
  * dW, whatever X, lse and dloss hold there (with a finite W).
  *

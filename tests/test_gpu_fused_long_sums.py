@@ -139,3 +139,30 @@ def test_bias_gradients_of_a_million_rows(tgemm, kernel, N):
     want = ((A.double() @ B.double()) * ref.act("silu", Z.double())[1]).sum(dim=0)
     tgemm.fused.set_fused_kernel(KERNELS[kernel])
     assert off(tgemm.gemm_act_grad(A, B, Z, "silu")[1], want) <= 5e-7
+
+
+@pytest.mark.parametrize("kernel", ["pairs", "few", "auto"])
+@pytest.mark.parametrize("k", [12, 16, 20])
+@pytest.mark.parametrize("T,V,D", [(1, 1000, 256), (40, 3000, 4096), (300, 1001, 1024), (600, 8000, 4096)])
+def test_gradients_of_sure_tokens(tgemm, kernel, k, T, V, D):
+    """Targets k above logits of spread 1: 1 - p is down to 1e-5, and p - 1, the most of a row's dX, is the difference of
+    an exponential and 1. Against the gradient with an exact lse it is off by lse's roundings (2^-23 of lse), an exponential's
+    (2^-21), what logits lose in parts of 4 stages (2.5e-7 of the target's, where lse and dz come from
+    different kernels), and its own rounding to BF16. The other entries share a row's relative error."""
+    W = normal(D + k, V, D, scale=D ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = (torch.randn((T, D), generator=g, device="cuda") + k * W[target].float()).to(BF16)
+    rows = torch.arange(T, device="cuda")
+    z = X.double() @ W.double().t()
+    exact = torch.logsumexp(z, dim=1)
+    p, picked = torch.exp(z - exact[:, None]), z[rows, target]
+    sure = -torch.expm1(picked - exact)
+    p[rows, target] = -sure
+    want_x, want_w = p @ W.double(), p.t() @ X.double()
+    each = 2.0 ** -8 + (2.0 ** -23 * exact + 2.0 ** -21 + 2.5e-7 * picked) / sure
+    tgemm.fused.set_fused_kernel(KERNELS[kernel])
+    _, lse = tgemm.gemm_ce(X, W, target)
+    dx, dw = tgemm.gemm_ce_grad(X, W, target, lse, torch.ones(T, device="cuda"), dx_dtype=F32, dw_dtype=F32)
+    assert (dx.double() - want_x).norm() <= (each * want_x.norm(dim=1)).norm()
+    assert (dw.double() - want_w).norm() <= (each[:, None] * (p.abs() * X.double().norm(dim=1)[:, None])).norm()

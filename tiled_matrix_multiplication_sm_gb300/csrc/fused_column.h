@@ -167,7 +167,8 @@ struct Column {
             for (int j = 0; j < 8; ++j)
                 if (FULL || j < n) {
                     const long long t = e.target[row + j];
-                    const float p = exp2_fast((x[j] * e.alpha - e.lse[row + j]) * LOG2E) - (t - e.first == c ? 1.0f : 0.0f);
+                    const float d = fmaf(x[j], e.alpha, -e.lse[row + j]);
+                    const float p = t - e.first == c ? expm1f(d) : exp2_fast(d * LOG2E);
                     // (A row left out may hold infinities.)
                     x[j] = t >= 0 && t < e.vocabulary ? p * (e.alpha * e.dloss[row + j]) : 0.0f;
                 }

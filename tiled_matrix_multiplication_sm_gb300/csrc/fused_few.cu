@@ -16,7 +16,7 @@
 //
 // Eighteen warps: 0 copies (TMA, as many stages as fit), 1 issues the MMAs, the
 // others are the epilogue, four sets of four on a quarter of the tokens each. Two accumulators (gated: of two halves each). Long sums that end in
-// 32 bits come in parts, as in fused_gemm.cu.
+// 32 bits, and logits, come in parts, as in fused_gemm.cu.
 
 #include "fused_column.h"
 
@@ -532,7 +532,8 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
     Params p;
     p.M = m.M;
     p.N = m.N;
-    p.chunks = kind == FUSED_CE && plan.chunks > 2 ? 2 : plan.chunks;     // (a part's 128 columns)
+    const bool logits = kind == FUSED_CE || kind == FUSED_CE_GRAD;
+    p.chunks = logits && plan.chunks > 2 ? 2 : plan.chunks;                // (a part's 128 columns)
     p.part_blocks = fused_parts(kind, true, (m.K - 1) / (plan.split * plan.slices) + 1, CHUNK_K * p.chunks).rest;
     p.kblocks = (int)(((long)m.K + p.chunks * CHUNK_K - 1) / (p.chunks * CHUNK_K));
     p.height = plan.height;
@@ -574,7 +575,7 @@ cudaError_t fused_few(FusedKind kind, const FusedProduct& m, const FusedEpilogue
         case FUSED_CE:
             return parts ? launch<FUSED_CE, false, true>(maps, p, s) : launch<FUSED_CE, false, false>(maps, p, s);
         default:
-            return launch<FUSED_CE_GRAD, false, false>(maps, p, s);
+            return parts ? launch<FUSED_CE_GRAD, false, true>(maps, p, s) : launch<FUSED_CE_GRAD, false, false>(maps, p, s);
     }
 }
 

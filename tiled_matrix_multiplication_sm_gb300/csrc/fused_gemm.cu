@@ -14,7 +14,7 @@
 // Gated products take 128 columns of g (the pair's first block) and the same 128
 // of u (its second) for a tile, so that a thread holds both of a row.
 //
-// Sums of more than a part's columns that end in 32 bits (LONG) come in parts,
+// Sums of more than a part's columns that end in 32 bits, and logits (LONG), come in parts,
 // accumulator by accumulator; the epilogue's warps add them up in registers and
 // work from there where they can, so that accumulators are free as soon as they
 // are read.
@@ -349,9 +349,9 @@ __device__ __forceinline__ void turn_boxes(const Params& p, const Maps* maps, ui
 }
 
 // ------------------------------------------------------------ cross entropy
-// Past this a row's differences from its maximum, or lse, are taken before their product with
-// log2(e): rounded, that product is off by as much as its bits are apart (128 and more from
-// 2^31 on: 2^128 is an infinity), and from 2.36e38 on an infinity itself.
+// Past this a row's differences from its maximum are taken before their product with log2(e):
+// rounded, that product is off by as much as its bits are apart (128 and more from 2^31 on:
+// 2^128 is an infinity), and from 2.36e38 on an infinity itself.
 constexpr float FAR = 1024.0f;
 
 // The maximum of this thread's row over its set's columns and the sum of exp(z -
@@ -410,13 +410,12 @@ struct CeRow {
     }
 };
 
-// 64 columns of the logits' gradient, rounded to BF16: operands of the two products that
-// follow. (In two BF16 numbers each those products, two thirds of the call's, would be twice as long.)
-__device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, uint32_t acc, int row0, int col,
+// 64 columns of the logits' gradient, whose sums sums(h, v) gives for either half, rounded to
+// BF16: operands of the two products that follow. (In two BF16 numbers each those products, two
+// thirds of the call's, would be twice as long.)
+template <typename Sums>
+__device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, uint8_t* bufs, Sums sums, int row0, int col,
                                              int& box, float lse, float scale, long long target, bool kept) {
-    // (Rounded once a row: 2^-24 of the logit, below BF16's rounding of the result by far up to FAR.)
-    const bool far = fabsf(lse) > FAR || fabsf(p.e.alpha) > FAR;
-    const float by = far ? LOG2E : p.e.alpha * LOG2E, less = far ? 0.0f : lse * LOG2E;
     const int lane = threadIdx.x & 31;
     uint8_t* buf = bufs + (box++ & 1) * BUF_BYTES;
     if (lane == 0) tma_store_wait_read<1>();
@@ -424,16 +423,22 @@ __device__ __forceinline__ void ce_grad_turn(const Params& p, const Maps* maps, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float v[32];
-        load_sums(acc + h * 32, v, p.kblocks);
+        sums(h, v);
         const long long t = target - (col + h * 32);
-        if (far)
+        const bool any = __any_sync(~0u, t >= 0 && t < 32);
+        float own = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], p.e.alpha, -lse);
+        for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], p.e.alpha, -lse);
+        if (any)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], by, -less));
-        if (__any_sync(~0u, t >= 0 && t < 32))
+            for (int j = 0; j < 32; ++j) own = t == j ? v[j] : own;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] -= t == j ? 1.0f : 0.0f;
+        for (int j = 0; j < 32; ++j) v[j] = exp2_fast(v[j] * LOG2E);
+        if (any) {
+            own = expm1f(own);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = t == j ? own : v[j];
+        }
         // (A row left out may hold infinities.)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = kept ? v[j] * scale : 0.0f;
@@ -802,8 +807,8 @@ __global__ void __launch_bounds__(Shape<KIND, GATED, BOXES>::THREADS, 1) fused_k
                         return true;
                     }
                     if constexpr (KIND == FUSED_CE_GRAD) {
-                        ce_grad_turn(p, &maps, bufs, acc + i * 64, row0, col, box, lse, scale, target - p.e.first,
-                                     target >= 0 && target < p.e.vocabulary);
+                        ce_grad_turn(p, &maps, bufs, [&](int h, float (&v)[32]) { sums(i * 2 + h, v); }, row0, col, box, lse,
+                                     scale, target - p.e.first, target >= 0 && target < p.e.vocabulary);
                         done();
                     } else if constexpr (BOXES) {
                         if (loads && !asked) ask(col);
@@ -952,7 +957,9 @@ cudaError_t fused_gemm(FusedKind kind, const FusedProduct& m, const FusedEpilogu
         case FUSED_CE:
             return parts ? launch_kernel<FUSED_CE, false, true, false>(maps, p, s)
                          : launch_kernel<FUSED_CE, false, false, false>(maps, p, s);
-        default: return launch_kernel<FUSED_CE_GRAD, false, false, true>(maps, p, s);
+        default:
+            return parts ? launch_kernel<FUSED_CE_GRAD, false, true, true>(maps, p, s)
+                         : launch_kernel<FUSED_CE_GRAD, false, false, true>(maps, p, s);
     }
 }
 

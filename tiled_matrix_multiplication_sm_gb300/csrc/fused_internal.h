@@ -85,7 +85,8 @@ constexpr int FUSED_FEW_RING = 209 * 1024;
 // 5001 x 1537 with R and Z in two parts 93 us for 76 in one of 1.6e-6; column sums of 65536 rows,
 // K = 4096, in parts of a mean of 14.5 1.04e-6). A loss is a small difference of large logits,
 // off by what its target's loses: parts of 4, for few tokens of 2 (8192 x 65536 x 4096, us, in
-// parts of 7, 5, 4, 3: 2206, 2203, 2213, 2287).
+// parts of 7, 5, 4, 3: 2206, 2203, 2213, 2287); and the logits that its gradient makes again
+// come in the same ones, or exp(z - lse) - 1 of a sure token is off by far more than lse is.
 //
 // On pairs the MMAs are two parts ahead of the epilogue at most, and that of a
 // gated gradient takes 9 us, the time of 34 stages: the first two parts are

@@ -72,7 +72,7 @@ FusedParts fused_parts(FusedKind kind, bool few, int K, int chunk_k) {
         const int n = stages > 0 ? (int)up(stages, up(stages, most)) : 1;
         return FusedParts{n, n};
     };
-    if (kind == FUSED_CE) return even(few ? 2 : 4);
+    if (kind == FUSED_CE || kind == FUSED_CE_GRAD) return even(few ? 2 : 4);
     // On pairs: the first two parts up to 18, as long as a mean of 13 allows it, the others even.
     constexpr int EVEN = 13;
     if (few || stages <= EVEN) return even(EVEN);
