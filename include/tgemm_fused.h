@@ -20,7 +20,7 @@
  * terms have random signs, 2e-6 where all have one (an FP32 C and db: parts of up to
  * 1152 columns of K; loss and lse: 256; a bias or residual that cancels
  * most of the sums leaves that much of the sums' norm, and a loss far below its
- * logits is off by 3e-7 of them; gemm_ce_grad's results are as exact as its BF16 dz).
+ * logits is off by 4e-7 of them; gemm_ce_grad's results are as exact as its BF16 dz).
  * Sums that end in BF16 are one part, which loses less than their rounding up to K =
  * 65536 (4e-4 of the norm where all terms have one sign, 1.6e-3 at 262144). Values
  * go from the sum to the result in FP32 and are rounded once, to nearest even,
